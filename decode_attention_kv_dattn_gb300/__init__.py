@@ -25,7 +25,7 @@ lib = ctypes.CDLL(LIB_PATH)
 # ---------------------------------------------------------------- C types
 
 OK, EINVAL, EXCEEDS, ECUDA, EINDEX, ETIMEOUT, EUNSUPPORTED, ELENGTH, ERANGE = range(9)
-CACHE_RING, CACHE_PAGED = 0, 1
+CACHE_RING, CACHE_PAGED, CACHE_STATE = 0, 1, 2
 KV_BF16, KV_E4M3 = 0, 1
 
 _vp = ctypes.c_void_p
@@ -36,7 +36,20 @@ class LayerConfig(ctypes.Structure):
     _fields_ = [("cache_kind", _int), ("ring_slots", _int), ("page_size", _int),
                 ("rotary_dim", _int), ("rope_theta", ctypes.c_double),
                 ("q_norm_weight", _vp), ("k_norm_weight", _vp), ("norm_eps", ctypes.c_double),
-                ("kv_format", _int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("kv_format", _int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("log_decay", _vp)]
+
+
+def _host_f32(x, n, what):
+    """A contiguous host array of n fp32 values (numpy, a CPU tensor or a list), or None."""
+    if x is None:
+        return None
+    if isinstance(x, torch.Tensor) and x.is_cuda:
+        raise TypeError(f"{what}: a host array")
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    if x.shape != (n,):
+        raise ValueError(f"{what}: shape {x.shape}, expected ({n},)")
+    return x
 
 
 def _host_bf16(w, D, what):
@@ -57,7 +70,8 @@ def _host_bf16(w, D, what):
 class Config(ctypes.Structure):
     _fields_ = [("num_q_heads", _int), ("num_kv_heads", _int), ("head_dim", _int),
                 ("max_streams", _int), ("max_context", _int), ("max_verify_rows", _int),
-                ("num_layers", _int), ("layers", ctypes.POINTER(LayerConfig))]
+                ("num_layers", _int), ("layers", ctypes.POINTER(LayerConfig)),
+                ("max_selected_pages", _int)]
 
 
 class Cache(ctypes.Structure):
@@ -69,6 +83,11 @@ class Cache(ctypes.Structure):
 class DecodeArgs(ctypes.Structure):
     _fields_ = [("num_streams", _int), ("q", _vp), ("k_new", _vp), ("v_new", _vp), ("gate", _vp),
                 ("pos", _vp), ("out", _vp), ("max_seq_len", _int), ("write_back", _int)]
+
+
+class PageSelection(ctypes.Structure):
+    _fields_ = [("summary", _vp), ("num_pages", _int), ("keep_first", _int), ("keep_last", _int),
+                ("selected", _vp)]
 
 
 class VerifyArgs(ctypes.Structure):
@@ -84,6 +103,11 @@ lib.dattn_append_kv.argtypes = [_vp, _int, ctypes.POINTER(Cache), _int, _int, _v
 lib.dattn_append_kv.restype = _int
 lib.dattn_decode.argtypes = [_vp, _int, ctypes.POINTER(Cache), ctypes.POINTER(DecodeArgs), _vp]
 lib.dattn_decode.restype = _int
+lib.dattn_sparse_decode.argtypes = [_vp, _int, ctypes.POINTER(Cache), ctypes.POINTER(DecodeArgs),
+                                    ctypes.POINTER(PageSelection), _vp]
+lib.dattn_sparse_decode.restype = _int
+lib.dattn_summarize.argtypes = [_vp, _int, ctypes.POINTER(Cache), _vp, _int, _int, _vp, _vp, _vp]
+lib.dattn_summarize.restype = _int
 lib.dattn_verify.argtypes = [_vp, _int, ctypes.POINTER(Cache), ctypes.POINTER(VerifyArgs), _vp]
 lib.dattn_verify.restype = _int
 lib.dattn_commit.argtypes = [_vp, _int, ctypes.POINTER(Cache), _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -105,7 +129,7 @@ DEBUG_WITHHOLD_Q = 1
 
 EXPORTS = ("dattn_create", "dattn_append_kv", "dattn_decode", "dattn_verify", "dattn_commit", "dattn_prefill",
            "dattn_get_error", "dattn_error_string", "dattn_destroy", "dattn_decode_noalloc",
-           "dattn_debug_config")
+           "dattn_debug_config", "dattn_sparse_decode", "dattn_summarize")
 
 
 class DattnError(RuntimeError):
@@ -160,34 +184,46 @@ def paged_cache(k, v, block_table, seq_len) -> Cache:
     return c
 
 
+def state_cache(state, stream_rows=None) -> Cache:
+    """state: [rows, Hkv, D, D] fp32 of a state layer; stream_rows: [B] int32 or None.
+    The descriptor holds the tensors it points to, so they live as long as it does."""
+    if state.dtype != torch.float32:
+        raise TypeError("a state layer's cache is fp32")
+    c = Cache(_ptr(state), None, state.shape[0], None, None, _ptr(stream_rows), None, 0, None)
+    c._tensors = (state, stream_rows)
+    return c
+
+
 # ---------------------------------------------------------------- handle
 
 class Handle:
     """A dattn handle: per-layer RoPE tables and the split-K workspace."""
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, layers, max_streams,
-                 max_context=0, max_verify_rows=0, device=None):
+                 max_context=0, max_verify_rows=0, device=None, max_selected_pages=0):
         if device is None:
             device = torch.cuda.current_device()
         self.device = device
-        # QK-norm weights (layer keys "q_norm", "k_norm", "norm_eps"): host
-        # arrays the config points at, kept alive with it (dattn_create copies
+        # QK-norm weights (layer keys "q_norm", "k_norm", "norm_eps") and state
+        # layers' decays ("log_decay" [Hkv]): host arrays the config points at, kept alive with it (dattn_create copies
         # them; decode_noalloc reads them on every call)
         self._norm_keep = []
         cfgs = []
         for l in layers:
             qn = _host_bf16(l.get("q_norm"), head_dim, "q_norm")
             kn = _host_bf16(l.get("k_norm"), head_dim, "k_norm")
-            self._norm_keep += [qn, kn]
+            ld = _host_f32(l.get("log_decay"), num_kv_heads, "log_decay")
+            self._norm_keep += [qn, kn, ld]
             cfgs.append(LayerConfig(l["kind"], l.get("ring_slots", 0), l.get("page_size", 0),
                                     l.get("rotary_dim", 0), float(l.get("rope_theta", 0.0)),
                                     None if qn is None else qn.ctypes.data,
                                     None if kn is None else kn.ctypes.data,
                                     float(l.get("norm_eps", 0.0)), int(l.get("kv_format", KV_BF16)),
-                                    float(l.get("k_scale", 1.0)), float(l.get("v_scale", 1.0))))
+                                    float(l.get("k_scale", 1.0)), float(l.get("v_scale", 1.0)),
+                                    None if ld is None else ld.ctypes.data))
         self._layers = (LayerConfig * len(layers))(*cfgs)
         self.config = Config(num_q_heads, num_kv_heads, head_dim, max_streams, max_context,
-                             max_verify_rows, len(layers), self._layers)
+                             max_verify_rows, len(layers), self._layers, max_selected_pages)
         h = _vp()
         _check(lib.dattn_create(ctypes.byref(self.config), device, ctypes.byref(h)), "dattn_create")
         self._h = h
@@ -220,6 +256,27 @@ class Handle:
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
                                 _stream_ptr(stream)), "dattn_decode")
 
+    def sparse_decode(self, layer, cache: Cache, summary, q, k_new, v_new, pos, out, num_pages, keep_first=1,
+                      keep_last=1, gate=None, max_seq_len=0, write_back=True, selected=None, stream=None):
+        """decode over the num_pages pages of each stream and KV head that score highest
+        (the first keep_first and the newest keep_last are always read): summary
+        [pages, Hkv, D] bf16 as `summarize` keeps it; selected [B, Hkv, num_pages] int32
+        receives the pages (ascending, then -1) if given. The handle needs
+        max_selected_pages >= num_pages."""
+        args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
+                          _ptr(out), int(max_seq_len), int(write_back))
+        sel = PageSelection(_ptr(summary), int(num_pages), int(keep_first), int(keep_last), _ptr(selected))
+        _check(lib.dattn_sparse_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args), ctypes.byref(sel),
+                                       _stream_ptr(stream)), "dattn_sparse_decode")
+
+    def summarize(self, layer, cache: Cache, summary, start_index, count, max_tokens, stream=None):
+        """Summaries (bf16 means of the stored keys, [pages, Hkv, D]) of the pages that the
+        new tokens [start_index, start_index + count) of each row completed; start_index,
+        count: [B] int32, count <= max_tokens."""
+        _check(lib.dattn_summarize(self._h, layer, ctypes.byref(cache), _ptr(summary), start_index.shape[0],
+                                   int(max_tokens), _ptr(start_index), _ptr(count), _stream_ptr(stream)),
+               "dattn_summarize")
+
     def verify(self, layer, cache: Cache, q, k, v, parent, out, gate=None, max_prefix_len=0,
                write_back=True, pos=None, stream=None):
         """q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16; parent [S, T] int32; out [S, T, Hq, D]
@@ -248,7 +305,7 @@ class Handle:
     def debug_config(self, flags=0, wait_limit_us=0):
         """Testing aid: the limit of the device's bounded waits and fault
         injection on the host's side of the wait (see dattn_debug_config)."""
-        _check(lib.dattn_debug_config(self._h, int(flags), int(wait_limit_us)), "dattn_debug_config")
+        _check(lib.dattn_debug_config(self._h, int(flags), int(wait_limit_us)), "dattn_debug_config", "dattn_sparse_decode", "dattn_summarize")
 
     def get_error(self, stream=None) -> int:
         """Synchronize the stream; return and clear the sticky device status."""

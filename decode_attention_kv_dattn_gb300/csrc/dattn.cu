@@ -69,6 +69,15 @@ struct dattn_handle {
   int32_t* chain = nullptr;    // prefill: chain-tree parents of a chunk, [S][Tc]
   int32_t* pmeta = nullptr;    // prefill chunk state: 5 arrays of [max_streams]
   size_t vpart_slots = 0;
+  // Decode over selected pages (max_selected_pages > 0): the screened scores
+  // and their bounds, the exact keys of a border with many pages, and the page
+  // table and lengths that the decode kernel then reads.
+  int max_selected = 0, sel_pitch = 0, sel_chunks = 0;
+  float *sel_scores = nullptr, *sel_cnorm = nullptr, *sel_qnorm = nullptr;
+  uint64_t* sel_keys = nullptr;
+  int32_t *sel_table = nullptr, *sel_len = nullptr;
+  std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
+  float* sums = nullptr;                  // state layers: the prompt form's segment states
   int* err = nullptr;
   uint64_t wait_ns = kDefaultWaitNs;  // limit of the kernels' bounded waits
   int debug_flags = 0;                // dattn_debug_config
@@ -128,7 +137,9 @@ CacheView make_view(const dattn_handle* h, const dattn_layer_config& L, const da
 }
 
 int check_cache(const dattn_layer_config& L, const dattn_cache* c) {
-  if (!c || !c->k || !c->v || c->n_rows <= 0) return DATTN_EINVAL;
+  if (!c || !c->k || c->n_rows <= 0) return DATTN_EINVAL;
+  if (L.cache_kind == DATTN_CACHE_STATE) return aligned16(c->k) ? DATTN_OK : DATTN_EINVAL;
+  if (!c->v) return DATTN_EINVAL;
   if (!aligned16(c->k) || !aligned16(c->v)) return DATTN_EINVAL;
   if (L.cache_kind == DATTN_CACHE_RING) {
     if (!c->ring_head || !c->ring_count) return DATTN_EINVAL;
@@ -136,6 +147,29 @@ int check_cache(const dattn_layer_config& L, const dattn_cache* c) {
     if (!c->block_table || !c->seq_len || c->bt_stride <= 0) return DATTN_EINVAL;
   }
   return DATTN_OK;
+}
+
+// The arguments that the step and the prompt form of a state layer share.
+LinearArgs linear_args(const dattn_handle* h, int layer, const dattn_cache* cache, int B, const void* q,
+                       const void* k, const void* v, const void* gate, float* out) {
+  LinearArgs a{};
+  a.state = static_cast<float*>(cache->k);
+  a.n_rows = cache->n_rows;
+  a.stream_rows = cache->stream_rows;
+  a.B = B;
+  a.Hkv = h->Hkv;
+  a.G = h->G;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.out = out;
+  a.decay = h->decay[layer];
+  a.log_decay = a.decay + static_cast<size_t>(h->Hkv) * kDecayStride;
+  a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(h->D)));
+  a.sums = h->sums;
+  a.err = h->err;
+  return a;
 }
 
 // One pass of the verify pipeline (three launches): the RoPE prologue, the
@@ -231,6 +265,167 @@ int verify_round(dattn_t* h, int layer, const VerifyRound& r, cudaStream_t s) {
   return cuda_status(launch_verify_combine(vc, h->D, s), "verify combine");
 }
 
+// Scores and selection of a decode over selected pages (two launches), into
+// the handle's page table and lengths.
+int select_pages(dattn_t* h, int layer, const CacheView& view, const dattn_decode_args* args,
+                 const dattn_page_selection* sel, int n_max, cudaStream_t s) {
+  const dattn_layer_config& L = h->layers[layer];
+  const int pages = static_cast<int>((static_cast<int64_t>(n_max) + L.page_size - 1) / L.page_size);
+  PageSelectArgs a{};
+  a.c = view;
+  a.B = args->num_streams;
+  a.Hkv = h->Hkv;
+  a.G = h->G;
+  a.max_len = n_max;
+  a.num_pages = sel->num_pages;
+  a.keep_first = sel->keep_first;
+  a.keep_last = sel->keep_last;
+  a.q = static_cast<const uint16_t*>(args->q);
+  a.pos = args->pos;
+  a.rope_step = h->rope_step[layer];
+  a.r = L.rotary_dim;
+  a.q_norm = h->q_norm[layer];
+  a.norm_eps = L.norm_eps;
+  a.summary = static_cast<const uint16_t*>(sel->summary);
+  a.chunk_pages = score_chunk_pages(a.B * a.Hkv, pages, h->num_sms);
+  a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
+  a.pitch = h->sel_pitch;
+  a.scores = h->sel_scores;
+  a.cnorm = h->sel_cnorm;
+  a.qnorm = h->sel_qnorm;
+  a.keys = h->sel_keys;
+  a.max_words = (pages + 31) / 32;
+  a.table = h->sel_table;
+  a.seq_out = h->sel_len;
+  a.selected = sel->selected;
+  a.err = h->err;
+  PageScoreArgs p{};
+  p.c = a.c;
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.G = a.G;
+  p.max_len = a.max_len;
+  p.num_pages = a.num_pages;
+  p.keep_first = a.keep_first;
+  p.keep_last = a.keep_last;
+  p.q = a.q;
+  p.pos = a.pos;
+  p.rope_step = a.rope_step;
+  p.r = a.r;
+  p.q_norm = a.q_norm;
+  p.norm_eps = a.norm_eps;
+  p.summary = a.summary;
+  p.chunk_pages = a.chunk_pages;
+  p.chunks = a.chunks;
+  p.pitch = a.pitch;
+  p.scores = h->sel_scores;
+  p.cnorm = h->sel_cnorm;
+  p.qnorm = h->sel_qnorm;
+  p.err = h->err;
+  int rc = DATTN_OK;
+  // (a call whose streams all have at most num_pages pages needs no score)
+  if (pages > sel->num_pages) rc = cuda_status(launch_page_scores(p, h->D, s), "page scores");
+  if (rc == DATTN_OK) rc = cuda_status(launch_page_select(a, h->D, s), "page selection");
+  return rc;
+}
+
+// dattn_decode, and dattn_sparse_decode with a selection: the pages' scores and
+// the selection first, then the same decode over the selected pages.
+int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
+                const dattn_page_selection* sel, dattn_stream_t stream) {
+  if (!h || !args || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
+  const dattn_layer_config& L = h->layers[layer];
+  int rc = check_cache(L, cache);
+  if (rc != DATTN_OK) return rc;
+  if (sel && L.cache_kind != DATTN_CACHE_PAGED) return DATTN_EUNSUPPORTED;
+  const int B = args->num_streams;
+  if (B <= 0) return DATTN_EINVAL;
+  if (B > h->max_streams) return DATTN_EXCEEDS;
+  if (!args->q || !args->k_new || !args->v_new || !args->pos || !args->out) return DATTN_EINVAL;
+  if (!aligned16(args->q) || !aligned16(args->k_new) || !aligned16(args->v_new) ||
+      !aligned16(args->out))
+    return DATTN_EINVAL;
+  if (L.cache_kind == DATTN_CACHE_STATE) {
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return DATTN_ECUDA;
+    LinearArgs la = linear_args(h, layer, cache, B, args->q, args->k_new, args->v_new, args->gate, args->out);
+    la.write_back = args->write_back;
+    rc = cuda_status(launch_linear_step(la, h->D, reinterpret_cast<cudaStream_t>(stream)), "linear step");
+    if (rc == DATTN_OK) record_launch(stream, args->write_back ? cache->k : nullptr);
+    return rc;
+  }
+  int n_max;
+  if (L.cache_kind == DATTN_CACHE_RING) {
+    n_max = L.ring_slots;
+  } else {
+    n_max = args->max_seq_len > 0 ? args->max_seq_len : h->max_context;
+    if (n_max > h->max_context) return DATTN_EXCEEDS;
+  }
+  if (sel) {
+    if (!sel->summary || !aligned16(sel->summary) || sel->keep_first < 0 || sel->keep_last < 1) return DATTN_EINVAL;
+    if (sel->num_pages > h->max_selected) return DATTN_EXCEEDS;
+    if (static_cast<int64_t>(sel->keep_first) + sel->keep_last > sel->num_pages) return DATTN_EINVAL;
+  }
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return DATTN_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+  CacheView view = make_view(h, L, cache);
+  if (sel) {
+    rc = select_pages(h, layer, view, args, sel, n_max, s);
+    if (rc != DATTN_OK) return rc;
+    view.block_table = h->sel_table;
+    view.bt_stride = sel->num_pages + 1;
+    view.bt_heads = 1;
+    view.seq_len = h->sel_len;
+    n_max = static_cast<int>(std::min<int64_t>(n_max, static_cast<int64_t>(sel->num_pages) * L.page_size));
+  }
+  const bool f8 = L.kv_format == DATTN_KV_E4M3;
+  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, f8));
+  if (static_cast<size_t>(ctas) + static_cast<size_t>(B) * h->Hkv > h->part_units) return DATTN_EXCEEDS;
+  DecodeArgs da{};
+  da.c = view;
+  if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) return DATTN_EUNSUPPORTED;
+  da.B = B;
+  da.Hkv = h->Hkv;
+  da.G = h->G;
+  da.max_len = n_max;
+  da.q = static_cast<const uint16_t*>(args->q);
+  da.k_new = static_cast<const uint16_t*>(args->k_new);
+  da.v_new = static_cast<const uint16_t*>(args->v_new);
+  da.gate = static_cast<const uint16_t*>(args->gate);
+  da.pos = args->pos;
+  da.rope_step = h->rope_step[layer];
+  da.r = L.rotary_dim;
+  da.q_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(h->D)));
+  da.out = args->out;
+  da.write_back = args->write_back;
+  const unsigned half = h->decode_calls & 1u;
+  da.part = h->part[half];
+  da.counters = h->counters[half];
+  da.err = h->err;
+  da.early = !sel && !prev_launch_writes(stream, cache->k);
+  da.late_meta = sel != nullptr;
+  da.wait_ns = h->wait_ns;
+  da.debug_flags = h->debug_flags;
+  da.q_norm = h->q_norm[layer];
+  da.k_norm = h->k_norm[layer];
+  da.norm_eps = L.norm_eps;
+  if (f8) {
+    // the K scale rides on q's pre-scale; V's is applied to each partial output
+    da.f8 = 1;
+    da.k_scale = L.k_scale;
+    da.v_scale = L.v_scale;
+    da.q_scale = static_cast<float>(static_cast<double>(da.q_scale) * L.k_scale);
+  }
+  rc = cuda_status(launch_decode(da, h->D, ctas, s), "decode");
+  if (rc == DATTN_OK) {
+    record_launch(stream, args->write_back ? cache->k : nullptr);
+    ++h->decode_calls;
+  }
+  return rc;
+}
+
 }  // namespace
 
 extern "C" {
@@ -267,6 +462,13 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
       if (L.ring_slots <= 0) return DATTN_EINVAL;
     } else if (L.cache_kind == DATTN_CACHE_PAGED) {
       if (L.page_size <= 0) return DATTN_EINVAL;
+    } else if (L.cache_kind == DATTN_CACHE_STATE) {
+      if (!L.log_decay) return DATTN_EINVAL;
+      for (int i = 0; i < Hkv; ++i)
+        if (!(L.log_decay[i] <= 0.f) || !std::isfinite(L.log_decay[i])) return DATTN_EINVAL;
+      // the decay carries the position; q, k and v enter as they are
+      if (L.rotary_dim != 0 || L.q_norm_weight || L.k_norm_weight || L.kv_format != DATTN_KV_BF16)
+        return DATTN_EUNSUPPORTED;
     } else {
       return DATTN_EINVAL;
     }
@@ -277,6 +479,16 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     if (L.kv_format == DATTN_KV_E4M3 &&
         !(L.k_scale > 0.f && L.v_scale > 0.f && std::isfinite(L.k_scale) && std::isfinite(L.v_scale)))
       return DATTN_EINVAL;
+  }
+  if (cfg->max_selected_pages < 0) return DATTN_EINVAL;
+  int sel_pitch = 0;  // pages of the longest stream
+  if (cfg->max_selected_pages > 0) {
+    for (int l = 0; l < cfg->num_layers; ++l)
+      if (cfg->layers[l].cache_kind == DATTN_CACHE_PAGED)
+        sel_pitch = std::max<int>(sel_pitch, static_cast<int>((static_cast<int64_t>(cfg->max_context) +
+                                                              cfg->layers[l].page_size - 1) / cfg->layers[l].page_size));
+    if ((static_cast<int64_t>(sel_pitch) + 31) / 32 * 4 + 16 + static_cast<int64_t>(G) * D * 8 > kSelectSmemMax)
+      return DATTN_EUNSUPPORTED;
   }
   DeviceGuard guard(device);
   if (!guard.ok) return DATTN_ECUDA;
@@ -337,6 +549,45 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     L.q_norm_weight = L.k_norm_weight = nullptr;
   }
 
+  // Decays of the state layers, from the logarithms in fp64, and the
+  // logarithms themselves; the handle keeps no host pointer of the caller's.
+  bool has_state = false;
+  for (dattn_layer_config& L : h->layers) {
+    float* dev = nullptr;
+    h->decay.push_back(nullptr);
+    if (L.cache_kind == DATTN_CACHE_STATE) {
+      has_state = true;
+      std::vector<float> f(static_cast<size_t>(Hkv) * (kDecayStride + 1));
+      for (int i = 0; i < Hkv; ++i) {
+        float* p = f.data() + static_cast<size_t>(i) * kDecayStride;
+        const double g = L.log_decay[i];
+        for (int x = 0; x <= kLinearChunk; ++x) p[x] = static_cast<float>(std::exp(g * x));
+        p[kLinearChunk + 1] = static_cast<float>(std::exp(g) - static_cast<double>(p[1]));
+        p[kLinearChunk + 2] = static_cast<float>(std::exp(g * kLinearChunk) - static_cast<double>(p[kLinearChunk]));
+        f[static_cast<size_t>(Hkv) * kDecayStride + i] = L.log_decay[i];
+      }
+      if (cudaMalloc(&dev, f.size() * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+      h->decay.back() = dev;
+      if (cudaMemcpy(dev, f.data(), f.size() * sizeof(float), cudaMemcpyHostToDevice) != cudaSuccess)
+        return fail(DATTN_ECUDA);
+    }
+    L.log_decay = nullptr;
+  }
+  (void)has_state;
+  if (sel_pitch > 0) {
+    const size_t units = static_cast<size_t>(h->max_streams) * Hkv;
+    h->max_selected = cfg->max_selected_pages;
+    h->sel_pitch = sel_pitch;
+    h->sel_chunks = (sel_pitch + kScoreMinPages - 1) / kScoreMinPages;
+    if (cudaMalloc(&h->sel_scores, units * h->sel_pitch * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_keys, units * h->sel_pitch * sizeof(uint64_t)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_cnorm, units * h->sel_chunks * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_qnorm, units * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_table, units * (static_cast<size_t>(h->max_selected) + 1) * sizeof(int32_t)) != cudaSuccess)
+      return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_len, h->max_streams * sizeof(int32_t)) != cudaSuccess) return fail(DATTN_ECUDA);
+  }
+
   // Workspace. Rows of rotated q/k: one per stream (decode) or per verify row.
   const size_t rows = static_cast<size_t>(h->max_streams) *
                       (h->max_verify_rows > 1 ? h->max_verify_rows : 1);
@@ -393,6 +644,14 @@ void dattn_destroy(dattn_t* h) {
     cudaFree(h->counters[i]);
   }
   cudaFree(h->vpart);
+  cudaFree(h->sel_scores);
+  cudaFree(h->sel_keys);
+  cudaFree(h->sel_cnorm);
+  cudaFree(h->sel_qnorm);
+  cudaFree(h->sel_table);
+  cudaFree(h->sel_len);
+  for (float* p : h->decay) cudaFree(p);
+  cudaFree(h->sums);
   cudaFree(h->tiles);
   cudaFree(h->err);
   delete h;
@@ -434,6 +693,7 @@ int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_str
                     dattn_stream_t stream) {
   if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind == DATTN_CACHE_STATE) return DATTN_EUNSUPPORTED;
   int rc = check_cache(L, cache);
   if (rc != DATTN_OK) return rc;
   if (num_streams <= 0 || max_tokens < 0 || !start_index || !count || !k || !v) return DATTN_EINVAL;
@@ -474,6 +734,7 @@ int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int num_stream
                  const int32_t* pos, dattn_stream_t stream) {
   if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind == DATTN_CACHE_STATE) return DATTN_EUNSUPPORTED;
   int rc = check_cache(L, cache);
   if (rc != DATTN_OK) return rc;
   if (num_streams <= 0 || rows <= 0 || !k || !v || !parent || !accepted || !num_accepted) return DATTN_EINVAL;
@@ -512,70 +773,41 @@ int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int num_stream
 
 int dattn_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                  dattn_stream_t stream) {
-  if (!h || !args || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
+  return decode_call(h, layer, cache, args, nullptr, stream);
+}
+
+int dattn_sparse_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
+                        const dattn_page_selection* sel, dattn_stream_t stream) {
+  if (!sel) return DATTN_EINVAL;
+  return decode_call(h, layer, cache, args, sel, stream);
+}
+
+int dattn_summarize(dattn_t* h, int layer, const dattn_cache* cache, void* summary, int num_streams, int max_tokens,
+                    const int32_t* start_index, const int32_t* count, dattn_stream_t stream) {
+  if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind != DATTN_CACHE_PAGED) return DATTN_EUNSUPPORTED;
   int rc = check_cache(L, cache);
   if (rc != DATTN_OK) return rc;
-  const int B = args->num_streams;
-  if (B <= 0) return DATTN_EINVAL;
-  if (B > h->max_streams) return DATTN_EXCEEDS;
-  if (!args->q || !args->k_new || !args->v_new || !args->pos || !args->out) return DATTN_EINVAL;
-  if (!aligned16(args->q) || !aligned16(args->k_new) || !aligned16(args->v_new) ||
-      !aligned16(args->out))
-    return DATTN_EINVAL;
-  int n_max;
-  if (L.cache_kind == DATTN_CACHE_RING) {
-    n_max = L.ring_slots;
-  } else {
-    n_max = args->max_seq_len > 0 ? args->max_seq_len : h->max_context;
-    if (n_max > h->max_context) return DATTN_EXCEEDS;
-  }
+  if (num_streams <= 0 || max_tokens < 0 || !summary || !start_index || !count) return DATTN_EINVAL;
+  if (!aligned16(summary)) return DATTN_EINVAL;
+  if (num_streams > 65535) return DATTN_EXCEEDS;
+  if (max_tokens == 0) return DATTN_OK;
   DeviceGuard guard(h->device);
   if (!guard.ok) return DATTN_ECUDA;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-
-  const bool f8 = L.kv_format == DATTN_KV_E4M3;
-  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, f8));
-  if (static_cast<size_t>(ctas) + static_cast<size_t>(B) * h->Hkv > h->part_units) return DATTN_EXCEEDS;
-  DecodeArgs da{};
-  da.c = make_view(h, L, cache);
-  if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) return DATTN_EUNSUPPORTED;
-  da.B = B;
-  da.Hkv = h->Hkv;
-  da.G = h->G;
-  da.max_len = n_max;
-  da.q = static_cast<const uint16_t*>(args->q);
-  da.k_new = static_cast<const uint16_t*>(args->k_new);
-  da.v_new = static_cast<const uint16_t*>(args->v_new);
-  da.gate = static_cast<const uint16_t*>(args->gate);
-  da.pos = args->pos;
-  da.rope_step = h->rope_step[layer];
-  da.r = L.rotary_dim;
-  da.q_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(h->D)));
-  da.out = args->out;
-  da.write_back = args->write_back;
-  const unsigned half = h->decode_calls & 1u;
-  da.part = h->part[half];
-  da.counters = h->counters[half];
-  da.err = h->err;
-  da.early = !prev_launch_writes(stream, cache->k);
-  da.wait_ns = h->wait_ns;
-  da.debug_flags = h->debug_flags;
-  da.q_norm = h->q_norm[layer];
-  da.k_norm = h->k_norm[layer];
-  da.norm_eps = L.norm_eps;
-  if (f8) {
-    // the K scale rides on q's pre-scale; V's is applied to each partial output
-    da.f8 = 1;
-    da.k_scale = L.k_scale;
-    da.v_scale = L.v_scale;
-    da.q_scale = static_cast<float>(static_cast<double>(da.q_scale) * L.k_scale);
-  }
-  rc = cuda_status(launch_decode(da, h->D, ctas, s), "decode");
-  if (rc == DATTN_OK) {
-    record_launch(stream, args->write_back ? cache->k : nullptr);
-    ++h->decode_calls;
-  }
+  SummarizeArgs a{};
+  a.c = make_view(h, L, cache);
+  a.B = num_streams;
+  a.Hkv = h->Hkv;
+  a.max_tokens = max_tokens;
+  a.start_index = start_index;
+  a.count = count;
+  a.summary = static_cast<uint16_t*>(summary);
+  a.f8 = L.kv_format == DATTN_KV_E4M3;
+  a.k_scale = L.k_scale;
+  a.err = h->err;
+  rc = cuda_status(launch_summarize(a, h->D, reinterpret_cast<cudaStream_t>(stream)), "summarize");
+  if (rc == DATTN_OK) record_launch(stream, nullptr);
   return rc;
 }
 
@@ -583,6 +815,7 @@ int dattn_verify(dattn_t* h, int layer, const dattn_cache* cache, const dattn_ve
                  dattn_stream_t stream) {
   if (!h || !args || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind == DATTN_CACHE_STATE) return DATTN_EUNSUPPORTED;
   const bool ring = L.cache_kind == DATTN_CACHE_RING;
   // the prefix pass reads pages as 16-row groups, of bf16
   if ((!ring && L.page_size % 16 != 0) || L.kv_format != DATTN_KV_BF16) return DATTN_EUNSUPPORTED;
@@ -629,6 +862,22 @@ int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_strea
                   const int32_t* start_pos, float* out, dattn_stream_t stream) {
   if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind == DATTN_CACHE_STATE) {
+    const int rc = check_cache(L, cache);
+    if (rc != DATTN_OK) return rc;
+    if (num_streams <= 0 || max_tokens < 0 || !q || !k || !v || !count || !out) return DATTN_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DATTN_EINVAL;
+    if (num_streams > h->max_streams) return DATTN_EXCEEDS;
+    if (max_tokens == 0) return DATTN_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return DATTN_ECUDA;
+    LinearArgs la = linear_args(h, layer, cache, num_streams, q, k, v, gate, out);
+    la.T = max_tokens;
+    la.count = count;
+    const int st = cuda_status(launch_linear_prompt(la, h->D, reinterpret_cast<cudaStream_t>(stream)), "linear prompt");
+    if (st == DATTN_OK) record_launch(stream, cache->k);
+    return st;
+  }
   const bool ring = L.cache_kind == DATTN_CACHE_RING;
   if ((!ring && L.page_size % 16 != 0) || L.kv_format != DATTN_KV_BF16) return DATTN_EUNSUPPORTED;
   int rc = check_cache(L, cache);

@@ -43,6 +43,8 @@ struct CacheView {
   const int32_t* block_table;  // [B, bt_stride]
   int bt_stride;
   const int32_t* seq_len;      // [B]
+  int bt_heads;                // nonzero: block_table is [B * Hkv, bt_stride], a table for each KV head
+                               // (decode over selected pages)
 };
 
 // RoPE prologue: rotates q (fp32 out, pre-scaled) and k (bf16 entry out) of
@@ -118,6 +120,96 @@ struct DecodeArgs {
   // cached value = e4m3 * scale. q_scale then includes k_scale.
   int f8;
   float k_scale, v_scale;
+  int late_meta;               // nonzero: the preceding launch writes the page table and lengths, so
+                               // nothing of them is read before it has completed (early is 0 then)
+};
+
+// Page summaries: the bf16 mean of a page's stored keys (times k_scale), for
+// every page whose last token is among a row's `count` new tokens.
+struct SummarizeArgs {
+  CacheView c;
+  int B, Hkv, max_tokens;
+  const int32_t* start_index;  // [B]
+  const int32_t* count;        // [B]
+  uint16_t* summary;           // [pages, Hkv, D]
+  int f8;
+  float k_scale;
+  int* err;
+};
+
+// Screened scores of every candidate page of each (stream, KV head) unit: the
+// pages [keep_first, pages - keep_last) of streams with more than num_pages.
+struct PageScoreArgs {
+  CacheView c;
+  int B, Hkv, G;
+  int max_len;
+  int num_pages, keep_first, keep_last;
+  const uint16_t* q;           // [B, Hq, D]
+  const int32_t* pos;          // [B]
+  const uint64_t* rope_step;
+  int r;
+  const uint16_t* q_norm;      // [D] or null
+  double norm_eps;
+  const uint16_t* summary;     // [pages, Hkv, D]
+  int chunk_pages, chunks;     // pages of a CTA, CTAs of a unit
+  int pitch;                   // floats between units' scores
+  float* scores;               // [units, pitch]
+  float* cnorm;                // [units, chunks] bound of the summaries' norms
+  float* qnorm;                // [units] bound of the group's query norms
+  int* err;
+};
+
+// The selection, and the cache as the decode kernel then reads it: a page
+// table of num_pages + 1 entries for each unit and the length of each stream's
+// selected tokens.
+struct PageSelectArgs {
+  CacheView c;
+  int B, Hkv, G;
+  int max_len;
+  int num_pages, keep_first, keep_last;
+  const uint16_t* q;
+  const int32_t* pos;
+  const uint64_t* rope_step;
+  int r;
+  const uint16_t* q_norm;
+  double norm_eps;
+  const uint16_t* summary;
+  int chunk_pages, chunks, pitch;
+  const float* scores;
+  const float* cnorm;
+  const float* qnorm;
+  uint64_t* keys;              // [units, pitch] scratch
+  int max_words;               // words of a bitmap of the call's longest stream's pages
+  int32_t* table;              // [units, num_pages + 1]
+  int32_t* seq_out;            // [B]
+  int32_t* selected;           // [units, num_pages] logical pages, or null
+  int* err;
+};
+
+// Linear attention over a state S [D, D] for each (row, KV head), with the
+// head's decay lam: S = lam S + k v^T, out = q^T S / sqrt(D).
+constexpr int kLinearChunk = 64;  // tokens of a chunk of the prompt form
+constexpr int kDecayStride = kLinearChunk + 3;
+struct LinearArgs {
+  float* state;                // [n_rows, Hkv, D, D], row = key dim
+  int n_rows;
+  const int32_t* stream_rows;  // [B] or null
+  int B, Hkv, G;
+  const uint16_t* q;           // [B, (T,) Hq, D]
+  const uint16_t* k;           // [B, (T,) Hkv, D]
+  const uint16_t* v;
+  const uint16_t* gate;        // [B, (T,) Hq] or null
+  float* out;                  // [B, (T,) Hq, D]
+  const float* decay;          // [Hkv][kDecayStride]: lam^0 .. lam^C in fp32, then what that drops of lam
+                               // (C + 1) and of lam^C (C + 2)
+  const float* log_decay;      // [Hkv] log lam
+  float scale;                 // 1 / sqrt(D)
+  int write_back;              // step: store the new state
+  int T;                       // prompt: tokens of a row's arrays
+  const int32_t* count;        // prompt: [B]
+  float* sums;                 // prompt: [B * Hkv * segments, D, D] states of the segments
+  int segments;
+  int* err;
 };
 
 struct AppendArgs {
@@ -260,6 +352,19 @@ int decode_ctas_per_sm(int D, int G);
 int decode_tile_keys(int D, int G, bool f8 = false);
 // Largest number of (stream, KV head) units of one decode call.
 int decode_max_units();
+
+cudaError_t launch_summarize(const SummarizeArgs& a, int D, cudaStream_t s);
+// Pages of a score CTA for `units` units of up to `pages` pages.
+int score_chunk_pages(int units, int pages, int num_sms);
+// Least value of score_chunk_pages (sizes the workspace).
+constexpr int kScoreMinPages = 128;
+// Shared memory of the selection: a bitmap of a stream's pages and the group's
+// query in fp64.
+constexpr int kSelectSmemMax = 160 * 1024;
+cudaError_t launch_page_scores(const PageScoreArgs& a, int D, cudaStream_t s);
+cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t s);
+cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
+cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s);
 
 // Launch order per stream, for early cache reads. A kernel launched with
 // programmatic stream serialization may run while the launch before it on the

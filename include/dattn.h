@@ -23,6 +23,14 @@
  * optional head-wise sigmoid gate scales each head's output (same commit).
  * Grouped-query attention maps query head h to KV head h / (Hq / Hkv)
  * ("vllm-omni commits", talker export commit: GQA by reshaping the query).
+ *
+ * Two kinds of layers have a cost per token that does not grow with the whole
+ * context (neither is on the pages): a paged layer can be decoded over the
+ * pages that a cheap score selects for each new token (dattn_sparse_decode,
+ * with dattn_summarize keeping the summaries that are scored), and a state
+ * layer (DATTN_CACHE_STATE) is linear attention with a decay for each head,
+ * whose decode and prefill calls are the recurrent and the chunked form.
+ *
  * Tree verify scores up to 16 rows per stream, each under its own tree mask
  * ("TensorFold PR #608": verify windows of up to 16 streams x 16 rows).
  *
@@ -73,7 +81,12 @@ enum {
                               P V (from dattn_get_error)                          */
 };
 
-enum { DATTN_CACHE_RING = 0, DATTN_CACHE_PAGED = 1 };
+enum {
+  DATTN_CACHE_RING = 0,
+  DATTN_CACHE_PAGED = 1,
+  DATTN_CACHE_STATE = 2  /* linear attention with a decay for each head: the layer's
+                            cache is one fp32 state [D, D] per (stream, KV head)     */
+};
 
 /* Element format of a layer's K/V pools. */
 enum {
@@ -115,6 +128,10 @@ typedef struct {
   int kv_format;
   float k_scale;
   float v_scale;
+  /* State layers: HOST pointer to [Hkv] logarithms of the heads' decays
+   * (finite, <= 0; 0 = no decay), copied by dattn_create. Such a layer takes
+   * no rotation, QK-norm or E4M3 format (DATTN_EUNSUPPORTED). */
+  const float* log_decay;
 } dattn_layer_config;
 
 typedef struct {
@@ -127,6 +144,9 @@ typedef struct {
   int max_verify_rows;   /* largest T of a verify call (<= 16); 0 = no verify     */
   int num_layers;
   const dattn_layer_config* layers; /* [num_layers], host memory                  */
+  int max_selected_pages; /* largest num_pages of a dattn_sparse_decode call; 0 =
+                            none. Takes 12 bytes of workspace for each page of
+                            max_context tokens, stream and KV head               */
 } dattn_config;
 
 typedef struct dattn_handle dattn_t;
@@ -140,7 +160,10 @@ typedef struct dattn_handle dattn_t;
  *   paged: k, v = [n_rows (pages), Hkv, P, D] bf16. Token t of call row b is
  *          offset t % P of page block_table[b * bt_stride + t / P]; the row
  *          holds seq_len[b] cached tokens; the new entry is written at token
- *          index seq_len[b]. */
+ *          index seq_len[b].
+ *   state: k = [n_rows, Hkv, D, D] fp32, row = key dim, column = value dim (v is
+ *          not read). Call row b uses state row stream_rows[b] (identity when
+ *          NULL); two rows of a call never name the same state. */
 typedef struct {
   void* k;
   void* v;
@@ -217,6 +240,10 @@ DATTN_API int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, i
                     dattn_stream_t stream);
 
 /* Decode attention for one layer (see dattn_decode_args). One kernel launch.
+ * On a state layer the step of linear attention: with lam = exp(log_decay),
+ * S' = lam S + k_new v_new^T and out = sigmoid(gate) q^T S' / sqrt(D), each
+ * query head with its KV head's state; S' is stored when write_back is set.
+ * A row that names no state is reported (DATTN_EINDEX) and taken as zeros.
  * Ordering: calls on one handle share its workspace, so they must be ordered
  * (one stream at a time, or streams joined by events). The launch may begin
  * while the launch before it on the stream is still running: it then streams
@@ -227,6 +254,45 @@ DATTN_API int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, i
  * immediately preceding launch if that launch is one of this library's. */
 DATTN_API int dattn_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                  dattn_stream_t stream);
+
+/* Which pages of a stream's cache a decode reads: of its ceil(seq_len / P)
+ * pages the first keep_first, the newest keep_last (at least 1; the last may be
+ * partly filled), and of the others those with the highest scores, num_pages
+ * in all - every page where there are no more. Each KV head selects for
+ * itself: the score of a page is the largest dot product of the group's query
+ * heads (normalised and rotated as for the attention) with the page's summary
+ * for that head, ties go to the lower page, and a score that is no number
+ * counts as infinite. The selection is that of the exact scores: those near
+ * the border are evaluated in fp64. */
+typedef struct {
+  const void* summary;   /* [n_rows (pages), Hkv, D] bf16 (dattn_summarize)        */
+  int num_pages;         /* 1 <= num_pages <= max_selected_pages                  */
+  int keep_first;        /* >= 0                                                   */
+  int keep_last;         /* >= 1; keep_first + keep_last <= num_pages              */
+  int32_t* selected;     /* out [B, Hkv, num_pages]: the selected pages of the
+                            stream (logical, ascending, then -1), or NULL          */
+} dattn_page_selection;
+
+/* Decode attention of a paged layer (bf16 or E4M3) over selected pages: as
+ * dattn_decode with the cached tokens of the selected pages, and the new token,
+ * in the one softmax. Summaries are read for the pages that compete only, so
+ * those must be up to date: every page below the newest keep_last. Three
+ * launches (two when max_seq_len is at most num_pages pages). Ring and state
+ * layers return DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
+DATTN_API int dattn_sparse_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
+                                  const dattn_page_selection* sel, dattn_stream_t stream);
+
+/* Page summaries of a paged layer: for every page of row b whose last token is
+ * among tokens [start_index[b], start_index[b] + count[b]), 0 <= count[b] <=
+ * max_tokens, the mean of its P keys as they are stored (E4M3: times k_scale),
+ * summed in fp32 and rounded to bf16, into summary [n_rows (pages), Hkv, D].
+ * Called after the entries are in the cache - an append, a prefill, a commit or
+ * a decode with write-back - on the same stream or behind it. Pages that are
+ * not full have no summary yet; other pages' summaries are left as they are.
+ * One launch. */
+DATTN_API int dattn_summarize(dattn_t* h, int layer, const dattn_cache* cache, void* summary, int num_streams,
+                              int max_tokens, const int32_t* start_index, const int32_t* count,
+                              dattn_stream_t stream);
 
 /* Tree verify for one layer, ring or paged (see dattn_verify_args). Three
  * launches. Shape limits: G * T <= 128 query rows per KV head and
@@ -268,7 +334,11 @@ DATTN_API int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int 
  * (seq_len[s] + count[s] <= max_context, pages in its table). A stream whose
  * count or ring metadata is out of range gets no tokens and is reported as
  * DATTN_EINDEX (dattn_get_error). The caller then advances its metadata by
- * count[s]. */
+ * count[s].
+ * On a state layer the chunked form of linear attention: the same outputs and
+ * final state as count[s] decode steps with write_back, whatever
+ * max_verify_rows is; start_pos is not read. A stream with a count out of range
+ * or without a state is reported and left as it is. */
 DATTN_API int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
                             const void* q, const void* k, const void* v, const void* gate,
                             const int32_t* count, const int32_t* start_pos, float* out, dattn_stream_t stream);
