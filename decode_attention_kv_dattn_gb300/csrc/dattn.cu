@@ -573,7 +573,8 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     }
     L.log_decay = nullptr;
   }
-  (void)has_state;
+  if (has_state && cudaMalloc(&h->sums, static_cast<size_t>(h->num_sms) * D * D * sizeof(float)) != cudaSuccess)
+    return fail(DATTN_ECUDA);
   if (sel_pitch > 0) {
     const size_t units = static_cast<size_t>(h->max_streams) * Hkv;
     h->max_selected = cfg->max_selected_pages;
@@ -874,6 +875,8 @@ int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_strea
     LinearArgs la = linear_args(h, layer, cache, num_streams, q, k, v, gate, out);
     la.T = max_tokens;
     la.count = count;
+    la.segments = linear_prompt_segments(num_streams * h->Hkv, max_tokens, h->D, h->num_sms, &la.seg_chunks);
+    if (encode_linear_maps(la, h->D) != cudaSuccess) return DATTN_EUNSUPPORTED;
     const int st = cuda_status(launch_linear_prompt(la, h->D, reinterpret_cast<cudaStream_t>(stream)), "linear prompt");
     if (st == DATTN_OK) record_launch(stream, cache->k);
     return st;

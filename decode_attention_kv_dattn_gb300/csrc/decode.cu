@@ -1615,6 +1615,27 @@ cudaError_t encode_verify_maps(const CacheView& c, int Hkv, int D, const uint16_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_linear_maps(LinearArgs& a, int D) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t tokens = static_cast<cuuint64_t>(a.B) * a.T;
+  if (tokens > 0x7fffffffull) return cudaErrorNotSupported;
+  const uint16_t* const src[3] = {a.q, a.k, a.v};
+  CUtensorMap* const dst[3] = {&a.tmap_q, &a.tmap_k, &a.tmap_v};
+  for (int i = 0; i < 3; ++i) {
+    const cuuint64_t heads = static_cast<cuuint64_t>(a.Hkv) * (i == 0 ? a.G : 1);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), heads, tokens};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, heads * D * 2};
+    const cuuint32_t box[3] = {64, i == 0 && a.G > 1 ? 2u : 1u, kLinearChunk};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const CUresult r = fn(dst[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(src[i]), dims, strides, box,
+                          estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
 cudaError_t launch_decode(const DecodeArgs& args, int D, int ctas, cudaStream_t s, bool pdl) {
   DecodeArgs a = args;
   a.unit_cost = kSegmentCost;

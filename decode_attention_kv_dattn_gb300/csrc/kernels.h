@@ -191,6 +191,9 @@ struct PageSelectArgs {
 constexpr int kLinearChunk = 64;  // tokens of a chunk of the prompt form
 constexpr int kDecayStride = kLinearChunk + 3;
 struct LinearArgs {
+  CUtensorMap tmap_q;          // prompt: q, k, v as (D, heads, B * T) bf16, boxes of (64 dims, 2 heads for q
+  CUtensorMap tmap_k;          // (1 where G is 1) or 1, 64 tokens), 128-byte swizzled
+  CUtensorMap tmap_v;
   float* state;                // [n_rows, Hkv, D, D], row = key dim
   int n_rows;
   const int32_t* stream_rows;  // [B] or null
@@ -207,8 +210,9 @@ struct LinearArgs {
   int write_back;              // step: store the new state
   int T;                       // prompt: tokens of a row's arrays
   const int32_t* count;        // prompt: [B]
-  float* sums;                 // prompt: [B * Hkv * segments, D, D] states of the segments
-  int segments;
+  float* sums;                 // prompt: [B * Hkv, segments, D, D]: the segments' own sums, then the states
+                               // they start from
+  int segments, seg_chunks;    // prompt: segments of the longest stream, chunks of a segment
   int* err;
 };
 
@@ -364,7 +368,13 @@ constexpr int kSelectSmemMax = 160 * 1024;
 cudaError_t launch_page_scores(const PageScoreArgs& a, int D, cudaStream_t s);
 cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t s);
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
+// The prompt form: one launch, or three with segments.
 cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s);
+// Segments that the streams of a call are cut into (and the chunks of one) for
+// `units` (stream, KV head) units of up to T tokens: at most num_sms CTAs where
+// there is more than one.
+int linear_prompt_segments(int units, int T, int D, int num_sms, int* seg_chunks);
+cudaError_t encode_linear_maps(LinearArgs& a, int D);
 
 // Launch order per stream, for early cache reads. A kernel launched with
 // programmatic stream serialization may run while the launch before it on the

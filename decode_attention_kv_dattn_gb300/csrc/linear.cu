@@ -7,8 +7,7 @@
 // with lam = exp(log_decay[h]) and the group's query heads reading their KV
 // head's state. lam is held as fp32 hi + lo: a decay near 1 acts over many
 // tokens, and an error of 2^-25 in each step would grow with that reach.
-#include "common.cuh"
-#include "mma.cuh"
+#include "linear.cuh"
 
 namespace dattn {
 
@@ -16,15 +15,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStepThreads = 256;
-
-// Cache row of call row b, or -1 (reported): a bad row reads a state of zeros
-// and writes nothing.
-__device__ __forceinline__ int state_row(const LinearArgs& a, int b, bool report) {
-  const int row = a.stream_rows ? a.stream_rows[b] : b;
-  if (row >= 0 && row < a.n_rows) return row;
-  if (report) raise_error(a.err, ERR_INDEX);
-  return -1;
-}
 
 // ---------------------------------------------------------------- one token
 
@@ -111,84 +101,6 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearA
   }
 }
 
-// ---------------------------------------------------------------- prompts
-
-// Token by token: one CTA per (unit, 32 columns), the columns' state in
-// registers.
-template <int D, int GP>
-__global__ void __launch_bounds__(256) linear_prompt_kernel(const LinearArgs a) {
-  constexpr int W = 32, LPR = 8, RP = 32, R = D / RP, SLICES = D / W;
-  __shared__ float ks[D];
-  __shared__ float qs[D * GP];
-  __shared__ float red[8][GP][W];
-  const int u = blockIdx.x / SLICES, slice = blockIdx.x - u * SLICES;
-  const int b = u / a.Hkv, h = u - b * a.Hkv;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int row0 = t / LPR, col = slice * W + (t % LPR) * 4;
-  pdl_wait();
-  pdl_trigger();
-  const int row = state_row(a, b, t == 0 && h == 0 && slice == 0);
-  int n = a.count[b];
-  if (n < 0 || n > a.T) {
-    if (t == 0 && h == 0 && slice == 0) raise_error(a.err, ERR_INDEX);
-    n = 0;
-  }
-  if (row < 0 || n == 0) return;
-  const float lam = a.decay[h * kDecayStride + 1], lam_lo = a.decay[h * kDecayStride + kLinearChunk + 1];
-  float* S = a.state + (static_cast<int64_t>(row) * a.Hkv + h) * D * D + col;
-  float4 w[R];
-  for (int x = 0; x < R; ++x) w[x] = *reinterpret_cast<const float4*>(S + static_cast<int64_t>(row0 + x * RP) * D);
-  for (int i = 0; i < n; ++i) {
-    const int64_t tok = static_cast<int64_t>(b) * a.T + i;
-    __syncthreads();
-    for (int d = t; d < D; d += 256) {
-      ks[d] = bf16_to_f32(a.k[(tok * a.Hkv + h) * D + d]);
-      for (int g = 0; g < GP; ++g)
-        qs[d * GP + g] = g < a.G ? bf16_to_f32(a.q[((tok * a.Hkv + h) * a.G + g) * D + d]) : 0.f;
-    }
-    const uint2 vw = *reinterpret_cast<const uint2*>(a.v + (tok * a.Hkv + h) * D + col);
-    const float v[4] = {bf16_lo(vw.x), bf16_hi(vw.x), bf16_lo(vw.y), bf16_hi(vw.y)};
-    __syncthreads();
-    float acc[GP][4] = {};
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-      const int d = row0 + x * RP;
-      const float kd = ks[d];
-      w[x].x = fmaf(w[x].x, lam, fmaf(w[x].x, lam_lo, kd * v[0]));
-      w[x].y = fmaf(w[x].y, lam, fmaf(w[x].y, lam_lo, kd * v[1]));
-      w[x].z = fmaf(w[x].z, lam, fmaf(w[x].z, lam_lo, kd * v[2]));
-      w[x].w = fmaf(w[x].w, lam, fmaf(w[x].w, lam_lo, kd * v[3]));
-#pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float qd = qs[d * GP + g];
-        acc[g][0] = fmaf(qd, w[x].x, acc[g][0]);
-        acc[g][1] = fmaf(qd, w[x].y, acc[g][1]);
-        acc[g][2] = fmaf(qd, w[x].z, acc[g][2]);
-        acc[g][3] = fmaf(qd, w[x].w, acc[g][3]);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < GP; ++g)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) acc[g][x] += __shfl_xor_sync(kFull, acc[g][x], o);
-        if (lane < LPR) red[warp][g][lane * 4 + x] = acc[g][x];
-      }
-    __syncthreads();
-    for (int e = t; e < a.G * W; e += 256) {
-      const int g = e / W, x = e - g * W;
-      float o = 0.f;
-      for (int y = 0; y < 8; ++y) o += red[y][g][x];
-      o *= a.scale;
-      const int64_t head = (tok * a.Hkv + h) * a.G + g;
-      if (a.gate) o /= 1.f + expf(-bf16_to_f32(a.gate[head]));
-      a.out[head * D + slice * W + x] = o;
-    }
-  }
-  for (int x = 0; x < R; ++x) *reinterpret_cast<float4*>(S + static_cast<int64_t>(row0 + x * RP) * D) = w[x];
-}
-
 template <int D, int W>
 cudaError_t step_launch(const LinearArgs& a, cudaStream_t s) {
   const dim3 grid(a.B * a.Hkv * (D / W));
@@ -201,13 +113,6 @@ cudaError_t step_launch(const LinearArgs& a, cudaStream_t s) {
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s) {
   if (D == 128) return step_launch<128, 32>(a, s);
   return step_launch<256, 32>(a, s);
-}
-
-cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s) {
-  const dim3 grid(a.B * a.Hkv * (D / 32));
-  auto k = D == 128 ? (a.G <= 4 ? linear_prompt_kernel<128, 4> : linear_prompt_kernel<128, 8>)
-                    : (a.G <= 4 ? linear_prompt_kernel<256, 4> : linear_prompt_kernel<256, 8>);
-  return launch_pdl(k, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace dattn

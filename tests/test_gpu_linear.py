@@ -222,6 +222,24 @@ def test_infinite_and_missing_values_stay_with_their_stream(dattn):
     assert torch.isfinite(out[0, :, 2:]).all()
 
 
+def test_outputs_and_states_on_16_byte_boundaries(dattn):
+    g = torch.Generator().manual_seed(8)
+    Hq, Hkv, D, T = 4, 2, 128, 66
+    ld = decays(Hkv)
+    h = dattn.Handle(Hq, Hkv, D, [{"kind": dattn.CACHE_STATE, "log_decay": ld}], 1)
+    q, k, v, _ = inputs(g, 1, T, Hq=Hq, Hkv=Hkv, D=D)
+    shifted = lambda *s: torch.zeros(math.prod(s) + 8, device="cuda")[4:-4].view(*s)  # noqa: E731
+    sd, out = shifted(1, Hkv, D, D), shifted(1, T, Hq, D)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    h.prefill(0, dattn.state_cache(sd), q.cuda(), k.cuda(), v.cuda(), i32([T]), i32([0]), out)
+    assert h.get_error() == dattn.OK
+    ref = Ref(torch.zeros(1, Hkv, D, D), ld)
+    for t in range(T):
+        want, size = ref.step(0, q[0, t], k[0, t], v[0, t])
+        close(out[0, t].cpu(), want, size, 2.0 ** -16 + (D + 128) * 2.0 ** -23, f"token {t}")
+    close(sd.cpu(), ref.s, ref.a, 2.0 ** -16 + (D + 128) * 2.0 ** -23, "state")
+
+
 def test_bad_metadata_is_reported(dattn):
     Hq, Hkv, D, T = 4, 2, 128, 8
     g = torch.Generator().manual_seed(5)
