@@ -71,11 +71,12 @@ struct dattn_handle {
   size_t vpart_slots = 0;
   // Decode over selected pages (max_selected_pages > 0): the screened scores
   // and their bounds, the exact keys of a border with many pages, and the page
-  // table and lengths that the decode kernel then reads.
+  // table that the attention then reads.
   int max_selected = 0, sel_pitch = 0, sel_chunks = 0;
   float *sel_scores = nullptr, *sel_cnorm = nullptr, *sel_qnorm = nullptr;
   uint64_t* sel_keys = nullptr;
-  int32_t *sel_table = nullptr, *sel_len = nullptr;
+  int32_t* sel_table = nullptr;
+  int* sel_done = nullptr;
   std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
   float* sums = nullptr;                  // state layers: the prompt form's segment states
   int* err = nullptr;
@@ -265,14 +266,16 @@ int verify_round(dattn_t* h, int layer, const VerifyRound& r, cudaStream_t s) {
   return cuda_status(launch_verify_combine(vc, h->D, s), "verify combine");
 }
 
-// Scores and selection of a decode over selected pages (two launches), into
-// the handle's page table and lengths.
-int select_pages(dattn_t* h, int layer, const CacheView& view, const dattn_decode_args* args,
-                 const dattn_page_selection* sel, int n_max, cudaStream_t s) {
+// Decode over selected pages: the scores and the selection, then the attention
+// (two launches).
+int sparse_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
+                const dattn_page_selection* sel, int n_max, cudaStream_t s) {
   const dattn_layer_config& L = h->layers[layer];
+  const int units = args->num_streams * h->Hkv;
   const int pages = static_cast<int>((static_cast<int64_t>(n_max) + L.page_size - 1) / L.page_size);
-  PageSelectArgs a{};
-  a.c = view;
+  const bool f8 = L.kv_format == DATTN_KV_E4M3;
+  PageArgs a{};
+  a.c = make_view(h, L, cache);
   a.B = args->num_streams;
   a.Hkv = h->Hkv;
   a.G = h->G;
@@ -281,56 +284,50 @@ int select_pages(dattn_t* h, int layer, const CacheView& view, const dattn_decod
   a.keep_first = sel->keep_first;
   a.keep_last = sel->keep_last;
   a.q = static_cast<const uint16_t*>(args->q);
+  a.k_new = static_cast<const uint16_t*>(args->k_new);
+  a.v_new = static_cast<const uint16_t*>(args->v_new);
+  a.gate = static_cast<const uint16_t*>(args->gate);
   a.pos = args->pos;
   a.rope_step = h->rope_step[layer];
   a.r = L.rotary_dim;
   a.q_norm = h->q_norm[layer];
+  a.k_norm = h->k_norm[layer];
   a.norm_eps = L.norm_eps;
+  a.out = args->out;
+  a.write_back = args->write_back;
   a.summary = static_cast<const uint16_t*>(sel->summary);
-  a.chunk_pages = score_chunk_pages(a.B * a.Hkv, pages, h->num_sms);
-  a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
+  a.selected = sel->selected;
+  a.chunk_pages = page_chunk_pages(units, pages, h->num_sms);
+  a.chunks = std::max(1, (pages + a.chunk_pages - 1) / a.chunk_pages);
   a.pitch = h->sel_pitch;
   a.scores = h->sel_scores;
   a.cnorm = h->sel_cnorm;
   a.qnorm = h->sel_qnorm;
   a.keys = h->sel_keys;
-  a.max_words = (pages + 31) / 32;
+  a.done = h->sel_done;
   a.table = h->sel_table;
-  a.seq_out = h->sel_len;
-  a.selected = sel->selected;
+  const int64_t groups = static_cast<int64_t>(std::min(pages, sel->num_pages)) * ((L.page_size + 15) / 16);
+  a.splits = page_splits(units, static_cast<int>(std::min<int64_t>(groups, INT32_MAX)), h->num_sms);
+  a.q_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(h->D)));
+  if (f8) {
+    a.k_scale = L.k_scale;
+    a.v_scale = L.v_scale;
+    a.q_scale = static_cast<float>(static_cast<double>(a.q_scale) * L.k_scale);
+  }
+  const unsigned half = h->decode_calls & 1u;
+  a.part = h->part[half];
+  a.counters = h->counters[half];
   a.err = h->err;
-  PageScoreArgs p{};
-  p.c = a.c;
-  p.B = a.B;
-  p.Hkv = a.Hkv;
-  p.G = a.G;
-  p.max_len = a.max_len;
-  p.num_pages = a.num_pages;
-  p.keep_first = a.keep_first;
-  p.keep_last = a.keep_last;
-  p.q = a.q;
-  p.pos = a.pos;
-  p.rope_step = a.rope_step;
-  p.r = a.r;
-  p.q_norm = a.q_norm;
-  p.norm_eps = a.norm_eps;
-  p.summary = a.summary;
-  p.chunk_pages = a.chunk_pages;
-  p.chunks = a.chunks;
-  p.pitch = a.pitch;
-  p.scores = h->sel_scores;
-  p.cnorm = h->sel_cnorm;
-  p.qnorm = h->sel_qnorm;
-  p.err = h->err;
-  int rc = DATTN_OK;
-  // (a call whose streams all have at most num_pages pages needs no score)
-  if (pages > sel->num_pages) rc = cuda_status(launch_page_scores(p, h->D, s), "page scores");
-  if (rc == DATTN_OK) rc = cuda_status(launch_page_select(a, h->D, s), "page selection");
+  int rc = cuda_status(launch_page_select(a, h->D, s), "page selection");
+  if (rc == DATTN_OK) rc = cuda_status(launch_page_attend(a, h->D, f8, s), "attention over selected pages");
+  if (rc == DATTN_OK) {
+    record_launch(s, args->write_back ? cache->k : nullptr);
+    ++h->decode_calls;
+  }
   return rc;
 }
 
-// dattn_decode, and dattn_sparse_decode with a selection: the pages' scores and
-// the selection first, then the same decode over the selected pages.
+// dattn_decode, and dattn_sparse_decode with a selection: one set of checks.
 int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                 const dattn_page_selection* sel, dattn_stream_t stream) {
   if (!h || !args || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
@@ -370,21 +367,12 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   if (!guard.ok) return DATTN_ECUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-  CacheView view = make_view(h, L, cache);
-  if (sel) {
-    rc = select_pages(h, layer, view, args, sel, n_max, s);
-    if (rc != DATTN_OK) return rc;
-    view.block_table = h->sel_table;
-    view.bt_stride = sel->num_pages + 1;
-    view.bt_heads = 1;
-    view.seq_len = h->sel_len;
-    n_max = static_cast<int>(std::min<int64_t>(n_max, static_cast<int64_t>(sel->num_pages) * L.page_size));
-  }
+  if (sel) return sparse_call(h, layer, cache, args, sel, n_max, s);
   const bool f8 = L.kv_format == DATTN_KV_E4M3;
   const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, f8));
   if (static_cast<size_t>(ctas) + static_cast<size_t>(B) * h->Hkv > h->part_units) return DATTN_EXCEEDS;
   DecodeArgs da{};
-  da.c = view;
+  da.c = make_view(h, L, cache);
   if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) return DATTN_EUNSUPPORTED;
   da.B = B;
   da.Hkv = h->Hkv;
@@ -404,8 +392,7 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   da.part = h->part[half];
   da.counters = h->counters[half];
   da.err = h->err;
-  da.early = !sel && !prev_launch_writes(stream, cache->k);
-  da.late_meta = sel != nullptr;
+  da.early = !prev_launch_writes(stream, cache->k);
   da.wait_ns = h->wait_ns;
   da.debug_flags = h->debug_flags;
   da.q_norm = h->q_norm[layer];
@@ -487,7 +474,8 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
       if (cfg->layers[l].cache_kind == DATTN_CACHE_PAGED)
         sel_pitch = std::max<int>(sel_pitch, static_cast<int>((static_cast<int64_t>(cfg->max_context) +
                                                               cfg->layers[l].page_size - 1) / cfg->layers[l].page_size));
-    if ((static_cast<int64_t>(sel_pitch) + 31) / 32 * 4 + 16 + static_cast<int64_t>(G) * D * 8 > kSelectSmemMax)
+    // (the selection's bitmap of a stream's pages beside its other shared memory)
+    if ((static_cast<int64_t>(sel_pitch) + 31) / 32 * 4 > kSelectBitmapMax)
       return DATTN_EUNSUPPORTED;
   }
   DeviceGuard guard(device);
@@ -579,14 +567,15 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     const size_t units = static_cast<size_t>(h->max_streams) * Hkv;
     h->max_selected = cfg->max_selected_pages;
     h->sel_pitch = sel_pitch;
-    h->sel_chunks = (sel_pitch + kScoreMinPages - 1) / kScoreMinPages;
+    h->sel_chunks = (sel_pitch + kPageChunkMin - 1) / kPageChunkMin;
     if (cudaMalloc(&h->sel_scores, units * h->sel_pitch * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_keys, units * h->sel_pitch * sizeof(uint64_t)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_cnorm, units * h->sel_chunks * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_qnorm, units * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
-    if (cudaMalloc(&h->sel_table, units * (static_cast<size_t>(h->max_selected) + 1) * sizeof(int32_t)) != cudaSuccess)
+    if (cudaMalloc(&h->sel_table, units * h->max_selected * sizeof(int32_t)) != cudaSuccess)
       return fail(DATTN_ECUDA);
-    if (cudaMalloc(&h->sel_len, h->max_streams * sizeof(int32_t)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_done, units * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMemset(h->sel_done, 0, units * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
   }
 
   // Workspace. Rows of rotated q/k: one per stream (decode) or per verify row.
@@ -650,7 +639,7 @@ void dattn_destroy(dattn_t* h) {
   cudaFree(h->sel_cnorm);
   cudaFree(h->sel_qnorm);
   cudaFree(h->sel_table);
-  cudaFree(h->sel_len);
+  cudaFree(h->sel_done);
   for (float* p : h->decay) cudaFree(p);
   cudaFree(h->sums);
   cudaFree(h->tiles);

@@ -200,11 +200,6 @@ __device__ __forceinline__ int ring_start(int head, int n, int R) {
   return head - n < 0 ? head - n + R : head - n;
 }
 
-// First entry of the page table of unit (b, j).
-__device__ __forceinline__ int64_t table_row(const CacheView& c, int Hkv, int b, int j) {
-  return static_cast<int64_t>(c.bt_heads ? b * Hkv + j : b) * c.bt_stride;
-}
-
 // 16-row groups of a paged unit with n cached keys.
 __device__ __forceinline__ int paged_groups(const CacheView& c, int n) {
   if (n <= 0) return 0;
@@ -352,7 +347,7 @@ __device__ __forceinline__ int64_t write_back_offset(const DecodeArgs& a, int b,
   if constexpr (PAGED) {
     const int n = min(max(c.seq_len[b], 0), min(a.max_len, c.bt_stride * c.P));
     const int pi = n / c.P;
-    const int pg = pi < c.bt_stride ? c.block_table[table_row(c, a.Hkv, b, j) + pi] : -1;
+    const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(b) * c.bt_stride + pi] : -1;
     if (pg >= 0 && pg < c.n_rows) return ((static_cast<int64_t>(pg) * a.Hkv + j) * c.P + n % c.P) * D;
     raise_error(a.err, ERR_INDEX);
     return -1;
@@ -763,7 +758,7 @@ __global__ void __launch_bounds__(Geo<D, NT, F8>::THREADS, 1) decode_kernel(cons
     // the page table into L2 (each CTA a share of its lines), for the window
     // fills that read it once the split is known
     const int64_t lines = (static_cast<int64_t>(a.B) * c.bt_stride + 31) / 32;
-    if (lines <= kPrefetchLines && !a.late_meta)
+    if (lines <= kPrefetchLines)
       for (int64_t i = static_cast<int64_t>(cta) * kThreads + threadIdx.x; i < lines;
            i += static_cast<int64_t>(NC) * kThreads)
         prefetch_l2(c.block_table + i * 32);
@@ -778,24 +773,6 @@ __global__ void __launch_bounds__(Geo<D, NT, F8>::THREADS, 1) decode_kernel(cons
     mbar_init(merge_empty, 1);
     fence_mbar_init();
   }
-
-  // Ordering with the preceding launch on the stream, which may still run:
-  // it may be writing its new entries into its own cache, its outputs and its
-  // partials (the other half of the double-buffered workspace). This call's
-  // inputs, metadata and partials are never written by it. So the pass over
-  // the cache runs before waiting for it when its cache is a different one
-  // (a.early); the outputs and the write-back always come after the wait.
-  // Each CTA waits before it lets the next launch begin, so at most two
-  // calls are ever in flight.
-  bool waited = false;
-  auto wait_prev = [&]() {
-    if (!waited) {
-      pdl_wait();
-      pdl_trigger();
-      waited = true;
-    }
-  };
-  if (PAGED && a.late_meta) wait_prev();  // (the page table and the lengths are that launch's output)
 
   // ---- unit table: tiles per unit, then their prefix sum. A paged unit's
   // tiles follow from its length (caller metadata; no kernel of this library
@@ -861,6 +838,22 @@ __global__ void __launch_bounds__(Geo<D, NT, F8>::THREADS, 1) decode_kernel(cons
     ++n_segs;
   }
 
+  // Ordering with the preceding launch on the stream, which may still run:
+  // it may be writing its new entries into its own cache, its outputs and its
+  // partials (the other half of the double-buffered workspace). This call's
+  // inputs, metadata and partials are never written by it. So the pass over
+  // the cache runs before waiting for it when its cache is a different one
+  // (a.early); the outputs and the write-back always come after the wait.
+  // Each CTA waits before it lets the next launch begin, so at most two
+  // calls are ever in flight.
+  bool waited = false;
+  auto wait_prev = [&]() {
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+  };
   if (!a.early) wait_prev();
 
   if (warp != kHelper) {
@@ -893,7 +886,7 @@ __global__ void __launch_bounds__(Geo<D, NT, F8>::THREADS, 1) decode_kernel(cons
             const int gi = (g - P[u]) * KG + kg;
             if (gi < groups) {
               const int pi = gi / gpp, gr = gi - pi * gpp;
-              int pg = c.block_table[table_row(c, Hkv, b, j) + pi];
+              int pg = c.block_table[static_cast<int64_t>(b) * c.bt_stride + pi];
               if (pg < 0 || pg >= c.n_rows) {
                 raise_error(a.err, ERR_INDEX);
                 pg = 0;

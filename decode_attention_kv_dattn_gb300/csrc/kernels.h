@@ -43,8 +43,6 @@ struct CacheView {
   const int32_t* block_table;  // [B, bt_stride]
   int bt_stride;
   const int32_t* seq_len;      // [B]
-  int bt_heads;                // nonzero: block_table is [B * Hkv, bt_stride], a table for each KV head
-                               // (decode over selected pages)
 };
 
 // RoPE prologue: rotates q (fp32 out, pre-scaled) and k (bf16 entry out) of
@@ -120,8 +118,6 @@ struct DecodeArgs {
   // cached value = e4m3 * scale. q_scale then includes k_scale.
   int f8;
   float k_scale, v_scale;
-  int late_meta;               // nonzero: the preceding launch writes the page table and lengths, so
-                               // nothing of them is read before it has completed (early is 0 then)
 };
 
 // Page summaries: the bf16 mean of a page's stored keys (times k_scale), for
@@ -137,52 +133,44 @@ struct SummarizeArgs {
   int* err;
 };
 
-// Screened scores of every candidate page of each (stream, KV head) unit: the
-// pages [keep_first, pages - keep_last) of streams with more than num_pages.
-struct PageScoreArgs {
+// Decode over selected pages: one launch scores the candidate pages [keep_first,
+// pages - keep_last) of every (stream, KV head) unit with more than num_pages
+// pages and selects, a second one attends to the selected pages.
+struct PageArgs {
   CacheView c;
   int B, Hkv, G;
-  int max_len;
+  int max_len;                 // host bound on cached length
   int num_pages, keep_first, keep_last;
   const uint16_t* q;           // [B, Hq, D]
+  const uint16_t* k_new;       // [B, Hkv, D]
+  const uint16_t* v_new;       // [B, Hkv, D]
+  const uint16_t* gate;        // [B, Hq] or null
   const int32_t* pos;          // [B]
   const uint64_t* rope_step;
   int r;
   const uint16_t* q_norm;      // [D] or null
+  const uint16_t* k_norm;
   double norm_eps;
+  float* out;                  // [B, Hq, D]
+  int write_back;
   const uint16_t* summary;     // [pages, Hkv, D]
+  int32_t* selected;           // [units, num_pages] logical pages, or null
+  // scores and selection
   int chunk_pages, chunks;     // pages of a CTA, CTAs of a unit
-  int pitch;                   // floats between units' scores
+  int pitch;                   // entries between units' scores
   float* scores;               // [units, pitch]
   float* cnorm;                // [units, chunks] bound of the summaries' norms
   float* qnorm;                // [units] bound of the group's query norms
-  int* err;
-};
-
-// The selection, and the cache as the decode kernel then reads it: a page
-// table of num_pages + 1 entries for each unit and the length of each stream's
-// selected tokens.
-struct PageSelectArgs {
-  CacheView c;
-  int B, Hkv, G;
-  int max_len;
-  int num_pages, keep_first, keep_last;
-  const uint16_t* q;
-  const int32_t* pos;
-  const uint64_t* rope_step;
-  int r;
-  const uint16_t* q_norm;
-  double norm_eps;
-  const uint16_t* summary;
-  int chunk_pages, chunks, pitch;
-  const float* scores;
-  const float* cnorm;
-  const float* qnorm;
-  uint64_t* keys;              // [units, pitch] scratch
-  int max_words;               // words of a bitmap of the call's longest stream's pages
-  int32_t* table;              // [units, num_pages + 1]
-  int32_t* seq_out;            // [B]
-  int32_t* selected;           // [units, num_pages] logical pages, or null
+  uint64_t* keys;              // [units, pitch] scratch of a border with many pages
+  int* done;                   // [units] finished chunks; zero between calls
+  int32_t* table;              // [units, num_pages] physical pages selected
+  int q64_off, staged_off;     // shared-memory layout (set by launch_page_select)
+  // attention
+  int splits;                  // CTAs of a unit
+  float q_scale;               // log2(e) / sqrt(D), with k_scale for E4M3
+  float k_scale, v_scale;      // E4M3
+  float* part;                 // [units * splits][G * (D + 2)]
+  int* counters;               // [units] finished splits; zero between calls
   int* err;
 };
 
@@ -358,15 +346,18 @@ int decode_tile_keys(int D, int G, bool f8 = false);
 int decode_max_units();
 
 cudaError_t launch_summarize(const SummarizeArgs& a, int D, cudaStream_t s);
-// Pages of a score CTA for `units` units of up to `pages` pages.
-int score_chunk_pages(int units, int pages, int num_sms);
-// Least value of score_chunk_pages (sizes the workspace).
-constexpr int kScoreMinPages = 128;
-// Shared memory of the selection: a bitmap of a stream's pages and the group's
-// query in fp64.
-constexpr int kSelectSmemMax = 160 * 1024;
-cudaError_t launch_page_scores(const PageScoreArgs& a, int D, cudaStream_t s);
-cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t s);
+// Pages of a CTA of the scores, for `units` units of up to `pages` pages, and
+// the least it ever is (sizes the workspace).
+int page_chunk_pages(int units, int pages, int num_sms);
+constexpr int kPageChunkMin = 128;
+// CTAs of a unit in the attention over up to `groups` 16-key groups.
+int page_splits(int units, int groups, int num_sms);
+// Shared memory of the selection: a bitmap of a stream's pages, the group's
+// query in fp64 and up to 16,384 scores.
+constexpr int kSelectSmemMax = 180 * 1024;
+constexpr int kSelectBitmapMax = 96 * 1024;  // what a longest stream's may take of it
+cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s);
+cudaError_t launch_page_attend(const PageArgs& a, int D, bool f8, cudaStream_t s);
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
 // The prompt form: one launch, or three with segments.
 cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s);
