@@ -73,7 +73,7 @@ struct dattn_handle {
   // and their bounds, the exact keys of a border with many pages, and the page
   // table that the attention then reads.
   int max_selected = 0, sel_pitch = 0, sel_chunks = 0;
-  float *sel_scores = nullptr, *sel_cnorm = nullptr, *sel_qnorm = nullptr;
+  float *sel_scores = nullptr, *sel_tiles = nullptr, *sel_cinfo = nullptr, *sel_qnorm = nullptr;
   uint64_t* sel_keys = nullptr;
   int32_t* sel_table = nullptr;
   int* sel_done = nullptr;
@@ -301,7 +301,9 @@ int sparse_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   a.chunks = std::max(1, (pages + a.chunk_pages - 1) / a.chunk_pages);
   a.pitch = h->sel_pitch;
   a.scores = h->sel_scores;
-  a.cnorm = h->sel_cnorm;
+  a.tile_max = h->sel_tiles;
+  a.tile_pitch = (h->sel_pitch + 15) / 16;
+  a.cinfo = h->sel_cinfo;
   a.qnorm = h->sel_qnorm;
   a.keys = h->sel_keys;
   a.done = h->sel_done;
@@ -570,7 +572,9 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     h->sel_chunks = (sel_pitch + kPageChunkMin - 1) / kPageChunkMin;
     if (cudaMalloc(&h->sel_scores, units * h->sel_pitch * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_keys, units * h->sel_pitch * sizeof(uint64_t)) != cudaSuccess) return fail(DATTN_ECUDA);
-    if (cudaMalloc(&h->sel_cnorm, units * h->sel_chunks * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_tiles, units * ((h->sel_pitch + 15) / 16) * sizeof(float)) != cudaSuccess)
+      return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->sel_cinfo, units * h->sel_chunks * 3 * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_qnorm, units * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMalloc(&h->sel_table, units * h->max_selected * sizeof(int32_t)) != cudaSuccess)
       return fail(DATTN_ECUDA);
@@ -589,6 +593,8 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
   // then one per CTA (the group counters of units merged in two levels).
   if (static_cast<int64_t>(h->max_streams) * Hkv > decode_max_units()) return fail(DATTN_EUNSUPPORTED);
   h->part_units = static_cast<size_t>(h->decode_resident) + static_cast<size_t>(h->max_streams) * Hkv;
+  // (the attention over selected pages runs two CTAs an SM)
+  if (sel_pitch > 0) h->part_units = std::max(h->part_units, static_cast<size_t>(2 * h->num_sms));
   for (int i = 0; i < 2; ++i) {
     const size_t nc = static_cast<size_t>(h->max_streams) * Hkv + static_cast<size_t>(h->decode_resident);
     if (cudaMalloc(&h->counters[i], nc * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
@@ -636,7 +642,8 @@ void dattn_destroy(dattn_t* h) {
   cudaFree(h->vpart);
   cudaFree(h->sel_scores);
   cudaFree(h->sel_keys);
-  cudaFree(h->sel_cnorm);
+  cudaFree(h->sel_tiles);
+  cudaFree(h->sel_cinfo);
   cudaFree(h->sel_qnorm);
   cudaFree(h->sel_table);
   cudaFree(h->sel_done);

@@ -159,12 +159,15 @@ struct PageArgs {
   int chunk_pages, chunks;     // pages of a CTA, CTAs of a unit
   int pitch;                   // entries between units' scores
   float* scores;               // [units, pitch]
-  float* cnorm;                // [units, chunks] bound of the summaries' norms
+  float* tile_max;             // [units, tile_pitch]: largest score of each 16 pages
+  int tile_pitch;
+  float* cinfo;                // [units, chunks][3]: least and largest score, bound of the summaries' norms
   float* qnorm;                // [units] bound of the group's query norms
   uint64_t* keys;              // [units, pitch] scratch of a border with many pages
   int* done;                   // [units] finished chunks; zero between calls
   int32_t* table;              // [units, num_pages] physical pages selected
-  int q64_off, staged_off;     // shared-memory layout (set by launch_page_select)
+  int q64_off, staged_off;     // shared-memory layout, and the scores that have room in it (set by
+  int staged;                  // launch_page_select; a multiple of 128)
   // attention
   int splits;                  // CTAs of a unit
   float q_scale;               // log2(e) / sqrt(D), with k_scale for E4M3
@@ -354,8 +357,8 @@ constexpr int kPageChunkMin = 128;
 int page_splits(int units, int groups, int num_sms);
 // Shared memory of the selection: a bitmap of a stream's pages, the group's
 // query in fp64 and up to 16,384 scores.
-constexpr int kSelectSmemMax = 180 * 1024;
-constexpr int kSelectBitmapMax = 96 * 1024;  // what a longest stream's may take of it
+constexpr int kSelectBitmapMax = 96 * 1024;
+constexpr int kSelectSmemMax = kSelectBitmapMax + (17 + 65) * 1024;
 cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s);
 cudaError_t launch_page_attend(const PageArgs& a, int D, bool f8, cudaStream_t s);
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
