@@ -166,7 +166,7 @@ struct PageArgs {
   uint64_t* keys;              // [units, pitch] scratch of a border with many pages
   int* done;                   // [units] finished chunks; zero between calls
   int32_t* table;              // [units, num_pages] physical pages selected
-  int q64_off, staged_off;     // shared-memory layout, and the scores that have room in it (set by
+  int q64_off, qf_off, staged_off;  // shared-memory layout, and the scores that have room in it (set by
   int staged;                  // launch_page_select; a multiple of 128)
   // attention
   int splits;                  // CTAs of a unit
@@ -358,7 +358,7 @@ int page_splits(int units, int groups, int num_sms);
 // Shared memory of the selection: a bitmap of a stream's pages, the group's
 // query in fp64 and up to 16,384 scores.
 constexpr int kSelectBitmapMax = 96 * 1024;
-constexpr int kSelectSmemMax = kSelectBitmapMax + (17 + 65) * 1024;
+constexpr int kSelectSmemMax = kSelectBitmapMax + (17 + 8 + 65) * 1024;
 cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s);
 cudaError_t launch_page_attend(const PageArgs& a, int D, bool f8, cudaStream_t s);
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);

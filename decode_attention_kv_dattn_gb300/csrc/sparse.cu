@@ -275,7 +275,7 @@ __device__ __forceinline__ bool last_to_arrive(int* counter, int parts, int* fla
 struct SelectShared {
   alignas(16) int hist[kBins];
   int list[kList];
-  float value[kList];
+  alignas(16) float value[kList];
   alignas(16) uint64_t list_key[kList];
   uint64_t step[128];  // the rotation's phase steps
   int buf[32];
@@ -477,11 +477,22 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
       }
       __syncthreads();
     };
+    // ---- few candidates: all of them listed, and ranked below
+    if (N <= 256) {
+      __syncthreads();
+      for (int i = t; i < N; i += NTH) {
+        s.list[i] = i;
+        s.value[i] = __ldcg(gsc + i);
+      }
+      if (t == 0) s.n_list = N;
+      __syncthreads();
+      listed = true;
+    }
     // ---- long streams, by way of the 16-page tiles' maxima: the k-th largest of
     // them has k scores at or above it, so the k-th largest score is no less,
     // and only tiles that reach it have scores to look at
     const int tile0 = lo >> 4, tiles = ((lo + N - 1) >> 4) - tile0 + 1;
-    if (tiles >= 4 * k && a1 > a0) {
+    if (!listed && tiles >= 4 * k && a1 > a0) {
       const float* gtm = a.tile_max + static_cast<int64_t>(u) * a.tile_pitch + tile0;
       const float inv = static_cast<float>(kBins) / (a1 - a0);
       if (inv > 0.f && inv < 1e38f) {
@@ -566,10 +577,15 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
       for (int y = t; y < all; y += NTH) {
         const float w = s.value[y];
         int more = 0, same = 0;
-        for (int x = 0; x < all; ++x) {
-          const float z = s.value[x];
-          more += z > w;
-          same += z == w;
+        int x = 0;
+        for (; x + 4 <= all; x += 4) {
+          const float4 z = *reinterpret_cast<const float4*>(s.value + x);
+          more += (z.x > w) + (z.y > w) + (z.z > w) + (z.w > w);
+          same += (z.x == w) + (z.y == w) + (z.z == w) + (z.w == w);
+        }
+        for (; x < all; ++x) {
+          more += s.value[x] > w;
+          same += s.value[x] == w;
         }
         if (more < k && k <= more + same) s.threshold = w;  // equal scores write the same
       }
@@ -625,6 +641,64 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
     want = k - block_sum<NTH>(lane == 0 ? in : 0, s.buf);  // k > 0: 1 <= want <= m
     m = s.n_list;
   }
+  // ---- the pages near the border again in fp32: a lane's 2 E products and five
+  // levels of sums, on the fp32 query
+  constexpr int E = D / 64;
+  uint32_t ahead[E];
+  auto fetch = [&](int x) {  // the summary of list entry x, 2 dims a lane
+    const uint16_t* src =
+        a.summary + (static_cast<int64_t>(physical_page(c, b, lo + s.list[x], a.err)) * a.Hkv + h) * D + lane * 2;
+#pragma unroll
+    for (int y = 0; y < E; ++y) ahead[y] = *reinterpret_cast<const uint32_t*>(src + 64 * y);
+  };
+  if (want < m && m <= 4 * W && border.screened) {
+    const float* qf = reinterpret_cast<const float*>(dyn + a.qf_off);
+    for (int x = warp; x < m; x += W) {
+      fetch(x);
+      float best = -INFINITY;
+      for (int g = 0; g < a.G; ++g) {
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int y = 0; y < E; ++y) {
+          const float2 qd = *reinterpret_cast<const float2*>(qf + g * D + 64 * y + lane * 2);
+          y0 = fmaf(qd.x, bf16_lo(ahead[y]), y0);
+          y1 = fmaf(qd.y, bf16_hi(ahead[y]), y1);
+        }
+        float z = y0 + y1;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+        best = fmaxf(best, z);
+      }
+      if (lane == 0) s.value[x] = best;
+    }
+    __syncthreads();
+    // Error, relative to |q| |summary|: 4 products a chain, the join and five
+    // sums (10 roundings of 2^-24: 6.0e-7) and the query: cosine and sine within
+    // 1.5e-7 each and two roundings (at most 1.5e-7 sqrt(2) + 2^-23: 3.4e-7).
+    const float e2 = fmaf(1.2e-6f * cn, qn, 7.9e-31f);
+    int sure = 0, i = -1;
+    if (t < m) {
+      const float v = s.value[t];
+      int over = 0, may = 0;  // those surely above this one; those possibly above or equal
+      for (int x = 0; x < m; ++x) {
+        over += s.value[x] > v + 2.f * e2;
+        may += x != t && s.value[x] >= v - 2.f * e2;
+      }
+      if (may < want) {  // surely among the best
+        select(s.list[t]);
+        sure = 1;
+      } else if (over < want) {
+        i = s.list[t];
+      }
+    }
+    const int taken = block_sum<NTH>(sure, s.buf);
+    want -= taken;
+    if (t == 0) s.n_list = 0;
+    __syncthreads();
+    if (i >= 0) s.list[atomicAdd(&s.n_list, 1)] = i;
+    __syncthreads();
+    m = s.n_list;
+  }
   if (want == m && m <= kList) {
     for (int x = t; x < m; x += NTH) select(s.list[x]);
   } else if (want == m) {
@@ -633,15 +707,7 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
   } else {
     // ---- exact scores of the pages near the border: q rotated in fp64. A warp
     // has a page and a head at a time; the first summaries load meanwhile.
-    constexpr int E = D / 64;
     const bool few = m <= kList;
-    uint32_t ahead[E];
-    auto fetch = [&](int x) {
-      const uint16_t* src =
-          a.summary + (static_cast<int64_t>(physical_page(c, b, lo + s.list[x], a.err)) * a.Hkv + h) * D + lane * 2;
-#pragma unroll
-      for (int y = 0; y < E; ++y) ahead[y] = *reinterpret_cast<const uint32_t*>(src + 64 * y);
-    };
     if (few && warp < m * a.G) fetch(warp / a.G);
     const int half = a.r / 2;
     const int64_t pos = a.pos[b];
@@ -764,7 +830,7 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page
     QueryPairs<D, GP, NTH> qp;
     qp.load(a, b, h, 1.f, sh.inv);
     for (int p = threadIdx.x; p < a.r / 2; p += NTH) sh.step[p] = a.rope_step[p];
-    float* qf = reinterpret_cast<float*>(dyn + a.q64_off);  // [GP][D] squares (the selection's fp64 query later)
+    float* qf = reinterpret_cast<float*>(dyn + a.qf_off);  // [GP][D]
 #pragma unroll
     for (int i = 0; i < qp.ITER; ++i) {
       const int g = qp.g0 + i * qp.STEP;
@@ -776,8 +842,8 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page
       qb[(GP + g) * PITCH + qp.d1] = f32_to_bf16(qp.v1[i] - bf16_to_f32(h1));
       q_raw[g * D + qp.d0] = qp.x[i];
       q_raw[g * D + qp.d1] = qp.y[i];
-      qf[g * D + qp.d0] = qp.v0[i] * qp.v0[i];
-      qf[g * D + qp.d1] = qp.v1[i] * qp.v1[i];
+      qf[g * D + qp.d0] = qp.v0[i];
+      qf[g * D + qp.d1] = qp.v1[i];
     }
     __syncthreads();
     // the largest query norm of the group, for the error bound
@@ -785,7 +851,7 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page
       float best = 0.f;
       for (int g = warp; g < a.G; g += W) {
         float ss = 0.f;
-        for (int d = lane; d < D; d += 32) ss += qf[g * D + d];
+        for (int d = lane; d < D; d += 32) ss = fmaf(qf[g * D + d], qf[g * D + d], ss);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
         best = fmaxf(best, nan_to_inf(ss));
@@ -1383,21 +1449,36 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
   // ---- the unit's last split joins them, in their order
   if (!last_to_arrive(a.counters + u, a.splits, &flag)) return;
   const float* p0 = a.part + static_cast<int64_t>(u) * a.splits * ps;
+  // 4 elements a thread at a time, in the splits' order, BATCH of them in flight;
+  // the first ones load while the weights are worked out
+  constexpr int BATCH = 16;
+  float4 y[BATCH];
+  auto load_batch = [&](int e, int w0) {
+#pragma unroll
+    for (int w = 0; w < BATCH; ++w)
+      y[w] = w0 + w < a.splits && e < G * D ? __ldcg(reinterpret_cast<const float4*>(p0 + (w0 + w) * ps + e))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load_batch(t * 4, 0);
   weights(a.splits, [&](int w, int g) { return __ldcg(p0 + w * ps + G * D + g); },
           [&](int w, int g) { return __ldcg(p0 + w * ps + G * D + G + g); }, nullptr);
   factors();
-  // 4 elements a thread at a time, 16 splits' loads in flight
   for (int e = t * 4; e < G * D; e += NTH * 4) {
     const int g = e / D;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-    for (int w = 0; w < a.splits; ++w) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p0 + w * ps + e));
-      const float f = fw[w][g];
-      x.x = fmaf(y.x, f, x.x);
-      x.y = fmaf(y.y, f, x.y);
-      x.z = fmaf(y.z, f, x.z);
-      x.w = fmaf(y.w, f, x.w);
+    for (int w0 = 0; w0 < a.splits; w0 += BATCH) {
+#pragma unroll
+      for (int w = 0; w < BATCH; ++w) {
+        const float f = w0 + w < a.splits ? fw[w0 + w][g] : 0.f;
+        x.x = fmaf(y[w].x, f, x.x);
+        x.y = fmaf(y[w].y, f, x.y);
+        x.z = fmaf(y[w].z, f, x.z);
+        x.w = fmaf(y[w].w, f, x.w);
+      }
+      if (w0 + BATCH < a.splits)
+        load_batch(e, w0 + BATCH);
+      else
+        load_batch(e + NTH * 4, 0);
     }
     const float f = lw[g];
     *reinterpret_cast<float4*>(dst + e) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
@@ -1449,7 +1530,8 @@ cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s) {
   const int pages = static_cast<int>((static_cast<int64_t>(a.max_len) + a.c.P - 1) / a.c.P);
   const size_t bits = (static_cast<size_t>(pages) + 31) / 32 * 4;
   a.q64_off = static_cast<int>((bits + 15) / 16 * 16);
-  a.staged_off = a.q64_off + std::max(a.G * 8, (a.G <= 4 ? 4 : 8) * 4) * D;
+  a.qf_off = a.q64_off + a.G * 8 * D;
+  a.staged_off = a.qf_off + (a.G <= 4 ? 4 : 8) * 4 * D;
   a.staged = (std::min(pages, kStaged) + 127) / 128 * 128;
   size_t smem = a.staged_off + static_cast<size_t>(a.staged) * 4;
   if (pages <= a.num_pages) smem = 0;  // no stream has more pages than it may read
