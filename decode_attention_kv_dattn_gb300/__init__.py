@@ -159,9 +159,19 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream_ptr(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+# The current stream of a device as an integer. (torch.cuda.current_stream builds
+# a Stream object on every call: 3.0 us of the 10 us that a call took on the
+# host, against 0.1 us.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_ptr(stream, device=None):
+    """A stream's handle; None: the current stream of `device` (of the current one if not given)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or device is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device)
 
 
 # ---------------------------------------------------------------- cache descriptors
@@ -203,10 +213,11 @@ class Handle:
                  max_context=0, max_verify_rows=0, device=None, max_selected_pages=0):
         if device is None:
             device = torch.cuda.current_device()
-        self.device = device
+        self.device = device = device if isinstance(device, int) else torch.device(device).index or 0
         # QK-norm weights (layer keys "q_norm", "k_norm", "norm_eps") and state
-        # layers' decays ("log_decay" [Hkv]): host arrays the config points at, kept alive with it (dattn_create copies
-        # them; decode_noalloc reads them on every call)
+        # layers' decays ("log_decay" [Hkv]): host arrays the config points at,
+        # kept alive with it (dattn_create copies them; decode_noalloc reads the
+        # weights on every call)
         self._norm_keep = []
         cfgs = []
         for l in layers:
@@ -245,7 +256,7 @@ class Handle:
         B, T = k.shape[0], k.shape[1]
         _check(lib.dattn_append_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index),
                                    _ptr(start_pos), _ptr(count), _ptr(k), _ptr(v), int(rotate),
-                                   _stream_ptr(stream)), "dattn_append_kv")
+                                   _stream_ptr(stream, self.device)), "dattn_append_kv")
 
     def decode(self, layer, cache: Cache, q, k_new, v_new, pos, out, gate=None, max_seq_len=0,
                write_back=True, stream=None):
@@ -254,7 +265,7 @@ class Handle:
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
-                                _stream_ptr(stream)), "dattn_decode")
+                                _stream_ptr(stream, self.device)), "dattn_decode")
 
     def sparse_decode(self, layer, cache: Cache, summary, q, k_new, v_new, pos, out, num_pages, keep_first=1,
                       keep_last=1, gate=None, max_seq_len=0, write_back=True, selected=None, stream=None):
@@ -265,16 +276,19 @@ class Handle:
         max_selected_pages >= num_pages."""
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
+        if selected is not None and (selected.dtype != torch.int32 or selected.numel() !=
+                                     q.shape[0] * self.config.num_kv_heads * num_pages):
+            raise ValueError("selected: int32 [B, Hkv, num_pages]")
         sel = PageSelection(_ptr(summary), int(num_pages), int(keep_first), int(keep_last), _ptr(selected))
         _check(lib.dattn_sparse_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args), ctypes.byref(sel),
-                                       _stream_ptr(stream)), "dattn_sparse_decode")
+                                       _stream_ptr(stream, self.device)), "dattn_sparse_decode")
 
     def summarize(self, layer, cache: Cache, summary, start_index, count, max_tokens, stream=None):
         """Summaries (bf16 means of the stored keys, [pages, Hkv, D]) of the pages that the
         new tokens [start_index, start_index + count) of each row completed; start_index,
         count: [B] int32, count <= max_tokens."""
         _check(lib.dattn_summarize(self._h, layer, ctypes.byref(cache), _ptr(summary), start_index.shape[0],
-                                   int(max_tokens), _ptr(start_index), _ptr(count), _stream_ptr(stream)),
+                                   int(max_tokens), _ptr(start_index), _ptr(count), _stream_ptr(stream, self.device)),
                "dattn_summarize")
 
     def verify(self, layer, cache: Cache, q, k, v, parent, out, gate=None, max_prefix_len=0,
@@ -285,7 +299,7 @@ class Handle:
         args = VerifyArgs(q.shape[0], q.shape[1], _ptr(q), _ptr(k), _ptr(v), _ptr(parent),
                           _ptr(gate), _ptr(out), int(max_prefix_len), int(write_back), _ptr(pos))
         _check(lib.dattn_verify(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
-                                _stream_ptr(stream)), "dattn_verify")
+                                _stream_ptr(stream, self.device)), "dattn_verify")
 
     def commit(self, layer, cache: Cache, k, v, parent, accepted, num_accepted, pos, stream=None):
         """Write each stream's accepted path (accepted [S, T] int32 node indices root
@@ -293,23 +307,23 @@ class Handle:
         k, v, parent as given to the verify call."""
         _check(lib.dattn_commit(self._h, layer, ctypes.byref(cache), k.shape[0], k.shape[1], _ptr(k),
                                 _ptr(v), _ptr(parent), _ptr(accepted), _ptr(num_accepted), _ptr(pos),
-                                _stream_ptr(stream)), "dattn_commit")
+                                _stream_ptr(stream, self.device)), "dattn_commit")
 
     def prefill(self, layer, cache: Cache, q, k, v, count, start_pos, out, gate=None, stream=None):
         """Ragged prefill: q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16, count/start_pos [S] int32,
         out [S, T, Hq, D] fp32 (rows t < count written), gate [S, T, Hq] bf16 or None."""
         _check(lib.dattn_prefill(self._h, layer, ctypes.byref(cache), q.shape[0], q.shape[1], _ptr(q), _ptr(k),
                                  _ptr(v), _ptr(gate), _ptr(count), _ptr(start_pos), _ptr(out),
-                                 _stream_ptr(stream)), "dattn_prefill")
+                                 _stream_ptr(stream, self.device)), "dattn_prefill")
 
     def debug_config(self, flags=0, wait_limit_us=0):
         """Testing aid: the limit of the device's bounded waits and fault
         injection on the host's side of the wait (see dattn_debug_config)."""
-        _check(lib.dattn_debug_config(self._h, int(flags), int(wait_limit_us)), "dattn_debug_config", "dattn_sparse_decode", "dattn_summarize")
+        _check(lib.dattn_debug_config(self._h, int(flags), int(wait_limit_us)), "dattn_debug_config")
 
     def get_error(self, stream=None) -> int:
         """Synchronize the stream; return and clear the sticky device status."""
-        return lib.dattn_get_error(self._h, _stream_ptr(stream))
+        return lib.dattn_get_error(self._h, _stream_ptr(stream, self.device))
 
 
 def decode_noalloc(config: Config, layer, cache: Cache, q, k_new, v_new, pos, out, gate=None,
