@@ -78,7 +78,7 @@ struct dattn_handle {
   int32_t* sel_table = nullptr;
   int* sel_done = nullptr;
   std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
-  float* sums = nullptr;                  // state layers: the prompt form's segment states
+  float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements a CTA
   int* err = nullptr;
   uint64_t wait_ns = kDefaultWaitNs;  // limit of the kernels' bounded waits
   int debug_flags = 0;                // dattn_debug_config
@@ -563,7 +563,7 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     }
     L.log_decay = nullptr;
   }
-  if (has_state && cudaMalloc(&h->sums, static_cast<size_t>(h->num_sms) * D * D * sizeof(float)) != cudaSuccess)
+  if (has_state && cudaMalloc(&h->sums, 2 * static_cast<size_t>(h->num_sms) * 16384 * sizeof(float)) != cudaSuccess)
     return fail(DATTN_ECUDA);
   if (sel_pitch > 0) {
     const size_t units = static_cast<size_t>(h->max_streams) * Hkv;
@@ -871,9 +871,8 @@ int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_strea
     LinearArgs la = linear_args(h, layer, cache, num_streams, q, k, v, gate, out);
     la.T = max_tokens;
     la.count = count;
-    la.segments = linear_prompt_segments(num_streams * h->Hkv, max_tokens, h->D, h->num_sms, &la.seg_chunks);
     if (encode_linear_maps(la, h->D) != cudaSuccess) return DATTN_EUNSUPPORTED;
-    const int st = cuda_status(launch_linear_prompt(la, h->D, reinterpret_cast<cudaStream_t>(stream)), "linear prompt");
+    const int st = cuda_status(launch_linear_prompt(la, h->D, h->num_sms, reinterpret_cast<cudaStream_t>(stream)), "linear prompt");
     if (st == DATTN_OK) record_launch(stream, cache->k);
     return st;
   }

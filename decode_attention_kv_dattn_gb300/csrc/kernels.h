@@ -185,6 +185,8 @@ struct LinearArgs {
   CUtensorMap tmap_q;          // prompt: q, k, v as (D, heads, B * T) bf16, boxes of (64 dims, 2 heads for q
   CUtensorMap tmap_k;          // (1 where G is 1) or 1, 64 tokens), 128-byte swizzled
   CUtensorMap tmap_v;
+  CUtensorMap tmap_o;          // prompt: out as (D, Hq, B * T) fp32, boxes of 32 rows of 32 dims (2 heads, 16 tokens
+                               // each; 32 tokens where G is 1)
   float* state;                // [n_rows, Hkv, D, D], row = key dim
   int n_rows;
   const int32_t* stream_rows;  // [B] or null
@@ -201,9 +203,10 @@ struct LinearArgs {
   int write_back;              // step: store the new state
   int T;                       // prompt: tokens of a row's arrays
   const int32_t* count;        // prompt: [B]
-  float* sums;                 // prompt: [B * Hkv, segments, D, D]: the segments' own sums, then the states
-                               // they start from
-  int segments, seg_chunks;    // prompt: segments of the longest stream, chunks of a segment
+  float* sums;                 // prompt: [2][num_sms][D, EB] a CTA's slot: its last piece's contribution to the
+                               // state, then the state that the next CTA starts from; and the state that its
+                               // last unit starts from
+  int split;                   // prompt: a CTA has a range of chunks (or one unit)
   int* err;
 };
 
@@ -362,12 +365,8 @@ constexpr int kSelectSmemMax = kSelectBitmapMax + (17 + 8 + 65) * 1024;
 cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s);
 cudaError_t launch_page_attend(const PageArgs& a, int D, bool f8, cudaStream_t s);
 cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
-// The prompt form: one launch, or three with segments.
-cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s);
-// Segments that the streams of a call are cut into (and the chunks of one) for
-// `units` (stream, KV head) units of up to T tokens: at most num_sms CTAs where
-// there is more than one.
-int linear_prompt_segments(int units, int T, int D, int num_sms, int* seg_chunks);
+// The prompt form: one launch, or three where the units' chunks are split.
+cudaError_t launch_linear_prompt(const LinearArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t encode_linear_maps(LinearArgs& a, int D);
 
 // Launch order per stream, for early cache reads. A kernel launched with

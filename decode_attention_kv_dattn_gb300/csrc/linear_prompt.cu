@@ -14,16 +14,26 @@
 // q, k and v are bf16 and enter exactly; the state itself stays in fp32, in
 // registers.
 //
-// Work split. A CTA has one (stream, KV head), EB of the state's columns (all
-// 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
-// shared memory beside Q, two chunks of K and V, and W) and a segment of the
-// stream's chunks. Streams are cut into segments where there are few of them:
-// a first pass sums each segment's own contribution to the state, a scan
-// carries the states across segments, and the main pass starts each segment
-// from its state.
+// Work split. A unit is one (stream, KV head, slice): EB of the state's columns
+// (all 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
+// shared memory beside Q, two chunks of K and V, and W). Where units are many, or
+// their streams short, a CTA has one unit. Otherwise the units' chunks are laid
+// end to end and one CTA an SM takes an equal range of them, worked out on the
+// device from the counts: a range begins and ends inside a unit, so a first pass
+// sums what each CTA's last unit contributes to the state (for the CTA after
+// it), a scan carries the states along, and the main pass starts each range from
+// its state.
 //
-// Roles: 8 compute warps (W, P, the epilogue, the state), one warp that copies
-// (TMA, 128-byte swizzle) and one that issues the MMAs.
+// Roles: 16 state warps (W, and the state: dS in, S's terms out), 4 row warps (P
+// and the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
+// issues the MMAs. The state warps' chain (W, dS, S) and the row warps' (P, O)
+// run beside one another; both end in tensor memory, which is full.
+//
+// An infinity or no number in v would reach earlier tokens of its chunk (its
+// weight in P is 0, and 0 times it is no number): the state warps replace it by
+// 0 for P V, and the row warps give its column no number from its token on -
+// what the recurrence makes of it, whose state column then holds infinities of
+// either sign.
 #include "linear.cuh"
 #include "mma.cuh"
 #include "tc.cuh"
@@ -33,46 +43,54 @@ namespace dattn {
 namespace {
 
 constexpr int C = kLinearChunk;
-constexpr int kComputeWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kStateWarps = 16, kRowWarps = 4;
+constexpr int kTmaWarp = 20, kMmaWarp = 21;
+constexpr int kThreads = 704;
+constexpr int kPieceCost = 1;  // a unit's share of a CTA's range, in chunks, besides its own
 
 enum : int {
-  B_KVFULL = 0,   // [2] K and V of a chunk have landed
-  B_KVFREE = 2,   // [2] every MMA that reads them has completed
-  B_QFULL = 4,    // [2]
-  B_QFREE = 6,    // [2]
+  B_KFULL = 0,    // [2] a chunk's K has landed
+  B_KFREE = 2,    // [2] every MMA that reads it has completed
+  B_VFULL = 4,    // [2] the same for V
+  B_VFREE = 6,    // [2]
   B_WREADY = 8,   // W (and the zeroed rows of a short chunk) written
   B_SREADY = 9,   // the state's two terms written
-  B_ADONE = 10,   // Q K^T complete
-  B_AFREE = 11,   // ... and read
-  B_PREADY = 12,  // P written
-  B_ODONE = 13,   // Q S and P V complete
-  B_OFREE = 14,   // ... and read
-  B_DSDONE = 15,  // K^T W complete
-  B_FINAL = 16,
-  B_COUNT = 17
+  B_SFREE = 10,   // every Q S of a chunk complete
+  B_ADONE = 11,   // Q K^T complete
+  B_AFREE = 12,   // ... and read
+  B_PREADY = 13,  // P written
+  B_ODONE = 14,   // Q S and P V complete
+  B_OFREE = 15,   // ... and read
+  B_DSDONE = 16,  // K^T W complete
+  B_FINAL = 17,
+  B_QFULL = 18,
+  B_QFREE = 19,
+  B_COUNT = 20
 };
 
 template <int D>
 struct Geo {
   static constexpr int EB = D == 128 ? 128 : 64;   // state columns of a CTA
   static constexpr int SLICES = D / EB;
-  static constexpr int QS = D == 128 ? 2 : 1;      // Q tiles in shared memory
+  static constexpr int KS = D == 128 ? 2 : 1;      // chunks of K in shared memory (of V: 2; one Q tile)
   static constexpr int ER = EB / 64, DR = D / 64;  // 64-element regions
   static constexpr int Q_TILE = DR * 16384;        // [region][128 rows][128 bytes]
   static constexpr int K_TILE = DR * 8192;         // [region][64 rows][128 bytes]
   static constexpr int V_TILE = ER * 8192;
   static constexpr int S_PLANE = ER * D * 128;     // [region][D rows][128 bytes]
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + QS * Q_TILE;
-  static constexpr int V_OFF = K_OFF + 2 * K_TILE;
+  static constexpr int K_OFF = Q_OFF + Q_TILE;
+  static constexpr int V_OFF = K_OFF + KS * K_TILE;
   static constexpr int W_OFF = V_OFF + 2 * V_TILE;  // hi, lo
   static constexpr int S_OFF = W_OFF + 2 * V_TILE;  // hi, lo
-  static constexpr int BAR_OFF = S_OFF + 2 * S_PLANE;
+  static constexpr int O_OFF = S_OFF + 2 * S_PLANE;  // [4 row warps][2][32 rows][128 bytes] outputs on their way
+  static constexpr int BAR_OFF = O_OFF + 4 * 8192;
   static constexpr int MISC_OFF = BAR_OFF + 8 * B_COUNT;
-  static constexpr int PW_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
-  static constexpr int SMEM = PW_OFF + (C + 3) * 4 + 1024;  // (1024: alignment)
+  static constexpr int BAD_OFF = (MISC_OFF + 16 + 15) / 16 * 16;  // [2][EB]: 64 chunk + 63 - token of the first
+                                                                  // token without a number in a column
+  static constexpr int FLAG_OFF = BAD_OFF + 2 * EB * 4;           // [2] latest chunk with such a token
+  static constexpr int PW_OFF = FLAG_OFF + 16;                    // [C] the row warps' decays
+  static constexpr int SMEM = PW_OFF + C * 4 + 1024;              // (1024: alignment)
   // tensor memory columns
   static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = T_O1 + EB, T_DS = T_O2 + EB;
   static constexpr int T_COLS = 512;
@@ -114,14 +132,104 @@ __device__ __forceinline__ void st_8(float* p, const float (&x)[8], bool wide) {
   }
 }
 
+// Limit of the wait for copies that may or may not be in flight.
+constexpr uint64_t kDrainNs = 1000000;
+
+// Shared memory to the box at element coordinates (x, y, z) of the tensor map, as
+// part of the thread's current bulk group; and the groups' ends: all but the
+// latest N have been read from shared memory, or all have been written.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Two floats as packed bf16 hi terms and what is left as lo terms.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
   lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
 }
 
-// One pass over a segment. SUMS: the segment's own contribution to the state
-// (from zero), nothing else.
+// The chunks of stream b (0, reported, for a row without a state or a count out
+// of range).
+__device__ __forceinline__ int stream_chunks(const LinearArgs& a, int b, bool report) {
+  int n = a.count[b];
+  if (n < 0 || n > a.T) {
+    if (report) raise_error(a.err, ERR_INDEX);
+    n = 0;
+  }
+  if (state_row(a, b, report) < 0) n = 0;
+  return (n + C - 1) / C;
+}
+
+// A place in the units laid end to end: unit and chunk.
+struct Place {
+  int u, k;
+};
+
+// Where CTA i of NC begins. `cum`: [B] inclusive sums over the streams of their
+// units' weights (HS units of chunks + kPieceCost each), in shared memory.
+__device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum, int HS, int i, int NC) {
+  const int64_t total = cum[a.B - 1];
+  const int64_t t = total * i / NC;
+  if (t >= total) return Place{a.B * HS, 0};
+  int lo = 0, hi = a.B - 1;  // the stream that holds t: the first with cum > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] > t) hi = mid; else lo = mid + 1;
+  }
+  const int before = lo ? cum[lo - 1] : 0;
+  const int w = (cum[lo] - before) / HS;
+  const int off = static_cast<int>(t - before);
+  const int r = off / w, k = off - r * w - kPieceCost;
+  return Place{lo * HS + r, max(k, 0)};
+}
+
+// The streams' weights summed (see range_start), by a whole block of NT threads.
+template <int NT>
+__device__ __forceinline__ void sum_weights(const LinearArgs& a, int* cum, int HS, bool report) {
+  for (int b = threadIdx.x; b < a.B; b += NT) {
+    const int n = stream_chunks(a, b, report);
+    cum[b] = n > 0 ? (n + kPieceCost) * HS : 0;
+  }
+  __syncthreads();
+  block_scan_inclusive<NT>(cum, a.B);
+}
+
+// The pieces of a CTA's range: chunks [k0, k1) of a unit; every role walks them.
+struct Pieces {
+  const LinearArgs& a;
+  int HS;
+  Place at, end;
+  int u, b, h, slice, k0, k1, count;
+  bool last;  // the unit's last piece
+  __device__ __forceinline__ bool next() {
+    while (at.u < end.u || (at.u == end.u && at.k < end.k)) {
+      u = at.u;
+      b = u / HS;
+      const int r = u - b * HS, slices = HS / a.Hkv;
+      h = r / slices;
+      slice = r - h * slices;
+      const int n = stream_chunks(a, b, false);
+      count = a.count[b];
+      k0 = at.k;
+      k1 = u == end.u ? min(n, end.k) : n;
+      last = k1 == n;
+      at = Place{u + 1, 0};
+      if (k1 > k0) return true;
+    }
+    return false;
+  }
+};
+
+// The main pass over a CTA's pieces or, with SUMS, what the CTA's last piece
+// contributes to the state if its unit goes on in the next CTA.
 template <int D, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid_constant__ LinearArgs a) {
   using Gm = Geo<D>;
@@ -131,98 +239,119 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bars = sbase + Gm::BAR_OFF;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::MISC_OFF + 8);
-  float* pw = reinterpret_cast<float*>(smem + Gm::PW_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- the CTA's work: (unit, slice, segment)
-  int x = blockIdx.x;
-  const int slice = x % Gm::SLICES;
-  x /= Gm::SLICES;
-  const int seg = x % a.segments, u = x / a.segments;
-  const int b = u / a.Hkv, h = u - b * a.Hkv;
+  const int HS = a.Hkv * Gm::SLICES;
   const int G = a.G, hpt = G > 1 ? 2 : 1;  // query heads of an M tile
   const int tiles = SUMS ? 0 : (G + hpt - 1) / hpt;
 
   pdl_wait();
   pdl_trigger();
-  const bool report = !SUMS && h == 0 && slice == 0 && seg == 0 && threadIdx.x == 0;
-  const int row = state_row(a, b, report);
-  int count = a.count[b];
-  if (count < 0 || count > a.T) {
-    if (report) raise_error(a.err, ERR_INDEX);
-    count = 0;
+  // ---- the CTA's range
+  Place begin, end;
+  if (a.split) {
+    int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
+    sum_weights<kThreads>(a, cum, HS, !SUMS && blockIdx.x == 0);
+    begin = range_start(a, cum, HS, blockIdx.x, gridDim.x);
+    end = range_start(a, cum, HS, blockIdx.x + 1, gridDim.x);
+    if (SUMS && begin.u < end.u) begin = Place{end.u, 0};
+    if (SUMS && end.k == 0) begin = end;
+    __syncthreads();
+  } else {
+    begin = Place{static_cast<int>(blockIdx.x), 0};
+    end = Place{static_cast<int>(blockIdx.x) + 1, 0};
+    const int b = blockIdx.x / HS;
+    stream_chunks(a, b, blockIdx.x == b * HS && threadIdx.x == 0);
   }
-  const int chunks_all = (count + C - 1) / C;
-  const int c0 = seg * a.seg_chunks, c1 = min(chunks_all, c0 + a.seg_chunks);
-  const bool last_seg = c1 == chunks_all;
-  const int nc = row < 0 ? 0 : c1 - c0;
-  if (nc <= 0 || (SUMS && last_seg)) return;  // (the whole CTA)
+  const Pieces all{a, HS, begin, end};
+  {
+    Pieces p = all;
+    if (!p.next()) return;  // (the whole CTA)
+  }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    mbar_init(bars + 8 * B_QFULL, 1);
+    mbar_init(bars + 8 * B_QFREE, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (B_KVFULL + i), 1);
-      mbar_init(bars + 8 * (B_KVFREE + i), 1);
-      mbar_init(bars + 8 * (B_QFULL + i), 1);
-      mbar_init(bars + 8 * (B_QFREE + i), 1);
+      mbar_init(bars + 8 * (B_KFULL + i), 1);
+      mbar_init(bars + 8 * (B_KFREE + i), 1);
+      mbar_init(bars + 8 * (B_VFULL + i), 1);
+      mbar_init(bars + 8 * (B_VFREE + i), 1);
+      reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[i] = -1;
     }
-    mbar_init(bars + 8 * B_WREADY, kComputeWarps);
-    mbar_init(bars + 8 * B_SREADY, kComputeWarps);
+    for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
+    mbar_init(bars + 8 * B_WREADY, kStateWarps);
+    mbar_init(bars + 8 * B_SREADY, kStateWarps);
+    mbar_init(bars + 8 * B_SFREE, 1);
     mbar_init(bars + 8 * B_ADONE, 1);
-    mbar_init(bars + 8 * B_AFREE, kComputeWarps);
-    mbar_init(bars + 8 * B_PREADY, kComputeWarps);
+    mbar_init(bars + 8 * B_AFREE, kRowWarps);
+    mbar_init(bars + 8 * B_PREADY, kRowWarps);
     mbar_init(bars + 8 * B_ODONE, 1);
-    mbar_init(bars + 8 * B_OFREE, kComputeWarps);
+    mbar_init(bars + 8 * B_OFREE, kRowWarps);
     mbar_init(bars + 8 * B_DSDONE, 1);
     mbar_init(bars + 8 * B_FINAL, 1);
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < C + 3; i += kThreads) pw[i] = a.decay[h * kDecayStride + i];
   if (warp == kMmaWarp) tc::alloc(sbase + Gm::MISC_OFF, Gm::T_COLS);
+  fence_proxy_async_smem();  // (the sums lay where copies go)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::MISC_OFF);
   const Waiter W{bars, abort_flag, a.err};
+  auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
+  auto arrive = [&](int bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * bar);
+  };
 
   if (warp == kTmaWarp) {
     // ================= copies =================
     if (lane == 0) {
       const uint64_t policy = l2_evict_first_policy();
       bool ok = true;
-      int kv = 0, qt = 0;  // copies issued
-      for (int c = 0; c < nc && ok; ++c) {
-        const int st = c & 1;
-        const int tok = b * a.T + (c0 + c) * C;
-        if (c >= 2) ok = W.wait(B_KVFREE + st, ((c >> 1) - 1) & 1);
-        if (!ok) break;
-        {
-          const uint32_t bar = bars + 8 * (B_KVFULL + st);
-          mbar_arrive_expect_tx(bar, Gm::K_TILE + Gm::V_TILE);
-          for (int r = 0; r < Gm::DR; ++r)
-            tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, h, tok, bar, policy);
-          for (int r = 0; r < Gm::ER; ++r)
-            tma_load_3d(sbase + Gm::V_OFF + st * Gm::V_TILE + r * 8192, &a.tmap_v, slice * EB + 64 * r, h, tok, bar,
-                        policy);
-          ++kv;
-        }
-        for (int mt = 0; mt < tiles && ok; ++mt, ++qt) {
-          const int qs = qt % Gm::QS;
-          if (qt >= Gm::QS) ok = W.wait(B_QFREE + qs, (qt / Gm::QS - 1) & 1);
-          if (!ok) break;
-          const uint32_t bar = bars + 8 * (B_QFULL + qs);
-          mbar_arrive_expect_tx(bar, Gm::DR * static_cast<uint32_t>(hpt) * 8192u);
-          for (int r = 0; r < Gm::DR; ++r)
-            tma_load_3d(sbase + Gm::Q_OFF + qs * Gm::Q_TILE + r * 16384, &a.tmap_q, 64 * r, h * G + mt * hpt, tok, bar,
-                        policy);
+      int cc = 0, qt = 0;  // chunks and Q tiles so far
+      Pieces p = all;
+      while (ok && p.next()) {
+        for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
+          const int tok = p.b * a.T + k * C;
+          {
+            const int st = cc & 1;
+            if (cc >= 2) ok = W.wait(B_VFREE + st, ((cc >> 1) - 1) & 1);
+            if (!ok) break;
+            const uint32_t bar = bars + 8 * (B_VFULL + st);
+            mbar_arrive_expect_tx(bar, Gm::V_TILE);
+            for (int r = 0; r < Gm::ER; ++r)
+              tma_load_3d(sbase + Gm::V_OFF + st * Gm::V_TILE + r * 8192, &a.tmap_v, p.slice * EB + 64 * r, p.h, tok,
+                          bar, policy);
+          }
+          {
+            const int st = cc % Gm::KS;
+            if (cc >= Gm::KS) ok = W.wait(B_KFREE + st, (cc / Gm::KS - 1) & 1);
+            if (!ok) break;
+            const uint32_t bar = bars + 8 * (B_KFULL + st);
+            mbar_arrive_expect_tx(bar, Gm::K_TILE);
+            for (int r = 0; r < Gm::DR; ++r)
+              tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
+          }
+          for (int mt = 0; mt < tiles && ok; ++mt, ++qt) {
+            if (qt >= 1) ok = W.wait(B_QFREE, (qt - 1) & 1);
+            if (!ok) break;
+            const uint32_t bar = bars + 8 * B_QFULL;
+            mbar_arrive_expect_tx(bar, Gm::DR * static_cast<uint32_t>(hpt) * 8192u);
+            for (int r = 0; r < Gm::DR; ++r)
+              tma_load_3d(sbase + Gm::Q_OFF + r * 16384, &a.tmap_q, 64 * r, p.h * G + mt * hpt, tok, bar, policy);
+          }
         }
       }
       // Copies still in flight exist only when a role gave up: they land
-      // before the CTA exits.
+      // before the CTA exits (a break above may have left the last chunk's
+      // copies without its count).
       if (*abort_flag) {
-        for (int i = max(0, kv - 2); i < kv; ++i) mbar_wait_bounded(bars + 8 * (B_KVFULL + (i & 1)), (i >> 1) & 1);
-        for (int i = max(0, qt - Gm::QS); i < qt; ++i)
-          mbar_wait_bounded(bars + 8 * (B_QFULL + i % Gm::QS), (i / Gm::QS) & 1);
+        for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
+        for (int i = max(0, cc - Gm::KS + 1); i <= cc; ++i)
+          mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
+        for (int i = max(0, qt - 1); i <= qt; ++i) mbar_wait_bounded(bars + 8 * B_QFULL, i & 1, kDrainNs);
       }
     }
     __syncwarp();
@@ -232,78 +361,91 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       constexpr uint32_t id_a = tc::f16_idesc_ab(128, C, 1, false, false);
       constexpr uint32_t id_o = tc::f16_idesc_ab(128, EB, 1, false, true);
       constexpr uint32_t id_s = tc::f16_idesc_ab(128, EB, 1, true, true);
-      auto issue_ds = [&](int c) -> bool {
-        const int st = c & 1;
-        if (!W.wait(B_WREADY, c & 1)) return false;
+      // A descriptor is a constant upper word and a lower one that the start
+      // address (16-byte units) is added to.
+      const uint64_t k_major = tc::sw128_desc(0, 16, 1024);
+      const uint64_t mn_major = tc::sw128_desc(0, 8192, 1024);
+      const uint64_t s_major = tc::sw128_desc(0, D * 128, 1024);
+      auto at = [&](uint64_t desc, uint32_t addr) { return desc + (addr >> 4); };
+      auto issue_ds = [&](int cc) -> bool {
+        if (!W.wait(B_WREADY, cc & 1)) return false;
         tc::fence_after();
-        const uint32_t kt = sbase + Gm::K_OFF + st * Gm::K_TILE, wt = sbase + Gm::W_OFF;
+        const uint32_t kt = sbase + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE, wt = sbase + Gm::W_OFF;
+#pragma unroll 1
+        for (int m = 0; m < D / 128; ++m) {
+          uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, wt);
 #pragma unroll
-        for (int m = 0; m < D / 128; ++m)
-#pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk) {
-            const uint64_t kd = tc::sw128_desc(kt + m * 16384 + kk * 2048, 8192, 1024);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              tc::mma(tmem + Gm::T_DS + m * EB, kd, tc::sw128_desc(wt + p * Gm::V_TILE + kk * 2048, 8192, 1024), id_s,
-                      kk > 0 || p > 0);
+          for (int kk = 0; kk < C / 16; ++kk, kd += 128, wd += 128) {
+            tc::mma(tmem + Gm::T_DS + m * EB, kd, wd, id_s, kk > 0);
+            tc::mma(tmem + Gm::T_DS + m * EB, kd, wd + Gm::V_TILE / 16, id_s, true);
           }
+        }
         tc::commit(bars + 8 * B_DSDONE);
         return true;
       };
       bool ok = true;
-      int t = 0;  // tiles so far
-      for (int c = 0; c < nc && ok; ++c) {
-        const int st = c & 1;
-        ok = W.wait(B_KVFULL + st, (c >> 1) & 1);
-        if (!ok) break;
-        if constexpr (SUMS) {
-          ok = issue_ds(c);
-          if (ok) tc::commit(bars + 8 * (B_KVFREE + st));
-        }
-        const uint32_t kt = sbase + Gm::K_OFF + st * Gm::K_TILE, vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
-        for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
-          const int qs = t % Gm::QS;
-          const uint32_t qt = sbase + Gm::Q_OFF + qs * Gm::Q_TILE;
-          // A = Q K^T
-          ok = W.wait(B_QFULL + qs, (t / Gm::QS) & 1) && (t == 0 || W.wait(B_AFREE, (t - 1) & 1));
+      int cc = 0, t = 0;  // chunks and Q tiles so far
+      Pieces p = all;
+      while (ok && p.next()) {
+        for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
+          const int st = cc & 1, ks = cc % Gm::KS;
+          ok = W.wait(B_KFULL + ks, (cc / Gm::KS) & 1);
           if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma(tmem + Gm::T_A, tc::sw128_desc(qt + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                    tc::sw128_desc(kt + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), id_a, kk > 0);
-          tc::commit(bars + 8 * B_ADONE);
-          // O1 = Q S
-          ok = (mt > 0 || W.wait(B_SREADY, c & 1)) && (t == 0 || W.wait(B_OFREE, (t - 1) & 1));
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t qd = tc::sw128_desc(qt + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              tc::mma(tmem + Gm::T_O1, qd,
-                      tc::sw128_desc(sbase + Gm::S_OFF + p * Gm::S_PLANE + kk * 2048, D * 128, 1024), id_o,
-                      kk > 0 || p > 0);
-          }
-          tc::commit(bars + 8 * (B_QFREE + qs));
-          if (mt == 0) {
-            ok = issue_ds(c);
+          if constexpr (SUMS) {
+            ok = issue_ds(cc);
             if (!ok) break;
+            tc::commit(bars + 8 * (B_KFREE + ks));
+            tc::commit(bars + 8 * (B_VFREE + st));
           }
-          // O2 = P V
-          ok = W.wait(B_PREADY, t & 1);
-          if (!ok) break;
-          tc::fence_after();
+          const uint32_t kt = sbase + Gm::K_OFF + ks * Gm::K_TILE, vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
+          for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
+            const uint32_t qt = sbase + Gm::Q_OFF;
+            // A = Q K^T
+            ok = W.wait(B_QFULL, t & 1) && (t == 0 || W.wait(B_AFREE, (t - 1) & 1));
+            if (!ok) break;
+            tc::fence_after();
+#pragma unroll 1
+            for (int reg = 0; reg < Gm::DR; ++reg) {
+              uint64_t qd = at(k_major, qt + reg * 16384), kd = at(k_major, kt + reg * 8192);
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk) {
-            const uint64_t vd = tc::sw128_desc(vt + kk * 2048, 8192, 1024);
+              for (int kk = 0; kk < 4; ++kk, qd += 2, kd += 2)
+                tc::mma(tmem + Gm::T_A, qd, kd, id_a, reg > 0 || kk > 0);
+            }
+            tc::commit(bars + 8 * B_ADONE);
+            if (tiles > 1 && mt == tiles - 1) tc::commit(bars + 8 * (B_KFREE + ks));  // (dS is behind it)
+            // O1 = Q S
+            ok = (mt > 0 || W.wait(B_SREADY, cc & 1)) && (t == 0 || W.wait(B_OFREE, (t - 1) & 1));
+            if (!ok) break;
+            tc::fence_after();
+#pragma unroll 1
+            for (int reg = 0; reg < Gm::DR; ++reg) {
+              uint64_t qd = at(k_major, qt + reg * 16384), sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-              tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + p * 32 + kk * 8, vd, id_o, kk > 0 || p > 0);
+              for (int kk = 0; kk < 4; ++kk, qd += 2, sd += 128) {
+                tc::mma(tmem + Gm::T_O1, qd, sd, id_o, reg > 0 || kk > 0);
+                tc::mma(tmem + Gm::T_O1, qd, sd + Gm::S_PLANE / 16, id_o, true);
+              }
+            }
+            tc::commit(bars + 8 * B_QFREE);
+            if (mt == tiles - 1) tc::commit(bars + 8 * B_SFREE);
+            if (mt == 0) {  // (before P V: it waits for the chunk's zeroed rows)
+              ok = issue_ds(cc);
+              if (!ok) break;
+              if (tiles == 1) tc::commit(bars + 8 * (B_KFREE + ks));
+            }
+            // O2 = P V
+            ok = W.wait(B_PREADY, t & 1);
+            if (!ok) break;
+            tc::fence_after();
+            uint64_t vd = at(mn_major, vt);
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk, vd += 128) {
+              tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + kk * 8, vd, id_o, kk > 0);
+              tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + 32 + kk * 8, vd, id_o, true);
+            }
+            tc::commit(bars + 8 * B_ODONE);
+            if (mt == tiles - 1) tc::commit(bars + 8 * (B_VFREE + st));
           }
-          tc::commit(bars + 8 * B_ODONE);
-          if (mt == tiles - 1) tc::commit(bars + 8 * (B_KVFREE + st));
         }
       }
       // every MMA issued has completed before the tensor memory is freed
@@ -311,78 +453,102 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       if (!mbar_wait_bounded(bars + 8 * B_FINAL, 0)) raise_error(a.err, ERR_TIMEOUT);
     }
     __syncwarp();
-  } else {
-    // ================= compute warps =================
-    const int q4 = warp & 3, w2 = warp >> 2;  // lane quarter of tensor memory, column half
+  } else if (warp < kStateWarps) {
+    // ================= state warps =================
+    const int q4 = warp & 3, w4 = warp >> 2;  // lane quarter of tensor memory, column quarter
     const int r = 32 * q4 + lane;             // tensor memory lane
-    const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
-    // the state: this thread's key dim (row) and 64 value dims
-    const int sd = D == 128 ? r : 128 * w2 + r;
-    const int se = D == 128 ? 64 * w2 : 0;
-    const uint32_t t_ds = tmem + lane_off + Gm::T_DS + 64 * w2;
-    float* state = a.state + (static_cast<int64_t>(row) * a.Hkv + h) * D * D + static_cast<int64_t>(sd) * D + slice * EB + se;
-    float* seg_state = a.sums + ((static_cast<int64_t>(u) * a.segments + seg) * D + sd) * D + slice * EB + se;
-    float S[64];
-    if constexpr (SUMS) {
-#pragma unroll
-      for (int e = 0; e < 64; ++e) S[e] = 0.f;
-    } else {
-      const float* src = a.segments > 1 ? seg_state : state;
-#pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src + e);
-        S[e] = y.x;
-        S[e + 1] = y.y;
-        S[e + 2] = y.z;
-        S[e + 3] = y.w;
-      }
-    }
-    auto arrive = [&](int bar) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * bar);
-    };
+    // this thread's key dim (row of the state) and 32 value dims. (Its code is
+    // unrolled over them; with 64, the roles' loops missed the instruction cache
+    // on 43% of the stalled cycles.)
+    const int sd = D == 128 ? r : 128 * (w4 >> 1) + r;
+    const int se = D == 128 ? 32 * w4 : 32 * (w4 & 1);
+    const uint32_t t_ds = tmem + (static_cast<uint32_t>(32 * q4) << 16) + Gm::T_DS + 32 * w4;
+    int* bad = reinterpret_cast<int*>(smem + Gm::BAD_OFF);
+    volatile int* bad_chunk = reinterpret_cast<volatile int*>(smem + Gm::FLAG_OFF);
+    float S[32];
     // the state's two terms as the B operand of Q S (value dims contiguous)
     auto store_s = [&]() {
-      uint8_t* dst = smem + Gm::S_OFF + (D == 128 ? w2 : 0) * (D * 128) + sd * 128;
+      uint8_t* dst = smem + Gm::S_OFF + (D == 128 ? w4 >> 1 : 0) * (D * 128) + sd * 128;
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
+      for (int ch = 0; ch < 4; ++ch) {
         uint4 hi, lo;
         split2(S[8 * ch], S[8 * ch + 1], hi.x, lo.x);
         split2(S[8 * ch + 2], S[8 * ch + 3], hi.y, lo.y);
         split2(S[8 * ch + 4], S[8 * ch + 5], hi.z, lo.z);
         split2(S[8 * ch + 6], S[8 * ch + 7], hi.w, lo.w);
-        const int off = (ch ^ (sd & 7)) << 4;
+        const int off = (((w4 & 1) * 4 + ch) ^ (sd & 7)) << 4;
         *reinterpret_cast<uint4*>(dst + off) = hi;
         *reinterpret_cast<uint4*>(dst + Gm::S_PLANE + off) = lo;
       }
       fence_proxy_async_smem();
       arrive(B_SREADY);
     };
-    if constexpr (!SUMS) store_s();
-    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     bool ok = true;
-    int t = 0;
-    for (int c = 0; c < nc && ok; ++c) {
-      const int st = c & 1;
-      const int tok0 = (c0 + c) * C;
-      const int n = min(C, count - tok0);  // valid tokens
-      ok = __all_sync(0xffffffffu, W.wait(B_KVFULL + st, (c >> 1) & 1));
-      if (!ok) break;
-      // ---- W = lam^(n-1-j) v_j as two terms; the rows past n become zeros in
-      // V, W and K (a zero weight would not stop a NaN there)
-      {
+    int cc = 0;
+    Pieces p = all;
+    while (ok && p.next()) {
+      const float* pw = a.decay + static_cast<int64_t>(p.h) * kDecayStride;
+      float* state = a.state + (static_cast<int64_t>(state_row(a, p.b, false)) * a.Hkv + p.h) * D * D +
+                     static_cast<int64_t>(sd) * D + p.slice * EB + se;
+      if constexpr (SUMS) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = 0.f;
+      } else {
+        // a whole unit starts from the cache's state; inside one, from what the
+        // scan left in the slot of the CTA before, and the first piece of a unit
+        // that goes on from the scan's copy of the state (the CTA that ends the
+        // unit may have stored the new one by now)
+        const float* src = state;
+        if (p.k0 > 0)
+          src = a.sums + (static_cast<int64_t>(blockIdx.x - 1) * D + sd) * EB + se;
+        else if (!p.last)
+          src = a.sums + (static_cast<int64_t>(gridDim.x + blockIdx.x) * D + sd) * EB + se;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src + e);
+          S[e] = y.x;
+          S[e + 1] = y.y;
+          S[e + 2] = y.z;
+          S[e + 3] = y.w;
+        }
+        // (the terms of the last piece are read no more)
+        if (cc > 0 && !warp_wait(B_SFREE, (cc - 1) & 1)) break;
+        store_s();
+      }
+      for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
+        const int st = cc & 1;
+        const int n = min(C, p.count - k * C);  // valid tokens
+        ok = warp_wait(B_VFULL + st, (cc >> 1) & 1);
+        if (!ok) break;
+        // ---- W = lam^(n-1-j) v_j as two terms; the rows past n become zeros in
+        // V, W and K (a zero weight would not stop a NaN there)
         uint8_t* vt = smem + Gm::V_OFF + st * Gm::V_TILE;
         uint8_t* wt = smem + Gm::W_OFF;
-#pragma unroll
-        for (int i = 0; i < Gm::V_TILE / 16 / 256; ++i) {
-          const int off = (threadIdx.x + i * 256) * 16;
+#pragma unroll 1
+        for (int off = threadIdx.x * 16; off < Gm::V_TILE; off += kStateWarps * 512) {
           const int j = (off >> 7) & (C - 1);
           uint4 y = *reinterpret_cast<const uint4*>(vt + off);
           if (j >= n) {
             y = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(vt + off) = y;
           }
-          const float w = j < n ? pw[n - 1 - j] : 0.f;
+          if constexpr (!SUMS) {
+            const uint32_t mag = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                          __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+            if ((mag & 0xffffu) >= 0x7f80u || (mag >> 16) >= 0x7f80u) {
+              // (rare) 0 in place of infinities and no numbers, and a note of the
+              // first such token of the column (a later chunk's note is larger)
+              uint16_t* e16 = reinterpret_cast<uint16_t*>(vt + off);
+              for (int x = 0; x < 8; ++x)
+                if ((e16[x] & 0x7f80u) == 0x7f80u) {
+                  const int e = (off / 8192) * 64 + ((((off >> 4) & 7) ^ (j & 7)) << 3) + x;
+                  atomicMax(bad + st * EB + e, cc * C + C - 1 - j);
+                  e16[x] = 0;
+                }
+              bad_chunk[st] = cc;
+            }
+          }
+          const float w = j < n ? __ldg(pw + n - 1 - j) : 0.f;
           uint4 hi, lo;
           split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
           split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
@@ -392,105 +558,172 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
         if (n < C) {
-          uint8_t* kt = smem + Gm::K_OFF + st * Gm::K_TILE;
-          for (int off = threadIdx.x * 16; off < Gm::K_TILE; off += 256 * 16)
+          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
+          if (!ok) break;
+          uint8_t* kt = smem + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
+          for (int off = threadIdx.x * 16; off < Gm::K_TILE; off += kStateWarps * 512)
             if (((off >> 7) & (C - 1)) >= n) *reinterpret_cast<uint4*>(kt + off) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         arrive(B_WREADY);
-      }
-      if constexpr (!SUMS) {
-        const int i = hpt == 2 ? r >> 1 : r;      // the row's token and head
-        const int hd = hpt == 2 ? r & 1 : 0;
-        for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
-          // ---- P: columns 32 w2 .. of A, masked and decayed
-          ok = __all_sync(0xffffffffu, W.wait(B_ADONE, t & 1));
-          if (!ok) break;
-          tc::fence_after();
+        // ---- the state: S = lam^n S + dS (lam^C with what fp32 drops of it)
+        const float ln = __ldg(pw + n), ln_lo = n == C ? __ldg(pw + C + 2) : 0.f;
+        ok = warp_wait(B_DSDONE, cc & 1);
+        if (!ok) break;
+        tc::fence_after();
+        {
           uint32_t y[32];
-          tc::ld32(tmem + lane_off + Gm::T_A + 32 * w2, y);
+          tc::ld32(t_ds, y);
           tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], ln, fmaf(S[e], ln_lo, __uint_as_float(y[e])));
+        }
+        tc::fence_before();
+        if constexpr (!SUMS) {
+          if (k + 1 < p.k1) {
+            ok = warp_wait(B_SFREE, cc & 1);
+            if (ok) store_s();
+          }
+        }
+      }
+      if (ok && (SUMS || p.last)) {
+        float* dst = SUMS ? a.sums + (static_cast<int64_t>(blockIdx.x) * D + sd) * EB + se : state;
+        const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float z[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) z[q] = S[e + q];
+          st_8(dst + e, z, wide);
+        }
+      }
+    }
+  } else if constexpr (!SUMS) {
+    // ================= row warps =================
+    const int r = 32 * (warp & 3) + lane;  // tensor memory lane: row of the M tile
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int i = hpt == 2 ? r >> 1 : r;  // the row's token and head
+    const int hd = hpt == 2 ? r & 1 : 0;
+    const int* bad = reinterpret_cast<const int*>(smem + Gm::BAD_OFF);
+    const volatile int* bad_chunk = reinterpret_cast<const volatile int*>(smem + Gm::FLAG_OFF);
+    uint8_t* stage = smem + Gm::O_OFF + (warp & 3) * 8192;
+    int stages = 0;  // staged so far
+    float* pw = reinterpret_cast<float*>(smem + Gm::PW_OFF);  // lam^0 .. lam^(C-1) of a head
+    int table_head = -1;
+    bool ok = true;
+    int cc = 0, t = 0;
+    Pieces p = all;
+    while (ok && p.next()) {
+      const float* gpw = a.decay + static_cast<int64_t>(p.h) * kDecayStride;
+      const float row_decay = __ldg(gpw + min(i, C - 1) + 1);
+      // (every row warp writes the whole table: none is still reading the last
+      // one, for P of every earlier tile is complete)
+      if (p.h != table_head) {
+        pw[lane] = __ldg(gpw + lane);
+        pw[lane + C / 2] = __ldg(gpw + lane + C / 2);
+        table_head = p.h;
+        __syncwarp();
+      }
+      for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
+        const int n = min(C, p.count - k * C);
+        for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
+          const int g = mt * hpt + hd;
+          const bool store = i < n && g < G;
+          const int64_t head =
+              (static_cast<int64_t>(p.b) * a.T + k * C + i) * a.Hkv * G + static_cast<int64_t>(p.h) * G + g;
+          const float gate = store && a.gate ? bf16_to_f32(a.gate[head]) : 0.f;
+          ok = warp_wait(B_ADONE, t & 1);
+          if (!ok) break;
+          // ---- P: A masked and decayed
+          tc::fence_after();
+          const int lim = min(i, C - 1);  // columns up to this one count
+#pragma unroll 1
+          for (int j0 = 0; j0 < C; j0 += 16) {
+            uint32_t y[16];
+            tc::ld16(tmem + lane_off + Gm::T_A + j0, y);
+            tc::wait_ld();
+            uint32_t hi[8], lo[8];
+            const float* pi = pw + lim - j0;
+#pragma unroll
+            for (int jj = 0; jj < 16; jj += 2) {
+              const float p0 = j0 + jj <= lim ? __uint_as_float(y[jj]) * pi[-jj] : 0.f;
+              const float p1 = j0 + jj + 1 <= lim ? __uint_as_float(y[jj + 1]) * pi[-jj - 1] : 0.f;
+              split2(p0, p1, hi[jj >> 1], lo[jj >> 1]);
+            }
+            tc::st8(tmem + lane_off + Gm::T_P + j0 / 2, hi);
+            tc::st8(tmem + lane_off + Gm::T_P + 32 + j0 / 2, lo);
+          }
           tc::fence_before();
           arrive(B_AFREE);
-          uint32_t hi[16], lo[16];
-          const int lim = min(i, C - 1) - 32 * w2;  // columns up to this one count
-          const float* pi = pw + (i & (C - 1)) - 32 * w2;
-#pragma unroll
-          for (int jj = 0; jj < 32; jj += 2) {
-            const float p0 = jj <= lim ? __uint_as_float(y[jj]) * pi[-jj] : 0.f;
-            const float p1 = jj + 1 <= lim ? __uint_as_float(y[jj + 1]) * pi[-jj - 1] : 0.f;
-            split2(p0, p1, hi[jj >> 1], lo[jj >> 1]);
-          }
-          tc::st16(tmem + lane_off + Gm::T_P + 16 * w2, hi);
-          tc::st16(tmem + lane_off + Gm::T_P + 32 + 16 * w2, lo);
           tc::wait_st();
-          fence_proxy_async_smem();  // (a short chunk's zeroed V rows)
           tc::fence_before();
           arrive(B_PREADY);
-          // ---- epilogue: this thread's row, half of the columns
-          const int g = mt * hpt + hd, tok = tok0 + i;
-          const bool store = i < n && g < G;
-          const int64_t head = (static_cast<int64_t>(b) * a.T + tok) * a.Hkv * G + static_cast<int64_t>(h) * G + g;
+          // ---- epilogue
           float f = a.scale;
-          if (store && a.gate) f /= 1.f + expf(-bf16_to_f32(a.gate[head]));
-          const float f1 = f * pw[min(i, C - 1) + 1];
-          ok = __all_sync(0xffffffffu, W.wait(B_ODONE, t & 1));
+          if (a.gate) f /= 1.f + expf(-gate);
+          const float f1 = f * row_decay;
+          float* dst = a.out + head * D + p.slice * EB;
+          ok = warp_wait(B_ODONE, t & 1);
           if (!ok) break;
           tc::fence_after();
-          float* dst = a.out + head * D + slice * EB + (EB / 2) * w2;
-#pragma unroll
-          for (int e0 = 0; e0 < EB / 2; e0 += 32) {
-            uint32_t o1[32], o2[32];
-            tc::ld32(tmem + lane_off + Gm::T_O1 + (EB / 2) * w2 + e0, o1);
-            tc::ld32(tmem + lane_off + Gm::T_O2 + (EB / 2) * w2 + e0, o2);
+          const bool odd = bad_chunk[cc & 1] == cc;
+          // whole boxes of rows leave by the TMA unit, through shared memory (a
+          // lane's store of 32 bytes in each of 32 rows takes the load/store path a
+          // cycle a row); short chunks and a group's odd head row by row
+          const bool box = n == C && (mt + 1) * hpt <= G;
+#pragma unroll 1
+          for (int e0 = 0; e0 < EB; e0 += 16) {
+            uint32_t o1[16], o2[16];
+            tc::ld16(tmem + lane_off + Gm::T_O1 + e0, o1);
+            tc::ld16(tmem + lane_off + Gm::T_O2 + e0, o2);
             tc::wait_ld();
-            if (e0 + 32 == EB / 2) {
+            if (odd) {
+              for (int e = 0; e < 16; ++e) {
+                const int x = bad[(cc & 1) * EB + e0 + e] - cc * C;
+                if (x >= 0 && i >= C - 1 - x) {
+#pragma unroll
+                  for (int y = 0; y < 16; ++y)
+                    if (y == e) o2[y] = 0x7fffffffu;
+                }
+              }
+            }
+            if (e0 + 16 == EB) {
               tc::fence_before();
               arrive(B_OFREE);
             }
-            if (store) {
+            float z[16];
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                float z[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  z[q] = fmaf(__uint_as_float(o1[e + q]), f1, __uint_as_float(o2[e + q]) * f);
-                st_8(dst + e0 + e, z, wide);
+            for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
+            if (box) {
+              uint8_t* buf = stage + (stages & 1) * 4096;
+              const int half = (e0 >> 4) & 1;  // of the box's 32 dims
+              if (half == 0) {
+                if (lane == 0) tma_stores_read<1>();
+                __syncwarp();
               }
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(buf + lane * 128 + (((half * 4 + (e >> 2)) ^ (lane & 7)) << 4)) =
+                    make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+              if (half == 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && 32 * (warp & 3) < hpt * C)
+                  tma_store_3d(&a.tmap_o, smem_addr(buf), p.slice * EB + e0 - 16, p.h * G + mt * hpt,
+                               p.b * a.T + k * C + (warp & 3) * (32 / hpt));
+                ++stages;
+              }
+            } else if (store) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(dst + e0 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
             }
           }
         }
-        if (!ok) break;
-      }
-      // ---- the state: S = lam^n S + dS (lam^C with what fp32 drops of it)
-      ok = __all_sync(0xffffffffu, W.wait(B_DSDONE, c & 1));
-      if (!ok) break;
-      tc::fence_after();
-      const float ln = pw[n], ln_lo = n == C ? pw[C + 2] : 0.f;
-#pragma unroll
-      for (int e0 = 0; e0 < 64; e0 += 32) {
-        uint32_t y[32];
-        tc::ld32(t_ds + e0, y);
-        tc::wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          S[e0 + e] = fmaf(S[e0 + e], ln, fmaf(S[e0 + e], ln_lo, __uint_as_float(y[e])));
-      }
-      tc::fence_before();
-      if constexpr (!SUMS) {
-        if (c + 1 < nc) store_s();
       }
     }
-    if (ok && (SUMS || last_seg)) {
-      float* dst = SUMS ? seg_state : state;
-#pragma unroll
-      for (int e = 0; e < 64; e += 8) {
-        float z[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) z[q] = S[e + q];
-        st_8(dst + e, z, (reinterpret_cast<uintptr_t>(dst) & 31u) == 0);
-      }
-    }
+    if (lane == 0) tma_stores_done();
+    __syncwarp();
   }
 
   tc::fence_before();
@@ -501,71 +734,96 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   }
 }
 
-// The states at the segments' starts from the segments' own sums: start 0 is
-// the cache's state, start s + 1 = lam^(tokens of a segment) start s + sum s.
-// One thread per 4 elements of a unit's state; every segment but a stream's
-// last is full.
-__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a, int DD) {
+// The states at the CTAs' starts from their sums (and a copy of the state that
+// a split unit starts from): the slot of a CTA whose last
+// unit goes on holds its piece's own contribution, and then the state after it.
+// The block row of the CTA that holds a unit's beginning carries the unit's state
+// through the slots; one thread per 4 elements. Every chunk of these pieces is
+// full.
+template <int D>
+__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a, int NC) {
+  using Gm = Geo<D>;
+  constexpr int EB = Gm::EB;
+  extern __shared__ float2 decay[];                    // [NC] lam^(tokens of a CTA's piece) as hi + lo
+  int* len = reinterpret_cast<int*>(decay + NC);       // [NC] its chunks, -1 past the unit's pieces
+  int* cum = len + NC;                                 // [B]
   pdl_wait();
   pdl_trigger();
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  const int u = static_cast<int>(e / DD), at = static_cast<int>(e - static_cast<int64_t>(u) * DD);
-  const int b = u / a.Hkv, h = u - b * a.Hkv;
-  if (b >= a.B) return;
-  const int row = state_row(a, b, false);
-  const int count = a.count[b];
-  if (row < 0 || count <= 0 || count > a.T) return;
-  const int segs = ((count + C - 1) / C + a.seg_chunks - 1) / a.seg_chunks;
-  const double l = exp(static_cast<double>(a.log_decay[h]) * a.seg_chunks * C);
-  const float lam = static_cast<float>(l), lam_lo = static_cast<float>(l - static_cast<double>(lam));
-  float4 s = *reinterpret_cast<const float4*>(a.state + (static_cast<int64_t>(row) * a.Hkv + h) * DD + at);
-  float* p = a.sums + static_cast<int64_t>(u) * a.segments * DD + at;
-  float4 next = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (segs > 1) next = *reinterpret_cast<const float4*>(p);
-  for (int i = 0; i < segs; ++i) {
-    const float4 y = next;
-    if (i + 2 < segs) next = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(i + 1) * DD);
-    *reinterpret_cast<float4*>(p + static_cast<int64_t>(i) * DD) = s;
-    s.x = fmaf(s.x, lam, fmaf(s.x, lam_lo, y.x));
-    s.y = fmaf(s.y, lam, fmaf(s.y, lam_lo, y.y));
-    s.z = fmaf(s.z, lam, fmaf(s.z, lam_lo, y.z));
-    s.w = fmaf(s.w, lam, fmaf(s.w, lam_lo, y.w));
+  const int HS = a.Hkv * Gm::SLICES;
+  sum_weights<256>(a, cum, HS, false);
+  const int c = blockIdx.y;
+  const Place begin = range_start(a, cum, HS, c, NC);
+  const Place end = range_start(a, cum, HS, c + 1, NC);
+  // the unit that CTA c leaves unfinished, if c has its beginning
+  if (end.k == 0 || (begin.u == end.u && begin.k > 0)) return;
+  const int u = end.u, b = u / HS, r = u - b * HS, h = r / Gm::SLICES, slice = r - h * Gm::SLICES;
+  for (int x = threadIdx.x; c + x < NC; x += 256) {
+    const Place p0 = range_start(a, cum, HS, c + x, NC), p1 = range_start(a, cum, HS, c + x + 1, NC);
+    // (0 chunks for a CTA with an empty range: its slot holds no sum)
+    len[x] = p1.u == u && p1.k > 0 ? p1.k - (p0.u == u ? p0.k : 0) : -1;
+    const double l = exp(static_cast<double>(a.log_decay[h]) * C * max(len[x], 0));
+    const float lam = static_cast<float>(l);
+    decay[x] = make_float2(lam, static_cast<float>(l - static_cast<double>(lam)));
+  }
+  __syncthreads();
+  const int at = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int d = at / EB, e = at - d * EB;
+  float4 s = *reinterpret_cast<const float4*>(
+      a.state + ((static_cast<int64_t>(state_row(a, b, false)) * a.Hkv + h) * D + d) * D + slice * EB + e);
+  constexpr int64_t SLOT = static_cast<int64_t>(D) * EB;
+  *reinterpret_cast<float4*>(a.sums + (NC + c) * SLOT + at) = s;
+  for (int x0 = 0; c + x0 < NC && len[x0] >= 0; x0 += 8) {  // 8 slots in flight
+    float4 y[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      y[x] = c + x0 + x < NC && len[x0 + x] > 0 ? *reinterpret_cast<const float4*>(a.sums + (c + x0 + x) * SLOT + at)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (c + x0 + x >= NC || len[x0 + x] < 0) return;
+      const float2 lam = decay[x0 + x];
+      s.x = fmaf(s.x, lam.x, fmaf(s.x, lam.y, y[x].x));
+      s.y = fmaf(s.y, lam.x, fmaf(s.y, lam.y, y[x].y));
+      s.z = fmaf(s.z, lam.x, fmaf(s.z, lam.y, y[x].z));
+      s.w = fmaf(s.w, lam.x, fmaf(s.w, lam.y, y[x].w));
+      *reinterpret_cast<float4*>(a.sums + (c + x0 + x) * SLOT + at) = s;
+    }
   }
 }
 
 template <int D, bool SUMS>
-cudaError_t prompt_launch(const LinearArgs& a, cudaStream_t s) {
+cudaError_t prompt_launch(const LinearArgs& a, int ctas, cudaStream_t s) {
   using Gm = Geo<D>;
   auto k = linear_prompt_kernel<D, SUMS>;
   static std::atomic<uint64_t> opted{0};
   const cudaError_t e = opt_in_smem(k, Gm::SMEM, opted);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv * a.segments * Gm::SLICES);
-  return launch_pdl(k, grid, dim3(kThreads), Gm::SMEM, s, a);
+  return launch_pdl(k, dim3(ctas), dim3(kThreads), Gm::SMEM, s, a);
+}
+
+template <int D>
+cudaError_t prompt_launches(const LinearArgs& a, int ctas, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (a.split) {
+    e = prompt_launch<D, true>(a, ctas, s);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(linear_scan_kernel<D>, dim3(D * Geo<D>::EB / 1024, ctas), dim3(256), (3 * ctas + a.B) * sizeof(int), s, a, ctas);
+    if (e != cudaSuccess) return e;
+  }
+  return prompt_launch<D, false>(a, ctas, s);
 }
 
 }  // namespace
 
-int linear_prompt_segments(int units, int T, int D, int num_sms, int* seg_chunks) {
-  const int chunks = (T + C - 1) / C;
-  const int ctas = units * (D == 128 ? Geo<128>::SLICES : Geo<256>::SLICES);
-  int segs = num_sms / ctas;
-  if (segs > chunks / 4) segs = chunks / 4;
-  if (segs < 1) segs = 1;
-  *seg_chunks = (chunks + segs - 1) / segs;
-  return (chunks + *seg_chunks - 1) / *seg_chunks;
-}
-
-cudaError_t launch_linear_prompt(const LinearArgs& a, int D, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (a.segments > 1) {
-    e = D == 128 ? prompt_launch<128, true>(a, s) : prompt_launch<256, true>(a, s);
-    if (e != cudaSuccess) return e;
-    const int64_t elems = static_cast<int64_t>(a.B) * a.Hkv * D * D / 4;
-    e = launch_pdl(linear_scan_kernel, dim3(static_cast<unsigned>((elems + 255) / 256)), dim3(256), 0, s, a, D * D);
-    if (e != cudaSuccess) return e;
-  }
-  return D == 128 ? prompt_launch<128, false>(a, s) : prompt_launch<256, false>(a, s);
+cudaError_t launch_linear_prompt(const LinearArgs& args, int D, int num_sms, cudaStream_t s) {
+  LinearArgs a = args;
+  const int units = a.B * a.Hkv * (D == 128 ? Geo<128>::SLICES : Geo<256>::SLICES);
+  const int chunks = (a.T + C - 1) / C;
+  // Ranges cost two more launches and, in the worst case, a second look at
+  // every K and V: not for short prompts, nor where there are units enough.
+  a.split = chunks > 4 && units < 4 * num_sms;
+  const int ctas = a.split ? num_sms : units;
+  return D == 128 ? prompt_launches<128>(a, ctas, s) : prompt_launches<256>(a, ctas, s);
 }
 
 }  // namespace dattn

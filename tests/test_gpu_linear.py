@@ -222,6 +222,69 @@ def test_infinite_and_missing_values_stay_with_their_stream(dattn):
     assert torch.isfinite(out[0, :, 2:]).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 2), (256, 3, 1)])
+def test_values_that_are_no_numbers_reach_no_earlier_token(dattn, D, Hq, Hkv):
+    """An infinity in v: its column has no number from its token on, everything before it and every other column
+    is as without it. A NaN in q: its own row."""
+    g = torch.Generator().manual_seed(14)
+    T, at, e = 150, 75, D - 3
+    ld = decays(Hkv)
+    q, k, v, _ = inputs(g, 1, T, Hq=Hq, Hkv=Hkv, D=D)
+    bad = v.clone()
+    bad[0, at, 0, e] = float("inf")
+    bad[0, at + 20, 0, e] = float("nan")
+    bq = q.clone()
+    bq[0, at - 5, 0, 1] = float("nan")
+    h = dattn.Handle(Hq, Hkv, D, [{"kind": dattn.CACHE_STATE, "log_decay": ld}], 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    runs = []
+    for qq, vv in ((q, v), (bq, bad)):
+        sd, out = torch.zeros(1, Hkv, D, D, device="cuda"), torch.zeros(1, T, Hq, D, device="cuda")
+        h.prefill(0, dattn.state_cache(sd), qq.cuda(), k.cuda(), vv.cuda(), i32([T]), i32([0]), out)
+        assert h.get_error() == dattn.OK
+        runs.append((out.cpu()[0], sd.cpu()[0]))
+    (o0, s0), (o1, s1) = runs
+    G = Hq // Hkv
+    clean = torch.ones_like(o0, dtype=torch.bool)
+    clean[at:, :G, e] = False
+    clean[at - 5, 0] = False
+    assert torch.equal(o0[clean], o1[clean])
+    assert not torch.isfinite(o1[~clean]).any()
+    keep = torch.ones_like(s0, dtype=torch.bool)
+    keep[0, :, e] = False
+    assert torch.equal(s0[keep], s1[keep]) and not torch.isfinite(s1[0, :, e]).any()
+
+
+@pytest.mark.parametrize("count", [[1000, 3, 0, 700, 64], [0, 0, 0, 0, 1], [0] * 5, [320, 320, 320, 320, 320]])
+def test_ragged_batch_cut_into_ranges(dattn, count):
+    """Streams of very different lengths, none at all, and lengths whose ranges end on unit borders."""
+    g = torch.Generator().manual_seed(15)
+    Hq, Hkv, D, B = 6, 3, 128, len(count)
+    T = max(max(count), 400)
+    ld = np.array([0.0, -0.003, -0.2], np.float32)
+    state = torch.randn(B, Hkv, D, D, generator=g)
+    q, k, v, _ = inputs(g, B, T, Hq=Hq, Hkv=Hkv, D=D)
+    for b in range(B):
+        for x in (q, k, v):
+            x[b, count[b]:] = float("nan")
+    h = dattn.Handle(Hq, Hkv, D, [{"kind": dattn.CACHE_STATE, "log_decay": ld}], B)
+    sd, out = state.cuda(), torch.full((B, T, Hq, D), 7.0, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    h.prefill(0, dattn.state_cache(sd), q.cuda(), k.cuda(), v.cuda(), i32(count), i32([0] * B), out)
+    assert h.get_error() == dattn.OK
+    ref, out = Ref(state, ld), out.cpu()
+    eps = 2.0 ** -16 + (D + 128) * 2.0 ** -23 + T * 2.0 ** -24
+    for b in range(B):
+        for t in range(count[b]):
+            want, size = ref.step(b, q[b, t], k[b, t], v[b, t])
+            if t % 29 == 0 or t > count[b] - 3:
+                close(out[b, t], want, size, eps, f"row {b} token {t}")
+        assert (out[b, count[b]:] == 7.0).all()
+        if count[b] == 0:
+            assert torch.equal(sd[b].cpu(), state[b])
+    close(sd.cpu(), ref.s, ref.a, eps, "state")
+
+
 def test_outputs_and_states_on_16_byte_boundaries(dattn):
     g = torch.Generator().manual_seed(8)
     Hq, Hkv, D, T = 4, 2, 128, 66
