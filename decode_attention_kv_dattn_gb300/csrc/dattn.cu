@@ -78,7 +78,7 @@ struct dattn_handle {
   int32_t* sel_table = nullptr;
   int* sel_done = nullptr;
   std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
-  float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements a CTA
+  float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements and a note a CTA
   int* err = nullptr;
   uint64_t wait_ns = kDefaultWaitNs;  // limit of the kernels' bounded waits
   int debug_flags = 0;                // dattn_debug_config
@@ -563,7 +563,8 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     }
     L.log_decay = nullptr;
   }
-  if (has_state && cudaMalloc(&h->sums, 2 * static_cast<size_t>(h->num_sms) * 16384 * sizeof(float)) != cudaSuccess)
+  if (has_state &&
+      cudaMalloc(&h->sums, static_cast<size_t>(h->num_sms) * (2 * 16384 * sizeof(float) + 16)) != cudaSuccess)
     return fail(DATTN_ECUDA);
   if (sel_pitch > 0) {
     const size_t units = static_cast<size_t>(h->max_streams) * Hkv;

@@ -43,56 +43,58 @@ namespace dattn {
 namespace {
 
 constexpr int C = kLinearChunk;
-constexpr int kStateWarps = 16, kRowWarps = 4;
-constexpr int kTmaWarp = 20, kMmaWarp = 21;
-constexpr int kThreads = 704;
+constexpr int kStateWarps = 16, kRowWarps = 8;
+constexpr int kTmaWarp = 24, kMmaWarp = 25;
+constexpr int kThreads = 832;
 constexpr int kPieceCost = 1;  // a unit's share of a CTA's range, in chunks, besides its own
 
 enum : int {
-  B_KFULL = 0,    // [2] a chunk's K has landed
-  B_KFREE = 2,    // [2] every MMA that reads it has completed
-  B_VFULL = 4,    // [2] the same for V
-  B_VFREE = 6,    // [2]
-  B_WREADY = 8,   // W (and the zeroed rows of a short chunk) written
-  B_SREADY = 9,   // the state's two terms written
-  B_SFREE = 10,   // every Q S of a chunk complete
-  B_ADONE = 11,   // Q K^T complete
-  B_AFREE = 12,   // ... and read
-  B_PREADY = 13,  // P written
-  B_ODONE = 14,   // Q S and P V complete
-  B_OFREE = 15,   // ... and read
-  B_DSDONE = 16,  // K^T W complete
-  B_FINAL = 17,
-  B_QFULL = 18,
-  B_QFREE = 19,
-  B_COUNT = 20
+  B_KFULL,              // a chunk's K has landed
+  B_KFREE,              // every MMA that reads it has completed
+  B_VFULL,              // [2] the same for V
+  B_VFREE = B_VFULL + 2,
+  B_WREADY = B_VFREE + 2,  // W (and the zeroed rows of a short chunk) written
+  B_SREADY,             // the state's two terms written
+  B_SFREE,              // every Q S of a chunk complete
+  B_ADONE,              // Q K^T complete
+  B_AFREE,              // ... and read
+  B_PREADY,             // P written
+  B_ODONE,              // Q S and P V complete
+  B_OFREE,              // ... and read
+  B_DSDONE,             // K^T W complete
+  B_FINAL,
+  B_QFULL,              // [5] 64 dims of a Q tile have landed
+  B_QFREE = B_QFULL + 5,  // [5] ... and the MMAs that read them completed
+  B_COUNT = B_QFREE + 5
 };
 
 template <int D>
 struct Geo {
   static constexpr int EB = D == 128 ? 128 : 64;   // state columns of a CTA
   static constexpr int SLICES = D / EB;
-  static constexpr int KS = D == 128 ? 2 : 1;      // chunks of K in shared memory (of V: 2; one Q tile)
   static constexpr int ER = EB / 64, DR = D / 64;  // 64-element regions
-  static constexpr int Q_TILE = DR * 16384;        // [region][128 rows][128 bytes]
+  static constexpr int QR = D == 128 ? 4 : 5;      // regions of Q in shared memory (a tile has DR): the next tile's
+                                                   // land while this one's are used
+  static constexpr int Q_REGION = 16384;           // [128 rows][128 bytes]
   static constexpr int K_TILE = DR * 8192;         // [region][64 rows][128 bytes]
   static constexpr int V_TILE = ER * 8192;
   static constexpr int S_PLANE = ER * D * 128;     // [region][D rows][128 bytes]
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + Q_TILE;
-  static constexpr int V_OFF = K_OFF + KS * K_TILE;
+  static constexpr int K_OFF = Q_OFF + QR * Q_REGION;
+  static constexpr int V_OFF = K_OFF + K_TILE;
   static constexpr int W_OFF = V_OFF + 2 * V_TILE;  // hi, lo
   static constexpr int S_OFF = W_OFF + 2 * V_TILE;  // hi, lo
-  static constexpr int O_OFF = S_OFF + 2 * S_PLANE;  // [4 row warps][2][32 rows][128 bytes] outputs on their way
-  static constexpr int BAR_OFF = O_OFF + 4 * 8192;
+  static constexpr int O_OFF = S_OFF + 2 * S_PLANE;  // [row warps][32 rows][64 bytes] outputs on their way
+  static constexpr int BAR_OFF = O_OFF + kRowWarps * 2048;
   static constexpr int MISC_OFF = BAR_OFF + 8 * B_COUNT;
   static constexpr int BAD_OFF = (MISC_OFF + 16 + 15) / 16 * 16;  // [2][EB]: 64 chunk + 63 - token of the first
                                                                   // token without a number in a column
   static constexpr int FLAG_OFF = BAD_OFF + 2 * EB * 4;           // [2] latest chunk with such a token
   static constexpr int PW_OFF = FLAG_OFF + 16;                    // [C] the row warps' decays
   static constexpr int SMEM = PW_OFF + C * 4 + 1024;              // (1024: alignment)
-  // tensor memory columns
-  static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = T_O1 + EB, T_DS = T_O2 + EB;
+  // tensor memory columns. At D = 256 the products with S's two terms have their
+  // own columns: one MMA of N = 128 then does both.
+  static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = 256, T_DS = 256 + EB;
   static constexpr int T_COLS = 512;
 };
 
@@ -115,6 +117,18 @@ struct Waiter {
         raise_error(err, ERR_TIMEOUT);
         return false;
       }
+    }
+  }
+  // Which of two phases completes first: 0 or 1 (1 too when neither does in time;
+  // the wait that follows then reports it).
+  __device__ __forceinline__ int first(int b0, uint32_t parity0, int b1, uint32_t parity1) const {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+      for (int i = 0; i < 32; ++i) {
+        if (mbar_test_wait(bars + 8 * b0, parity0)) return 0;
+        if (mbar_test_wait(bars + 8 * b1, parity1)) return 1;
+      }
+      if (*abort || global_timer_ns() - t0 > kDefaultWaitNs) return 1;
     }
   }
 };
@@ -228,9 +242,8 @@ struct Pieces {
   }
 };
 
-// The main pass over a CTA's pieces or, with SUMS, what the CTA's last piece
-// contributes to the state if its unit goes on in the next CTA.
-template <int D, bool SUMS>
+// The main pass over a CTA's pieces.
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid_constant__ LinearArgs a) {
   using Gm = Geo<D>;
   constexpr int EB = Gm::EB;
@@ -242,19 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HS = a.Hkv * Gm::SLICES;
   const int G = a.G, hpt = G > 1 ? 2 : 1;  // query heads of an M tile
-  const int tiles = SUMS ? 0 : (G + hpt - 1) / hpt;
+  const int tiles = (G + hpt - 1) / hpt;
 
-  pdl_wait();
-  pdl_trigger();
-  // ---- the CTA's range
+  // ---- the CTA's range (the counts and rows are the caller's)
   Place begin, end;
   if (a.split) {
     int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
-    sum_weights<kThreads>(a, cum, HS, !SUMS && blockIdx.x == 0);
+    sum_weights<kThreads>(a, cum, HS, blockIdx.x == 0);
     begin = range_start(a, cum, HS, blockIdx.x, gridDim.x);
     end = range_start(a, cum, HS, blockIdx.x + 1, gridDim.x);
-    if (SUMS && begin.u < end.u) begin = Place{end.u, 0};
-    if (SUMS && end.k == 0) begin = end;
     __syncthreads();
   } else {
     begin = Place{static_cast<int>(blockIdx.x), 0};
@@ -265,31 +274,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const Pieces all{a, HS, begin, end};
   {
     Pieces p = all;
-    if (!p.next()) return;  // (the whole CTA)
+    if (!p.next()) {  // (the whole CTA)
+      pdl_wait();
+      return;
+    }
   }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    mbar_init(bars + 8 * B_QFULL, 1);
-    mbar_init(bars + 8 * B_QFREE, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (B_KFULL + i), 1);
-      mbar_init(bars + 8 * (B_KFREE + i), 1);
-      mbar_init(bars + 8 * (B_VFULL + i), 1);
-      mbar_init(bars + 8 * (B_VFREE + i), 1);
-      reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[i] = -1;
-    }
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY                     ? kStateWarps
+                              : i == B_AFREE || i == B_PREADY || i == B_OFREE ? kRowWarps
+                                                                              : 1);
+    reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[0] = reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[1] = -1;
     for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
-    mbar_init(bars + 8 * B_WREADY, kStateWarps);
-    mbar_init(bars + 8 * B_SREADY, kStateWarps);
-    mbar_init(bars + 8 * B_SFREE, 1);
-    mbar_init(bars + 8 * B_ADONE, 1);
-    mbar_init(bars + 8 * B_AFREE, kRowWarps);
-    mbar_init(bars + 8 * B_PREADY, kRowWarps);
-    mbar_init(bars + 8 * B_ODONE, 1);
-    mbar_init(bars + 8 * B_OFREE, kRowWarps);
-    mbar_init(bars + 8 * B_DSDONE, 1);
-    mbar_init(bars + 8 * B_FINAL, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tc::alloc(sbase + Gm::MISC_OFF, Gm::T_COLS);
@@ -297,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::MISC_OFF);
   const Waiter W{bars, abort_flag, a.err};
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     if (lane == 0) {
       const uint64_t policy = l2_evict_first_policy();
       bool ok = true;
-      int cc = 0, qt = 0;  // chunks and Q tiles so far
+      int cc = 0, qr = 0;  // chunks and regions of Q so far
       Pieces p = all;
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
@@ -326,22 +326,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                           bar, policy);
           }
           {
-            const int st = cc % Gm::KS;
-            if (cc >= Gm::KS) ok = W.wait(B_KFREE + st, (cc / Gm::KS - 1) & 1);
+            if (cc >= 1) ok = W.wait(B_KFREE, (cc - 1) & 1);
             if (!ok) break;
-            const uint32_t bar = bars + 8 * (B_KFULL + st);
+            const uint32_t bar = bars + 8 * B_KFULL;
             mbar_arrive_expect_tx(bar, Gm::K_TILE);
             for (int r = 0; r < Gm::DR; ++r)
-              tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
+              tma_load_3d(sbase + Gm::K_OFF + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
           }
-          for (int mt = 0; mt < tiles && ok; ++mt, ++qt) {
-            if (qt >= 1) ok = W.wait(B_QFREE, (qt - 1) & 1);
-            if (!ok) break;
-            const uint32_t bar = bars + 8 * B_QFULL;
-            mbar_arrive_expect_tx(bar, Gm::DR * static_cast<uint32_t>(hpt) * 8192u);
-            for (int r = 0; r < Gm::DR; ++r)
-              tma_load_3d(sbase + Gm::Q_OFF + r * 16384, &a.tmap_q, 64 * r, p.h * G + mt * hpt, tok, bar, policy);
-          }
+          for (int mt = 0; mt < tiles && ok; ++mt)
+            for (int r = 0; r < Gm::DR; ++r, ++qr) {
+              const int slot = qr % Gm::QR;
+              if (qr >= Gm::QR) ok = W.wait(B_QFREE + slot, (qr / Gm::QR - 1) & 1);
+              if (!ok) break;
+              const uint32_t bar = bars + 8 * (B_QFULL + slot);
+              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(hpt) * 8192u);
+              tma_load_3d(sbase + Gm::Q_OFF + slot * Gm::Q_REGION, &a.tmap_q, 64 * r, p.h * G + mt * hpt, tok, bar,
+                          policy);
+            }
         }
       }
       // Copies still in flight exist only when a role gave up: they land
@@ -349,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       // copies without its count).
       if (*abort_flag) {
         for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
-        for (int i = max(0, cc - Gm::KS + 1); i <= cc; ++i)
-          mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
-        for (int i = max(0, qt - 1); i <= qt; ++i) mbar_wait_bounded(bars + 8 * B_QFULL, i & 1, kDrainNs);
+        for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * B_KFULL, i & 1, kDrainNs);
+        for (int i = max(0, qr - Gm::QR); i <= qr; ++i)
+          mbar_wait_bounded(bars + 8 * (B_QFULL + i % Gm::QR), (i / Gm::QR) & 1, kDrainNs);
       }
     }
     __syncwarp();
@@ -359,18 +360,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     // ================= MMA issue =================
     if (lane == 0) {
       constexpr uint32_t id_a = tc::f16_idesc_ab(128, C, 1, false, false);
+      constexpr uint32_t id_q = tc::f16_idesc_ab(128, 128, 1, false, true);
       constexpr uint32_t id_o = tc::f16_idesc_ab(128, EB, 1, false, true);
       constexpr uint32_t id_s = tc::f16_idesc_ab(128, EB, 1, true, true);
-      // A descriptor is a constant upper word and a lower one that the start
-      // address (16-byte units) is added to.
+      // A descriptor is a constant and the start address in 16-byte units.
       const uint64_t k_major = tc::sw128_desc(0, 16, 1024);
       const uint64_t mn_major = tc::sw128_desc(0, 8192, 1024);
-      const uint64_t s_major = tc::sw128_desc(0, D * 128, 1024);
+      // S as an N = 128 operand: at D = 128 one term's two regions of 64 value
+      // dims, at D = 256 both terms' one region
+      const uint64_t s_major = tc::sw128_desc(0, D == 128 ? D * 128 : Gm::S_PLANE, 1024);
       auto at = [&](uint64_t desc, uint32_t addr) { return desc + (addr >> 4); };
+      const uint32_t kt = sbase + Gm::K_OFF, wt = sbase + Gm::W_OFF;
       auto issue_ds = [&](int cc) -> bool {
         if (!W.wait(B_WREADY, cc & 1)) return false;
         tc::fence_after();
-        const uint32_t kt = sbase + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE, wt = sbase + Gm::W_OFF;
 #pragma unroll 1
         for (int m = 0; m < D / 128; ++m) {
           uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, wt);
@@ -381,57 +384,68 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           }
         }
         tc::commit(bars + 8 * B_DSDONE);
+        if (tiles == 1) tc::commit(bars + 8 * B_KFREE);
         return true;
       };
       bool ok = true;
-      int cc = 0, t = 0;  // chunks and Q tiles so far
+      int cc = 0, t = 0, qr = 0;  // chunks, Q tiles and regions of Q so far
       Pieces p = all;
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
-          const int st = cc & 1, ks = cc % Gm::KS;
-          ok = W.wait(B_KFULL + ks, (cc / Gm::KS) & 1);
+          const int st = cc & 1;
+          const uint32_t vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
+          ok = W.wait(B_KFULL, cc & 1);
           if (!ok) break;
-          if constexpr (SUMS) {
-            ok = issue_ds(cc);
-            if (!ok) break;
-            tc::commit(bars + 8 * (B_KFREE + ks));
-            tc::commit(bars + 8 * (B_VFREE + st));
-          }
-          const uint32_t kt = sbase + Gm::K_OFF + ks * Gm::K_TILE, vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
-          for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
-            const uint32_t qt = sbase + Gm::Q_OFF;
+          for (int mt = 0; mt < tiles && ok; ++mt, ++t, qr += Gm::DR) {
             // A = Q K^T
-            ok = W.wait(B_QFULL, t & 1) && (t == 0 || W.wait(B_AFREE, (t - 1) & 1));
+            ok = t == 0 || W.wait(B_AFREE, (t - 1) & 1);
             if (!ok) break;
-            tc::fence_after();
 #pragma unroll 1
             for (int reg = 0; reg < Gm::DR; ++reg) {
-              uint64_t qd = at(k_major, qt + reg * 16384), kd = at(k_major, kt + reg * 8192);
+              const int slot = (qr + reg) % Gm::QR;
+              ok = W.wait(B_QFULL + slot, ((qr + reg) / Gm::QR) & 1);
+              if (!ok) break;
+              tc::fence_after();
+              uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION), kd = at(k_major, kt + reg * 8192);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk, qd += 2, kd += 2)
                 tc::mma(tmem + Gm::T_A, qd, kd, id_a, reg > 0 || kk > 0);
             }
+            if (!ok) break;
             tc::commit(bars + 8 * B_ADONE);
-            if (tiles > 1 && mt == tiles - 1) tc::commit(bars + 8 * (B_KFREE + ks));  // (dS is behind it)
+            if (tiles > 1 && mt == tiles - 1) tc::commit(bars + 8 * B_KFREE);  // (dS went before)
+            // dS and Q S in the order in which they can start; dS before P V in any
+            // case (which waits for the chunk's zeroed rows)
+            bool ds = mt == 0;
+            if (ds) {
+              ok = W.wait(B_SREADY, cc & 1);
+              if (!ok) break;
+              if (t > 0 && W.first(B_OFREE, (t - 1) & 1, B_WREADY, cc & 1) != 0) {
+                ok = issue_ds(cc);
+                if (!ok) break;
+                ds = false;
+              }
+            }
             // O1 = Q S
-            ok = (mt > 0 || W.wait(B_SREADY, cc & 1)) && (t == 0 || W.wait(B_OFREE, (t - 1) & 1));
+            ok = t == 0 || W.wait(B_OFREE, (t - 1) & 1);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll 1
             for (int reg = 0; reg < Gm::DR; ++reg) {
-              uint64_t qd = at(k_major, qt + reg * 16384), sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
+              const int slot = (qr + reg) % Gm::QR;
+              uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
+              uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk, qd += 2, sd += 128) {
-                tc::mma(tmem + Gm::T_O1, qd, sd, id_o, reg > 0 || kk > 0);
-                tc::mma(tmem + Gm::T_O1, qd, sd + Gm::S_PLANE / 16, id_o, true);
+                tc::mma(tmem + Gm::T_O1, qd, sd, id_q, reg > 0 || kk > 0);
+                if constexpr (D == 128) tc::mma(tmem + Gm::T_O1, qd, sd + Gm::S_PLANE / 16, id_q, true);
               }
+              tc::commit(bars + 8 * (B_QFREE + slot));
             }
-            tc::commit(bars + 8 * B_QFREE);
             if (mt == tiles - 1) tc::commit(bars + 8 * B_SFREE);
-            if (mt == 0) {  // (before P V: it waits for the chunk's zeroed rows)
+            if (ds) {
               ok = issue_ds(cc);
               if (!ok) break;
-              if (tiles == 1) tc::commit(bars + 8 * (B_KFREE + ks));
             }
             // O2 = P V
             ok = W.wait(B_PREADY, t & 1);
@@ -490,31 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       const float* pw = a.decay + static_cast<int64_t>(p.h) * kDecayStride;
       float* state = a.state + (static_cast<int64_t>(state_row(a, p.b, false)) * a.Hkv + p.h) * D * D +
                      static_cast<int64_t>(sd) * D + p.slice * EB + se;
-      if constexpr (SUMS) {
+      // a whole unit starts from the cache's state; inside one, from what the scan
+      // left in the slot of the CTA before, and the first piece of a unit that
+      // goes on from the scan's copy of the state (the CTA that ends the unit may
+      // have stored the new one by now)
+      const float* src = state;
+      if (p.k0 > 0)
+        src = a.sums + (static_cast<int64_t>(blockIdx.x - 1) * D + sd) * EB + se;
+      else if (!p.last)
+        src = a.sums + (static_cast<int64_t>(gridDim.x + blockIdx.x) * D + sd) * EB + se;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = 0.f;
-      } else {
-        // a whole unit starts from the cache's state; inside one, from what the
-        // scan left in the slot of the CTA before, and the first piece of a unit
-        // that goes on from the scan's copy of the state (the CTA that ends the
-        // unit may have stored the new one by now)
-        const float* src = state;
-        if (p.k0 > 0)
-          src = a.sums + (static_cast<int64_t>(blockIdx.x - 1) * D + sd) * EB + se;
-        else if (!p.last)
-          src = a.sums + (static_cast<int64_t>(gridDim.x + blockIdx.x) * D + sd) * EB + se;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src + e);
-          S[e] = y.x;
-          S[e + 1] = y.y;
-          S[e + 2] = y.z;
-          S[e + 3] = y.w;
-        }
-        // (the terms of the last piece are read no more)
-        if (cc > 0 && !warp_wait(B_SFREE, (cc - 1) & 1)) break;
-        store_s();
+      for (int e = 0; e < 32; e += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src + e);
+        S[e] = y.x;
+        S[e + 1] = y.y;
+        S[e + 2] = y.z;
+        S[e + 3] = y.w;
       }
+      // (the terms of the last piece are read no more)
+      if (cc > 0 && !warp_wait(B_SFREE, (cc - 1) & 1)) break;
+      store_s();
       for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
         const int st = cc & 1;
         const int n = min(C, p.count - k * C);  // valid tokens
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             y = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(vt + off) = y;
           }
-          if constexpr (!SUMS) {
+          {
             const uint32_t mag = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
                                           __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
             if ((mag & 0xffffu) >= 0x7f80u || (mag >> 16) >= 0x7f80u) {
@@ -558,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
         if (n < C) {
-          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
+          ok = warp_wait(B_KFULL, cc & 1);
           if (!ok) break;
-          uint8_t* kt = smem + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
+          uint8_t* kt = smem + Gm::K_OFF;
           for (int off = threadIdx.x * 16; off < Gm::K_TILE; off += kStateWarps * 512)
             if (((off >> 7) & (C - 1)) >= n) *reinterpret_cast<uint4*>(kt + off) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -571,23 +580,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         ok = warp_wait(B_DSDONE, cc & 1);
         if (!ok) break;
         tc::fence_after();
-        {
-          uint32_t y[32];
-          tc::ld32(t_ds, y);
+#pragma unroll
+        for (int e0 = 0; e0 < 32; e0 += 16) {
+          uint32_t y[16];
+          tc::ld16(t_ds + e0, y);
           tc::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], ln, fmaf(S[e], ln_lo, __uint_as_float(y[e])));
+          for (int e = 0; e < 16; ++e)
+            S[e0 + e] = fmaf(S[e0 + e], ln, fmaf(S[e0 + e], ln_lo, __uint_as_float(y[e])));
         }
         tc::fence_before();
-        if constexpr (!SUMS) {
-          if (k + 1 < p.k1) {
-            ok = warp_wait(B_SFREE, cc & 1);
-            if (ok) store_s();
-          }
+        if (k + 1 < p.k1) {
+          ok = warp_wait(B_SFREE, cc & 1);
+          if (ok) store_s();
         }
       }
-      if (ok && (SUMS || p.last)) {
-        float* dst = SUMS ? a.sums + (static_cast<int64_t>(blockIdx.x) * D + sd) * EB + se : state;
+      if (ok && p.last) {
+        float* dst = state;
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
@@ -598,16 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         }
       }
     }
-  } else if constexpr (!SUMS) {
+  } else {
     // ================= row warps =================
     const int r = 32 * (warp & 3) + lane;  // tensor memory lane: row of the M tile
+    const int w2 = (warp - kStateWarps) >> 2;  // half of the columns
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int i = hpt == 2 ? r >> 1 : r;  // the row's token and head
     const int hd = hpt == 2 ? r & 1 : 0;
     const int* bad = reinterpret_cast<const int*>(smem + Gm::BAD_OFF);
     const volatile int* bad_chunk = reinterpret_cast<const volatile int*>(smem + Gm::FLAG_OFF);
-    uint8_t* stage = smem + Gm::O_OFF + (warp & 3) * 8192;
-    int stages = 0;  // staged so far
+    uint8_t* stage = smem + Gm::O_OFF + (warp - kStateWarps) * 2048;
     float* pw = reinterpret_cast<float*>(smem + Gm::PW_OFF);  // lam^0 .. lam^(C-1) of a head
     int table_head = -1;
     bool ok = true;
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           tc::fence_after();
           const int lim = min(i, C - 1);  // columns up to this one count
 #pragma unroll 1
-          for (int j0 = 0; j0 < C; j0 += 16) {
+          for (int j0 = 32 * w2; j0 < 32 * w2 + 32; j0 += 16) {
             uint32_t y[16];
             tc::ld16(tmem + lane_off + Gm::T_A + j0, y);
             tc::wait_ld();
@@ -672,10 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           // cycle a row); short chunks and a group's odd head row by row
           const bool box = n == C && (mt + 1) * hpt <= G;
 #pragma unroll 1
-          for (int e0 = 0; e0 < EB; e0 += 16) {
+          for (int e0 = EB / 2 * w2; e0 < EB / 2 * (w2 + 1); e0 += 16) {
             uint32_t o1[16], o2[16];
             tc::ld16(tmem + lane_off + Gm::T_O1 + e0, o1);
             tc::ld16(tmem + lane_off + Gm::T_O2 + e0, o2);
+            if constexpr (D == 256) {
+              uint32_t lo[16];
+              tc::ld16(tmem + lane_off + Gm::T_O1 + 64 + e0, lo);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(__uint_as_float(o1[e]) + __uint_as_float(lo[e]));
+            }
             tc::wait_ld();
             if (odd) {
               for (int e = 0; e < 16; ++e) {
@@ -687,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                 }
               }
             }
-            if (e0 + 16 == EB) {
+            if (e0 + 16 == EB / 2 * (w2 + 1)) {
               tc::fence_before();
               arrive(B_OFREE);
             }
@@ -695,24 +711,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
             if (box) {
-              uint8_t* buf = stage + (stages & 1) * 4096;
-              const int half = (e0 >> 4) & 1;  // of the box's 32 dims
-              if (half == 0) {
-                if (lane == 0) tma_stores_read<1>();
-                __syncwarp();
-              }
+              if (lane == 0) tma_stores_read<0>();
+              __syncwarp();
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(buf + lane * 128 + (((half * 4 + (e >> 2)) ^ (lane & 7)) << 4)) =
+                *reinterpret_cast<float4*>(stage + lane * 64 + (((e >> 2) ^ ((lane >> 1) & 3)) << 4)) =
                     make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
-              if (half == 1) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && 32 * (warp & 3) < hpt * C)
-                  tma_store_3d(&a.tmap_o, smem_addr(buf), p.slice * EB + e0 - 16, p.h * G + mt * hpt,
-                               p.b * a.T + k * C + (warp & 3) * (32 / hpt));
-                ++stages;
-              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && 32 * (warp & 3) < hpt * C)
+                tma_store_3d(&a.tmap_o, smem_addr(stage), p.slice * EB + e0, p.h * G + mt * hpt,
+                             p.b * a.T + k * C + (warp & 3) * (32 / hpt));
             } else if (store) {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
@@ -734,6 +743,207 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------------- the sums
+
+// What each CTA's last piece contributes to the state, if its unit goes on in the
+// next CTA: K^T W over chunks (all full), in tensor memory over groups of up to
+// kSumGroup of them - W's weights reach to the group's end - and from group to
+// group in registers. The state warps make W, the rest is copies and MMAs; K, V
+// and W are rings, so the pass runs at the rate of its copies.
+constexpr int kSumGroup = 4, kSumStages = 4;
+constexpr int kSumThreads = (kStateWarps + 2) * 32;
+enum : int { R_FULL, R_FREE = R_FULL + kSumStages, R_WREADY = R_FREE + kSumStages, R_WFREE = R_WREADY + 2,
+             R_DONE = R_WFREE + 2, R_FINAL, R_COUNT };
+
+template <int D>
+struct SumGeo {
+  using Gm = Geo<D>;
+  static constexpr int STAGE = Gm::K_TILE + Gm::V_TILE;
+  static constexpr int W_OFF = kSumStages * STAGE;             // [2] hi, lo
+  static constexpr int BAR_OFF = W_OFF + 4 * Gm::V_TILE;
+  static constexpr int MISC_OFF = BAR_OFF + 8 * R_COUNT;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  static constexpr int T_COLS = 128;
+};
+
+// What the scan knows of a CTA's slot: the unit that goes on in the next CTA (-1:
+// none), whether the slot holds a sum (1; 2 when it is from the unit's beginning)
+// and the decay over its tokens as hi + lo. Behind the slots and their copies.
+struct alignas(16) SlotNote {
+  int unit, kind;
+  float lam, lam_lo;
+};
+template <int D>
+__device__ __forceinline__ SlotNote* slot_notes(const LinearArgs& a, int ctas) {
+  return reinterpret_cast<SlotNote*>(a.sums + static_cast<int64_t>(2) * ctas * D * Geo<D>::EB);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __grid_constant__ LinearArgs a) {
+  using Gm = Geo<D>;
+  using Sg = SumGeo<D>;
+  constexpr int EB = Gm::EB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bars = sbase + Sg::BAR_OFF;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sg::MISC_OFF + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int HS = a.Hkv * Gm::SLICES;
+  int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
+  sum_weights<kSumThreads>(a, cum, HS, false);
+  const Place begin = range_start(a, cum, HS, blockIdx.x, gridDim.x);
+  const Place end = range_start(a, cum, HS, blockIdx.x + 1, gridDim.x);
+  const int k0 = begin.u == end.u ? begin.k : 0, chunks = end.k - k0;
+  const int b = end.u / HS, r0 = end.u - b * HS, h = r0 / Gm::SLICES, slice = r0 - h * Gm::SLICES;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    SlotNote n{-1, 0, 0.f, 0.f};
+    if (end.k > 0) {
+      const double l = exp(static_cast<double>(a.log_decay[h]) * C * chunks);
+      const float lam = static_cast<float>(l);
+      n = SlotNote{end.u, chunks > 0 ? (k0 == 0 ? 2 : 1) : 0, lam, static_cast<float>(l - static_cast<double>(lam))};
+    }
+    slot_notes<D>(a, gridDim.x)[blockIdx.x] = n;
+  }
+  if (end.k == 0 || chunks <= 0) return;  // (the whole CTA)
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < R_COUNT; ++i)
+      mbar_init(bars + 8 * i, i == R_WREADY || i == R_WREADY + 1 ? kStateWarps : 1);
+    fence_mbar_init();
+  }
+  if (warp == kStateWarps + 1) tc::alloc(sbase + Sg::MISC_OFF, Sg::T_COLS);
+  fence_proxy_async_smem();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Sg::MISC_OFF);
+  const Waiter W{bars, abort_flag, a.err};
+  auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
+
+  if (warp == kStateWarps) {
+    // ================= copies =================
+    if (lane == 0) {
+      const uint64_t policy = l2_evict_first_policy();
+      int c = 0;
+      for (; c < chunks; ++c) {
+        const int st = c % kSumStages;
+        if (c >= kSumStages && !W.wait(R_FREE + st, (c / kSumStages - 1) & 1)) break;
+        const uint32_t bar = bars + 8 * (R_FULL + st), dst = sbase + st * Sg::STAGE;
+        const int tok = b * a.T + (k0 + c) * C;
+        mbar_arrive_expect_tx(bar, Sg::STAGE);
+        for (int r = 0; r < Gm::DR; ++r) tma_load_3d(dst + r * 8192, &a.tmap_k, 64 * r, h, tok, bar, policy);
+        for (int r = 0; r < Gm::ER; ++r)
+          tma_load_3d(dst + Gm::K_TILE + r * 8192, &a.tmap_v, slice * EB + 64 * r, h, tok, bar, policy);
+      }
+      // (a role gave up: copies in flight land before the CTA exits)
+      if (*abort_flag)
+        for (int i = max(0, c - kSumStages); i < c; ++i)
+          mbar_wait_bounded(bars + 8 * (R_FULL + i % kSumStages), (i / kSumStages) & 1, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == kStateWarps + 1) {
+    // ================= MMA issue =================
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc::f16_idesc_ab(128, EB, 1, true, true);
+      const uint64_t mn_major = tc::sw128_desc(0, 8192, 1024);
+      for (int c = 0; c < chunks; ++c) {
+        const int st = c % kSumStages;
+        if (!W.wait(R_FULL + st, (c / kSumStages) & 1) || !W.wait(R_WREADY + (c & 1), (c >> 1) & 1)) break;
+        tc::fence_after();
+        const uint32_t kt = sbase + st * Sg::STAGE, wt = sbase + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+#pragma unroll 1
+        for (int m = 0; m < D / 128; ++m) {
+          uint64_t kd = mn_major + ((kt + m * 16384) >> 4), wd = mn_major + (wt >> 4);
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk, kd += 128, wd += 128) {
+            tc::mma(tmem + m * EB, kd, wd, id_s, kk > 0 || c % kSumGroup > 0);
+            tc::mma(tmem + m * EB, kd, wd + Gm::V_TILE / 16, id_s, true);
+          }
+        }
+        tc::commit(bars + 8 * (R_FREE + st));
+        tc::commit(bars + 8 * (R_WFREE + (c & 1)));
+        if (c % kSumGroup == kSumGroup - 1 || c == chunks - 1) tc::commit(bars + 8 * R_DONE);
+      }
+      tc::commit(bars + 8 * R_FINAL);
+      if (!mbar_wait_bounded(bars + 8 * R_FINAL, 0)) raise_error(a.err, ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ================= state warps =================
+    const int q4 = warp & 3, w4 = warp >> 2, r = 32 * q4 + lane;
+    const int sd = D == 128 ? r : 128 * (w4 >> 1) + r;
+    const int se = D == 128 ? 32 * w4 : 32 * (w4 & 1);
+    const float* pw = a.decay + static_cast<int64_t>(h) * kDecayStride;
+    const float lam = __ldg(pw + C), lam_lo = __ldg(pw + C + 2);
+    float S[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S[e] = 0.f;
+    int groups = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int st = c % kSumStages;
+      const int after = min(kSumGroup - 1 - c % kSumGroup, chunks - 1 - c);  // chunks of the group behind this one
+      float g = 1.f;
+      for (int i = 0; i < after; ++i) g *= lam;
+      if (!warp_wait(R_FULL + st, (c / kSumStages) & 1)) break;
+      if (c >= 2 && !warp_wait(R_WFREE + (c & 1), ((c >> 1) - 1) & 1)) break;
+      const uint8_t* vt = smem + st * Sg::STAGE + Gm::K_TILE;
+      uint8_t* wt = smem + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+#pragma unroll 1
+      for (int off = threadIdx.x * 16; off < Gm::V_TILE; off += kStateWarps * 512) {
+        const uint4 y = *reinterpret_cast<const uint4*>(vt + off);
+        const float w = __ldg(pw + C - 1 - ((off >> 7) & (C - 1))) * g;
+        uint4 hi, lo;
+        split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
+        split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
+        split2(bf16_lo(y.z) * w, bf16_hi(y.z) * w, hi.z, lo.z);
+        split2(bf16_lo(y.w) * w, bf16_hi(y.w) * w, hi.w, lo.w);
+        *reinterpret_cast<uint4*>(wt + off) = hi;
+        *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (R_WREADY + (c & 1)));
+      if (after == 0) {
+        // the group's end: S = lam^(its tokens) S + sum
+        const int len = c % kSumGroup + 1;
+        if (!warp_wait(R_DONE, groups & 1)) break;
+        ++groups;
+        tc::fence_after();
+        for (int i = 0; i < len; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], lam, S[e] * lam_lo);
+#pragma unroll
+        for (int e0 = 0; e0 < 32; e0 += 16) {
+          uint32_t y[16];
+          tc::ld16(tmem + (static_cast<uint32_t>(32 * q4) << 16) + 32 * w4 + e0, y);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[e0 + e] += __uint_as_float(y[e]);
+        }
+        tc::fence_before();
+      }
+    }
+    float* dst = a.sums + (static_cast<int64_t>(blockIdx.x) * D + sd) * EB + se;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      float z[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] = S[e + q];
+      st_8(dst + e, z, true);
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kStateWarps + 1) {
+    tc::fence_after();
+    tc::dealloc(tmem, Sg::T_COLS);
+  }
+}
+
 // The states at the CTAs' starts from their sums (and a copy of the state that
 // a split unit starts from): the slot of a CTA whose last
 // unit goes on holds its piece's own contribution, and then the state after it.
@@ -744,73 +954,58 @@ template <int D>
 __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a, int NC) {
   using Gm = Geo<D>;
   constexpr int EB = Gm::EB;
-  extern __shared__ float2 decay[];                    // [NC] lam^(tokens of a CTA's piece) as hi + lo
-  int* len = reinterpret_cast<int*>(decay + NC);       // [NC] its chunks, -1 past the unit's pieces
-  int* cum = len + NC;                                 // [B]
+  constexpr int64_t SLOT = static_cast<int64_t>(D) * EB;
+  constexpr int SLOTS = 8;  // in flight
+  extern __shared__ SlotNote note[];  // [NC]
+  const int HS = a.Hkv * Gm::SLICES, c = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  const int HS = a.Hkv * Gm::SLICES;
-  sum_weights<256>(a, cum, HS, false);
-  const int c = blockIdx.y;
-  const Place begin = range_start(a, cum, HS, c, NC);
-  const Place end = range_start(a, cum, HS, c + 1, NC);
-  // the unit that CTA c leaves unfinished, if c has its beginning
-  if (end.k == 0 || (begin.u == end.u && begin.k > 0)) return;
-  const int u = end.u, b = u / HS, r = u - b * HS, h = r / Gm::SLICES, slice = r - h * Gm::SLICES;
-  for (int x = threadIdx.x; c + x < NC; x += 256) {
-    const Place p0 = range_start(a, cum, HS, c + x, NC), p1 = range_start(a, cum, HS, c + x + 1, NC);
-    // (0 chunks for a CTA with an empty range: its slot holds no sum)
-    len[x] = p1.u == u && p1.k > 0 ? p1.k - (p0.u == u ? p0.k : 0) : -1;
-    const double l = exp(static_cast<double>(a.log_decay[h]) * C * max(len[x], 0));
-    const float lam = static_cast<float>(l);
-    decay[x] = make_float2(lam, static_cast<float>(l - static_cast<double>(lam)));
-  }
-  __syncthreads();
+  const SlotNote* notes = slot_notes<D>(a, NC) + c;
+  const SlotNote first = notes[0];
+  if (first.kind != 2) return;
+  const int u = first.unit, b = u / HS, r = u - b * HS, h = r / Gm::SLICES, slice = r - h * Gm::SLICES;
   const int at = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int d = at / EB, e = at - d * EB;
   float4 s = *reinterpret_cast<const float4*>(
       a.state + ((static_cast<int64_t>(state_row(a, b, false)) * a.Hkv + h) * D + d) * D + slice * EB + e);
-  constexpr int64_t SLOT = static_cast<int64_t>(D) * EB;
+  for (int x = threadIdx.x; c + x < NC; x += 256) note[x] = notes[x];
+  __syncthreads();
   *reinterpret_cast<float4*>(a.sums + (NC + c) * SLOT + at) = s;
-  for (int x0 = 0; c + x0 < NC && len[x0] >= 0; x0 += 8) {  // 8 slots in flight
-    float4 y[8];
+  for (int x0 = 0; c + x0 < NC && note[x0].unit == u; x0 += SLOTS) {
+    float4 y[SLOTS];
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-      y[x] = c + x0 + x < NC && len[x0 + x] > 0 ? *reinterpret_cast<const float4*>(a.sums + (c + x0 + x) * SLOT + at)
-                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < SLOTS; ++x)
+      y[x] = c + x0 + x < NC && note[x0 + x].unit == u && note[x0 + x].kind > 0
+                 ? *reinterpret_cast<const float4*>(a.sums + (c + x0 + x) * SLOT + at)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      if (c + x0 + x >= NC || len[x0 + x] < 0) return;
-      const float2 lam = decay[x0 + x];
-      s.x = fmaf(s.x, lam.x, fmaf(s.x, lam.y, y[x].x));
-      s.y = fmaf(s.y, lam.x, fmaf(s.y, lam.y, y[x].y));
-      s.z = fmaf(s.z, lam.x, fmaf(s.z, lam.y, y[x].z));
-      s.w = fmaf(s.w, lam.x, fmaf(s.w, lam.y, y[x].w));
+    for (int x = 0; x < SLOTS; ++x) {
+      if (c + x0 + x >= NC || note[x0 + x].unit != u) return;
+      // (the decay of a slot without a sum is 1)
+      const float lam = note[x0 + x].lam, lo = note[x0 + x].lam_lo;
+      s.x = fmaf(s.x, lam, fmaf(s.x, lo, y[x].x));
+      s.y = fmaf(s.y, lam, fmaf(s.y, lo, y[x].y));
+      s.z = fmaf(s.z, lam, fmaf(s.z, lo, y[x].z));
+      s.w = fmaf(s.w, lam, fmaf(s.w, lo, y[x].w));
       *reinterpret_cast<float4*>(a.sums + (c + x0 + x) * SLOT + at) = s;
     }
   }
 }
 
-template <int D, bool SUMS>
-cudaError_t prompt_launch(const LinearArgs& a, int ctas, cudaStream_t s) {
-  using Gm = Geo<D>;
-  auto k = linear_prompt_kernel<D, SUMS>;
-  static std::atomic<uint64_t> opted{0};
-  const cudaError_t e = opt_in_smem(k, Gm::SMEM, opted);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(ctas), dim3(kThreads), Gm::SMEM, s, a);
-}
-
 template <int D>
 cudaError_t prompt_launches(const LinearArgs& a, int ctas, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
+  using Gm = Geo<D>;
+  static std::atomic<uint64_t> opted[2];
+  cudaError_t e = opt_in_smem(linear_prompt_kernel<D>, Gm::SMEM, opted[0]);
+  if (e == cudaSuccess) e = opt_in_smem(linear_sums_kernel<D>, SumGeo<D>::SMEM, opted[1]);
+  if (e != cudaSuccess) return e;
   if (a.split) {
-    e = prompt_launch<D, true>(a, ctas, s);
+    e = launch_pdl(linear_sums_kernel<D>, dim3(ctas), dim3(kSumThreads), SumGeo<D>::SMEM, s, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(linear_scan_kernel<D>, dim3(D * Geo<D>::EB / 1024, ctas), dim3(256), (3 * ctas + a.B) * sizeof(int), s, a, ctas);
+    e = launch_pdl(linear_scan_kernel<D>, dim3(D * Gm::EB / 1024, ctas), dim3(256), ctas * sizeof(SlotNote), s, a, ctas);
     if (e != cudaSuccess) return e;
   }
-  return prompt_launch<D, false>(a, ctas, s);
+  return launch_pdl(linear_prompt_kernel<D>, dim3(ctas), dim3(kThreads), Gm::SMEM, s, a);
 }
 
 }  // namespace
