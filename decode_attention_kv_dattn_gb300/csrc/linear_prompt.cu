@@ -49,9 +49,9 @@ constexpr int kThreads = 832;
 constexpr int kPieceCost = 1;  // a unit's share of a CTA's range, in chunks, besides its own
 
 enum : int {
-  B_KFULL,              // a chunk's K has landed
-  B_KFREE,              // every MMA that reads it has completed
-  B_VFULL,              // [2] the same for V
+  B_KFULL,              // [2] a chunk's K has landed
+  B_KFREE = B_KFULL + 2,  // [2] every MMA that reads it has completed
+  B_VFULL = B_KFREE + 2,  // [2] the same for V
   B_VFREE = B_VFULL + 2,
   B_WREADY = B_VFREE + 2,  // W (and the zeroed rows of a short chunk) written
   B_SREADY,             // the state's two terms written
@@ -63,9 +63,10 @@ enum : int {
   B_OFREE,              // ... and read
   B_DSDONE,             // K^T W complete
   B_FINAL,
-  B_QFULL,              // [5] 64 dims of a Q tile have landed
-  B_QFREE = B_QFULL + 5,  // [5] ... and the MMAs that read them completed
-  B_COUNT = B_QFREE + 5
+  B_STAGED,             // [2] a tile's outputs have left its Q
+  B_QFULL = B_STAGED + 2,  // [6] 64 dims of a Q tile have landed
+  B_QFREE = B_QFULL + 6,   // [6] ... and the MMAs that read them completed
+  B_COUNT = B_QFREE + 6
 };
 
 template <int D>
@@ -73,19 +74,19 @@ struct Geo {
   static constexpr int EB = D == 128 ? 128 : 64;   // state columns of a CTA
   static constexpr int SLICES = D / EB;
   static constexpr int ER = EB / 64, DR = D / 64;  // 64-element regions
-  static constexpr int QR = D == 128 ? 4 : 5;      // regions of Q in shared memory (a tile has DR): the next tile's
+  static constexpr int QR = D == 128 ? 4 : 6;      // regions of Q in shared memory (a tile has DR): the next tile's
                                                    // land while this one's are used
+  static constexpr int KS = D == 128 ? 2 : 1;      // chunks of K
   static constexpr int Q_REGION = 16384;           // [128 rows][128 bytes]
   static constexpr int K_TILE = DR * 8192;         // [region][64 rows][128 bytes]
   static constexpr int V_TILE = ER * 8192;
   static constexpr int S_PLANE = ER * D * 128;     // [region][D rows][128 bytes]
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + QR * Q_REGION;
-  static constexpr int V_OFF = K_OFF + K_TILE;
+  static constexpr int V_OFF = K_OFF + KS * K_TILE;
   static constexpr int W_OFF = V_OFF + 2 * V_TILE;  // hi, lo
   static constexpr int S_OFF = W_OFF + 2 * V_TILE;  // hi, lo
-  static constexpr int O_OFF = S_OFF + 2 * S_PLANE;  // [row warps][32 rows][64 bytes] outputs on their way
-  static constexpr int BAR_OFF = O_OFF + kRowWarps * 2048;
+  static constexpr int BAR_OFF = S_OFF + 2 * S_PLANE;
   static constexpr int MISC_OFF = BAR_OFF + 8 * B_COUNT;
   static constexpr int BAD_OFF = (MISC_OFF + 16 + 15) / 16 * 16;  // [2][EB]: 64 chunk + 63 - token of the first
                                                                   // token without a number in a column
@@ -98,6 +99,22 @@ struct Geo {
   static constexpr int T_COLS = 512;
 };
 
+// A bounded wait that did not succeed at once (out of line: the roles' loops have
+// to stay in the instruction cache).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kDefaultWaitNs) {
+      *abort = 1;
+      raise_error(err, ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 struct Waiter {
   uint32_t bars;
   volatile int* abort;
@@ -105,19 +122,7 @@ struct Waiter {
   // Bounded wait by a whole warp or one thread; after a timeout (or when
   // another role gave up) every role leaves its loop.
   __device__ __forceinline__ bool wait(int b, uint32_t parity) const {
-    const uint32_t bar = bars + 8 * b;
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-      for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > kDefaultWaitNs) {
-        *abort = 1;
-        raise_error(err, ERR_TIMEOUT);
-        return false;
-      }
-    }
+    return mbar_try_wait(bars + 8 * b, parity) || wait_on(bars + 8 * b, parity, abort, err);
   }
   // Which of two phases completes first: 0 or 1 (1 too when neither does in time;
   // the wait that follows then reports it).
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bars = sbase + Gm::BAR_OFF;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::MISC_OFF + 8);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int HS = a.Hkv * Gm::SLICES;
   const int G = a.G, hpt = G > 1 ? 2 : 1;  // query heads of an M tile
   const int tiles = (G + hpt - 1) / hpt;
@@ -283,9 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY                     ? kStateWarps
-                              : i == B_AFREE || i == B_PREADY || i == B_OFREE ? kRowWarps
-                                                                              : 1);
+      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY ? kStateWarps
+                              : i == B_AFREE || i == B_PREADY || i == B_OFREE || i == B_STAGED || i == B_STAGED + 1
+                                  ? kRowWarps
+                                  : 1);
     reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[0] = reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[1] = -1;
     for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
     fence_mbar_init();
@@ -300,6 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::MISC_OFF);
   const Waiter W{bars, abort_flag, a.err};
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
+  auto first = [&](int bar0, uint32_t parity0, int bar1, uint32_t parity1) {
+    return __shfl_sync(0xffffffffu, W.first(bar0, parity0, bar1, parity1), 0);
+  };
   auto arrive = [&](int bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * bar);
@@ -326,17 +335,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                           bar, policy);
           }
           {
-            if (cc >= 1) ok = W.wait(B_KFREE, (cc - 1) & 1);
+            const int st = cc % Gm::KS;
+            if (cc >= Gm::KS) ok = W.wait(B_KFREE + st, (cc / Gm::KS - 1) & 1);
             if (!ok) break;
-            const uint32_t bar = bars + 8 * B_KFULL;
+            const uint32_t bar = bars + 8 * (B_KFULL + st);
             mbar_arrive_expect_tx(bar, Gm::K_TILE);
             for (int r = 0; r < Gm::DR; ++r)
-              tma_load_3d(sbase + Gm::K_OFF + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
+              tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
           }
           for (int mt = 0; mt < tiles && ok; ++mt)
             for (int r = 0; r < Gm::DR; ++r, ++qr) {
               const int slot = qr % Gm::QR;
-              if (qr >= Gm::QR) ok = W.wait(B_QFREE + slot, (qr / Gm::QR - 1) & 1);
+              if (qr >= Gm::QR) {
+                const int was = qr - Gm::QR, t = was / Gm::DR;  // its region before, and that one's tile
+                ok = W.wait(B_QFREE + slot, (qr / Gm::QR - 1) & 1) &&
+                     (was % Gm::DR < Gm::DR - 2 || W.wait(B_STAGED + (t & 1), (t >> 1) & 1));
+              }
               if (!ok) break;
               const uint32_t bar = bars + 8 * (B_QFULL + slot);
               mbar_arrive_expect_tx(bar, static_cast<uint32_t>(hpt) * 8192u);
@@ -350,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       // copies without its count).
       if (*abort_flag) {
         for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
-        for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * B_KFULL, i & 1, kDrainNs);
+        for (int i = max(0, cc - Gm::KS + 1); i <= cc; ++i)
+          mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
         for (int i = max(0, qr - Gm::QR); i <= qr; ++i)
           mbar_wait_bounded(bars + 8 * (B_QFULL + i % Gm::QR), (i / Gm::QR) & 1, kDrainNs);
       }
@@ -358,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ================= MMA issue =================
-    if (lane == 0) {
+    // (the whole warp walks the loops, so that descriptors stay in uniform
+    // registers; one thread issues)
+    {
+      const bool lead = tc::elect();
       constexpr uint32_t id_a = tc::f16_idesc_ab(128, C, 1, false, false);
       constexpr uint32_t id_q = tc::f16_idesc_ab(128, 128, 1, false, true);
       constexpr uint32_t id_o = tc::f16_idesc_ab(128, EB, 1, false, true);
@@ -370,23 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       // dims, at D = 256 both terms' one region
       const uint64_t s_major = tc::sw128_desc(0, D == 128 ? D * 128 : Gm::S_PLANE, 1024);
       auto at = [&](uint64_t desc, uint32_t addr) { return desc + (addr >> 4); };
-      const uint32_t kt = sbase + Gm::K_OFF, wt = sbase + Gm::W_OFF;
-      auto issue_ds = [&](int cc) -> bool {
-        if (!W.wait(B_WREADY, cc & 1)) return false;
-        tc::fence_after();
-#pragma unroll 1
-        for (int m = 0; m < D / 128; ++m) {
-          uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, wt);
-#pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk, kd += 128, wd += 128) {
-            tc::mma(tmem + Gm::T_DS + m * EB, kd, wd, id_s, kk > 0);
-            tc::mma(tmem + Gm::T_DS + m * EB, kd, wd + Gm::V_TILE / 16, id_s, true);
-          }
-        }
-        tc::commit(bars + 8 * B_DSDONE);
-        if (tiles == 1) tc::commit(bars + 8 * B_KFREE);
-        return true;
-      };
       bool ok = true;
       int cc = 0, t = 0, qr = 0;  // chunks, Q tiles and regions of Q so far
       Pieces p = all;
@@ -394,77 +395,97 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
           const int st = cc & 1;
           const uint32_t vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
-          ok = W.wait(B_KFULL, cc & 1);
+          const uint32_t kt = sbase + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
+          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
           if (!ok) break;
           for (int mt = 0; mt < tiles && ok; ++mt, ++t, qr += Gm::DR) {
             // A = Q K^T
-            ok = t == 0 || W.wait(B_AFREE, (t - 1) & 1);
+            ok = t == 0 || warp_wait(B_AFREE, (t - 1) & 1);
             if (!ok) break;
 #pragma unroll 1
             for (int reg = 0; reg < Gm::DR; ++reg) {
               const int slot = (qr + reg) % Gm::QR;
-              ok = W.wait(B_QFULL + slot, ((qr + reg) / Gm::QR) & 1);
+              ok = warp_wait(B_QFULL + slot, ((qr + reg) / Gm::QR) & 1);
               if (!ok) break;
               tc::fence_after();
-              uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION), kd = at(k_major, kt + reg * 8192);
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION), kd = at(k_major, kt + reg * 8192);
+              if (lead)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk, qd += 2, kd += 2)
-                tc::mma(tmem + Gm::T_A, qd, kd, id_a, reg > 0 || kk > 0);
+                for (int kk = 0; kk < 4; ++kk) tc::mma(tmem + Gm::T_A, qd + 2 * kk, kd + 2 * kk, id_a, reg > 0 || kk > 0);
             }
             if (!ok) break;
-            tc::commit(bars + 8 * B_ADONE);
-            if (tiles > 1 && mt == tiles - 1) tc::commit(bars + 8 * B_KFREE);  // (dS went before)
+            if (lead) tc::commit(bars + 8 * B_ADONE);
+            if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));  // (dS went before)
             // dS and Q S in the order in which they can start; dS before P V in any
             // case (which waits for the chunk's zeroed rows)
-            bool ds = mt == 0;
-            if (ds) {
-              ok = W.wait(B_SREADY, cc & 1);
+            bool ds_first = false;
+            if (mt == 0) {
+              ok = warp_wait(B_SREADY, cc & 1);
               if (!ok) break;
-              if (t > 0 && W.first(B_OFREE, (t - 1) & 1, B_WREADY, cc & 1) != 0) {
-                ok = issue_ds(cc);
-                if (!ok) break;
-                ds = false;
-              }
+              ds_first = t > 0 && first(B_OFREE, (t - 1) & 1, B_WREADY, cc & 1) != 0;
             }
-            // O1 = Q S
-            ok = t == 0 || W.wait(B_OFREE, (t - 1) & 1);
-            if (!ok) break;
-            tc::fence_after();
 #pragma unroll 1
-            for (int reg = 0; reg < Gm::DR; ++reg) {
-              const int slot = (qr + reg) % Gm::QR;
-              uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
-              uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
+            for (int x = mt == 0 ? 0 : 1; x < 2 && ok; ++x) {
+              if ((x == 0) == ds_first && mt == 0) {
+                // dS = K^T W
+                ok = warp_wait(B_WREADY, cc & 1);
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll 1
+                for (int m = 0; m < D / 128; ++m) {
+                  const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
+                  const uint32_t d = tmem + Gm::T_DS + m * EB;
+                  if (lead)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk, qd += 2, sd += 128) {
-                tc::mma(tmem + Gm::T_O1, qd, sd, id_q, reg > 0 || kk > 0);
-                if constexpr (D == 128) tc::mma(tmem + Gm::T_O1, qd, sd + Gm::S_PLANE / 16, id_q, true);
+                    for (int kk = 0; kk < C / 16; ++kk) {
+                      tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
+                      tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
+                    }
+                }
+                if (lead) tc::commit(bars + 8 * B_DSDONE);
+                if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+                continue;
               }
-              tc::commit(bars + 8 * (B_QFREE + slot));
-            }
-            if (mt == tiles - 1) tc::commit(bars + 8 * B_SFREE);
-            if (ds) {
-              ok = issue_ds(cc);
+              // O1 = Q S
+              ok = t == 0 || warp_wait(B_OFREE, (t - 1) & 1);
               if (!ok) break;
+              tc::fence_after();
+#pragma unroll 1
+              for (int reg = 0; reg < Gm::DR; ++reg) {
+                const int slot = (qr + reg) % Gm::QR;
+                const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
+                const uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
+                if (lead)
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) {
+                    tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk, id_q, reg > 0 || kk > 0);
+                    if constexpr (D == 128)
+                      tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk + Gm::S_PLANE / 16, id_q, true);
+                  }
+                if (lead) tc::commit(bars + 8 * (B_QFREE + slot));
+              }
+              if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
             }
+            if (!ok) break;
             // O2 = P V
-            ok = W.wait(B_PREADY, t & 1);
+            ok = warp_wait(B_PREADY, t & 1);
             if (!ok) break;
             tc::fence_after();
-            uint64_t vd = at(mn_major, vt);
+            const uint64_t vd = at(mn_major, vt);
+            if (lead)
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk, vd += 128) {
-              tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + kk * 8, vd, id_o, kk > 0);
-              tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + 32 + kk * 8, vd, id_o, true);
-            }
-            tc::commit(bars + 8 * B_ODONE);
-            if (mt == tiles - 1) tc::commit(bars + 8 * (B_VFREE + st));
+              for (int kk = 0; kk < C / 16; ++kk) {
+                tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + kk * 8, vd + 128 * kk, id_o, kk > 0);
+                tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + 32 + kk * 8, vd + 128 * kk, id_o, true);
+              }
+            if (lead) tc::commit(bars + 8 * B_ODONE);
+            if (mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_VFREE + st));
           }
         }
       }
       // every MMA issued has completed before the tensor memory is freed
-      tc::commit(bars + 8 * B_FINAL);
-      if (!mbar_wait_bounded(bars + 8 * B_FINAL, 0)) raise_error(a.err, ERR_TIMEOUT);
+      if (lead) tc::commit(bars + 8 * B_FINAL);
+      if (!mbar_wait_bounded(bars + 8 * B_FINAL, 0) && lead) raise_error(a.err, ERR_TIMEOUT);
     }
     __syncwarp();
   } else if (warp < kStateWarps) {
@@ -567,9 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
         if (n < C) {
-          ok = warp_wait(B_KFULL, cc & 1);
+          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
           if (!ok) break;
-          uint8_t* kt = smem + Gm::K_OFF;
+          uint8_t* kt = smem + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
           for (int off = threadIdx.x * 16; off < Gm::K_TILE; off += kStateWarps * 512)
             if (((off >> 7) & (C - 1)) >= n) *reinterpret_cast<uint4*>(kt + off) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -616,9 +637,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     const int hd = hpt == 2 ? r & 1 : 0;
     const int* bad = reinterpret_cast<const int*>(smem + Gm::BAD_OFF);
     const volatile int* bad_chunk = reinterpret_cast<const volatile int*>(smem + Gm::FLAG_OFF);
-    uint8_t* stage = smem + Gm::O_OFF + (warp - kStateWarps) * 2048;
     float* pw = reinterpret_cast<float*>(smem + Gm::PW_OFF);  // lam^0 .. lam^(C-1) of a head
     int table_head = -1;
+    // a tile's outputs have been read from shared memory: its Q's last two regions,
+    // where they were staged, take the next Q
+    auto left = [&](int tile) {
+      if (lane == 0) {
+        tma_stores_read<0>();
+        mbar_arrive(bars + 8 * (B_STAGED + (tile & 1)));
+      }
+    };
     bool ok = true;
     int cc = 0, t = 0;
     Pieces p = all;
@@ -667,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           tc::wait_st();
           tc::fence_before();
           arrive(B_PREADY);
+          if (t > 0) left(t - 1);
           // ---- epilogue
           float f = a.scale;
           if (a.gate) f /= 1.f + expf(-gate);
@@ -680,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           // lane's store of 32 bytes in each of 32 rows takes the load/store path a
           // cycle a row); short chunks and a group's odd head row by row
           const bool box = n == C && (mt + 1) * hpt <= G;
+          uint8_t* stage = smem + Gm::Q_OFF + (t * Gm::DR + Gm::DR - 2 + w2) % Gm::QR * Gm::Q_REGION + (warp & 3) * 4096;
 #pragma unroll 1
           for (int e0 = EB / 2 * w2; e0 < EB / 2 * (w2 + 1); e0 += 16) {
             uint32_t o1[16], o2[16];
@@ -711,16 +741,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
             if (box) {
-              if (lane == 0) tma_stores_read<0>();
+              uint8_t* buf = stage + ((e0 >> 4) & 1) * 2048;
+              if (lane == 0) tma_stores_read<1>();
               __syncwarp();
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(stage + lane * 64 + (((e >> 2) ^ ((lane >> 1) & 3)) << 4)) =
+                *reinterpret_cast<float4*>(buf + lane * 64 + (((e >> 2) ^ ((lane >> 1) & 3)) << 4)) =
                     make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0 && 32 * (warp & 3) < hpt * C)
-                tma_store_3d(&a.tmap_o, smem_addr(stage), p.slice * EB + e0, p.h * G + mt * hpt,
+                tma_store_3d(&a.tmap_o, smem_addr(buf), p.slice * EB + e0, p.h * G + mt * hpt,
                              p.b * a.T + k * C + (warp & 3) * (32 / hpt));
             } else if (store) {
 #pragma unroll
