@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           const float gate = store && a.gate ? bf16_to_f32(a.gate[head]) : 0.f;
           ok = warp_wait(B_ADONE, t & 1);
           if (!ok) break;
+          if (t > 0) left(t - 1);
           // ---- P: A masked and decayed
           tc::fence_after();
           const int lim = min(i, C - 1);  // columns up to this one count
@@ -695,7 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           tc::wait_st();
           tc::fence_before();
           arrive(B_PREADY);
-          if (t > 0) left(t - 1);
           // ---- epilogue
           float f = a.scale;
           if (a.gate) f /= 1.f + expf(-gate);
@@ -723,16 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(__uint_as_float(o1[e]) + __uint_as_float(lo[e]));
             }
             tc::wait_ld();
-            if (odd) {
-              for (int e = 0; e < 16; ++e) {
-                const int x = bad[(cc & 1) * EB + e0 + e] - cc * C;
-                if (x >= 0 && i >= C - 1 - x) {
-#pragma unroll
-                  for (int y = 0; y < 16; ++y)
-                    if (y == e) o2[y] = 0x7fffffffu;
-                }
-              }
-            }
             if (e0 + 16 == EB / 2 * (w2 + 1)) {
               tc::fence_before();
               arrive(B_OFREE);
@@ -740,6 +730,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             float z[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
+            if (odd) {
+              uint32_t mask = 0;
+#pragma unroll 1
+              for (int e = 0; e < 16; ++e) {
+                const int x = bad[(cc & 1) * EB + e0 + e] - cc * C;
+                if (x >= 0 && i >= C - 1 - x) mask |= 1u << e;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (mask >> e & 1) z[e] = __uint_as_float(0x7fffffffu);
+            }
             if (box) {
               uint8_t* buf = stage + ((e0 >> 4) & 1) * 2048;
               if (lane == 0) tma_stores_read<1>();
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 constexpr int kSumGroup = 4, kSumStages = 4;
 constexpr int kSumThreads = (kStateWarps + 2) * 32;
 enum : int { R_FULL, R_FREE = R_FULL + kSumStages, R_WREADY = R_FREE + kSumStages, R_WFREE = R_WREADY + 2,
-             R_DONE = R_WFREE + 2, R_FINAL, R_COUNT };
+             R_DONE = R_WFREE + 2, R_FINAL = R_DONE + 2, R_COUNT };
 
 template <int D>
 struct SumGeo {
@@ -794,7 +795,8 @@ struct SumGeo {
   static constexpr int BAR_OFF = W_OFF + 4 * Gm::V_TILE;
   static constexpr int MISC_OFF = BAR_OFF + 8 * R_COUNT;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
-  static constexpr int T_COLS = 128;
+  static constexpr int ACC = D / 128 * Gm::EB;  // tensor memory columns of a group's sum, of which there are two
+  static constexpr int T_COLS = 2 * ACC;
 };
 
 // What the scan knows of a CTA's slot: the unit that goes on in the next CTA (-1:
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bars = sbase + Sg::BAR_OFF;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sg::MISC_OFF + 8);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int HS = a.Hkv * Gm::SLICES;
   int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
   sum_weights<kSumThreads>(a, cum, HS, false);
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < R_COUNT; ++i)
-      mbar_init(bars + 8 * i, i == R_WREADY || i == R_WREADY + 1 ? kStateWarps : 1);
+      mbar_init(bars + 8 * i, i == R_WREADY || i == R_WREADY + 1 ? kStateWarps / 2 : 1);
     fence_mbar_init();
   }
   if (warp == kStateWarps + 1) tc::alloc(sbase + Sg::MISC_OFF, Sg::T_COLS);
@@ -877,29 +879,34 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
     __syncwarp();
   } else if (warp == kStateWarps + 1) {
     // ================= MMA issue =================
-    if (lane == 0) {
+    {
+      const bool lead = tc::elect();
       constexpr uint32_t id_s = tc::f16_idesc_ab(128, EB, 1, true, true);
       const uint64_t mn_major = tc::sw128_desc(0, 8192, 1024);
       for (int c = 0; c < chunks; ++c) {
         const int st = c % kSumStages;
-        if (!W.wait(R_FULL + st, (c / kSumStages) & 1) || !W.wait(R_WREADY + (c & 1), (c >> 1) & 1)) break;
+        if (!warp_wait(R_FULL + st, (c / kSumStages) & 1) || !warp_wait(R_WREADY + (c & 1), (c >> 1) & 1)) break;
         tc::fence_after();
         const uint32_t kt = sbase + st * Sg::STAGE, wt = sbase + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+        const uint32_t d0 = tmem + ((c / kSumGroup) & 1) * Sg::ACC;
 #pragma unroll 1
         for (int m = 0; m < D / 128; ++m) {
-          uint64_t kd = mn_major + ((kt + m * 16384) >> 4), wd = mn_major + (wt >> 4);
+          const uint64_t kd = mn_major + ((kt + m * 16384) >> 4), wd = mn_major + (wt >> 4);
+          const uint32_t d = d0 + m * EB;
+          if (lead)
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk, kd += 128, wd += 128) {
-            tc::mma(tmem + m * EB, kd, wd, id_s, kk > 0 || c % kSumGroup > 0);
-            tc::mma(tmem + m * EB, kd, wd + Gm::V_TILE / 16, id_s, true);
-          }
+            for (int kk = 0; kk < C / 16; ++kk) {
+              tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0 || c % kSumGroup > 0);
+              tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
+            }
         }
-        tc::commit(bars + 8 * (R_FREE + st));
-        tc::commit(bars + 8 * (R_WFREE + (c & 1)));
-        if (c % kSumGroup == kSumGroup - 1 || c == chunks - 1) tc::commit(bars + 8 * R_DONE);
+        if (lead) tc::commit(bars + 8 * (R_FREE + st));
+        if (lead) tc::commit(bars + 8 * (R_WFREE + (c & 1)));
+        if (lead && (c % kSumGroup == kSumGroup - 1 || c == chunks - 1))
+          tc::commit(bars + 8 * (R_DONE + ((c / kSumGroup) & 1)));
       }
-      tc::commit(bars + 8 * R_FINAL);
-      if (!mbar_wait_bounded(bars + 8 * R_FINAL, 0)) raise_error(a.err, ERR_TIMEOUT);
+      if (lead) tc::commit(bars + 8 * R_FINAL);
+      if (!mbar_wait_bounded(bars + 8 * R_FINAL, 0) && lead) raise_error(a.err, ERR_TIMEOUT);
     }
     __syncwarp();
   } else {
@@ -912,51 +919,60 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
     float S[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) S[e] = 0.f;
-    int groups = 0;
-    for (int c = 0; c < chunks; ++c) {
+    // S = lam^(its tokens) S + sum, for group g
+    auto add = [&](int g) -> bool {
+      if (!warp_wait(R_DONE + (g & 1), (g >> 1) & 1)) return false;
+      tc::fence_after();
+      for (int i = min(kSumGroup, chunks - g * kSumGroup); i > 0; --i)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], lam, S[e] * lam_lo);
+#pragma unroll
+      for (int e0 = 0; e0 < 32; e0 += 16) {
+        uint32_t y[16];
+        tc::ld16(tmem + (static_cast<uint32_t>(32 * q4) << 16) + (g & 1) * Sg::ACC + 32 * w4 + e0, y);
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e0 + e] += __uint_as_float(y[e]);
+      }
+      tc::fence_before();
+      return true;
+    };
+    bool ok = true;
+    int added = 0;  // groups
+    for (int c = 0; c < chunks && ok; ++c) {
       const int st = c % kSumStages;
-      const int after = min(kSumGroup - 1 - c % kSumGroup, chunks - 1 - c);  // chunks of the group behind this one
-      float g = 1.f;
-      for (int i = 0; i < after; ++i) g *= lam;
-      if (!warp_wait(R_FULL + st, (c / kSumStages) & 1)) break;
-      if (c >= 2 && !warp_wait(R_WFREE + (c & 1), ((c >> 1) - 1) & 1)) break;
-      const uint8_t* vt = smem + st * Sg::STAGE + Gm::K_TILE;
-      uint8_t* wt = smem + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
-#pragma unroll 1
-      for (int off = threadIdx.x * 16; off < Gm::V_TILE; off += kStateWarps * 512) {
-        const uint4 y = *reinterpret_cast<const uint4*>(vt + off);
-        const float w = __ldg(pw + C - 1 - ((off >> 7) & (C - 1))) * g;
-        uint4 hi, lo;
-        split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
-        split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
-        split2(bf16_lo(y.z) * w, bf16_hi(y.z) * w, hi.z, lo.z);
-        split2(bf16_lo(y.w) * w, bf16_hi(y.w) * w, hi.w, lo.w);
-        *reinterpret_cast<uint4*>(wt + off) = hi;
-        *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (R_WREADY + (c & 1)));
-      if (after == 0) {
-        // the group's end: S = lam^(its tokens) S + sum
-        const int len = c % kSumGroup + 1;
-        if (!warp_wait(R_DONE, groups & 1)) break;
-        ++groups;
-        tc::fence_after();
-        for (int i = 0; i < len; ++i)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) S[e] = fmaf(S[e], lam, S[e] * lam_lo);
-#pragma unroll
-        for (int e0 = 0; e0 < 32; e0 += 16) {
-          uint32_t y[16];
-          tc::ld16(tmem + (static_cast<uint32_t>(32 * q4) << 16) + 32 * w4 + e0, y);
-          tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) S[e0 + e] += __uint_as_float(y[e]);
+      // W: even chunks by one half of the warps, odd ones by the other, so that two
+      // are on their way
+      if ((c & 1) == warp >> 3) {
+        const int after = min(kSumGroup - 1 - c % kSumGroup, chunks - 1 - c);  // chunks of the group behind this one
+        float g = 1.f;
+        for (int i = 0; i < after; ++i) g *= lam;
+        ok = warp_wait(R_FULL + st, (c / kSumStages) & 1) && (c < 2 || warp_wait(R_WFREE + (c & 1), ((c >> 1) - 1) & 1));
+        if (!ok) break;
+        const uint8_t* vt = smem + st * Sg::STAGE + Gm::K_TILE;
+        uint8_t* wt = smem + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+#pragma unroll 2
+        for (int off = (threadIdx.x & 255) * 16; off < Gm::V_TILE; off += kStateWarps / 2 * 512) {
+          const uint4 y = *reinterpret_cast<const uint4*>(vt + off);
+          const float w = __ldg(pw + C - 1 - ((off >> 7) & (C - 1))) * g;
+          uint4 hi, lo;
+          split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
+          split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
+          split2(bf16_lo(y.z) * w, bf16_hi(y.z) * w, hi.z, lo.z);
+          split2(bf16_lo(y.w) * w, bf16_hi(y.w) * w, hi.w, lo.w);
+          *reinterpret_cast<uint4*>(wt + off) = hi;
+          *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
-        tc::fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (R_WREADY + (c & 1)));
       }
+      // a group's sum once the next group is under way (its accumulator is written
+      // again from the group after that, whose first MMA waits for W of a chunk
+      // that either half makes after this)
+      if (c % kSumGroup == 1 && c > kSumGroup) ok = add(added++);
     }
+    for (; ok && added * kSumGroup < chunks; ++added) ok = add(added);
     float* dst = a.sums + (static_cast<int64_t>(blockIdx.x) * D + sd) * EB + se;
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {
