@@ -261,12 +261,14 @@ __device__ __forceinline__ float block_max(float x, int* buf) {
 // which then sees what the others wrote before. The counter is left at zero.
 __device__ __forceinline__ bool last_to_arrive(int* counter, int parts, int* flag) {
   __syncthreads();
+  if (parts == 1) return true;
   if (threadIdx.x == 0) {
-    __threadfence();
-    const bool last = atomicAdd(counter, 1) == parts - 1;
+    // (release: the block's writes, after the barrier; acquire: the other blocks')
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    const bool last = before == parts - 1;
     if (last) *counter = 0;
     *flag = last;
-    __threadfence();
   }
   __syncthreads();
   return *flag != 0;
