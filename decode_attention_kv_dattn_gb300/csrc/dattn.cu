@@ -349,7 +349,7 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
     if (!guard.ok) return DATTN_ECUDA;
     LinearArgs la = linear_args(h, layer, cache, B, args->q, args->k_new, args->v_new, args->gate, args->out);
     la.write_back = args->write_back;
-    rc = cuda_status(launch_linear_step(la, h->D, reinterpret_cast<cudaStream_t>(stream)), "linear step");
+    rc = cuda_status(launch_linear_step(la, h->D, h->num_sms, reinterpret_cast<cudaStream_t>(stream)), "linear step");
     if (rc == DATTN_OK) record_launch(stream, args->write_back ? cache->k : nullptr);
     return rc;
   }

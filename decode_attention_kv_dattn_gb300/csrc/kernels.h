@@ -206,7 +206,8 @@ struct LinearArgs {
   float* sums;                 // prompt: [2][num_sms][D, EB] a CTA's slot: its last piece's contribution to the
                                // state, then the state that the next CTA starts from; and the state that its
                                // last unit starts from
-  int split;                   // prompt: a CTA has a range of chunks (or one unit)
+  int split;                   // prompt: units may be cut into ranges of chunks, by `ctas` CTAs (else one each)
+  int ctas;
   int* err;
 };
 
@@ -364,7 +365,7 @@ constexpr int kSelectBitmapMax = 96 * 1024;
 constexpr int kSelectSmemMax = kSelectBitmapMax + (17 + 8 + 65) * 1024;
 cudaError_t launch_page_select(PageArgs a, int D, cudaStream_t s);
 cudaError_t launch_page_attend(const PageArgs& a, int D, bool f8, cudaStream_t s);
-cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s);
+cudaError_t launch_linear_step(const LinearArgs& a, int D, int num_sms, cudaStream_t s);
 // The prompt form: one launch, or three where the units' chunks are split.
 cudaError_t launch_linear_prompt(const LinearArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t encode_linear_maps(LinearArgs& a, int D);

@@ -110,9 +110,16 @@ cudaError_t step_launch(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear_step(const LinearArgs& a, int D, cudaStream_t s) {
-  if (D == 128) return step_launch<128, 32>(a, s);
-  return step_launch<256, 32>(a, s);
+cudaError_t launch_linear_step(const LinearArgs& a, int D, int num_sms, cudaStream_t s) {
+  // Few units: narrower slices as long as there is an SM for each (a slice's time
+  // is its rows' round trips), with 32-byte rows at the least. Measured, in a
+  // graph, slices of 32 / 16 / 8 columns: 2 units of 256 3.3 / 2.7 / 2.1 us, 8 of
+  // 256 3.3 / 2.4 / 3.0 us, 16 of 128 2.2 / 1.7 / 2.1 us, 16 of 256 2.9 / 3.2 /
+  // 4.8 us, 512 of 128 7.9 / 12.1 us.
+  const int units = a.B * a.Hkv;
+  const int W = units * (D / 8) <= num_sms ? 8 : units * (D / 16) <= num_sms ? 16 : 32;
+  if (D == 128) return W == 8 ? step_launch<128, 8>(a, s) : W == 16 ? step_launch<128, 16>(a, s) : step_launch<128, 32>(a, s);
+  return W == 8 ? step_launch<256, 8>(a, s) : W == 16 ? step_launch<256, 16>(a, s) : step_launch<256, 32>(a, s);
 }
 
 }  // namespace dattn

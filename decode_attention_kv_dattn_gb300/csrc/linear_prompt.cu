@@ -210,15 +210,25 @@ __device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum
   return Place{lo * HS + r, max(k, 0)};
 }
 
-// The streams' weights summed (see range_start), by a whole block of NT threads.
+// The streams' weights summed (see range_start), by a whole block of NT threads;
+// returns whether the units are worth cutting. In chunks' times: uncut, the
+// longest unit's chunks; cut, everything spread evenly, with 40% more for the
+// sums and 2.5 chunks' time for what is launched between. Measured, cut / uncut:
+// 16 streams of 512 - 4,096 tokens (128 units of 256) 218 / 320 us, 4 x 512 (32
+// units of 128) 29.9 / 33.6 us, 1 x 32,768 (8 of 128) 142 / 1,647 us.
 template <int NT>
-__device__ __forceinline__ void sum_weights(const LinearArgs& a, int* cum, int HS, bool report) {
+__device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int HS, bool report) {
+  __shared__ int longest;
+  if (threadIdx.x == 0) longest = 0;
+  __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += NT) {
     const int n = stream_chunks(a, b, report);
     cum[b] = n > 0 ? (n + kPieceCost) * HS : 0;
+    atomicMax(&longest, n);
   }
   __syncthreads();
   block_scan_inclusive<NT>(cum, a.B);
+  return static_cast<int64_t>(14) * cum[a.B - 1] / a.ctas + 25 < static_cast<int64_t>(10) * longest;
 }
 
 // The pieces of a CTA's range: chunks [k0, k1) of a unit; every role walks them.
@@ -266,9 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   Place begin, end;
   if (a.split) {
     int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
-    sum_weights<kThreads>(a, cum, HS, blockIdx.x == 0);
-    begin = range_start(a, cum, HS, blockIdx.x, gridDim.x);
-    end = range_start(a, cum, HS, blockIdx.x + 1, gridDim.x);
+    const int i = blockIdx.x;
+    if (sum_weights<kThreads>(a, cum, HS, i == 0)) {
+      begin = range_start(a, cum, HS, min(i, a.ctas), a.ctas);
+      end = range_start(a, cum, HS, min(i + 1, a.ctas), a.ctas);
+    } else {
+      begin = Place{min(i, a.B * HS), 0};
+      end = Place{min(i + 1, a.B * HS), 0};
+    }
     __syncthreads();
   } else {
     begin = Place{static_cast<int>(blockIdx.x), 0};
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       if (p.k0 > 0)
         src = a.sums + (static_cast<int64_t>(blockIdx.x - 1) * D + sd) * EB + se;
       else if (!p.last)
-        src = a.sums + (static_cast<int64_t>(gridDim.x + blockIdx.x) * D + sd) * EB + se;
+        src = a.sums + (static_cast<int64_t>(a.ctas + blockIdx.x) * D + sd) * EB + se;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 y = *reinterpret_cast<const float4*>(src + e);
@@ -807,8 +822,8 @@ struct alignas(16) SlotNote {
   float lam, lam_lo;
 };
 template <int D>
-__device__ __forceinline__ SlotNote* slot_notes(const LinearArgs& a, int ctas) {
-  return reinterpret_cast<SlotNote*>(a.sums + static_cast<int64_t>(2) * ctas * D * Geo<D>::EB);
+__device__ __forceinline__ SlotNote* slot_notes(const LinearArgs& a) {
+  return reinterpret_cast<SlotNote*>(a.sums + static_cast<int64_t>(2) * a.ctas * D * Geo<D>::EB);
 }
 
 template <int D>
@@ -824,9 +839,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int HS = a.Hkv * Gm::SLICES;
   int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
-  sum_weights<kSumThreads>(a, cum, HS, false);
-  const Place begin = range_start(a, cum, HS, blockIdx.x, gridDim.x);
-  const Place end = range_start(a, cum, HS, blockIdx.x + 1, gridDim.x);
+  const bool cut = sum_weights<kSumThreads>(a, cum, HS, false);
+  const Place begin = cut ? range_start(a, cum, HS, blockIdx.x, a.ctas) : Place{0, 0};
+  const Place end = cut ? range_start(a, cum, HS, blockIdx.x + 1, a.ctas) : Place{0, 0};
   const int k0 = begin.u == end.u ? begin.k : 0, chunks = end.k - k0;
   const int b = end.u / HS, r0 = end.u - b * HS, h = r0 / Gm::SLICES, slice = r0 - h * Gm::SLICES;
   pdl_wait();
@@ -838,7 +853,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
       const float lam = static_cast<float>(l);
       n = SlotNote{end.u, chunks > 0 ? (k0 == 0 ? 2 : 1) : 0, lam, static_cast<float>(l - static_cast<double>(lam))};
     }
-    slot_notes<D>(a, gridDim.x)[blockIdx.x] = n;
+    slot_notes<D>(a)[blockIdx.x] = n;
   }
   if (end.k == 0 || chunks <= 0) return;  // (the whole CTA)
   if (threadIdx.x == 0) {
@@ -998,16 +1013,16 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
 // through the slots; one thread per 4 elements. Every chunk of these pieces is
 // full.
 template <int D>
-__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a, int NC) {
+__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
   using Gm = Geo<D>;
   constexpr int EB = Gm::EB;
   constexpr int64_t SLOT = static_cast<int64_t>(D) * EB;
   constexpr int SLOTS = 8;  // in flight
   extern __shared__ SlotNote note[];  // [NC]
-  const int HS = a.Hkv * Gm::SLICES, c = blockIdx.y;
+  const int HS = a.Hkv * Gm::SLICES, c = blockIdx.y, NC = a.ctas;
   pdl_wait();
   pdl_trigger();
-  const SlotNote* notes = slot_notes<D>(a, NC) + c;
+  const SlotNote* notes = slot_notes<D>(a) + c;
   const SlotNote first = notes[0];
   if (first.kind != 2) return;
   const int u = first.unit, b = u / HS, r = u - b * HS, h = r / Gm::SLICES, slice = r - h * Gm::SLICES;
@@ -1047,9 +1062,9 @@ cudaError_t prompt_launches(const LinearArgs& a, int ctas, cudaStream_t s) {
   if (e == cudaSuccess) e = opt_in_smem(linear_sums_kernel<D>, SumGeo<D>::SMEM, opted[1]);
   if (e != cudaSuccess) return e;
   if (a.split) {
-    e = launch_pdl(linear_sums_kernel<D>, dim3(ctas), dim3(kSumThreads), SumGeo<D>::SMEM, s, a);
+    e = launch_pdl(linear_sums_kernel<D>, dim3(a.ctas), dim3(kSumThreads), SumGeo<D>::SMEM, s, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(linear_scan_kernel<D>, dim3(D * Gm::EB / 1024, ctas), dim3(256), ctas * sizeof(SlotNote), s, a, ctas);
+    e = launch_pdl(linear_scan_kernel<D>, dim3(D * Gm::EB / 1024, a.ctas), dim3(256), a.ctas * sizeof(SlotNote), s, a);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(linear_prompt_kernel<D>, dim3(ctas), dim3(kThreads), Gm::SMEM, s, a);
@@ -1061,9 +1076,14 @@ cudaError_t launch_linear_prompt(const LinearArgs& args, int D, int num_sms, cud
   LinearArgs a = args;
   const int units = a.B * a.Hkv * (D == 128 ? Geo<128>::SLICES : Geo<256>::SLICES);
   const int chunks = (a.T + C - 1) / C;
-  // Ranges cost two more launches and, in the worst case, a second look at
-  // every K and V: not for short prompts, nor where there are units enough.
-  a.split = chunks > 4 && units < 4 * num_sms;
+  // Whether units are cut is decided on the device, from the counts (that costs
+  // 10 us where it comes out against it); not even considered for short prompts
+  // (cut / uncut: 4 x 330 tokens of 8 heads of 128 28.8 / 26.3 us, 4 x 256 28.3 /
+  // 20.8) nor with more units than SMs, which even each other out (20 x 512 -
+  // 2,048, 160 units: 131 / 115 us, 32 x 1,024: 144 / 127, 48 x 512 - 2,048: 252 /
+  // 255, 64 x 16 - 4,096: 485 / 472).
+  a.split = chunks > 6 && units <= num_sms;
+  a.ctas = num_sms;
   const int ctas = a.split ? num_sms : units;
   return D == 128 ? prompt_launches<128>(a, ctas, s) : prompt_launches<256>(a, ctas, s);
 }

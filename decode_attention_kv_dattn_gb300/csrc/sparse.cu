@@ -480,7 +480,7 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
       __syncthreads();
     };
     // ---- few candidates: all of them listed, and ranked below
-    if (N <= 256) {
+    if (N <= 128) {
       __syncthreads();
       for (int i = t; i < N; i += NTH) {
         s.list[i] = i;
