@@ -21,7 +21,9 @@ constexpr int kStepThreads = 256;
 // One CTA per (unit, W columns of the state). Each thread holds 4 columns of
 // every RP-th row: the update and the group's dot products are done on the
 // registers between one read and one write of the state, which bound the step
-// (2 D^2 fp32 a unit).
+// (2 D^2 fp32 a unit): 64 streams of 8 heads of 128, 67 MB, 7.9 us in a graph
+// that repeats the step (the states then stay in the L2 cache; 10 us at the
+// memory's rate), 1 stream of 2 heads of 256 2.1 us.
 template <int D, int W, int GP>
 __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const LinearArgs a) {
   constexpr int LPR = W / 4;                // lanes of a row

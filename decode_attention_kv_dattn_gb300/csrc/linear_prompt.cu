@@ -16,18 +16,29 @@
 //
 // Work split. A unit is one (stream, KV head, slice): EB of the state's columns
 // (all 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
-// shared memory beside Q, two chunks of K and V, and W). Where units are many, or
-// their streams short, a CTA has one unit. Otherwise the units' chunks are laid
-// end to end and one CTA an SM takes an equal range of them, worked out on the
-// device from the counts: a range begins and ends inside a unit, so a first pass
-// sums what each CTA's last unit contributes to the state (for the CTA after
-// it), a scan carries the states along, and the main pass starts each range from
+// shared memory beside Q, K, V and W). Where units are many, or their streams
+// short or alike, a CTA has one unit. Otherwise the units' chunks are laid end to
+// end and one CTA an SM takes an equal range of them, worked out on the device
+// from the counts: a range begins and ends inside a unit, so a first kernel sums
+// what each CTA's last unit contributes to the state (for the CTA after it), a
+// second carries the states along, and the main kernel starts each range from
 // its state.
 //
-// Roles: 16 state warps (W, and the state: dS in, S's terms out), 4 row warps (P
+// Roles: 16 state warps (W, and the state: dS in, S's terms out), 8 row warps (P
 // and the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
 // issues the MMAs. The state warps' chain (W, dS, S) and the row warps' (P, O)
-// run beside one another; both end in tensor memory, which is full.
+// run beside one another; both end in tensor memory, which is full, so that the
+// next chunk's Q S waits until the outputs are read. 832 threads leave 72
+// registers each, and the roles' loops are kept small: when they missed the
+// instruction cache, that was 43% of the stalls.
+//
+// Bound by the chunk's chain of dependent steps, not by a unit: at D = 128 3.6 us
+// a chunk and Q tile, of which the row warps' reads of the outputs and their
+// staging are 1.9, P 0.9; the MMAs of it take 1.3 us of the tensor pipe (each
+// waits for its operands from shared memory: 25 ns at N = 64, 34 at N = 128) and
+// the copies 2.9 us at the memory's rate. 1 x 32,768 tokens, 16 / 8 heads of 128:
+// 142 us = sums 32, scan 8, main 108 (537 MB, 4.5 TB/s, overlapping a little). 16
+// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 218 us = 34, 8, 186.
 //
 // An infinity or no number in v would reach earlier tokens of its chunk (its
 // weight in P is 0, and 0 times it is no number): the state warps replace it by

@@ -92,6 +92,8 @@ __device__ __forceinline__ float nan_to_inf(float x) { return x == x ? x : INFIN
 // One warp per (completed page, KV head): 16-byte loads, every lane the same
 // dims of a few rows at a time, fp32 sums joined across the warp's row groups.
 // Bound by reading the keys once; the page's rows of one head are contiguous.
+// 64 prompts of 64 - 4,096 tokens, 8 heads of 128, pages of 16: 274 MB in 45 us
+// (6.1 TB/s); after one decode step of 64 streams 2.4 us in a graph.
 template <int D, bool F8>
 __global__ void __launch_bounds__(256) summarize_kernel(const SummarizeArgs a) {
   constexpr int EPL = F8 ? 16 : 8;          // elements of a 16-byte load
@@ -479,7 +481,9 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
       }
       __syncthreads();
     };
-    // ---- few candidates: all of them listed, and ranked below
+    // ---- few candidates: all of them listed, and ranked below (64 streams of 8
+    // heads: 96 - 120 candidates 45.4 us this way, 46.9 by histograms; 215 - 251
+    // candidates 53.8 and 49.6)
     if (N <= 128) {
       __syncthreads();
       for (int i = t; i < N; i += NTH) {
@@ -492,9 +496,11 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
     }
     // ---- long streams, by way of the 16-page tiles' maxima: the k-th largest of
     // them has k scores at or above it, so the k-th largest score is no less,
-    // and only tiles that reach it have scores to look at
+    // and only tiles that reach it have scores to look at (1 x 1,048,576 tokens
+    // 25.4 us, 29.5 without; where tiles are fewer than twice what is chosen it
+    // does not pay: 64 x 16,384 tokens 48.7 us with, 45.9 without)
     const int tile0 = lo >> 4, tiles = ((lo + N - 1) >> 4) - tile0 + 1;
-    if (!listed && tiles >= 4 * k && a1 > a0) {
+    if (!listed && tiles >= 2 * k && a1 > a0) {
       const float* gtm = a.tile_max + static_cast<int64_t>(u) * a.tile_pitch + tile0;
       const float inv = static_cast<float>(kBins) / (a1 - a0);
       if (inv > 0.f && inv < 1e38f) {
@@ -805,8 +811,13 @@ __device__ void select_unit(const PageArgs& a, int u, int b, int h, int pages, c
 // stays in registers. Columns: the group's heads as bf16 hi and, 4 (or one
 // 8-column tile) further, what is left as bf16 lo.
 // Bound by reading the candidates' summaries once (D * 2 bytes a page and
-// head); the squared norm that the error bound needs is one bf16x2 FMA a
-// loaded word.
+// head) only where there are many - E4M3 64 x 16,384 tokens, 128 units of about
+// 980 pages: 64 MB in 7.3 us of the CTAs' 16; the squared norm that the error
+// bound needs is one bf16x2 FMA a loaded word. The rest is the chain of a unit's
+// selection: q 1.6 us, scores 2 - 3, the chunks' join 1.5 - 2, the border 2 - 4,
+// exact scores and the pages in order 2. In all (under ncu) 15 us at 1 x
+// 1,048,576 tokens, 21 at 8 x 262,144, 18 at 64 ragged streams, 24 at E4M3 64 x
+// 16,384, 12 at 1 x 5,003.
 template <int D, int NT, int NTH>
 __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page_select_kernel(const PageArgs a) {
   constexpr int W = NTH / 32;
@@ -1026,6 +1037,12 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page
 // Few selected keys a unit: what counts is the chain of dependent steps, so
 // there is no ring to fill, and q is rotated and split while the selection is
 // still running.
+// Bound by the keys' bytes where units are many: 64 ragged streams of 8 heads
+// of 128, 32 pages of 16 tokens each, read 128 MB in the loop's 21 us (6.1
+// TB/s) of 36 in all under ncu. With few units by the chain: 13 us at 1 x 5,003
+// tokens, 15 at 1 x 1,048,576 (64 pages of 64), of which the loop is 3 - 5.
+// Groups prefetched to the L2 cache ahead of the registers' changed nothing to
+// speak of (64 ragged streams 47.4 - 54 us for 0 - 8 of them).
 template <int D, bool F8>
 struct AttendGeo {
   static constexpr int TERMS = F8 ? 2 : 3;
@@ -1499,11 +1516,16 @@ cudaError_t launch_summarize(const SummarizeArgs& a, int D, cudaStream_t s) {
 
 // Threads of the score and selection kernel: 16 warps for long streams, whose
 // selection is one CTA's passes over all scores, 8 otherwise (more CTAs an SM).
+// Calls with 8 / 16 warps: 1 x 1,048,576 tokens (16,384 pages) 27.4 / 25.3 us, 8
+// x 262,144 (4,096) 40.2 / 39.3, E4M3 64 x 16,384 (1,024) 45.4 / 44.8, 64 ragged
+// (up to 256) 49.4 / 61.5, 1 x 5,003 (313) 20.5 / 21.7.
 static int select_threads(int pages) { return pages > 2048 ? 512 : 256; }
 
 int page_chunk_pages(int units, int pages, int num_sms) {
   // Every CTA first rotates the group's queries, so: as many 16-page tiles a
-  // warp as leave the grid within the 16 warps an SM that run at once.
+  // warp as leave the grid within the 16 warps an SM that run at once (with 8 /
+  // 16 / 32: 8 x 262,144 tokens 59.3 / 39.3 / 37.9 us, E4M3 64 x 16,384 49.0 /
+  // 46.0 / 48.9, 1 x 1,048,576 116 / 25.4 / 25.7).
   const int threads = select_threads(pages), tile = threads / 2;
   const int64_t tiles = (pages + tile - 1) / tile;
   const int64_t ctas = std::max<int64_t>(1, static_cast<int64_t>(512 / threads) * num_sms / units);
@@ -1511,10 +1533,12 @@ int page_chunk_pages(int units, int pages, int num_sms) {
 }
 
 int page_splits(int units, int groups, int num_sms) {
-  // two groups a warp where there are few of them (the splits of a unit are
-  // joined by one CTA); no more CTAs than run at once (two an SM at D = 256)
+  // A group a warp where there are few of them (one / two / four: 1 x 5,003
+  // tokens 20.0 / 20.4 / 23.7 us, 1 x 1,048,576 25.4 / 25.5 / 28.3); no more CTAs
+  // than run at once, two an SM at D = 256 (one / two / four: 8 x 262,144 tokens
+  // 44.9 / 39.3 / 43.5 us, E4M3 64 x 16,384 56.4 / 46.0 / 51.6).
   int s = 2 * num_sms / units;
-  s = std::min(s, (groups + 2 * kWarps - 1) / (2 * kWarps));
+  s = std::min(s, (groups + kWarps - 1) / kWarps);
   return std::min(std::max(s, 1), kMaxSplits);
 }
 

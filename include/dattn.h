@@ -145,7 +145,7 @@ typedef struct {
   int num_layers;
   const dattn_layer_config* layers; /* [num_layers], host memory                  */
   int max_selected_pages; /* largest num_pages of a dattn_sparse_decode call; 0 =
-                            none. Takes 12 bytes of workspace for each page of
+                            none. Takes 12.4 bytes of workspace for each page of
                             max_context tokens, stream and KV head               */
 } dattn_config;
 
@@ -276,9 +276,8 @@ typedef struct {
 /* Decode attention of a paged layer (bf16 or E4M3) over selected pages: as
  * dattn_decode with the cached tokens of the selected pages, and the new token,
  * in the one softmax. Summaries are read for the pages that compete only, so
- * those must be up to date: every page below the newest keep_last. Three
- * launches (two when max_seq_len is at most num_pages pages). Ring and state
- * layers return DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
+ * those must be up to date: every page below the newest keep_last. Two launches.
+ * Ring and state layers return DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
 DATTN_API int dattn_sparse_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                                   const dattn_page_selection* sel, dattn_stream_t stream);
 
