@@ -102,8 +102,7 @@ struct Geo {
   static constexpr int BAD_OFF = (MISC_OFF + 16 + 15) / 16 * 16;  // [2][EB]: 64 chunk + 63 - token of the first
                                                                   // token without a number in a column
   static constexpr int FLAG_OFF = BAD_OFF + 2 * EB * 4;           // [2] latest chunk with such a token
-  static constexpr int PW_OFF = FLAG_OFF + 16;                    // [C] the row warps' decays
-  static constexpr int SMEM = PW_OFF + C * 4 + 1024;              // (1024: alignment)
+  static constexpr int SMEM = FLAG_OFF + 16 + 1024;               // (1024: alignment)
   // tensor memory columns. At D = 256 the products with S's two terms have their
   // own columns: one MMA of N = 128 then does both.
   static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = 256, T_DS = 256 + EB;
@@ -314,10 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY ? kStateWarps
-                              : i == B_AFREE || i == B_PREADY || i == B_OFREE || i == B_STAGED || i == B_STAGED + 1
-                                  ? kRowWarps
-                                  : 1);
+      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY || i == B_AFREE || i == B_PREADY ? kStateWarps
+                              : i == B_OFREE || i == B_STAGED || i == B_STAGED + 1              ? kRowWarps
+                                                                                                : 1);
     reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[0] = reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[1] = -1;
     for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
     fence_mbar_init();
@@ -544,8 +542,42 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       fence_proxy_async_smem();
       arrive(B_SREADY);
     };
+    // P of a tile: 16 columns of A a warp, masked and decayed (pw: lam^0 .. lam^C)
+    const int pi = min(hpt == 2 ? r >> 1 : r, C - 1);         // the row's token
+    const int top = min((r | 31) >> (hpt - 1), C - 1);        // the last token of the warp's rows
+    auto write_p = [&](int t, const float* pw) -> bool {
+      // (P V of the tile before has read its P)
+      if (!warp_wait(B_ADONE, t & 1) || (t > 0 && !warp_wait(B_ODONE, (t - 1) & 1))) return false;
+      tc::fence_after();
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+#pragma unroll 1
+      for (int j0 = 16 * w4; j0 < 16 * w4 + 16; j0 += 8) {
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        if (j0 <= top) {  // (some of the warp's rows reach these columns)
+          uint32_t y[8];
+          tc::ld8(lanes + Gm::T_A + j0, y);
+          const int m = pi - j0;  // columns up to this one count
+          float w[8];
+#pragma unroll
+          for (int jj = 0; jj < 8; ++jj) w[jj] = jj <= m ? __ldg(pw + m - jj) : 0.f;
+          tc::wait_ld();
+#pragma unroll
+          for (int jj = 0; jj < 8; jj += 2)
+            split2(jj <= m ? __uint_as_float(y[jj]) * w[jj] : 0.f, jj + 1 <= m ? __uint_as_float(y[jj + 1]) * w[jj + 1] : 0.f,
+                   hi[jj >> 1], lo[jj >> 1]);
+        }
+        tc::st4(lanes + Gm::T_P + j0 / 2, hi);
+        tc::st4(lanes + Gm::T_P + 32 + j0 / 2, lo);
+      }
+      tc::fence_before();
+      arrive(B_AFREE);
+      tc::wait_st();
+      tc::fence_before();
+      arrive(B_PREADY);
+      return true;
+    };
     bool ok = true;
-    int cc = 0;
+    int cc = 0, t = 0;
     Pieces p = all;
     while (ok && p.next()) {
       const float* pw = a.decay + static_cast<int64_t>(p.h) * kDecayStride;
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         arrive(B_WREADY);
         // ---- the state: S = lam^n S + dS (lam^C with what fp32 drops of it)
         const float ln = __ldg(pw + n), ln_lo = n == C ? __ldg(pw + C + 2) : 0.f;
-        ok = warp_wait(B_DSDONE, cc & 1);
+        ok = write_p(t++, pw) && warp_wait(B_DSDONE, cc & 1);
         if (!ok) break;
         tc::fence_after();
 #pragma unroll
@@ -637,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             S[e0 + e] = fmaf(S[e0 + e], ln, fmaf(S[e0 + e], ln_lo, __uint_as_float(y[e])));
         }
         tc::fence_before();
-        if (k + 1 < p.k1) {
+        for (int mt = 1; mt < tiles && ok; ++mt) ok = write_p(t++, pw);
+        if (ok && k + 1 < p.k1) {
           ok = warp_wait(B_SFREE, cc & 1);
           if (ok) store_s();
         }
@@ -663,8 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     const int hd = hpt == 2 ? r & 1 : 0;
     const int* bad = reinterpret_cast<const int*>(smem + Gm::BAD_OFF);
     const volatile int* bad_chunk = reinterpret_cast<const volatile int*>(smem + Gm::FLAG_OFF);
-    float* pw = reinterpret_cast<float*>(smem + Gm::PW_OFF);  // lam^0 .. lam^(C-1) of a head
-    int table_head = -1;
     // a tile's outputs have been read from shared memory: its Q's last two regions,
     // where they were staged, take the next Q
     auto left = [&](int tile) {
@@ -679,14 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     while (ok && p.next()) {
       const float* gpw = a.decay + static_cast<int64_t>(p.h) * kDecayStride;
       const float row_decay = __ldg(gpw + min(i, C - 1) + 1);
-      // (every row warp writes the whole table: none is still reading the last
-      // one, for P of every earlier tile is complete)
-      if (p.h != table_head) {
-        pw[lane] = __ldg(gpw + lane);
-        pw[lane + C / 2] = __ldg(gpw + lane + C / 2);
-        table_head = p.h;
-        __syncwarp();
-      }
       for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
         const int n = min(C, p.count - k * C);
         for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
@@ -695,33 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           const int64_t head =
               (static_cast<int64_t>(p.b) * a.T + k * C + i) * a.Hkv * G + static_cast<int64_t>(p.h) * G + g;
           const float gate = store && a.gate ? bf16_to_f32(a.gate[head]) : 0.f;
-          ok = warp_wait(B_ADONE, t & 1);
-          if (!ok) break;
-          if (t > 0) left(t - 1);
-          // ---- P: A masked and decayed
-          tc::fence_after();
-          const int lim = min(i, C - 1);  // columns up to this one count
-#pragma unroll 1
-          for (int j0 = 32 * w2; j0 < 32 * w2 + 32; j0 += 16) {
-            uint32_t y[16];
-            tc::ld16(tmem + lane_off + Gm::T_A + j0, y);
-            tc::wait_ld();
-            uint32_t hi[8], lo[8];
-            const float* pi = pw + lim - j0;
-#pragma unroll
-            for (int jj = 0; jj < 16; jj += 2) {
-              const float p0 = j0 + jj <= lim ? __uint_as_float(y[jj]) * pi[-jj] : 0.f;
-              const float p1 = j0 + jj + 1 <= lim ? __uint_as_float(y[jj + 1]) * pi[-jj - 1] : 0.f;
-              split2(p0, p1, hi[jj >> 1], lo[jj >> 1]);
-            }
-            tc::st8(tmem + lane_off + Gm::T_P + j0 / 2, hi);
-            tc::st8(tmem + lane_off + Gm::T_P + 32 + j0 / 2, lo);
-          }
-          tc::fence_before();
-          arrive(B_AFREE);
-          tc::wait_st();
-          tc::fence_before();
-          arrive(B_PREADY);
           // ---- epilogue
           float f = a.scale;
           if (a.gate) f /= 1.f + expf(-gate);
@@ -749,10 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(__uint_as_float(o1[e]) + __uint_as_float(lo[e]));
             }
             tc::wait_ld();
-            if (e0 + 16 == EB / 2 * (w2 + 1)) {
-              tc::fence_before();
-              arrive(B_OFREE);
-            }
             float z[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
@@ -766,6 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (mask >> e & 1) z[e] = __uint_as_float(0x7fffffffu);
+            }
+            // (the notes too are free then: their place is written again two chunks on,
+            // after the next chunk's Q S)
+            if (e0 + 16 == EB / 2 * (w2 + 1)) {
+              tc::fence_before();
+              arrive(B_OFREE);
             }
             if (box) {
               uint8_t* buf = stage + ((e0 >> 4) & 1) * 2048;
@@ -786,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                 *reinterpret_cast<float4*>(dst + e0 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
             }
           }
+          left(t);
         }
       }
     }
