@@ -134,18 +134,6 @@ struct Waiter {
   __device__ __forceinline__ bool wait(int b, uint32_t parity) const {
     return mbar_try_wait(bars + 8 * b, parity) || wait_on(bars + 8 * b, parity, abort, err);
   }
-  // Which of two phases completes first: 0 or 1 (1 too when neither does in time;
-  // the wait that follows then reports it).
-  __device__ __forceinline__ int first(int b0, uint32_t parity0, int b1, uint32_t parity1) const {
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-      for (int i = 0; i < 32; ++i) {
-        if (mbar_test_wait(bars + 8 * b0, parity0)) return 0;
-        if (mbar_test_wait(bars + 8 * b1, parity1)) return 1;
-      }
-      if (*abort || global_timer_ns() - t0 > kDefaultWaitNs) return 1;
-    }
-  }
 };
 
 // 8 consecutive floats: one 32-byte store (a whole sector) where the array is
@@ -179,10 +167,29 @@ __device__ __forceinline__ void tma_stores_read() {
 }
 __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Two floats in one instruction: a b + c and a b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Two floats as packed bf16 hi terms and what is left as lo terms.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 left = fma2(make_float2(bf16_lo(hi), bf16_hi(hi)), make_float2(-1.f, -1.f), x);
+  lo = pack_bf16x2(left.x, left.y);
 }
 
 // The chunks of stream b (0, reported, for a row without a state or a count out
@@ -330,9 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::MISC_OFF);
   const Waiter W{bars, abort_flag, a.err};
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
-  auto first = [&](int bar0, uint32_t parity0, int bar1, uint32_t parity1) {
-    return __shfl_sync(0xffffffffu, W.first(bar0, parity0, bar1, parity1), 0);
-  };
   auto arrive = [&](int bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * bar);
@@ -439,58 +443,46 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             }
             if (!ok) break;
             if (lead) tc::commit(bars + 8 * B_ADONE);
-            if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));  // (dS went before)
-            // dS and Q S in the order in which they can start; dS before P V in any
-            // case (which waits for the chunk's zeroed rows)
-            bool ds_first = false;
-            if (mt == 0) {
-              ok = warp_wait(B_SREADY, cc & 1);
-              if (!ok) break;
-              ds_first = t > 0 && first(B_OFREE, (t - 1) & 1, B_WREADY, cc & 1) != 0;
-            }
+            // (dS went before)
+            if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+            // O1 = Q S
+            ok = (mt > 0 || warp_wait(B_SREADY, cc & 1)) && (t == 0 || warp_wait(B_OFREE, (t - 1) & 1));
+            if (!ok) break;
+            tc::fence_after();
 #pragma unroll 1
-            for (int x = mt == 0 ? 0 : 1; x < 2 && ok; ++x) {
-              if ((x == 0) == ds_first && mt == 0) {
-                // dS = K^T W
-                ok = warp_wait(B_WREADY, cc & 1);
-                if (!ok) break;
-                tc::fence_after();
-#pragma unroll 1
-                for (int m = 0; m < D / 128; ++m) {
-                  const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
-                  const uint32_t d = tmem + Gm::T_DS + m * EB;
-                  if (lead)
+            for (int reg = 0; reg < Gm::DR; ++reg) {
+              const int slot = (qr + reg) % Gm::QR;
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
+              const uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
+              if (lead)
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk) {
-                      tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
-                      tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
-                    }
+                for (int kk = 0; kk < 4; ++kk) {
+                  tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk, id_q, reg > 0 || kk > 0);
+                  if constexpr (D == 128)
+                    tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk + Gm::S_PLANE / 16, id_q, true);
                 }
-                if (lead) tc::commit(bars + 8 * B_DSDONE);
-                if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
-                continue;
-              }
-              // O1 = Q S
-              ok = t == 0 || warp_wait(B_OFREE, (t - 1) & 1);
+              if (lead) tc::commit(bars + 8 * (B_QFREE + slot));
+            }
+            if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
+            if (mt == 0) {
+              // dS = K^T W, before P V (which wants the chunk's zeroed rows)
+              ok = warp_wait(B_WREADY, cc & 1);
               if (!ok) break;
               tc::fence_after();
 #pragma unroll 1
-              for (int reg = 0; reg < Gm::DR; ++reg) {
-                const int slot = (qr + reg) % Gm::QR;
-                const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
-                const uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
+              for (int m = 0; m < D / 128; ++m) {
+                const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
+                const uint32_t d = tmem + Gm::T_DS + m * EB;
                 if (lead)
 #pragma unroll
-                  for (int kk = 0; kk < 4; ++kk) {
-                    tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk, id_q, reg > 0 || kk > 0);
-                    if constexpr (D == 128)
-                      tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk + Gm::S_PLANE / 16, id_q, true);
+                  for (int kk = 0; kk < C / 16; ++kk) {
+                    tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
+                    tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
                   }
-                if (lead) tc::commit(bars + 8 * (B_QFREE + slot));
               }
-              if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
+              if (lead) tc::commit(bars + 8 * B_DSDONE);
+              if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
             }
-            if (!ok) break;
             // O2 = P V
             ok = warp_wait(B_PREADY, t & 1);
             if (!ok) break;
@@ -531,10 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         uint4 hi, lo;
-        split2(S[8 * ch], S[8 * ch + 1], hi.x, lo.x);
-        split2(S[8 * ch + 2], S[8 * ch + 3], hi.y, lo.y);
-        split2(S[8 * ch + 4], S[8 * ch + 5], hi.z, lo.z);
-        split2(S[8 * ch + 6], S[8 * ch + 7], hi.w, lo.w);
+        split2(make_float2(S[8 * ch], S[8 * ch + 1]), hi.x, lo.x);
+        split2(make_float2(S[8 * ch + 2], S[8 * ch + 3]), hi.y, lo.y);
+        split2(make_float2(S[8 * ch + 4], S[8 * ch + 5]), hi.z, lo.z);
+        split2(make_float2(S[8 * ch + 6], S[8 * ch + 7]), hi.w, lo.w);
         const int off = (((w4 & 1) * 4 + ch) ^ (sd & 7)) << 4;
         *reinterpret_cast<uint4*>(dst + off) = hi;
         *reinterpret_cast<uint4*>(dst + Gm::S_PLANE + off) = lo;
@@ -559,11 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           const int m = pi - j0;  // columns up to this one count
           float w[8];
 #pragma unroll
-          for (int jj = 0; jj < 8; ++jj) w[jj] = jj <= m ? __ldg(pw + m - jj) : 0.f;
+          for (int jj = 0; jj < 8; ++jj) w[jj] = __ldg(pw + max(m - jj, 0));
           tc::wait_ld();
 #pragma unroll
           for (int jj = 0; jj < 8; jj += 2)
-            split2(jj <= m ? __uint_as_float(y[jj]) * w[jj] : 0.f, jj + 1 <= m ? __uint_as_float(y[jj + 1]) * w[jj + 1] : 0.f,
+            split2(mul2(make_float2(jj <= m ? __uint_as_float(y[jj]) : 0.f, jj + 1 <= m ? __uint_as_float(y[jj + 1]) : 0.f),
+                        make_float2(w[jj], w[jj + 1])),
                    hi[jj >> 1], lo[jj >> 1]);
         }
         tc::st4(lanes + Gm::T_P + j0 / 2, hi);
@@ -638,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           }
           const float w = j < n ? __ldg(pw + n - 1 - j) : 0.f;
           uint4 hi, lo;
-          split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
-          split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
-          split2(bf16_lo(y.z) * w, bf16_hi(y.z) * w, hi.z, lo.z);
-          split2(bf16_lo(y.w) * w, bf16_hi(y.w) * w, hi.w, lo.w);
+          split2(mul2(make_float2(bf16_lo(y.x), bf16_hi(y.x)), make_float2(w, w)), hi.x, lo.x);
+          split2(mul2(make_float2(bf16_lo(y.y), bf16_hi(y.y)), make_float2(w, w)), hi.y, lo.y);
+          split2(mul2(make_float2(bf16_lo(y.z), bf16_hi(y.z)), make_float2(w, w)), hi.z, lo.z);
+          split2(mul2(make_float2(bf16_lo(y.w), bf16_hi(y.w)), make_float2(w, w)), hi.w, lo.w);
           *reinterpret_cast<uint4*>(wt + off) = hi;
           *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
@@ -665,8 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           tc::ld16(t_ds + e0, y);
           tc::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[e0 + e] = fmaf(S[e0 + e], ln, fmaf(S[e0 + e], ln_lo, __uint_as_float(y[e])));
+          for (int e = 0; e < 16; e += 2) {
+            const float2 x = make_float2(S[e0 + e], S[e0 + e + 1]);
+            const float2 z = fma2(x, make_float2(ln, ln),
+                                  fma2(x, make_float2(ln_lo, ln_lo),
+                                       make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))));
+            S[e0 + e] = z.x;
+            S[e0 + e + 1] = z.y;
+          }
         }
         tc::fence_before();
         for (int mt = 1; mt < tiles && ok; ++mt) ok = write_p(t++, pw);
@@ -747,7 +746,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             tc::wait_ld();
             float z[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o2[e]) * f);
+            for (int e = 0; e < 16; e += 2) {
+              const float2 y = fma2(make_float2(__uint_as_float(o1[e]), __uint_as_float(o1[e + 1])), make_float2(f1, f1),
+                                    mul2(make_float2(__uint_as_float(o2[e]), __uint_as_float(o2[e + 1])), make_float2(f, f)));
+              z[e] = y.x;
+              z[e + 1] = y.y;
+            }
             if (odd) {
               uint32_t mask = 0;
 #pragma unroll 1
@@ -981,10 +985,10 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
           const uint4 y = *reinterpret_cast<const uint4*>(vt + off);
           const float w = __ldg(pw + C - 1 - ((off >> 7) & (C - 1))) * g;
           uint4 hi, lo;
-          split2(bf16_lo(y.x) * w, bf16_hi(y.x) * w, hi.x, lo.x);
-          split2(bf16_lo(y.y) * w, bf16_hi(y.y) * w, hi.y, lo.y);
-          split2(bf16_lo(y.z) * w, bf16_hi(y.z) * w, hi.z, lo.z);
-          split2(bf16_lo(y.w) * w, bf16_hi(y.w) * w, hi.w, lo.w);
+          split2(mul2(make_float2(bf16_lo(y.x), bf16_hi(y.x)), make_float2(w, w)), hi.x, lo.x);
+          split2(mul2(make_float2(bf16_lo(y.y), bf16_hi(y.y)), make_float2(w, w)), hi.y, lo.y);
+          split2(mul2(make_float2(bf16_lo(y.z), bf16_hi(y.z)), make_float2(w, w)), hi.z, lo.z);
+          split2(mul2(make_float2(bf16_lo(y.w), bf16_hi(y.w)), make_float2(w, w)), hi.w, lo.w);
           *reinterpret_cast<uint4*>(wt + off) = hi;
           *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
         }
