@@ -17,9 +17,11 @@
 // Work split. A unit is one (stream, KV head, slice): EB of the state's columns
 // (all 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
 // shared memory beside Q, K, V and W). Where units are many, or their streams
-// short or alike, a CTA has one unit. Otherwise the units' chunks are laid end to
-// end and one CTA an SM takes an equal range of them, worked out on the device
-// from the counts: a range begins and ends inside a unit, so a first kernel sums
+// short or alike, a CTA has one unit. Otherwise the heads' chunks are laid end to
+// end and one CTA an SM - at D = 256 four, a slice each, which so read the same Q
+// and K at the same time: 210 -> 186 us for 16 ragged prompts, whose Q and K came
+// from memory four times before - takes an equal range of them, worked out on
+// the device from the counts: a range begins and ends inside a unit, so a first kernel sums
 // what each CTA's last unit contributes to the state (for the CTA after it), a
 // second carries the states along, and the main kernel starts each range from
 // its state.
@@ -204,14 +206,16 @@ __device__ __forceinline__ int stream_chunks(const LinearArgs& a, int b, bool re
   return (n + C - 1) / C;
 }
 
-// A place in the units laid end to end: unit and chunk.
+// A place in the (stream, KV head)s laid end to end: which of them, and chunk.
 struct Place {
   int u, k;
 };
 
-// Where CTA i of NC begins. `cum`: [B] inclusive sums over the streams of their
-// units' weights (HS units of chunks + kPieceCost each), in shared memory.
-__device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum, int HS, int i, int NC) {
+// Where the i-th of NC groups of CTAs (one a slice) begins. `cum`: [B] inclusive
+// sums over the streams of their heads' weights (chunks + kPieceCost each), in
+// shared memory.
+__device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum, int i, int NC) {
+  const int HS = a.Hkv;
   const int64_t total = cum[a.B - 1];
   const int64_t t = total * i / NC;
   if (t >= total) return Place{a.B * HS, 0};
@@ -234,34 +238,33 @@ __device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum
 // 16 streams of 512 - 4,096 tokens (128 units of 256) 218 / 320 us, 4 x 512 (32
 // units of 128) 29.9 / 33.6 us, 1 x 32,768 (8 of 128) 142 / 1,647 us.
 template <int NT>
-__device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int HS, bool report) {
+__device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int groups, bool report) {
   __shared__ int longest;
   if (threadIdx.x == 0) longest = 0;
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += NT) {
     const int n = stream_chunks(a, b, report);
-    cum[b] = n > 0 ? (n + kPieceCost) * HS : 0;
+    cum[b] = n > 0 ? (n + kPieceCost) * a.Hkv : 0;
     atomicMax(&longest, n);
   }
   __syncthreads();
   block_scan_inclusive<NT>(cum, a.B);
-  return static_cast<int64_t>(14) * cum[a.B - 1] / a.ctas + 25 < static_cast<int64_t>(10) * longest;
+  return static_cast<int64_t>(14) * cum[a.B - 1] / groups + 25 < static_cast<int64_t>(10) * longest;
 }
 
-// The pieces of a CTA's range: chunks [k0, k1) of a unit; every role walks them.
+// The pieces of a CTA's range: chunks [k0, k1) of a (stream, KV head); every
+// role walks them.
 struct Pieces {
   const LinearArgs& a;
-  int HS;
   Place at, end;
-  int u, b, h, slice, k0, k1, count;
+  int slice;
+  int b, h, k0, k1, count;
   bool last;  // the unit's last piece
   __device__ __forceinline__ bool next() {
     while (at.u < end.u || (at.u == end.u && at.k < end.k)) {
-      u = at.u;
-      b = u / HS;
-      const int r = u - b * HS, slices = HS / a.Hkv;
-      h = r / slices;
-      slice = r - h * slices;
+      const int u = at.u;
+      b = u / a.Hkv;
+      h = u - b * a.Hkv;
       const int n = stream_chunks(a, b, false);
       count = a.count[b];
       k0 = at.k;
@@ -285,30 +288,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   const uint32_t bars = sbase + Gm::BAR_OFF;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Gm::MISC_OFF + 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int HS = a.Hkv * Gm::SLICES;
   const int G = a.G, hpt = G > 1 ? 2 : 1;  // query heads of an M tile
   const int tiles = (G + hpt - 1) / hpt;
 
   // ---- the CTA's range (the counts and rows are the caller's)
-  Place begin, end;
+  const int group = blockIdx.x / Gm::SLICES, slice = blockIdx.x - group * Gm::SLICES;
+  Place begin{group, 0}, end{group + 1, 0};
   if (a.split) {
     int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
-    const int i = blockIdx.x;
-    if (sum_weights<kThreads>(a, cum, HS, i == 0)) {
-      begin = range_start(a, cum, HS, min(i, a.ctas), a.ctas);
-      end = range_start(a, cum, HS, min(i + 1, a.ctas), a.ctas);
+    const int groups = a.ctas / Gm::SLICES, heads = a.B * a.Hkv;
+    if (sum_weights<kThreads>(a, cum, groups, blockIdx.x == 0)) {
+      begin = range_start(a, cum, min(group, groups), groups);
+      end = range_start(a, cum, min(group + 1, groups), groups);
     } else {
-      begin = Place{min(i, a.B * HS), 0};
-      end = Place{min(i + 1, a.B * HS), 0};
+      begin = Place{min(group, heads), 0};
+      end = Place{min(group + 1, heads), 0};
     }
     __syncthreads();
   } else {
-    begin = Place{static_cast<int>(blockIdx.x), 0};
-    end = Place{static_cast<int>(blockIdx.x) + 1, 0};
-    const int b = blockIdx.x / HS;
-    stream_chunks(a, b, blockIdx.x == b * HS && threadIdx.x == 0);
+    stream_chunks(a, group / a.Hkv, group % a.Hkv == 0 && slice == 0 && threadIdx.x == 0);
   }
-  const Pieces all{a, HS, begin, end};
+  const Pieces all{a, begin, end, slice};
   {
     Pieces p = all;
     if (!p.next()) {  // (the whole CTA)
@@ -345,7 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   if (warp == kTmaWarp) {
     // ================= copies =================
     if (lane == 0) {
-      const uint64_t policy = l2_evict_first_policy();
+      // (not evict-first: the other slices' CTAs read the same Q and K)
+      uint64_t policy;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
       bool ok = true;
       int cc = 0, qr = 0;  // chunks and regions of Q so far
       Pieces p = all;
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       // have stored the new one by now)
       const float* src = state;
       if (p.k0 > 0)
-        src = a.sums + (static_cast<int64_t>(blockIdx.x - 1) * D + sd) * EB + se;
+        src = a.sums + (static_cast<int64_t>(blockIdx.x - Gm::SLICES) * D + sd) * EB + se;
       else if (!p.last)
         src = a.sums + (static_cast<int64_t>(a.ctas + blockIdx.x) * D + sd) * EB + se;
 #pragma unroll
@@ -851,13 +853,13 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
   const uint32_t bars = sbase + Sg::BAR_OFF;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sg::MISC_OFF + 8);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int HS = a.Hkv * Gm::SLICES;
   int* cum = reinterpret_cast<int*>(smem);  // (before the copies)
-  const bool cut = sum_weights<kSumThreads>(a, cum, HS, false);
-  const Place begin = cut ? range_start(a, cum, HS, blockIdx.x, a.ctas) : Place{0, 0};
-  const Place end = cut ? range_start(a, cum, HS, blockIdx.x + 1, a.ctas) : Place{0, 0};
+  const int groups = a.ctas / Gm::SLICES, group = blockIdx.x / Gm::SLICES, slice = blockIdx.x - group * Gm::SLICES;
+  const bool cut = sum_weights<kSumThreads>(a, cum, groups, false);
+  const Place begin = cut ? range_start(a, cum, min(group, groups), groups) : Place{0, 0};
+  const Place end = cut ? range_start(a, cum, min(group + 1, groups), groups) : Place{0, 0};
   const int k0 = begin.u == end.u ? begin.k : 0, chunks = end.k - k0;
-  const int b = end.u / HS, r0 = end.u - b * HS, h = r0 / Gm::SLICES, slice = r0 - h * Gm::SLICES;
+  const int b = end.u / a.Hkv, h = end.u - b * a.Hkv;
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -1033,37 +1035,38 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
   constexpr int64_t SLOT = static_cast<int64_t>(D) * EB;
   constexpr int SLOTS = 8;  // in flight
   extern __shared__ SlotNote note[];  // [NC]
-  const int HS = a.Hkv * Gm::SLICES, c = blockIdx.y, NC = a.ctas;
+  constexpr int SL = Gm::SLICES;
+  const int c = blockIdx.y, NC = a.ctas, slice = c % SL;  // the CTA, and those after it on its slice
   pdl_wait();
   pdl_trigger();
   const SlotNote* notes = slot_notes<D>(a) + c;
   const SlotNote first = notes[0];
   if (first.kind != 2) return;
-  const int u = first.unit, b = u / HS, r = u - b * HS, h = r / Gm::SLICES, slice = r - h * Gm::SLICES;
+  const int u = first.unit, b = u / a.Hkv, h = u - b * a.Hkv;
   const int at = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int d = at / EB, e = at - d * EB;
   float4 s = *reinterpret_cast<const float4*>(
       a.state + ((static_cast<int64_t>(state_row(a, b, false)) * a.Hkv + h) * D + d) * D + slice * EB + e);
-  for (int x = threadIdx.x; c + x < NC; x += 256) note[x] = notes[x];
+  for (int x = threadIdx.x; c + x * SL < NC; x += 256) note[x] = notes[x * SL];
   __syncthreads();
   *reinterpret_cast<float4*>(a.sums + (NC + c) * SLOT + at) = s;
-  for (int x0 = 0; c + x0 < NC && note[x0].unit == u; x0 += SLOTS) {
+  for (int x0 = 0; c + x0 * SL < NC && note[x0].unit == u; x0 += SLOTS) {
     float4 y[SLOTS];
 #pragma unroll
     for (int x = 0; x < SLOTS; ++x)
-      y[x] = c + x0 + x < NC && note[x0 + x].unit == u && note[x0 + x].kind > 0
-                 ? *reinterpret_cast<const float4*>(a.sums + (c + x0 + x) * SLOT + at)
+      y[x] = c + (x0 + x) * SL < NC && note[x0 + x].unit == u && note[x0 + x].kind > 0
+                 ? *reinterpret_cast<const float4*>(a.sums + (c + (x0 + x) * SL) * SLOT + at)
                  : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int x = 0; x < SLOTS; ++x) {
-      if (c + x0 + x >= NC || note[x0 + x].unit != u) return;
+      if (c + (x0 + x) * SL >= NC || note[x0 + x].unit != u) return;
       // (the decay of a slot without a sum is 1)
       const float lam = note[x0 + x].lam, lo = note[x0 + x].lam_lo;
       s.x = fmaf(s.x, lam, fmaf(s.x, lo, y[x].x));
       s.y = fmaf(s.y, lam, fmaf(s.y, lo, y[x].y));
       s.z = fmaf(s.z, lam, fmaf(s.z, lo, y[x].z));
       s.w = fmaf(s.w, lam, fmaf(s.w, lo, y[x].w));
-      *reinterpret_cast<float4*>(a.sums + (c + x0 + x) * SLOT + at) = s;
+      *reinterpret_cast<float4*>(a.sums + (c + (x0 + x) * SL) * SLOT + at) = s;
     }
   }
 }
