@@ -18,29 +18,31 @@
 // (all 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
 // shared memory beside Q, K, V and W). Where units are many, or their streams
 // short or alike, a CTA has one unit. Otherwise the heads' chunks are laid end to
-// end and one CTA an SM - at D = 256 four, a slice each, which so read the same Q
-// and K at the same time: 210 -> 186 us for 16 ragged prompts, whose Q and K came
-// from memory four times before - takes an equal range of them, worked out on
-// the device from the counts: a range begins and ends inside a unit, so a first kernel sums
+// end and one CTA an SM takes an equal range of them, worked out on the device
+// from the counts: a range begins and ends inside a unit, so a first kernel sums
 // what each CTA's last unit contributes to the state (for the CTA after it), a
 // second carries the states along, and the main kernel starts each range from
-// its state.
+// its state. At D = 256 four CTAs have the same range, a slice each: they read
+// the same Q and K at the same time (16 ragged prompts: 216 MB from memory; 671
+// MB and 210 in place of 184 us when each had a range of its own).
 //
-// Roles: 16 state warps (W, and the state: dS in, S's terms out), 8 row warps (P
-// and the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
-// issues the MMAs. The state warps' chain (W, dS, S) and the row warps' (P, O)
-// run beside one another; both end in tensor memory, which is full, so that the
-// next chunk's Q S waits until the outputs are read. 832 threads leave 72
-// registers each, and the roles' loops are kept small: when they missed the
-// instruction cache, that was 43% of the stalls.
+// Roles: 16 state warps (W, P, and the state: dS in, S's terms out), 8 row warps
+// (the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
+// issues the MMAs. The state warps' chain and the row warps' run beside one
+// another; both end in tensor memory, which is full, so that the next chunk's Q S
+// waits until the outputs are read. 832 threads leave 72 registers each, and the
+// roles' loops are kept small: when they missed the instruction cache, that was
+// 43% of the stalls. The MMA warp walks its loops as a whole: descriptors worked
+// out by one thread took it 60 - 120 ns an MMA (1 x 32,768 tokens 157 us, 149 so).
 //
-// Bound by the chunk's chain of dependent steps, not by a unit: at D = 128 3.6 us
-// a chunk and Q tile, of which the row warps' reads of the outputs and their
-// staging are 1.9, P 0.9; the MMAs of it take 1.3 us of the tensor pipe (each
-// waits for its operands from shared memory: 25 ns at N = 64, 34 at N = 128) and
-// the copies 2.9 us at the memory's rate. 1 x 32,768 tokens, 16 / 8 heads of 128:
-// 142 us = sums 32, scan 8, main 108 (537 MB, 4.5 TB/s, overlapping a little). 16
-// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 218 us = 34, 8, 186.
+// Bound by a chunk's chain of dependent steps, not by a unit: at D = 128 3.6 us a
+// chunk and Q tile - the state warps' W 0.9, P 0.9 and the state's update and
+// terms 1.1; beside it the row warps' 2.4 for the outputs - of which the MMAs
+// take 1.3 us of the tensor pipe (25 ns each at N = 64, 34 at N = 128: their
+// operands' way from shared memory) and the copies 2.9 us at the memory's rate.
+// 1 x 32,768 tokens, 16 / 8 heads of 128: 138 us = sums 32, scan 8, main 106
+// (505 MB of it from and to memory, 4.8 TB/s), partly beside one another. 16
+// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 184 us = 33, 8, 152.
 //
 // An infinity or no number in v would reach earlier tokens of its chunk (its
 // weight in P is 0, and 0 times it is no number): the state warps replace it by
@@ -235,8 +237,8 @@ __device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum
 // returns whether the units are worth cutting. In chunks' times: uncut, the
 // longest unit's chunks; cut, everything spread evenly, with 40% more for the
 // sums and 2.5 chunks' time for what is launched between. Measured, cut / uncut:
-// 16 streams of 512 - 4,096 tokens (128 units of 256) 218 / 320 us, 4 x 512 (32
-// units of 128) 29.9 / 33.6 us, 1 x 32,768 (8 of 128) 142 / 1,647 us.
+// 16 streams of 512 - 4,096 tokens (128 units of 256) 184 / 291 us, 16 x 4,096
+// 348 / 328, 4 x 512 (32 units of 128) 30.0 / 33.6, 1 x 32,768 (8) 138 / 1,647.
 template <int NT>
 __device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int groups, bool report) {
   __shared__ int longest;
@@ -812,7 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 // next CTA: K^T W over chunks (all full), in tensor memory over groups of up to
 // kSumGroup of them - W's weights reach to the group's end - and from group to
 // group in registers. The state warps make W, the rest is copies and MMAs; K, V
-// and W are rings, so the pass runs at the rate of its copies.
+// and W are rings. 31 - 33 us at 1 x 32,768 tokens (134 MB, 4.2 TB/s) and at 16
+// ragged prompts, about 0.9 us a chunk: neither a fifth stage nor four W's on
+// their way at once (31 - 34 us) changed it.
 constexpr int kSumGroup = 4, kSumStages = 4;
 constexpr int kSumThreads = (kStateWarps + 2) * 32;
 enum : int { R_FULL, R_FREE = R_FULL + kSumStages, R_WREADY = R_FREE + kSumStages, R_WFREE = R_WREADY + 2,
@@ -1093,12 +1097,12 @@ cudaError_t launch_linear_prompt(const LinearArgs& args, int D, int num_sms, cud
   LinearArgs a = args;
   const int units = a.B * a.Hkv * (D == 128 ? Geo<128>::SLICES : Geo<256>::SLICES);
   const int chunks = (a.T + C - 1) / C;
-  // Whether units are cut is decided on the device, from the counts (that costs
-  // 10 us where it comes out against it); not even considered for short prompts
-  // (cut / uncut: 4 x 330 tokens of 8 heads of 128 28.8 / 26.3 us, 4 x 256 28.3 /
-  // 20.8) nor with more units than SMs, which even each other out (20 x 512 -
-  // 2,048, 160 units: 131 / 115 us, 32 x 1,024: 144 / 127, 48 x 512 - 2,048: 252 /
-  // 255, 64 x 16 - 4,096: 485 / 472).
+  // Whether units are cut is decided on the device, from the counts (9 us where it
+  // comes out against it); not even considered for short prompts (cut / uncut: 4 x
+  // 330 tokens of 8 heads of 128 29.1 / 26.6 us, 4 x 256 28.5 / 20.6) nor with more
+  // units than SMs, which even each other out (20 x 512 - 2,048, 160 units: 131 /
+  // 115 us, 32 x 1,024: 141 / 128, 48 x 512 - 2,048: 253 / 257, 64 x 16 - 4,096:
+  // 486 / 471).
   a.split = chunks > 6 && units <= num_sms;
   a.ctas = num_sms;
   const int ctas = a.split ? num_sms : units;
