@@ -44,7 +44,7 @@
 // operands' way from shared memory) and the copies 2.9 us at the memory's rate.
 // 1 x 32,768 tokens, 16 / 8 heads of 128: 138 us = sums 32, scan 8, main 106
 // (505 MB of it from and to memory, 4.8 TB/s), partly beside one another. 16
-// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 184 us = 33, 8, 152.
+// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 178 us = 33, 8, 148.
 //
 // An infinity or no number in v would reach earlier tokens of its chunk (its
 // weight in P is 0, and 0 times it is no number): the state warps replace it by
@@ -81,9 +81,9 @@ enum : int {
   B_DSDONE,             // K^T W complete
   B_FINAL,
   B_STAGED,             // [2] a tile's outputs have left its Q
-  B_QFULL = B_STAGED + 2,  // [6] 64 dims of a Q tile have landed
-  B_QFREE = B_QFULL + 6,   // [6] ... and the MMAs that read them completed
-  B_COUNT = B_QFREE + 6
+  B_QFULL = B_STAGED + 2,  // [2] a Q tile has landed (an arrival for each two regions)
+  B_QFREE = B_QFULL + 2,   // [3] the MMAs that read two regions of Q completed
+  B_COUNT = B_QFREE + 3
 };
 
 template <int D>
@@ -91,15 +91,16 @@ struct Geo {
   static constexpr int EB = D == 128 ? 128 : 64;   // state columns of a CTA
   static constexpr int SLICES = D / EB;
   static constexpr int ER = EB / 64, DR = D / 64;  // 64-element regions
-  static constexpr int QR = D == 128 ? 4 : 6;      // regions of Q in shared memory (a tile has DR): the next tile's
-                                                   // land while this one's are used
+  static constexpr int QP = D == 128 ? 2 : 3;      // pairs of Q's regions in shared memory (a tile has DP): the next
+  static constexpr int DP = DR / 2;                // tile's land while this one's are used
   static constexpr int KS = D == 128 ? 2 : 1;      // chunks of K
   static constexpr int Q_REGION = 16384;           // [128 rows][128 bytes]
+  static constexpr int Q_PAIR = 2 * Q_REGION;
   static constexpr int K_TILE = DR * 8192;         // [region][64 rows][128 bytes]
   static constexpr int V_TILE = ER * 8192;
   static constexpr int S_PLANE = ER * D * 128;     // [region][D rows][128 bytes]
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + QR * Q_REGION;
+  static constexpr int K_OFF = Q_OFF + QP * Q_PAIR;
   static constexpr int V_OFF = K_OFF + KS * K_TILE;
   static constexpr int W_OFF = V_OFF + 2 * V_TILE;  // hi, lo
   static constexpr int S_OFF = W_OFF + 2 * V_TILE;  // hi, lo
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     for (int i = 0; i < B_COUNT; ++i)
       mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY || i == B_AFREE || i == B_PREADY ? kStateWarps
                               : i == B_OFREE || i == B_STAGED || i == B_STAGED + 1              ? kRowWarps
+                              : i == B_QFULL || i == B_QFULL + 1                                ? Gm::DP
                                                                                                 : 1);
     reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[0] = reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[1] = -1;
     for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       uint64_t policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
       bool ok = true;
-      int cc = 0, qr = 0;  // chunks and regions of Q so far
+      int cc = 0, qp = 0;  // chunks and pairs of Q's regions so far
       Pieces p = all;
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
@@ -378,18 +380,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
           }
           for (int mt = 0; mt < tiles && ok; ++mt)
-            for (int r = 0; r < Gm::DR; ++r, ++qr) {
-              const int slot = qr % Gm::QR;
-              if (qr >= Gm::QR) {
-                const int was = qr - Gm::QR, t = was / Gm::DR;  // its region before, and that one's tile
-                ok = W.wait(B_QFREE + slot, (qr / Gm::QR - 1) & 1) &&
-                     (was % Gm::DR < Gm::DR - 2 || W.wait(B_STAGED + (t & 1), (t >> 1) & 1));
+            for (int i = 0; i < Gm::DP; ++i, ++qp) {
+              const int slot = qp % Gm::QP, t = qp / Gm::DP;
+              if (qp >= Gm::QP) {
+                const int was = qp - Gm::QP, tw = was / Gm::DP;  // its pair before, and that one's tile
+                ok = W.wait(B_QFREE + slot, (qp / Gm::QP - 1) & 1) &&
+                     (was % Gm::DP < Gm::DP - 1 || W.wait(B_STAGED + (tw & 1), (tw >> 1) & 1));
               }
               if (!ok) break;
-              const uint32_t bar = bars + 8 * (B_QFULL + slot);
-              mbar_arrive_expect_tx(bar, static_cast<uint32_t>(hpt) * 8192u);
-              tma_load_3d(sbase + Gm::Q_OFF + slot * Gm::Q_REGION, &a.tmap_q, 64 * r, p.h * G + mt * hpt, tok, bar,
-                          policy);
+              const uint32_t bar = bars + 8 * (B_QFULL + (t & 1)), dst = sbase + Gm::Q_OFF + slot * Gm::Q_PAIR;
+              mbar_arrive_expect_tx(bar, 2 * static_cast<uint32_t>(hpt) * 8192u);
+              for (int r = 0; r < 2; ++r)
+                tma_load_3d(dst + r * Gm::Q_REGION, &a.tmap_q, 64 * (2 * i + r), p.h * G + mt * hpt, tok, bar, policy);
             }
         }
       }
@@ -400,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
         for (int i = max(0, cc - Gm::KS + 1); i <= cc; ++i)
           mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
-        for (int i = max(0, qr - Gm::QR); i <= qr; ++i)
-          mbar_wait_bounded(bars + 8 * (B_QFULL + i % Gm::QR), (i / Gm::QR) & 1, kDrainNs);
+        for (int t = max(0, qp / Gm::DP - 1); t <= qp / Gm::DP; ++t)
+          mbar_wait_bounded(bars + 8 * (B_QFULL + (t & 1)), (t >> 1) & 1, kDrainNs);
       }
     }
     __syncwarp();
@@ -422,8 +424,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       // dims, at D = 256 both terms' one region
       const uint64_t s_major = tc::sw128_desc(0, D == 128 ? D * 128 : Gm::S_PLANE, 1024);
       auto at = [&](uint64_t desc, uint32_t addr) { return desc + (addr >> 4); };
+      // dS = K^T W
+      auto issue_ds = [&](uint32_t kt, int cc) {
+#pragma unroll 1
+        for (int m = 0; m < D / 128; ++m) {
+          const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
+          const uint32_t d = tmem + Gm::T_DS + m * EB;
+          if (lead)
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) {
+              tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
+              tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
+            }
+        }
+        if (lead) tc::commit(bars + 8 * B_DSDONE);
+        if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+      };
       bool ok = true;
-      int cc = 0, t = 0, qr = 0;  // chunks, Q tiles and regions of Q so far
+      int cc = 0, t = 0;  // chunks and Q tiles so far
       Pieces p = all;
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
@@ -432,22 +450,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           const uint32_t kt = sbase + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
           ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
           if (!ok) break;
-          for (int mt = 0; mt < tiles && ok; ++mt, ++t, qr += Gm::DR) {
+          for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
             // A = Q K^T
-            ok = t == 0 || warp_wait(B_AFREE, (t - 1) & 1);
+            ok = (t == 0 || warp_wait(B_AFREE, (t - 1) & 1)) && warp_wait(B_QFULL + (t & 1), (t >> 1) & 1);
             if (!ok) break;
+            tc::fence_after();
 #pragma unroll 1
-            for (int reg = 0; reg < Gm::DR; ++reg) {
-              const int slot = (qr + reg) % Gm::QR;
-              ok = warp_wait(B_QFULL + slot, ((qr + reg) / Gm::QR) & 1);
-              if (!ok) break;
-              tc::fence_after();
-              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION), kd = at(k_major, kt + reg * 8192);
+            for (int i = 0; i < Gm::DP; ++i) {
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + (t * Gm::DP + i) % Gm::QP * Gm::Q_PAIR);
+              const uint64_t kd = at(k_major, kt + i * 16384);
               if (lead)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) tc::mma(tmem + Gm::T_A, qd + 2 * kk, kd + 2 * kk, id_a, reg > 0 || kk > 0);
+                for (int kk = 0; kk < 8; ++kk)
+                  tc::mma(tmem + Gm::T_A, qd + (kk >> 2) * (Gm::Q_REGION / 16) + 2 * (kk & 3), kd + (kk >> 2) * 512 + 2 * (kk & 3),
+                          id_a, i > 0 || kk > 0);
             }
-            if (!ok) break;
             if (lead) tc::commit(bars + 8 * B_ADONE);
             // (dS went before)
             if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
@@ -456,39 +473,32 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             if (!ok) break;
             tc::fence_after();
 #pragma unroll 1
-            for (int reg = 0; reg < Gm::DR; ++reg) {
-              const int slot = (qr + reg) % Gm::QR;
-              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_REGION);
-              const uint64_t sd = at(s_major, sbase + Gm::S_OFF + reg * 8192);
-              if (lead)
+            for (int i = 0; i < Gm::DP; ++i) {
+              const int slot = (t * Gm::DP + i) % Gm::QP;
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_PAIR);
+              const uint64_t sd = at(s_major, sbase + Gm::S_OFF + i * 16384);
+              if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk, id_q, reg > 0 || kk > 0);
-                  if constexpr (D == 128)
-                    tc::mma(tmem + Gm::T_O1, qd + 2 * kk, sd + 128 * kk + Gm::S_PLANE / 16, id_q, true);
+                for (int kk = 0; kk < 8; ++kk) {
+                  const uint64_t q = qd + (kk >> 2) * (Gm::Q_REGION / 16) + 2 * (kk & 3), x = sd + 128 * kk;
+                  tc::mma(tmem + Gm::T_O1, q, x, id_q, i > 0 || kk > 0);
+                  if constexpr (D == 128) tc::mma(tmem + Gm::T_O1, q, x + Gm::S_PLANE / 16, id_q, true);
                 }
-              if (lead) tc::commit(bars + 8 * (B_QFREE + slot));
+                tc::commit(bars + 8 * (B_QFREE + slot));
+              }
             }
             if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
+            // W, and with it the chunk's zeroed rows
             if (mt == 0) {
-              // dS = K^T W, before P V (which wants the chunk's zeroed rows)
               ok = warp_wait(B_WREADY, cc & 1);
               if (!ok) break;
               tc::fence_after();
-#pragma unroll 1
-              for (int m = 0; m < D / 128; ++m) {
-                const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
-                const uint32_t d = tmem + Gm::T_DS + m * EB;
-                if (lead)
-#pragma unroll
-                  for (int kk = 0; kk < C / 16; ++kk) {
-                    tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
-                    tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
-                  }
-              }
-              if (lead) tc::commit(bars + 8 * B_DSDONE);
-              if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
             }
+            // dS ahead of P V at D = 128, where the state's chain is the longer one
+            // (1 x 32,768 tokens 138 us, 142 behind it), behind it at D = 256 (16
+            // ragged prompts 182 and 178 us)
+            if constexpr (D == 128)
+              if (mt == 0) issue_ds(kt, cc);
             // O2 = P V
             ok = warp_wait(B_PREADY, t & 1);
             if (!ok) break;
@@ -502,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               }
             if (lead) tc::commit(bars + 8 * B_ODONE);
             if (mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_VFREE + st));
+            if constexpr (D == 256)
+              if (mt == 0) issue_ds(kt, cc);
           }
         }
       }
@@ -736,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           // lane's store of 32 bytes in each of 32 rows takes the load/store path a
           // cycle a row); short chunks and a group's odd head row by row
           const bool box = n == C && (mt + 1) * hpt <= G;
-          uint8_t* stage = smem + Gm::Q_OFF + (t * Gm::DR + Gm::DR - 2 + w2) % Gm::QR * Gm::Q_REGION + (warp & 3) * 4096;
+          uint8_t* stage = smem + Gm::Q_OFF + (t * Gm::DP + Gm::DP - 1) % Gm::QP * Gm::Q_PAIR + w2 * Gm::Q_REGION + (warp & 3) * 4096;
 #pragma unroll 1
           for (int e0 = EB / 2 * w2; e0 < EB / 2 * (w2 + 1); e0 += 16) {
             uint32_t o1[16], o2[16];
