@@ -26,7 +26,7 @@
 // second carries the states along, and the main kernel starts each range from
 // its state. At D = 256 four CTAs have the same range, a slice each: they read
 // the same Q and K at the same time (16 ragged prompts: 216 MB from memory; 671
-// MB and 210 in place of 184 us when each had a range of its own).
+// MB, and 26 us more, when each had a range of its own).
 //
 // Roles: 16 state warps (W, P, and the state: dS in, S's terms out), 8 row warps
 // (the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
@@ -240,8 +240,8 @@ __device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum
 // returns whether the units are worth cutting. In chunks' times: uncut, the
 // longest unit's chunks; cut, everything spread evenly, with 40% more for the
 // sums and 2.5 chunks' time for what is launched between. Measured, cut / uncut:
-// 16 streams of 512 - 4,096 tokens (128 units of 256) 184 / 291 us, 16 x 4,096
-// 348 / 328, 4 x 512 (32 units of 128) 30.0 / 33.6, 1 x 32,768 (8) 138 / 1,647.
+// 16 streams of 512 - 4,096 tokens (128 units of 256) 178 / 277 us, 16 x 4,096
+// 333 / 312, 4 x 512 (32 units of 128) 30.1 / 33.4, 1 x 32,768 (8) 137 / 1,623.
 template <int NT>
 __device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int groups, bool report) {
   __shared__ int longest;
@@ -1111,12 +1111,12 @@ cudaError_t launch_linear_prompt(const LinearArgs& args, int D, int num_sms, cud
   LinearArgs a = args;
   const int units = a.B * a.Hkv * (D == 128 ? Geo<128>::SLICES : Geo<256>::SLICES);
   const int chunks = (a.T + C - 1) / C;
-  // Whether units are cut is decided on the device, from the counts (9 us where it
+  // Whether units are cut is decided on the device, from the counts (10 us where it
   // comes out against it); not even considered for short prompts (cut / uncut: 4 x
-  // 330 tokens of 8 heads of 128 29.1 / 26.6 us, 4 x 256 28.5 / 20.6) nor with more
-  // units than SMs, which even each other out (20 x 512 - 2,048, 160 units: 131 /
-  // 115 us, 32 x 1,024: 141 / 128, 48 x 512 - 2,048: 253 / 257, 64 x 16 - 4,096:
-  // 486 / 471).
+  // 330 tokens of 8 heads of 128 29.2 / 26.5 us, 4 x 256 28.7 / 20.6) nor with more
+  // units than SMs, which even each other out (20 x 512 - 2,048, 160 units: 130 /
+  // 114 us, 32 x 1,024: 142 / 128, 48 x 512 - 2,048: 253 / 255, 64 x 16 - 4,096:
+  // 485 / 466).
   a.split = chunks > 6 && units <= num_sms;
   a.ctas = num_sms;
   const int ctas = a.split ? num_sms : units;
