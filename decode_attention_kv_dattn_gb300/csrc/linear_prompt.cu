@@ -42,9 +42,9 @@
 // terms 1.1; beside it the row warps' 2.4 for the outputs - of which the MMAs
 // take 1.3 us of the tensor pipe (25 ns each at N = 64, 34 at N = 128: their
 // operands' way from shared memory) and the copies 2.9 us at the memory's rate.
-// 1 x 32,768 tokens, 16 / 8 heads of 128: 138 us = sums 32, scan 8, main 106
+// 1 x 32,768 tokens, 16 / 8 heads of 128: 136 us = sums 32, scan 8, main 104
 // (505 MB of it from and to memory, 4.8 TB/s), partly beside one another. 16
-// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 178 us = 33, 8, 148.
+// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 176 us = 33, 8, 146.
 //
 // An infinity or no number in v would reach earlier tokens of its chunk (its
 // weight in P is 0, and 0 times it is no number): the state warps replace it by
@@ -468,6 +468,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             if (lead) tc::commit(bars + 8 * B_ADONE);
             // (dS went before)
             if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+            // At D = 128, where the outputs of the tile before are still being read,
+            // dS goes first (1 x 32,768 tokens 136 us, 138 between Q S and P V, 142
+            // behind P V); at D = 256 last (16 ragged prompts 178 us, 182 ahead of P V).
+            // W comes with the chunk's zeroed rows, which P V wants too.
+            if constexpr (D == 128)
+              if (mt == 0) {
+                ok = warp_wait(B_WREADY, cc & 1);
+                if (!ok) break;
+                tc::fence_after();
+                issue_ds(kt, cc);
+              }
             // O1 = Q S
             ok = (mt > 0 || warp_wait(B_SREADY, cc & 1)) && (t == 0 || warp_wait(B_OFREE, (t - 1) & 1));
             if (!ok) break;
@@ -488,17 +499,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               }
             }
             if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
-            // W, and with it the chunk's zeroed rows
-            if (mt == 0) {
-              ok = warp_wait(B_WREADY, cc & 1);
-              if (!ok) break;
-              tc::fence_after();
-            }
-            // dS ahead of P V at D = 128, where the state's chain is the longer one
-            // (1 x 32,768 tokens 138 us, 142 behind it), behind it at D = 256 (16
-            // ragged prompts 182 and 178 us)
-            if constexpr (D == 128)
-              if (mt == 0) issue_ds(kt, cc);
+            if constexpr (D == 256)
+              if (mt == 0) {
+                ok = warp_wait(B_WREADY, cc & 1);
+                if (!ok) break;
+                tc::fence_after();
+              }
             // O2 = P V
             ok = warp_wait(B_PREADY, t & 1);
             if (!ok) break;
@@ -740,13 +746,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           if (a.gate) f /= 1.f + expf(-gate);
           const float f1 = f * row_decay;
           float* dst = a.out + head * D + p.slice * EB;
+          const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
           ok = warp_wait(B_ODONE, t & 1);
           if (!ok) break;
           tc::fence_after();
           const bool odd = bad_chunk[cc & 1] == cc;
-          // whole boxes of rows leave by the TMA unit, through shared memory (a
-          // lane's store of 32 bytes in each of 32 rows takes the load/store path a
-          // cycle a row); short chunks and a group's odd head row by row
+          // whole boxes of rows leave by the TMA unit, through shared memory (1 x
+          // 32,768 tokens 136 us; 169 with a lane's stores of 32 bytes in each of 32
+          // rows, which take the load/store path a cycle a row, 196 with 16); short
+          // chunks and a group's odd head row by row
           const bool box = n == C && (mt + 1) * hpt <= G;
           uint8_t* stage = smem + Gm::Q_OFF + (t * Gm::DP + Gm::DP - 1) % Gm::QP * Gm::Q_PAIR + w2 * Gm::Q_REGION + (warp & 3) * 4096;
 #pragma unroll 1
@@ -802,8 +810,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                              p.b * a.T + k * C + (warp & 3) * (32 / hpt));
             } else if (store) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(dst + e0 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+              for (int e = 0; e < 16; e += 8) {
+                float half[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) half[y] = z[e + y];
+                st_8(dst + e0 + e, half, wide);
+              }
             }
           }
           left(t);
