@@ -334,11 +334,11 @@ DATTN_API int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int 
  * count or ring metadata is out of range gets no tokens and is reported as
  * DATTN_EINDEX (dattn_get_error). The caller then advances its metadata by
  * count[s].
- * On a state layer the chunked form of linear attention: the same outputs and
- * final state as count[s] decode steps with write_back, whatever
- * max_verify_rows is, in one launch, or three where long streams are few;
- * start_pos is not read. A stream with a count out of range
- * or without a state is reported and left as it is. */
+ * On a state layer the chunked form of linear attention: up to rounding (about
+ * 3e-6 of the outputs' size) the outputs and final state of count[s] decode
+ * steps with write_back, whatever max_verify_rows is, in one launch, or three
+ * where long streams are few; start_pos is not read. A stream with a count out
+ * of range or without a state is reported and left as it is. */
 DATTN_API int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
                             const void* q, const void* k, const void* v, const void* gate,
                             const int32_t* count, const int32_t* start_pos, float* out, dattn_stream_t stream);
