@@ -36,6 +36,7 @@ constexpr int kList = 1024;           // pages near the border ranked in shared 
 constexpr int kBins = 1024;           // histogram bins of the threshold search
 constexpr int kStaged = 16384;        // scores held in shared memory during the selection
 constexpr int kMaxSplits = 160;       // CTAs of a unit in the attention
+constexpr float kWeightUp = 32768.f;  // E4M3: the softmax weights' factor in fp16
 
 // The cached tokens of stream b as every paged call reads them: clamped to the
 // call's bound, with the error reported once.
@@ -1032,8 +1033,10 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? (D == 128 ? 4 : 2) : 1) page
 // four) MMAs; a lane's 16 bytes of a V row, transposed 8 x 8 in registers, are
 // rows of V^T in an order that only the final store has to know. Q and P are
 // split into three bf16 terms (24 bits; K and V enter exactly); E4M3 is widened
-// to fp16, with Q and P as two fp16 terms (22 bits). Terms are MMAs into the
-// same accumulator.
+// to fp16, with Q and P as two fp16 terms (22 bits, which fp16's range allows for
+// P down to 2^-18: P is split at 2^15 times its value, so smaller weights lose at
+// most 2^-40 each, of sums that are 1 or more). Terms are MMAs into the same
+// accumulator.
 // Few selected keys a unit: what counts is the chain of dependent steps, so
 // there is no ring to fill, and q is rotated and split while the selection is
 // still running.
@@ -1305,8 +1308,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
       }
       mrun[x] = mnew;
     }
-    // ---- P^T, in terms
+    // ---- P^T, in terms (E4M3: of 2^15 P, the largest power of two below the fp16
+    // range; taken back exactly from the outputs)
     uint32_t pt[TERMS][2];
+    if constexpr (F8) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) p[x] *= kWeightUp;
+    }
 #pragma unroll
     for (int y = 0; y < TERMS; ++y) {
       const uint32_t w0 = F8 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
@@ -1378,7 +1386,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
       // and lane of the quad they came from
       const int j = i / (F8 ? 4 : 2), w = (i % (F8 ? 4 : 2)) * 2 + (x >> 1);
       const int d = j * Gm::DPJ + (r0 >> 1) * (Gm::DPJ / 4) + 2 * w + (r0 & 1);
-      if (g < G) qf[(warp * G + g) * PO + d] = o[i][x];
+      if (g < G) qf[(warp * G + g) * PO + d] = F8 ? o[i][x] * (1.f / kWeightUp) : o[i][x];
     }
   __syncthreads();
   const int parts = kWarps + (sp == 0 ? 1 : 0);

@@ -1,0 +1,86 @@
+"""How exact the attention over selected pages is, against 64 bits.
+
+Bounds are relative to the softmax-weighted sum of |v| of a (head, dim), A. If
+every weight p_i is off by at most e relative to itself, numerator and sum move
+by e A and e, so the output by 2 e A.
+
+Scores of keys with one dim other than zero, s (natural logarithms): q times
+the scale rounds twice and q's terms (three bf16 or two fp16) drop 2^-22 at
+most, the terms' sum rounds three times at 2^-24: below 2^-21 |s|. Weights add
+the exponential (2^-21), P's terms (2^-22) and the sums (2^-20 for the few keys
+here): e = 2^-21 |s| + 2^-19.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_sparse import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dattn():
+    import decode_attention_kv_dattn_gb300 as d
+    return d
+
+
+def repeat(c, B):
+    """The case's one stream B times over, in the same pages: with 304 (stream, KV head) units or more each unit is
+    one CTA's, with few it is split."""
+    c.lens = c.lens * B
+    c.table = c.table.repeat(B, 1)
+    c.pos = c.pos.repeat(B)
+    c.q, c.k_new, c.v_new = c.q.repeat(B, 1, 1), c.k_new.repeat(B, 1, 1), c.v_new.repeat(B, 1, 1)
+    if c.gate is not None:
+        c.gate = c.gate.repeat(B, 1)
+    return c
+
+
+def exact(c):
+    """Stream 0 over all its pages, no gate: outputs, A, and sum |q_d k_d| / sqrt(D) of the widest key of a head."""
+    n = c.lens[0]
+    m = -(-n // c.P)
+    out, size, reach = [], [], []
+    for h in range(c.Hkv):
+        rows = c.table[0, :m].long()
+        k = c.k.float()[rows, h].double().reshape(-1, c.D)[:n] * c.ks
+        v = c.v.float()[rows, h].double().reshape(-1, c.D)[:n] * c.vs
+        k1, v1 = c.entries(0, h)
+        k, v = torch.cat([k, k1.double()[None] * c.ks]), torch.cat([v, v1.double()[None] * c.vs])
+        q = c.rotated(0, h)
+        p = torch.softmax(q @ k.T / c.D ** 0.5, -1)
+        out.append(p @ v)
+        size.append(p @ v.abs())
+        reach.append((q.abs() @ k.abs().T).amax(-1) / c.D ** 0.5)
+    return torch.cat(out), torch.cat(size), torch.cat(reach)
+
+
+def check(got, want, bound):
+    assert torch.isfinite(got).all()
+    assert all(torch.equal(x, got[0]) for x in got)
+    d = (got[0].double() - want).abs() - bound
+    assert (d <= 0).all(), f"{d.max():.3g} over a bound of {bound.flatten()[d.argmax()]:.3g}"
+
+
+@pytest.mark.parametrize("B", [1, 40])
+def test_e4m3_many_small_weights(dattn, B):
+    """Four keys without a value (one for each warp of an unsplit unit) and 4,092 keys 15 to 18 nats below them: their
+    weights, 2^-22 to 2^-26, are what the output is made of. Two fp16 terms of such a weight times 2^15 leave 2^-25
+    of at least 2^-11, 2^-14 in all; the scores (30 nats) add 2^-16 and the sums over 1,024 keys a warp (64 steps of
+    17 addends at 2^-23, of positive values) 2^-13. e = 2^-12."""
+    c = Case(31, 16, 8, 256, 16, [4096], fp8=True, r=0, gate=False)
+    c.ks = 1.0
+    c.q[:] = 0
+    c.q[..., 0] = 16.0  # the score of a key is its dim 0
+    k = torch.zeros(c.k.shape)
+    k[..., 0] = torch.randint(12, 16, c.k.shape[:3], generator=c.g).float()
+    v = torch.rand(c.v.shape, generator=c.g) + 0.5
+    first = c.table[0, :4].long()
+    k[first, :, 0, 0] = 30.0
+    v[first, :, 0] = 0.0
+    c.k, c.v = k.to(c.kind), v.to(c.kind)
+    c.k_new[:] = 0
+    want, size, _ = exact(c)
+    out, _ = repeat(c, B).run(dattn, 300, 1, 1)
+    check(out, want, 2 * 2.0 ** -12 * size)
