@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
 
   // ---- the query (base-2 scores) and, in split 0, the new token: its K entry
   // and value as they are stored
-  float q_up = 1.f;  // E4M3: a power of two that brings the query into the fp16 range, and back
+  float q_up = 1.f;  // E4M3: a power of two that brings the query to the top of the fp16 range, and back
   {
     QueryPairs<D, 8, NTH> qp;
     qp.load(a, b, h, a.q_scale, inv_s);
@@ -1089,10 +1089,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
 #pragma unroll
       for (int i = 0; i < qp.ITER; ++i) mx = fmaxf(mx, fmaxf(fabsf(qp.v0[i]), fabsf(qp.v1[i])));
       mx = block_max<NTH>(mx, reinterpret_cast<int*>(&ms[0][0]));
-      // 2^ex <= mx < 2^(ex + 1); both powers are normal numbers
-      const int ex = min(max(((__float_as_int(mx) >> 23) & 255) - 127, -126), 126);
-      q_up = __int_as_float((127 + ex) << 23);
-      q_down = __int_as_float((127 - ex) << 23);
+      // 2^ex <= mx < 2^(ex + 1): the largest element comes to [2^14, 2^15), so that
+      // the second term's last place, 2^-24, is 2^-38 of it or less and heads (and
+      // dims) far below the largest keep their 22 bits too; both powers are normal
+      // numbers
+      const int ex = min(max(((__float_as_int(mx) >> 23) & 255) - 127, -112), 127);
+      q_up = __int_as_float((127 + ex - 14) << 23);
+      q_down = __int_as_float((127 - ex + 14) << 23);
     }
 #pragma unroll
     for (int i = 0; i < qp.ITER; ++i) {

@@ -84,3 +84,27 @@ def test_e4m3_many_small_weights(dattn, B):
     want, size, _ = exact(c)
     out, _ = repeat(c, B).run(dattn, 300, 1, 1)
     check(out, want, 2 * 2.0 ** -12 * size)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_of_very_different_sizes(dattn, fp8):
+    """One query head of a group 2^12 times the others: theirs keep their own precision."""
+    c = Case(32, 8, 2, 128, 16, [100], fp8=fp8, r=0, gate=False)
+    c.ks = 1.0
+    c.q = (100 + 28 * torch.rand(c.q.shape, generator=c.g)).to(torch.bfloat16)
+    c.q[:, ::4] *= 2.0 ** 12
+    one_hot(c)
+    want, size, reach = exact(c)
+    out, _ = c.run(dattn, 8, 1, 1)
+    check(out[:, [1, 2, 3, 5, 6, 7]], want[[1, 2, 3, 5, 6, 7]],
+          2 * ((reach * 2.0 ** -21 + 2.0 ** -19)[:, None] * size)[[1, 2, 3, 5, 6, 7]])
+
+
+def one_hot(c, least=0):
+    """Keys of one dim each, 1 in dim i for token i + least; the new token's is the last dim."""
+    k = torch.zeros(c.k.shape)
+    for i in range(c.lens[0]):
+        k[int(c.table[0, i // c.P]), :, i % c.P, i + least] = 1.0
+    c.k = k.to(c.kind)
+    c.k_new[:] = 0
+    c.k_new[..., c.D - 1] = 1.0
