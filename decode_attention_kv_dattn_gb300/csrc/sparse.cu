@@ -1456,8 +1456,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
       part[e] = x;
   }
   // ---- the new entry into its slot: no key of it is read as valid by this
-  // call, and masked rows' values are replaced by zeros
-  if (sp == 0 && a.write_back) {
+  // call, and masked rows' values are replaced by zeros. A stream whose length was
+  // clamped has no slot: the one after the bound holds a token of it.
+  if (sp == 0 && a.write_back && c.seq_len[b] == n) {
     const int pi = n / c.P;
     const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(b) * c.bt_stride + pi] : -1;
     if (pg < 0 || pg >= c.n_rows) {

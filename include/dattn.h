@@ -276,8 +276,10 @@ typedef struct {
 /* Decode attention of a paged layer (bf16 or E4M3) over selected pages: as
  * dattn_decode with the cached tokens of the selected pages, and the new token,
  * in the one softmax. Summaries are read for the pages that compete only, so
- * those must be up to date: every page below the newest keep_last. Two launches.
- * Ring and state layers return DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
+ * those must be up to date: every page below the newest keep_last. A stream
+ * whose length is outside the call's bound is reported (DATTN_ELENGTH), read up
+ * to the bound and not written. Two launches. Ring and state layers return
+ * DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
 DATTN_API int dattn_sparse_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                                   const dattn_page_selection* sel, dattn_stream_t stream);
 
