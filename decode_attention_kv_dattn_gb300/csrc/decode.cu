@@ -340,12 +340,16 @@ struct Merge8 {
 
 // Where unit (b, j)'s new entry goes: its element offset in the K and V
 // pools (bytes for E4M3), or -1 when the metadata is out of range (a bad
-// page is reported here; a bad ring was reported when the unit table was read).
+// page is reported here; a bad ring or length was reported when the unit table
+// was read).
 template <bool PAGED>
 __device__ __forceinline__ int64_t write_back_offset(const DecodeArgs& a, int b, int j, int D) {
   const CacheView& c = a.c;
   if constexpr (PAGED) {
-    const int n = min(max(c.seq_len[b], 0), min(a.max_len, c.bt_stride * c.P));
+    // a length outside the bound has no slot: the one after the bound holds a token
+    // of the longer stream
+    const int n = c.seq_len[b];
+    if (n < 0 || n > min(a.max_len, c.bt_stride * c.P)) return -1;
     const int pi = n / c.P;
     const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(b) * c.bt_stride + pi] : -1;
     if (pg >= 0 && pg < c.n_rows) return ((static_cast<int64_t>(pg) * a.Hkv + j) * c.P + n % c.P) * D;

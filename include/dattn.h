@@ -189,7 +189,10 @@ typedef struct {
                             (0 = max_context); sizes the key split. Ignored for
                             ring layers (the bound is R).                          */
   int write_back;        /* nonzero: store the rotated bf16 k_new and v_new into
-                            the new token's slot after every read of the cache   */
+                            the new token's slot after every read of the cache.
+                            A paged stream whose length is outside the bound
+                            (DATTN_ELENGTH) or a ring with bad metadata
+                            (DATTN_EINDEX) is not written                          */
 } dattn_decode_args;
 
 /* One verify round: S streams x T rows ("TensorFold PR #608": verify windows
@@ -277,9 +280,9 @@ typedef struct {
  * dattn_decode with the cached tokens of the selected pages, and the new token,
  * in the one softmax. Summaries are read for the pages that compete only, so
  * those must be up to date: every page below the newest keep_last. A stream
- * whose length is outside the call's bound is reported (DATTN_ELENGTH), read up
- * to the bound and not written. Two launches. Ring and state layers return
- * DATTN_EUNSUPPORTED. The ordering rules of dattn_decode hold. */
+ * whose length is outside the call's bound is reported, read up to the bound and
+ * not written. Two launches. Ring and state layers return DATTN_EUNSUPPORTED.
+ * The ordering rules of dattn_decode hold. */
 DATTN_API int dattn_sparse_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                                   const dattn_page_selection* sel, dattn_stream_t stream);
 
