@@ -753,16 +753,18 @@ __global__ void __launch_bounds__(256, 6) verify_combine_kernel(const VerifyComb
   if (a.gate && stored) sig = 1.f / (1.f + expf(-bf16_to_f32(a.gate[ctok * Hq + h])));
   int64_t wb_off = -1;
   if (a.write_back && c.paged && g == 0) {  // (ring layers commit the accepted path instead)
-    int n = c.seq_len[s];
-    const int cap = min(a.max_len, c.bt_stride * c.P);
-    n = n < 0 ? 0 : (n > cap ? cap : n);
-    const int idx = n + i;
-    const int pi = idx / c.P;
-    const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(s) * c.bt_stride + pi] : -1;
-    if (pg >= 0 && pg < c.n_rows)
-      wb_off = ((static_cast<int64_t>(pg) * Hkv + j) * c.P + idx % c.P) * D;
-    else if (lane == 0)
-      raise_error(a.err, ERR_INDEX);
+    // (a stream whose length is outside the bound, reported by the prefix pass, has
+    // no free slots that are known)
+    const int n = c.seq_len[s];
+    if (n >= 0 && n <= min(a.max_len, c.bt_stride * c.P)) {
+      const int idx = n + i;
+      const int pi = idx / c.P;
+      const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(s) * c.bt_stride + pi] : -1;
+      if (pg >= 0 && pg < c.n_rows)
+        wb_off = ((static_cast<int64_t>(pg) * Hkv + j) * c.P + idx % c.P) * D;
+      else if (lane == 0)
+        raise_error(a.err, ERR_INDEX);
+    }
   }
   __syncthreads();
   const int np = npath_s;

@@ -216,8 +216,9 @@ typedef struct {
   float* out;            /* [S, T, Hq, D] fp32                                    */
   int max_prefix_len;    /* host bound on seq_len[s] (0 = max_context)            */
   int write_back;        /* paged layers: nonzero writes window entry i to token
-                            index seq_len[s] + i (node order). Ring layers: must
-                            be 0 (DATTN_EINVAL otherwise)                         */
+                            index seq_len[s] + i (node order); not for a stream
+                            whose length is outside the bound (DATTN_ELENGTH).
+                            Ring layers: must be 0 (DATTN_EINVAL otherwise)       */
   const int32_t* pos;    /* [S] position of the window's root, or NULL for
                             seq_len[s] (paged layers only: ring layers need it)   */
 } dattn_verify_args;

@@ -68,3 +68,29 @@ def test_decode_writes_nothing(dattn, fp8, bad):
         status, kd, vd = dense(dattn, c, 16 * 60, max_seq_len=16 * 45, noalloc=noalloc)
         assert status == dattn.ELENGTH
         assert torch.equal(bits(kd), k) and torch.equal(bits(vd), v)
+
+
+@pytest.mark.parametrize("bad", [16 * 45 + 1, 16 * 50, -3])
+def test_verify_writes_nothing(dattn, bad):
+    """The other streams' windows land behind their prefixes."""
+    T = 5
+    c = Case(43, 8, 2, 256, 16, [16 * 40 + 3, 16 * 50 + T, 77 + T])
+    c.lens = [16 * 40 + 3, bad, 77]
+    x = lambda *s: torch.randn(*s, generator=c.g).to(torch.bfloat16)  # noqa: E731
+    q, k, v = x(3, T, 8, 256), x(3, T, 2, 256), x(3, T, 2, 256)
+    h = dattn.Handle(8, 2, 256, [c.layer(dattn)], 3, max_context=16 * 60, max_verify_rows=T)
+    kd, vd = c.k.cuda(), c.v.cuda()
+    nd = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    parent = (torch.arange(T, dtype=torch.int32) - 1).repeat(3, 1).cuda()
+    out = torch.empty(3, T, 8, 256, device="cuda")
+    h.verify(0, dattn.paged_cache(kd, vd, c.table.cuda(), nd), q.cuda(), k.cuda(), v.cuda(), parent, out,
+             max_prefix_len=16 * 45, pos=torch.zeros(3, dtype=torch.int32).cuda())
+    assert h.get_error() == dattn.ELENGTH
+    want = c.v.clone()
+    for b in (0, 2):
+        for i in range(T):
+            n = c.lens[b] + i
+            want[int(c.table[b, n // 16]), :, n % 16] = v[b, i]
+    assert torch.equal(vd.cpu(), want)
+    pages = [int(p) for p in c.table[1] if p >= 0]
+    assert torch.equal(kd.cpu()[pages], c.k[pages])
