@@ -396,13 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         }
       }
       // Copies still in flight exist only when a role gave up: they land
-      // before the CTA exits (a break above may have left the last chunk's
-      // copies without its count).
+      // before the CTA exits. They are those of the last two chunks (K: KS) and
+      // tiles behind the one that was not requested any more, or in part: a wait
+      // for a place's release that ran out says nothing of the copy into it.
       if (*abort_flag) {
-        for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
-        for (int i = max(0, cc - Gm::KS + 1); i <= cc; ++i)
+        for (int i = max(0, cc - 2); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
+        for (int i = max(0, cc - Gm::KS); i <= cc; ++i)
           mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
-        for (int t = max(0, qp / Gm::DP - 1); t <= qp / Gm::DP; ++t)
+        for (int t = max(0, qp / Gm::DP - 2); t <= qp / Gm::DP; ++t)
           mbar_wait_bounded(bars + 8 * (B_QFULL + (t & 1)), (t >> 1) & 1, kDrainNs);
       }
     }
