@@ -170,6 +170,8 @@ LinearArgs linear_args(const dattn_handle* h, int layer, const dattn_cache* cach
   a.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(h->D)));
   a.sums = h->sums;
   a.err = h->err;
+  a.wait_ns = h->wait_ns;
+  a.debug_flags = h->debug_flags;
   return a;
 }
 

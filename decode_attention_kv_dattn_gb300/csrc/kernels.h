@@ -26,7 +26,8 @@ enum : int { ERR_INDEX = 1, ERR_TIMEOUT = 2, ERR_LENGTH = 4, ERR_RANGE = 8 };
 // Limit of a bounded device wait unless the handle sets another (2 s).
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 // Testing aid (dattn_debug_config): the decode kernel's helper warp withholds
-// the first unit's rotated query, so the streaming warps' waits run out.
+// the first unit's rotated query, so the streaming warps' waits run out. Prompts of
+// state layers: a CTA's first Q tile is not copied.
 constexpr int kDebugWithholdQ = 1;
 
 // One layer's cache as the kernels see it.
@@ -209,6 +210,8 @@ struct LinearArgs {
   int split;                   // prompt: units may be cut into ranges of chunks, by `ctas` CTAs (else one each)
   int ctas;
   int* err;
+  uint64_t wait_ns;            // prompt: limit of the bounded waits
+  int debug_flags;             // prompt: kDebugWithholdQ
 };
 
 struct AppendArgs {

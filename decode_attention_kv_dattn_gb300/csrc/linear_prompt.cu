@@ -118,13 +118,13 @@ struct Geo {
 
 // A bounded wait that did not succeed at once (out of line: the roles' loops have
 // to stay in the instruction cache).
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* err, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (global_timer_ns() - t0 > kDefaultWaitNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       *abort = 1;
       raise_error(err, ERR_TIMEOUT);
       return false;
@@ -135,11 +135,11 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 struct Waiter {
   uint32_t bars;
   volatile int* abort;
-  int* err;
+  const LinearArgs& a;
   // Bounded wait by a whole warp or one thread; after a timeout (or when
   // another role gave up) every role leaves its loop.
   __device__ __forceinline__ bool wait(int b, uint32_t parity) const {
-    return mbar_try_wait(bars + 8 * b, parity) || wait_on(bars + 8 * b, parity, abort, err);
+    return mbar_try_wait(bars + 8 * b, parity) || wait_on(bars + 8 * b, parity, abort, a.err, a.wait_ns);
   }
 };
 
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   pdl_wait();
   pdl_trigger();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Gm::MISC_OFF);
-  const Waiter W{bars, abort_flag, a.err};
+  const Waiter W{bars, abort_flag, a};
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
   auto arrive = [&](int bar) {
     __syncwarp();
@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                      (was % Gm::DP < Gm::DP - 1 || W.wait(B_STAGED + (tw & 1), (tw >> 1) & 1));
               }
               if (!ok) break;
+              if (t == 0 && (a.debug_flags & kDebugWithholdQ)) continue;
               const uint32_t bar = bars + 8 * (B_QFULL + (t & 1)), dst = sbase + Gm::Q_OFF + slot * Gm::Q_PAIR;
               mbar_arrive_expect_tx(bar, 2 * static_cast<uint32_t>(hpt) * 8192u);
               for (int r = 0; r < 2; ++r)
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           if (ok) store_s();
         }
       }
-      if (ok && p.last) {
+      if (ok && p.last && !*abort_flag) {
         float* dst = state;
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll
@@ -915,7 +916,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Sg::MISC_OFF);
-  const Waiter W{bars, abort_flag, a.err};
+  const Waiter W{bars, abort_flag, a};
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, W.wait(bar, parity)); };
 
   if (warp == kStateWarps) {

@@ -358,13 +358,16 @@ DATTN_API int dattn_get_error(dattn_t* h, dattn_stream_t stream);
  * device wait of the library is bounded, and one that runs out ends the call
  * with DATTN_ETIMEOUT from dattn_get_error instead of hanging the GPU.
  *   wait_limit_us - limit of the handle's bounded waits in microseconds for
- *                   its later decode calls (0 = the default, 2 s).
+ *                   its later decode calls and prompts on state layers (0 = the
+ *                   default, 2 s).
  *   flags         - DATTN_DEBUG_WITHHOLD_Q: in each later decode call, the
  *                   kernel's helper warp withholds every CTA's first rotated
  *                   query, so the streaming warps' waits for it run out after
  *                   the limit. The call still completes (the copies it issued
  *                   land before it exits) and the context stays usable; the
  *                   output and any write-back of that call are undefined.
+ *                   Prompts on state layers: a CTA's first tile of queries is
+ *                   not copied; the heads that wait for it keep their state.
  *                   0 restores normal operation.
  * Returns DATTN_EINVAL for a null handle or an unknown flag. */
 enum { DATTN_DEBUG_WITHHOLD_Q = 1 };
