@@ -125,7 +125,7 @@ lib.dattn_decode_noalloc.argtypes = [ctypes.POINTER(Config), _int, ctypes.POINTE
 lib.dattn_decode_noalloc.restype = _int
 lib.dattn_debug_config.argtypes = [_vp, _int, ctypes.c_uint]
 lib.dattn_debug_config.restype = _int
-DEBUG_WITHHOLD_Q = 1
+DEBUG_WITHHOLD_Q, DEBUG_WITHHOLD_KV = 1, 2
 
 EXPORTS = ("dattn_create", "dattn_append_kv", "dattn_decode", "dattn_verify", "dattn_commit", "dattn_prefill",
            "dattn_get_error", "dattn_error_string", "dattn_destroy", "dattn_decode_noalloc",

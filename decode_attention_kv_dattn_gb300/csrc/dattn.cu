@@ -78,7 +78,8 @@ struct dattn_handle {
   int32_t* sel_table = nullptr;
   int* sel_done = nullptr;
   std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
-  float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements and a note a CTA
+  float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements and a note a CTA,
+                                          // and two words
   int* err = nullptr;
   uint64_t wait_ns = kDefaultWaitNs;  // limit of the kernels' bounded waits
   int debug_flags = 0;                // dattn_debug_config
@@ -565,9 +566,12 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     }
     L.log_decay = nullptr;
   }
-  if (has_state &&
-      cudaMalloc(&h->sums, static_cast<size_t>(h->num_sms) * (2 * 16384 * sizeof(float) + 16)) != cudaSuccess)
-    return fail(DATTN_ECUDA);
+  if (has_state) {
+    const size_t notes = static_cast<size_t>(h->num_sms) * (2 * 16384 * sizeof(float) + 16);
+    if (cudaMalloc(&h->sums, notes + 2 * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMemset(reinterpret_cast<uint8_t*>(h->sums) + notes, 0, 2 * sizeof(int)) != cudaSuccess)
+      return fail(DATTN_ECUDA);
+  }
   if (sel_pitch > 0) {
     const size_t units = static_cast<size_t>(h->max_streams) * Hkv;
     h->max_selected = cfg->max_selected_pages;
@@ -658,8 +662,9 @@ void dattn_destroy(dattn_t* h) {
 }
 
 int dattn_debug_config(dattn_t* h, int flags, unsigned wait_limit_us) {
-  if (!h || (flags & ~DATTN_DEBUG_WITHHOLD_Q) != 0) return DATTN_EINVAL;
-  h->debug_flags = (flags & DATTN_DEBUG_WITHHOLD_Q) ? kDebugWithholdQ : 0;
+  if (!h || (flags & ~(DATTN_DEBUG_WITHHOLD_Q | DATTN_DEBUG_WITHHOLD_KV)) != 0) return DATTN_EINVAL;
+  h->debug_flags = ((flags & DATTN_DEBUG_WITHHOLD_Q) ? kDebugWithholdQ : 0) |
+                   ((flags & DATTN_DEBUG_WITHHOLD_KV) ? kDebugWithholdKV : 0);
   h->wait_ns = wait_limit_us ? static_cast<uint64_t>(wait_limit_us) * 1000ull : kDefaultWaitNs;
   return DATTN_OK;
 }

@@ -27,8 +27,10 @@ enum : int { ERR_INDEX = 1, ERR_TIMEOUT = 2, ERR_LENGTH = 4, ERR_RANGE = 8 };
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 // Testing aid (dattn_debug_config): the decode kernel's helper warp withholds
 // the first unit's rotated query, so the streaming warps' waits run out. Prompts of
-// state layers: a CTA's first Q tile is not copied.
+// state layers: a CTA's first Q tile is not copied, or, in the pass that sums what
+// the ranges contribute, its first K and V.
 constexpr int kDebugWithholdQ = 1;
+constexpr int kDebugWithholdKV = 2;
 
 // One layer's cache as the kernels see it.
 struct CacheView {
@@ -206,12 +208,13 @@ struct LinearArgs {
   const int32_t* count;        // prompt: [B]
   float* sums;                 // prompt: [2][num_sms][D, EB] a CTA's slot: its last piece's contribution to the
                                // state, then the state that the next CTA starts from; and the state that its
-                               // last unit starts from
+                               // last unit starts from. Behind them a note a CTA, and two words: whether this
+                               // call's sums gave up waiting, and the same for the main pass (zero between calls)
   int split;                   // prompt: units may be cut into ranges of chunks, by `ctas` CTAs (else one each)
   int ctas;
   int* err;
   uint64_t wait_ns;            // prompt: limit of the bounded waits
-  int debug_flags;             // prompt: kDebugWithholdQ
+  int debug_flags;             // prompt: kDebugWithholdQ, kDebugWithholdKV
 };
 
 struct AppendArgs {

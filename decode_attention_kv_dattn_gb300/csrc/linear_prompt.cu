@@ -282,6 +282,24 @@ struct Pieces {
   }
 };
 
+// What the scan knows of a CTA's slot: the unit that goes on in the next CTA (-1:
+// none), whether the slot holds a sum (1; 2 when it is from the unit's beginning)
+// and the decay over its tokens as hi + lo. Behind the slots and their copies.
+struct alignas(16) SlotNote {
+  int unit, kind;
+  float lam, lam_lo;
+};
+template <int D>
+__device__ __forceinline__ SlotNote* slot_notes(const LinearArgs& a) {
+  return reinterpret_cast<SlotNote*>(a.sums + static_cast<int64_t>(2) * a.ctas * D * Geo<D>::EB);
+}
+// Whether the sums gave up waiting: set by them, then moved on to the main pass by
+// the scan.
+template <int D>
+__device__ __forceinline__ int* gave_up(const LinearArgs& a) {
+  return reinterpret_cast<int*>(slot_notes<D>(a) + a.ctas);
+}
+
 // The main pass over a CTA's pieces.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid_constant__ LinearArgs a) {
@@ -611,6 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         src = a.sums + (static_cast<int64_t>(blockIdx.x - Gm::SLICES) * D + sd) * EB + se;
       else if (!p.last)
         src = a.sums + (static_cast<int64_t>(a.ctas + blockIdx.x) * D + sd) * EB + se;
+      // (sums that gave up waiting: the call has failed, and the cache's states
+      // stay as they are)
+      const bool lost = a.split && __ldcg(gave_up<D>(a) + 1);
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 y = *reinterpret_cast<const float4*>(src + e);
@@ -618,6 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         S[e + 1] = y.y;
         S[e + 2] = y.z;
         S[e + 3] = y.w;
+      }
+      if (lost) {
+        *abort_flag = 1;
+        break;
       }
       // (the terms of the last piece are read no more)
       if (cc > 0 && !warp_wait(B_SFREE, (cc - 1) & 1)) break;
@@ -862,18 +887,6 @@ struct SumGeo {
   static constexpr int T_COLS = 2 * ACC;
 };
 
-// What the scan knows of a CTA's slot: the unit that goes on in the next CTA (-1:
-// none), whether the slot holds a sum (1; 2 when it is from the unit's beginning)
-// and the decay over its tokens as hi + lo. Behind the slots and their copies.
-struct alignas(16) SlotNote {
-  int unit, kind;
-  float lam, lam_lo;
-};
-template <int D>
-__device__ __forceinline__ SlotNote* slot_notes(const LinearArgs& a) {
-  return reinterpret_cast<SlotNote*>(a.sums + static_cast<int64_t>(2) * a.ctas * D * Geo<D>::EB);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __grid_constant__ LinearArgs a) {
   using Gm = Geo<D>;
@@ -929,6 +942,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
         if (c >= kSumStages && !W.wait(R_FREE + st, (c / kSumStages - 1) & 1)) break;
         const uint32_t bar = bars + 8 * (R_FULL + st), dst = sbase + st * Sg::STAGE;
         const int tok = b * a.T + (k0 + c) * C;
+        if (c == 0 && (a.debug_flags & kDebugWithholdKV)) continue;
         mbar_arrive_expect_tx(bar, Sg::STAGE);
         for (int r = 0; r < Gm::DR; ++r) tma_load_3d(dst + r * 8192, &a.tmap_k, 64 * r, h, tok, bar, policy);
         for (int r = 0; r < Gm::ER; ++r)
@@ -969,7 +983,10 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
           tc::commit(bars + 8 * (R_DONE + ((c / kSumGroup) & 1)));
       }
       if (lead) tc::commit(bars + 8 * R_FINAL);
-      if (!mbar_wait_bounded(bars + 8 * R_FINAL, 0) && lead) raise_error(a.err, ERR_TIMEOUT);
+      if (!mbar_wait_bounded(bars + 8 * R_FINAL, 0) && lead) {
+        *abort_flag = 1;
+        raise_error(a.err, ERR_TIMEOUT);
+      }
     }
     __syncwarp();
   } else {
@@ -1052,6 +1069,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
     tc::fence_after();
     tc::dealloc(tmem, Sg::T_COLS);
   }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(gave_up<D>(a), 1);
 }
 
 // The states at the CTAs' starts from their sums (and a copy of the state that
@@ -1071,6 +1089,12 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
   const int c = blockIdx.y, NC = a.ctas, slice = c % SL;  // the CTA, and those after it on its slice
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && c == 0 && threadIdx.x == 0) {
+    // what the sums say of this call, for its main pass; the next call's begin anew
+    int* f = gave_up<D>(a);
+    f[1] = f[0];
+    f[0] = 0;
+  }
   const SlotNote* notes = slot_notes<D>(a) + c;
   const SlotNote first = notes[0];
   if (first.kind != 2) return;

@@ -368,9 +368,13 @@ DATTN_API int dattn_get_error(dattn_t* h, dattn_stream_t stream);
  *                   output and any write-back of that call are undefined.
  *                   Prompts on state layers: a CTA's first tile of queries is
  *                   not copied; the heads that wait for it keep their state.
+ *                   DATTN_DEBUG_WITHHOLD_KV: in each later prompt on a state
+ *                   layer that is cut into ranges, the pass that sums what the
+ *                   ranges contribute does not copy a range's first keys and
+ *                   values; every state of the call stays as it was.
  *                   0 restores normal operation.
  * Returns DATTN_EINVAL for a null handle or an unknown flag. */
-enum { DATTN_DEBUG_WITHHOLD_Q = 1 };
+enum { DATTN_DEBUG_WITHHOLD_Q = 1, DATTN_DEBUG_WITHHOLD_KV = 2 };
 DATTN_API int dattn_debug_config(dattn_t* h, int flags, unsigned wait_limit_us);
 
 /* Static description of a status code. */
