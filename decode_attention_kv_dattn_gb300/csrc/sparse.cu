@@ -106,15 +106,18 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SummarizeArgs a) {
   const CacheView& c = a.c;
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  const int job = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int64_t job = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
   const int cnt = a.count[b], start = a.start_index[b];
   if (cnt < 0 || cnt > a.max_tokens || start < 0 || cnt > INT32_MAX - start) {
     if (job == 0 && lane == 0) raise_error(a.err, ERR_INDEX);
     return;
   }
-  const int i = job / a.Hkv, h = job - i * a.Hkv;
-  const int p = start / c.P + i;
-  if (p >= (start + cnt) / c.P) return;
+  const int i = static_cast<int>(job / a.Hkv), h = static_cast<int>(job - static_cast<int64_t>(i) * a.Hkv);
+  const int first = start / c.P, done = (start + cnt) / c.P;
+  // (the grid covers a table's pages, whatever max_tokens says; the others are none)
+  if (job == 0 && lane == 0 && first < done && done > c.bt_stride) raise_error(a.err, ERR_INDEX);
+  if (i >= done - first) return;
+  const int p = first + i;
   const int pg = p < c.bt_stride ? c.block_table[static_cast<int64_t>(b) * c.bt_stride + p] : -1;
   if (pg < 0 || pg >= c.n_rows) {
     if (lane == 0) raise_error(a.err, ERR_INDEX);
@@ -1519,8 +1522,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? 4 : 2) page_attend_ker
 }  // namespace
 
 cudaError_t launch_summarize(const SummarizeArgs& a, int D, cudaStream_t s) {
-  const int64_t jobs = (static_cast<int64_t>(a.max_tokens) + a.c.P - 1) / a.c.P * a.Hkv;
-  const dim3 grid(static_cast<unsigned>((jobs + 7) / 8), a.B);
+  const int64_t pages = std::min<int64_t>((static_cast<int64_t>(a.max_tokens) + a.c.P - 1) / a.c.P, a.c.bt_stride);
+  const dim3 grid(static_cast<unsigned>((pages * a.Hkv + 7) / 8), a.B);
   auto k = D == 128 ? (a.f8 ? summarize_kernel<128, true> : summarize_kernel<128, false>)
                     : (a.f8 ? summarize_kernel<256, true> : summarize_kernel<256, false>);
   return launch_pdl(k, grid, dim3(256), 0, s, a);
