@@ -211,9 +211,12 @@ class Handle:
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, layers, max_streams,
                  max_context=0, max_verify_rows=0, device=None, max_selected_pages=0):
-        if device is None:
-            device = torch.cuda.current_device()
-        self.device = device = device if isinstance(device, int) else torch.device(device).index or 0
+        if device is not None and not isinstance(device, int):
+            device = torch.device(device)
+            if device.type != "cuda":
+                raise ValueError(f"a handle is on a CUDA device, not {device}")
+            device = device.index  # (None: the current one)
+        self.device = device = torch.cuda.current_device() if device is None else device
         # QK-norm weights (layer keys "q_norm", "k_norm", "norm_eps") and state
         # layers' decays ("log_decay" [Hkv]): host arrays the config points at,
         # kept alive with it (dattn_create copies them; decode_noalloc reads the
