@@ -199,6 +199,10 @@ def state_cache(state, stream_rows=None) -> Cache:
     The descriptor holds the tensors it points to, so they live as long as it does."""
     if state.dtype != torch.float32:
         raise TypeError("a state layer's cache is fp32")
+    if state.dim() != 4 or state.shape[2] != state.shape[3]:
+        raise ValueError(f"state: shape {tuple(state.shape)}, expected (rows, Hkv, D, D)")
+    if stream_rows is not None and stream_rows.dtype != torch.int32:
+        raise TypeError("stream_rows: int32")
     c = Cache(_ptr(state), None, state.shape[0], None, None, _ptr(stream_rows), None, 0, None)
     c._tensors = (state, stream_rows)
     return c
@@ -253,6 +257,31 @@ class Handle:
 
     __del__ = close
 
+    def _kind(self, layer):
+        return self._layers[layer].cache_kind if 0 <= layer < len(self._layers) else None
+
+    def _check_state(self, layer, cache, streams):
+        """A state layer's call has states of this handle's heads, and a row for each stream."""
+        if self._kind(layer) != CACHE_STATE or not hasattr(cache, "_tensors"):
+            return
+        state, rows = cache._tensors[0], cache._tensors[-1]
+        want = (self.config.num_kv_heads, self.config.head_dim, self.config.head_dim)
+        if state.dtype != torch.float32 or tuple(state.shape[1:]) != want:
+            raise ValueError(f"a state layer's cache: {state.dtype} {tuple(state.shape)}, expected fp32 (rows, "
+                             f"{', '.join(map(str, want))})")
+        if rows is not None and rows.numel() < streams:
+            raise ValueError(f"stream_rows: {rows.numel()} rows for {streams} streams")
+
+    def _check_summary(self, layer, cache, summary):
+        """A paged layer's summaries: one for each page and KV head."""
+        if self._kind(layer) != CACHE_PAGED or summary is None:
+            return
+        want = (self.config.num_kv_heads, self.config.head_dim)
+        if summary.dtype != torch.bfloat16:
+            raise TypeError(f"summary: {summary.dtype}, expected bf16")
+        if summary.dim() != 3 or tuple(summary.shape[1:]) != want or summary.shape[0] < cache.n_rows:
+            raise ValueError(f"summary: shape {tuple(summary.shape)}, expected ({cache.n_rows} pages, {want[0]}, {want[1]})")
+
     def append_kv(self, layer, cache: Cache, k, v, start_index, count, start_pos=None,
                   rotate=True, stream=None):
         """k, v: [B, T, Hkv, D] bf16; start_index, count (, start_pos): [B] int32."""
@@ -265,6 +294,7 @@ class Handle:
                write_back=True, stream=None):
         """q [B, Hq, D], k_new/v_new [B, Hkv, D] bf16; pos [B] int32; out [B, Hq, D] fp32;
         gate [B, Hq] bf16 or None."""
+        self._check_state(layer, cache, q.shape[0])
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
@@ -277,6 +307,7 @@ class Handle:
         [pages, Hkv, D] bf16 as `summarize` keeps it; selected [B, Hkv, num_pages] int32
         receives the pages (ascending, then -1) if given. The handle needs
         max_selected_pages >= num_pages."""
+        self._check_summary(layer, cache, summary)
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         if selected is not None and (selected.dtype != torch.int32 or selected.numel() !=
@@ -290,6 +321,9 @@ class Handle:
         """Summaries (bf16 means of the stored keys, [pages, Hkv, D]) of the pages that the
         new tokens [start_index, start_index + count) of each row completed; start_index,
         count: [B] int32, count <= max_tokens."""
+        self._check_summary(layer, cache, summary)
+        if start_index.dtype != torch.int32 or count.dtype != torch.int32 or count.numel() != start_index.shape[0]:
+            raise ValueError("start_index, count: int32 [B]")
         _check(lib.dattn_summarize(self._h, layer, ctypes.byref(cache), _ptr(summary), start_index.shape[0],
                                    int(max_tokens), _ptr(start_index), _ptr(count), _stream_ptr(stream, self.device)),
                "dattn_summarize")
@@ -315,6 +349,7 @@ class Handle:
     def prefill(self, layer, cache: Cache, q, k, v, count, start_pos, out, gate=None, stream=None):
         """Ragged prefill: q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16, count/start_pos [S] int32,
         out [S, T, Hq, D] fp32 (rows t < count written), gate [S, T, Hq] bf16 or None."""
+        self._check_state(layer, cache, q.shape[0])
         _check(lib.dattn_prefill(self._h, layer, ctypes.byref(cache), q.shape[0], q.shape[1], _ptr(q), _ptr(k),
                                  _ptr(v), _ptr(gate), _ptr(count), _ptr(start_pos), _ptr(out),
                                  _stream_ptr(stream, self.device)), "dattn_prefill")
