@@ -1630,15 +1630,7 @@ cudaError_t encode_linear_maps(LinearArgs& a, int D) {
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
-  const cuuint64_t heads = static_cast<cuuint64_t>(a.Hkv) * a.G;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), heads, tokens};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 4, heads * D * 4};
-  const cuuint32_t box[3] = {16, a.G > 1 ? 2u : 1u, a.G > 1 ? 16u : 32u};
-  const cuuint32_t estride[3] = {1, 1, 1};
-  const CUresult r = fn(&a.tmap_o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.out, dims, strides, box, estride,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return cudaSuccess;
 }
 
 cudaError_t launch_decode(const DecodeArgs& args, int D, int ctas, cudaStream_t s, bool pdl) {

@@ -188,8 +188,6 @@ struct LinearArgs {
   CUtensorMap tmap_q;          // prompt: q, k, v as (D, heads, B * T) bf16, boxes of (64 dims, 2 heads for q
   CUtensorMap tmap_k;          // (1 where G is 1) or 1, 64 tokens), 128-byte swizzled
   CUtensorMap tmap_v;
-  CUtensorMap tmap_o;          // prompt: out as (D, Hq, B * T) fp32, boxes of 32 rows of 16 dims (2 heads, 16 tokens
-                               // each; 32 tokens where G is 1)
   float* state;                // [n_rows, Hkv, D, D], row = key dim
   int n_rows;
   const int32_t* stream_rows;  // [B] or null

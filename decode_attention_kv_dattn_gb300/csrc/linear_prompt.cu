@@ -7,17 +7,20 @@
 //   S'  = lam^n S + sum_j lam^(n-1-j) k_j v_j^T
 // as four products, each an fp32 sum in tensor memory:
 //   A  = Q K^T          rows: 64 tokens x 2 query heads (or 1), columns: tokens
-//   O1 = Q S            S as two bf16 terms (hi + lo: 16 significant bits)
-//   O2 = P V            P = A masked and decayed, as two bf16 terms, from tensor
+//   O1 = Q S            S as three bf16 terms (24 significant bits)
+//   O2 = P V            P = A masked and decayed, as three bf16 terms, from tensor
 //                       memory
-//   dS = K^T W          W = lam^(n-1-j) v_j as two bf16 terms
+//   dS = K^T W          W = lam^(n-1-j) v_j as three bf16 terms
 // q, k and v are bf16 and enter exactly; the state itself stays in fp32, in
-// registers. Two bf16 terms keep an operand to 2^-17: the outputs' error is 2.8e-6
-// of their size; a third term would take half as many MMAs again
-// and, for S, shared memory that is not there.
+// registers. Three terms keep the operands' 24 bits, so that the error is that of
+// fp32 sums: 2.7e-7 of the outputs' size (root mean squares; 5.4e-7 over 1 x 32,768
+// tokens). With two (2^-17 of each operand) it was 2.8e-6, 11 to 14 times what the
+// same products in fp32 leave, in 137 us for 1 x 32,768 tokens (161 now) and 177
+// for 16 ragged prompts (216): a third more MMAs and terms, and S's third term in
+// the place of a second Q tile and a second K, whose copies are now waited for.
 //
 // Work split. A unit is one (stream, KV head, slice): EB of the state's columns
-// (all 128 at D = 128, 64 of 256 at D = 256: what S's two terms leave room for in
+// (all 128 at D = 128, 64 of 256 at D = 256: what S's terms leave room for in
 // shared memory beside Q, K, V and W). Where units are many, or their streams
 // short or alike, a CTA has one unit. Otherwise the heads' chunks are laid end to
 // end and one CTA an SM takes an equal range of them, worked out on the device
@@ -25,8 +28,8 @@
 // what each CTA's last unit contributes to the state (for the CTA after it), a
 // second carries the states along, and the main kernel starts each range from
 // its state. At D = 256 four CTAs have the same range, a slice each: they read
-// the same Q and K at the same time (16 ragged prompts: 216 MB from memory; 671
-// MB, and 26 us more, when each had a range of its own).
+// the same Q and K at the same time (16 ragged prompts: 214 MB from memory; 671
+// MB when each had a range of its own).
 //
 // Roles: 16 state warps (W, P, and the state: dS in, S's terms out), 8 row warps
 // (the epilogue), one warp that copies (TMA, 128-byte swizzle) and one that
@@ -35,16 +38,17 @@
 // waits until the outputs are read. 832 threads leave 72 registers each, and the
 // roles' loops are kept small: when they missed the instruction cache, that was
 // 43% of the stalls. The MMA warp walks its loops as a whole: descriptors worked
-// out by one thread took it 60 - 120 ns an MMA (1 x 32,768 tokens 157 us, 149 so).
+// out by one thread took it 60 - 120 ns an MMA.
 //
-// Bound by a chunk's chain of dependent steps, not by a unit: at D = 128 3.6 us a
-// chunk and Q tile - the state warps' W 0.9, P 0.9 and the state's update and
-// terms 1.1; beside it the row warps' 2.4 for the outputs - of which the MMAs
-// take 1.3 us of the tensor pipe (25 ns each at N = 64, 34 at N = 128: their
-// operands' way from shared memory) and the copies 2.9 us at the memory's rate.
-// 1 x 32,768 tokens, 16 / 8 heads of 128: 136 us = sums 32, scan 8, main 104
-// (505 MB of it from and to memory, 4.8 TB/s), partly beside one another. 16
-// streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 176 us = 33, 8, 146.
+// Bound by a chunk's chain of dependent steps, not by a unit: 4.5 us a chunk at D =
+// 128 and two query heads a KV head, 6.0 at D = 256 and four (two Q tiles). The
+// state warps make W, P and S's terms one after another, and a Q tile is copied
+// once Q S has read the one before; beside them the row warps' outputs. Tensor
+// pipe 40% and 45% of the main pass; at the memory's rate the chunk's copies take
+// 2.9 us at D = 128. 1 x 32,768 tokens, 16 / 8 heads of 128: 161 us, under ncu sums
+// 36, scan 11, main 124 (503 MB of it from and to memory, 4.1 TB/s), partly beside
+// one another. 16 streams of 512 - 4,096 tokens, 8 / 2 heads of 256: 216 us, 41,
+// 10, 178.
 //
 // An infinity or no number in v would reach earlier tokens of its chunk (its
 // weight in P is 0, and 0 times it is no number): the state warps replace it by
@@ -63,27 +67,26 @@ constexpr int C = kLinearChunk;
 constexpr int kStateWarps = 16, kRowWarps = 8;
 constexpr int kTmaWarp = 24, kMmaWarp = 25;
 constexpr int kThreads = 832;
+constexpr int kTerms = 3;      // bf16 terms of an fp32 operand
 constexpr int kPieceCost = 1;  // a unit's share of a CTA's range, in chunks, besides its own
 
 enum : int {
-  B_KFULL,              // [2] a chunk's K has landed
-  B_KFREE = B_KFULL + 2,  // [2] every MMA that reads it has completed
-  B_VFULL = B_KFREE + 2,  // [2] the same for V
+  B_KFULL,              // a chunk's K has landed
+  B_KFREE,              // every MMA that reads it has completed
+  B_VFULL,              // [2] the same for V
   B_VFREE = B_VFULL + 2,
   B_WREADY = B_VFREE + 2,  // W (and the zeroed rows of a short chunk) written
-  B_SREADY,             // the state's two terms written
+  B_SREADY,             // the state's terms written
   B_SFREE,              // every Q S of a chunk complete
   B_ADONE,              // Q K^T complete
-  B_AFREE,              // ... and read
   B_PREADY,             // P written
   B_ODONE,              // Q S and P V complete
   B_OFREE,              // ... and read
   B_DSDONE,             // K^T W complete
   B_FINAL,
-  B_STAGED,             // [2] a tile's outputs have left its Q
-  B_QFULL = B_STAGED + 2,  // [2] a Q tile has landed (an arrival for each two regions)
-  B_QFREE = B_QFULL + 2,   // [3] the MMAs that read two regions of Q completed
-  B_COUNT = B_QFREE + 3
+  B_QFULL,              // [2] a Q tile has landed (an arrival for each two regions)
+  B_QFREE = B_QFULL + 2,  // [2] the MMAs that read two regions of Q completed
+  B_COUNT = B_QFREE + 2
 };
 
 template <int D>
@@ -91,29 +94,32 @@ struct Geo {
   static constexpr int EB = D == 128 ? 128 : 64;   // state columns of a CTA
   static constexpr int SLICES = D / EB;
   static constexpr int ER = EB / 64, DR = D / 64;  // 64-element regions
-  static constexpr int QP = D == 128 ? 2 : 3;      // pairs of Q's regions in shared memory (a tile has DP): the next
-  static constexpr int DP = DR / 2;                // tile's land while this one's are used
-  static constexpr int KS = D == 128 ? 2 : 1;      // chunks of K
+  static constexpr int DP = DR / 2;                // pairs of Q's regions: one tile, each pair handed back by itself
+  static constexpr int VS = D == 128 ? 2 : 1;      // chunks of V
   static constexpr int Q_REGION = 16384;           // [128 rows][128 bytes]
   static constexpr int Q_PAIR = 2 * Q_REGION;
   static constexpr int K_TILE = DR * 8192;         // [region][64 rows][128 bytes]
   static constexpr int V_TILE = ER * 8192;
   static constexpr int S_PLANE = ER * D * 128;     // [region][D rows][128 bytes]
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + QP * Q_PAIR;
-  static constexpr int V_OFF = K_OFF + KS * K_TILE;
-  static constexpr int W_OFF = V_OFF + 2 * V_TILE;  // hi, lo
-  static constexpr int S_OFF = W_OFF + 2 * V_TILE;  // hi, lo
-  static constexpr int BAR_OFF = S_OFF + 2 * S_PLANE;
+  static constexpr int K_OFF = Q_OFF + DP * Q_PAIR;
+  static constexpr int V_OFF = K_OFF + K_TILE;
+  static constexpr int W_OFF = V_OFF + VS * V_TILE;      // the terms, the largest first
+  static constexpr int S_OFF = W_OFF + kTerms * V_TILE;  // the same
+  static constexpr int BAR_OFF = S_OFF + kTerms * S_PLANE;
   static constexpr int MISC_OFF = BAR_OFF + 8 * B_COUNT;
   static constexpr int BAD_OFF = (MISC_OFF + 16 + 15) / 16 * 16;  // [2][EB]: 64 chunk + 63 - token of the first
                                                                   // token without a number in a column
   static constexpr int FLAG_OFF = BAD_OFF + 2 * EB * 4;           // [2] latest chunk with such a token
   static constexpr int SMEM = FLAG_OFF + 16 + 1024;               // (1024: alignment)
-  // tensor memory columns. At D = 256 the products with S's two terms have their
-  // own columns: one MMA of N = 128 then does both.
-  static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = 256, T_DS = 256 + EB;
+  // tensor memory columns, all 512. At D = 256 the products with S's terms have
+  // their own columns: one MMA of N = 192 then does all three. P's first two terms
+  // are beside A, the third is in A's place, each warp's 16 columns over what it
+  // has read of A.
+  static constexpr int T_A = 0, T_P = 64, T_O1 = 128, T_O2 = T_O1 + (D == 128 ? 128 : 192), T_DS = T_O2 + EB;
   static constexpr int T_COLS = 512;
+  static_assert(T_DS + D / 128 * EB == T_COLS);
+  static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
 // A bounded wait that did not succeed at once (out of line: the roles' loops have
@@ -156,23 +162,15 @@ __device__ __forceinline__ void st_8(float* p, const float (&x)[8], bool wide) {
   }
 }
 
+// Brings the box at element coordinates (x, y, z) of the tensor map to the L2 cache.
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y),
+               "r"(z)
+               : "memory");
+}
+
 // Limit of the wait for copies that may or may not be in flight.
 constexpr uint64_t kDrainNs = 1000000;
-
-// Shared memory to the box at element coordinates (x, y, z) of the tensor map, as
-// part of the thread's current bulk group; and the groups' ends: all but the
-// latest N have been read from shared memory, or all have been written.
-__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
-               "r"(src), "r"(x), "r"(y), "r"(z)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void tma_stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Two floats in one instruction: a b + c and a b.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -192,11 +190,29 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
-// Two floats as packed bf16 hi terms and what is left as lo terms.
-__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x.x, x.y);
-  const float2 left = fma2(make_float2(bf16_lo(hi), bf16_hi(hi)), make_float2(-1.f, -1.f), x);
-  lo = pack_bf16x2(left.x, left.y);
+// Two floats as three packed bf16 terms, each what the ones before it leave
+// (differences are exact): 24 bits together.
+__device__ __forceinline__ void split3(float2 x, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  t0 = pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(bf16_lo(t0), bf16_hi(t0)), make_float2(-1.f, -1.f), x);
+  t1 = pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(bf16_lo(t1), bf16_hi(t1)), make_float2(-1.f, -1.f), x);
+  t2 = pack_bf16x2(x.x, x.y);
+}
+// Eight floats as 16 bytes of each term.
+__device__ __forceinline__ void split3(const float (&x)[8], uint4 (&t)[kTerms]) {
+  split3(make_float2(x[0], x[1]), t[0].x, t[1].x, t[2].x);
+  split3(make_float2(x[2], x[3]), t[0].y, t[1].y, t[2].y);
+  split3(make_float2(x[4], x[5]), t[0].z, t[1].z, t[2].z);
+  split3(make_float2(x[6], x[7]), t[0].w, t[1].w, t[2].w);
+}
+// The same of eight bf16 values times w.
+__device__ __forceinline__ void split3(uint4 y, float w, uint4 (&t)[kTerms]) {
+  const float2 w2 = make_float2(w, w);
+  split3(mul2(make_float2(bf16_lo(y.x), bf16_hi(y.x)), w2), t[0].x, t[1].x, t[2].x);
+  split3(mul2(make_float2(bf16_lo(y.y), bf16_hi(y.y)), w2), t[0].y, t[1].y, t[2].y);
+  split3(mul2(make_float2(bf16_lo(y.z), bf16_hi(y.z)), w2), t[0].z, t[1].z, t[2].z);
+  split3(mul2(make_float2(bf16_lo(y.w), bf16_hi(y.w)), w2), t[0].w, t[1].w, t[2].w);
 }
 
 // The chunks of stream b (0, reported, for a row without a state or a count out
@@ -240,8 +256,8 @@ __device__ __forceinline__ Place range_start(const LinearArgs& a, const int* cum
 // returns whether the units are worth cutting. In chunks' times: uncut, the
 // longest unit's chunks; cut, everything spread evenly, with 40% more for the
 // sums and 2.5 chunks' time for what is launched between. Measured, cut / uncut:
-// 16 streams of 512 - 4,096 tokens (128 units of 256) 178 / 277 us, 16 x 4,096
-// 333 / 312, 4 x 512 (32 units of 128) 30.1 / 33.4, 1 x 32,768 (8) 137 / 1,623.
+// 16 streams of 512 - 4,096 tokens (128 units of 256) 216 / 350 us, 16 x 4,096
+// 416 / 391, 4 x 512 (32 units of 128) 32.2 / 39.0, 1 x 32,768 (8) 160 / 1,973.
 template <int NT>
 __device__ __forceinline__ bool sum_weights(const LinearArgs& a, int* cum, int groups, bool report) {
   __shared__ int longest;
@@ -343,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY || i == B_AFREE || i == B_PREADY ? kStateWarps
-                              : i == B_OFREE || i == B_STAGED || i == B_STAGED + 1              ? kRowWarps
-                              : i == B_QFULL || i == B_QFULL + 1                                ? Gm::DP
-                                                                                                : 1);
+      mbar_init(bars + 8 * i, i == B_WREADY || i == B_SREADY || i == B_PREADY ? kStateWarps
+                              : i == B_OFREE                                  ? kRowWarps
+                              : i == B_QFULL || i == B_QFULL + 1              ? Gm::DP
+                                                                              : 1);
     reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[0] = reinterpret_cast<int*>(smem + Gm::FLAG_OFF)[1] = -1;
     for (int i = 0; i < 2 * EB; ++i) reinterpret_cast<int*>(smem + Gm::BAD_OFF)[i] = -1;
     fence_mbar_init();
@@ -378,9 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
           const int tok = p.b * a.T + k * C;
+          // Q has one place, so a tile's copy waits until the tile before is done with
+          // it: its data come to the L2 cache meanwhile (8 prompts of 1,000 tokens, 24 /
+          // 4 heads of 256, 148 us, 162 without; 16 ragged ones 217, 229; at D = 128,
+          // where a copy is half as long, 163, 162)
+          if constexpr (D == 256)
+            if (cc > 0)
+              for (int mt = 0; mt < tiles; ++mt)
+                for (int r = 0; r < Gm::DR; ++r) tma_prefetch_3d(&a.tmap_q, 64 * r, p.h * G + mt * hpt, tok);
           {
-            const int st = cc & 1;
-            if (cc >= 2) ok = W.wait(B_VFREE + st, ((cc >> 1) - 1) & 1);
+            const int st = cc % Gm::VS;
+            if (cc >= Gm::VS) ok = W.wait(B_VFREE + st, (cc / Gm::VS - 1) & 1);
             if (!ok) break;
             const uint32_t bar = bars + 8 * (B_VFULL + st);
             mbar_arrive_expect_tx(bar, Gm::V_TILE);
@@ -389,25 +413,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
                           bar, policy);
           }
           {
-            const int st = cc % Gm::KS;
-            if (cc >= Gm::KS) ok = W.wait(B_KFREE + st, (cc / Gm::KS - 1) & 1);
+            if (cc > 0) ok = W.wait(B_KFREE, (cc - 1) & 1);
             if (!ok) break;
-            const uint32_t bar = bars + 8 * (B_KFULL + st);
+            const uint32_t bar = bars + 8 * B_KFULL;
             mbar_arrive_expect_tx(bar, Gm::K_TILE);
             for (int r = 0; r < Gm::DR; ++r)
-              tma_load_3d(sbase + Gm::K_OFF + st * Gm::K_TILE + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
+              tma_load_3d(sbase + Gm::K_OFF + r * 8192, &a.tmap_k, 64 * r, p.h, tok, bar, policy);
           }
           for (int mt = 0; mt < tiles && ok; ++mt)
             for (int i = 0; i < Gm::DP; ++i, ++qp) {
-              const int slot = qp % Gm::QP, t = qp / Gm::DP;
-              if (qp >= Gm::QP) {
-                const int was = qp - Gm::QP, tw = was / Gm::DP;  // its pair before, and that one's tile
-                ok = W.wait(B_QFREE + slot, (qp / Gm::QP - 1) & 1) &&
-                     (was % Gm::DP < Gm::DP - 1 || W.wait(B_STAGED + (tw & 1), (tw >> 1) & 1));
-              }
+              const int t = qp / Gm::DP;
+              if (t > 0) ok = W.wait(B_QFREE + i, (t - 1) & 1);
               if (!ok) break;
               if (t == 0 && (a.debug_flags & kDebugWithholdQ)) continue;
-              const uint32_t bar = bars + 8 * (B_QFULL + (t & 1)), dst = sbase + Gm::Q_OFF + slot * Gm::Q_PAIR;
+              const uint32_t bar = bars + 8 * (B_QFULL + (t & 1)), dst = sbase + Gm::Q_OFF + i * Gm::Q_PAIR;
               mbar_arrive_expect_tx(bar, 2 * static_cast<uint32_t>(hpt) * 8192u);
               for (int r = 0; r < 2; ++r)
                 tma_load_3d(dst + r * Gm::Q_REGION, &a.tmap_q, 64 * (2 * i + r), p.h * G + mt * hpt, tok, bar, policy);
@@ -415,14 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
         }
       }
       // Copies still in flight exist only when a role gave up: they land
-      // before the CTA exits. They are those of the last two chunks (K: KS) and
-      // tiles behind the one that was not requested any more, or in part: a wait
-      // for a place's release that ran out says nothing of the copy into it.
+      // before the CTA exits. They are those of the chunks and the tile behind the
+      // one that was not requested any more, or in part: a wait for a place's
+      // release that ran out says nothing of the copy into it.
       if (*abort_flag) {
-        for (int i = max(0, cc - 2); i <= cc; ++i) mbar_wait_bounded(bars + 8 * (B_VFULL + (i & 1)), (i >> 1) & 1, kDrainNs);
-        for (int i = max(0, cc - Gm::KS); i <= cc; ++i)
-          mbar_wait_bounded(bars + 8 * (B_KFULL + i % Gm::KS), (i / Gm::KS) & 1, kDrainNs);
-        for (int t = max(0, qp / Gm::DP - 2); t <= qp / Gm::DP; ++t)
+        for (int i = max(0, cc - Gm::VS); i <= cc; ++i)
+          mbar_wait_bounded(bars + 8 * (B_VFULL + i % Gm::VS), (i / Gm::VS) & 1, kDrainNs);
+        for (int i = max(0, cc - 1); i <= cc; ++i) mbar_wait_bounded(bars + 8 * B_KFULL, i & 1, kDrainNs);
+        for (int t = max(0, qp / Gm::DP - 1); t <= qp / Gm::DP; ++t)
           mbar_wait_bounded(bars + 8 * (B_QFULL + (t & 1)), (t >> 1) & 1, kDrainNs);
       }
     }
@@ -434,50 +453,50 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     {
       const bool lead = tc::elect();
       constexpr uint32_t id_a = tc::f16_idesc_ab(128, C, 1, false, false);
-      constexpr uint32_t id_q = tc::f16_idesc_ab(128, 128, 1, false, true);
+      constexpr uint32_t id_q = tc::f16_idesc_ab(128, D == 128 ? 128 : 192, 1, false, true);
       constexpr uint32_t id_o = tc::f16_idesc_ab(128, EB, 1, false, true);
       constexpr uint32_t id_s = tc::f16_idesc_ab(128, EB, 1, true, true);
       // A descriptor is a constant and the start address in 16-byte units.
       const uint64_t k_major = tc::sw128_desc(0, 16, 1024);
       const uint64_t mn_major = tc::sw128_desc(0, 8192, 1024);
-      // S as an N = 128 operand: at D = 128 one term's two regions of 64 value
-      // dims, at D = 256 both terms' one region
+      // S as an operand: at D = 128 one term's two regions of 64 value dims (N =
+      // 128), at D = 256 the three terms' one region (N = 192). Sums take the small
+      // terms first: they round as often as there are MMAs, by what is there then.
       const uint64_t s_major = tc::sw128_desc(0, D == 128 ? D * 128 : Gm::S_PLANE, 1024);
       auto at = [&](uint64_t desc, uint32_t addr) { return desc + (addr >> 4); };
       // dS = K^T W
-      auto issue_ds = [&](uint32_t kt, int cc) {
+      auto issue_ds = [&](uint32_t kt) {
 #pragma unroll 1
         for (int m = 0; m < D / 128; ++m) {
           const uint64_t kd = at(mn_major, kt + m * 16384), wd = at(mn_major, sbase + Gm::W_OFF);
           const uint32_t d = tmem + Gm::T_DS + m * EB;
           if (lead)
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) {
-              tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0);
-              tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
-            }
+            for (int x = kTerms - 1; x >= 0; --x)
+#pragma unroll
+              for (int kk = 0; kk < C / 16; ++kk)
+                tc::mma(d, kd + 128 * kk, wd + 128 * kk + x * (Gm::V_TILE / 16), id_s, x < kTerms - 1 || kk > 0);
         }
         if (lead) tc::commit(bars + 8 * B_DSDONE);
-        if (tiles == 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+        if (tiles == 1 && lead) tc::commit(bars + 8 * B_KFREE);
       };
       bool ok = true;
       int cc = 0, t = 0;  // chunks and Q tiles so far
       Pieces p = all;
       while (ok && p.next()) {
         for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
-          const int st = cc & 1;
-          const uint32_t vt = sbase + Gm::V_OFF + st * Gm::V_TILE;
-          const uint32_t kt = sbase + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
-          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
+          const int st = cc % Gm::VS;
+          const uint32_t vt = sbase + Gm::V_OFF + st * Gm::V_TILE, kt = sbase + Gm::K_OFF;
+          ok = warp_wait(B_KFULL, cc & 1);
           if (!ok) break;
           for (int mt = 0; mt < tiles && ok; ++mt, ++t) {
-            // A = Q K^T
-            ok = (t == 0 || warp_wait(B_AFREE, (t - 1) & 1)) && warp_wait(B_QFULL + (t & 1), (t >> 1) & 1);
+            // A = Q K^T (over the last tile's third term of P, so behind its P V)
+            ok = (t == 0 || warp_wait(B_ODONE, (t - 1) & 1)) && warp_wait(B_QFULL + (t & 1), (t >> 1) & 1);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll 1
             for (int i = 0; i < Gm::DP; ++i) {
-              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + (t * Gm::DP + i) % Gm::QP * Gm::Q_PAIR);
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + i * Gm::Q_PAIR);
               const uint64_t kd = at(k_major, kt + i * 16384);
               if (lead)
 #pragma unroll
@@ -487,17 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             }
             if (lead) tc::commit(bars + 8 * B_ADONE);
             // (dS went before)
-            if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_KFREE + cc % Gm::KS));
+            if (tiles > 1 && mt == tiles - 1 && lead) tc::commit(bars + 8 * B_KFREE);
             // At D = 128, where the outputs of the tile before are still being read,
-            // dS goes first (1 x 32,768 tokens 136 us, 138 between Q S and P V, 142
-            // behind P V); at D = 256 last (16 ragged prompts 178 us, 182 ahead of P V).
+            // dS goes first; at D = 256 last (16 ragged prompts 230 us, 246 first).
             // W comes with the chunk's zeroed rows, which P V wants too.
             if constexpr (D == 128)
               if (mt == 0) {
                 ok = warp_wait(B_WREADY, cc & 1);
                 if (!ok) break;
                 tc::fence_after();
-                issue_ds(kt, cc);
+                issue_ds(kt);
               }
             // O1 = Q S
             ok = (mt > 0 || warp_wait(B_SREADY, cc & 1)) && (t == 0 || warp_wait(B_OFREE, (t - 1) & 1));
@@ -505,17 +523,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             tc::fence_after();
 #pragma unroll 1
             for (int i = 0; i < Gm::DP; ++i) {
-              const int slot = (t * Gm::DP + i) % Gm::QP;
-              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + slot * Gm::Q_PAIR);
+              const uint64_t qd = at(k_major, sbase + Gm::Q_OFF + i * Gm::Q_PAIR);
               const uint64_t sd = at(s_major, sbase + Gm::S_OFF + i * 16384);
               if (lead) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                  const uint64_t q = qd + (kk >> 2) * (Gm::Q_REGION / 16) + 2 * (kk & 3), x = sd + 128 * kk;
-                  tc::mma(tmem + Gm::T_O1, q, x, id_q, i > 0 || kk > 0);
-                  if constexpr (D == 128) tc::mma(tmem + Gm::T_O1, q, x + Gm::S_PLANE / 16, id_q, true);
-                }
-                tc::commit(bars + 8 * (B_QFREE + slot));
+                for (int x = D == 128 ? kTerms - 1 : 0; x >= 0; --x)
+#pragma unroll
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc::mma(tmem + Gm::T_O1, qd + (kk >> 2) * (Gm::Q_REGION / 16) + 2 * (kk & 3),
+                            sd + 128 * kk + x * (Gm::S_PLANE / 16), id_q, i > 0 || kk > 0 || (D == 128 && x < kTerms - 1));
+                tc::commit(bars + 8 * (B_QFREE + i));
               }
             }
             if (mt == tiles - 1 && lead) tc::commit(bars + 8 * B_SFREE);
@@ -532,14 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             const uint64_t vd = at(mn_major, vt);
             if (lead)
 #pragma unroll
-              for (int kk = 0; kk < C / 16; ++kk) {
-                tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + kk * 8, vd + 128 * kk, id_o, kk > 0);
-                tc::mma_ts(tmem + Gm::T_O2, tmem + Gm::T_P + 32 + kk * 8, vd + 128 * kk, id_o, true);
-              }
+              for (int x = kTerms - 1; x >= 0; --x)
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                  tc::mma_ts(tmem + Gm::T_O2, tmem + (x == 2 ? Gm::T_A + 16 * kk : Gm::T_P + 32 * x + 8 * kk),
+                             vd + 128 * kk, id_o, x < kTerms - 1 || kk > 0);
             if (lead) tc::commit(bars + 8 * B_ODONE);
             if (mt == tiles - 1 && lead) tc::commit(bars + 8 * (B_VFREE + st));
             if constexpr (D == 256)
-              if (mt == 0) issue_ds(kt, cc);
+              if (mt == 0) issue_ds(kt);
           }
         }
       }
@@ -561,19 +579,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     int* bad = reinterpret_cast<int*>(smem + Gm::BAD_OFF);
     volatile int* bad_chunk = reinterpret_cast<volatile int*>(smem + Gm::FLAG_OFF);
     float S[32];
-    // the state's two terms as the B operand of Q S (value dims contiguous)
+    // the state's terms as the B operand of Q S (value dims contiguous)
     auto store_s = [&]() {
       uint8_t* dst = smem + Gm::S_OFF + (D == 128 ? w4 >> 1 : 0) * (D * 128) + sd * 128;
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
-        uint4 hi, lo;
-        split2(make_float2(S[8 * ch], S[8 * ch + 1]), hi.x, lo.x);
-        split2(make_float2(S[8 * ch + 2], S[8 * ch + 3]), hi.y, lo.y);
-        split2(make_float2(S[8 * ch + 4], S[8 * ch + 5]), hi.z, lo.z);
-        split2(make_float2(S[8 * ch + 6], S[8 * ch + 7]), hi.w, lo.w);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = S[8 * ch + e];
+        uint4 y[kTerms];
+        split3(x, y);
         const int off = (((w4 & 1) * 4 + ch) ^ (sd & 7)) << 4;
-        *reinterpret_cast<uint4*>(dst + off) = hi;
-        *reinterpret_cast<uint4*>(dst + Gm::S_PLANE + off) = lo;
+#pragma unroll
+        for (int e = 0; e < kTerms; ++e) *reinterpret_cast<uint4*>(dst + e * Gm::S_PLANE + off) = y[e];
       }
       fence_proxy_async_smem();
       arrive(B_SREADY);
@@ -582,13 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     const int pi = min(hpt == 2 ? r >> 1 : r, C - 1);         // the row's token
     const int top = min((r | 31) >> (hpt - 1), C - 1);        // the last token of the warp's rows
     auto write_p = [&](int t, const float* pw) -> bool {
-      // (P V of the tile before has read its P)
-      if (!warp_wait(B_ADONE, t & 1) || (t > 0 && !warp_wait(B_ODONE, (t - 1) & 1))) return false;
+      // (Q K^T waited for P V of the tile before, which has read its P)
+      if (!warp_wait(B_ADONE, t & 1)) return false;
       tc::fence_after();
       const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16);
 #pragma unroll 1
       for (int j0 = 16 * w4; j0 < 16 * w4 + 16; j0 += 8) {
-        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        uint32_t p0[4] = {0, 0, 0, 0}, p1[4] = {0, 0, 0, 0}, p2[4] = {0, 0, 0, 0};
         if (j0 <= top) {  // (some of the warp's rows reach these columns)
           uint32_t y[8];
           tc::ld8(lanes + Gm::T_A + j0, y);
@@ -599,15 +617,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           tc::wait_ld();
 #pragma unroll
           for (int jj = 0; jj < 8; jj += 2)
-            split2(mul2(make_float2(jj <= m ? __uint_as_float(y[jj]) : 0.f, jj + 1 <= m ? __uint_as_float(y[jj + 1]) : 0.f),
+            split3(mul2(make_float2(jj <= m ? __uint_as_float(y[jj]) : 0.f, jj + 1 <= m ? __uint_as_float(y[jj + 1]) : 0.f),
                         make_float2(w[jj], w[jj + 1])),
-                   hi[jj >> 1], lo[jj >> 1]);
+                   p0[jj >> 1], p1[jj >> 1], p2[jj >> 1]);
         }
-        tc::st4(lanes + Gm::T_P + j0 / 2, hi);
-        tc::st4(lanes + Gm::T_P + 32 + j0 / 2, lo);
+        tc::st4(lanes + Gm::T_P + j0 / 2, p0);
+        tc::st4(lanes + Gm::T_P + 32 + j0 / 2, p1);
+        // (over columns of A that this warp has read, in this pass or the one before)
+        tc::st4(lanes + Gm::T_A + 16 * w4 + (j0 & 8) / 2, p2);
       }
-      tc::fence_before();
-      arrive(B_AFREE);
       tc::wait_st();
       tc::fence_before();
       arrive(B_PREADY);
@@ -648,13 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
       if (cc > 0 && !warp_wait(B_SFREE, (cc - 1) & 1)) break;
       store_s();
       for (int k = p.k0; k < p.k1 && ok; ++k, ++cc) {
-        const int st = cc & 1;
+        const int st = cc & 1;                  // (of the notes)
         const int n = min(C, p.count - k * C);  // valid tokens
-        ok = warp_wait(B_VFULL + st, (cc >> 1) & 1);
+        ok = warp_wait(B_VFULL + cc % Gm::VS, (cc / Gm::VS) & 1);
         if (!ok) break;
-        // ---- W = lam^(n-1-j) v_j as two terms; the rows past n become zeros in
+        // ---- W = lam^(n-1-j) v_j in terms; the rows past n become zeros in
         // V, W and K (a zero weight would not stop a NaN there)
-        uint8_t* vt = smem + Gm::V_OFF + st * Gm::V_TILE;
+        uint8_t* vt = smem + Gm::V_OFF + cc % Gm::VS * Gm::V_TILE;
         uint8_t* wt = smem + Gm::W_OFF;
 #pragma unroll 1
         for (int off = threadIdx.x * 16; off < Gm::V_TILE; off += kStateWarps * 512) {
@@ -681,18 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             }
           }
           const float w = j < n ? __ldg(pw + n - 1 - j) : 0.f;
-          uint4 hi, lo;
-          split2(mul2(make_float2(bf16_lo(y.x), bf16_hi(y.x)), make_float2(w, w)), hi.x, lo.x);
-          split2(mul2(make_float2(bf16_lo(y.y), bf16_hi(y.y)), make_float2(w, w)), hi.y, lo.y);
-          split2(mul2(make_float2(bf16_lo(y.z), bf16_hi(y.z)), make_float2(w, w)), hi.z, lo.z);
-          split2(mul2(make_float2(bf16_lo(y.w), bf16_hi(y.w)), make_float2(w, w)), hi.w, lo.w);
-          *reinterpret_cast<uint4*>(wt + off) = hi;
-          *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
+          uint4 z[kTerms];
+          split3(y, w, z);
+#pragma unroll
+          for (int e = 0; e < kTerms; ++e) *reinterpret_cast<uint4*>(wt + e * Gm::V_TILE + off) = z[e];
         }
         if (n < C) {
-          ok = warp_wait(B_KFULL + cc % Gm::KS, (cc / Gm::KS) & 1);
+          ok = warp_wait(B_KFULL, cc & 1);
           if (!ok) break;
-          uint8_t* kt = smem + Gm::K_OFF + cc % Gm::KS * Gm::K_TILE;
+          uint8_t* kt = smem + Gm::K_OFF;
           for (int off = threadIdx.x * 16; off < Gm::K_TILE; off += kStateWarps * 512)
             if (((off >> 7) & (C - 1)) >= n) *reinterpret_cast<uint4*>(kt + off) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -746,14 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
     const int hd = hpt == 2 ? r & 1 : 0;
     const int* bad = reinterpret_cast<const int*>(smem + Gm::BAD_OFF);
     const volatile int* bad_chunk = reinterpret_cast<const volatile int*>(smem + Gm::FLAG_OFF);
-    // a tile's outputs have been read from shared memory: its Q's last two regions,
-    // where they were staged, take the next Q
-    auto left = [&](int tile) {
-      if (lane == 0) {
-        tma_stores_read<0>();
-        mbar_arrive(bars + 8 * (B_STAGED + (tile & 1)));
-      }
-    };
     bool ok = true;
     int cc = 0, t = 0;
     Pieces p = all;
@@ -772,18 +779,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
           float f = a.scale;
           if (a.gate) f /= 1.f + expf(-gate);
           const float f1 = f * row_decay;
-          float* dst = a.out + head * D + p.slice * EB;
-          const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
+          // Two lanes with two rows (a token's heads, or two tokens of one head): each
+          // stores half of a step's columns of both, so that a store instruction is
+          // in 16 rows, 64 bytes in each. (dst: of the even row; the odd one's is `next`
+          // behind it.)
+          const int odd_lane = lane & 1;
+          const int64_t next = hpt == 2 ? D : static_cast<int64_t>(a.Hkv) * G * D;
+          float* dst = a.out + head * D - odd_lane * next + p.slice * EB + 8 * odd_lane;
+          const bool store0 = __shfl_sync(0xffffffffu, store, lane & ~1), store1 = __shfl_sync(0xffffffffu, store, lane | 1);
+          const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
           ok = warp_wait(B_ODONE, t & 1);
           if (!ok) break;
           tc::fence_after();
           const bool odd = bad_chunk[cc & 1] == cc;
-          // whole boxes of rows leave by the TMA unit, through shared memory (1 x
-          // 32,768 tokens 136 us; 169 with a lane's stores of 32 bytes in each of 32
-          // rows, which take the load/store path a cycle a row, 196 with 16); short
-          // chunks and a group's odd head row by row
-          const bool box = n == C && (mt + 1) * hpt <= G;
-          uint8_t* stage = smem + Gm::Q_OFF + (t * Gm::DP + Gm::DP - 1) % Gm::QP * Gm::Q_PAIR + w2 * Gm::Q_REGION + (warp & 3) * 4096;
 #pragma unroll 1
           for (int e0 = EB / 2 * w2; e0 < EB / 2 * (w2 + 1); e0 += 16) {
             uint32_t o1[16], o2[16];
@@ -792,6 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
             if constexpr (D == 256) {
               uint32_t lo[16];
               tc::ld16(tmem + lane_off + Gm::T_O1 + 64 + e0, lo);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(__uint_as_float(o1[e]) + __uint_as_float(lo[e]));
+              tc::ld16(tmem + lane_off + Gm::T_O1 + 128 + e0, lo);
               tc::wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o1[e] = __float_as_uint(__uint_as_float(o1[e]) + __uint_as_float(lo[e]));
@@ -822,35 +834,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
               tc::fence_before();
               arrive(B_OFREE);
             }
-            if (box) {
-              uint8_t* buf = stage + ((e0 >> 4) & 1) * 2048;
-              if (lane == 0) tma_stores_read<1>();
-              __syncwarp();
+            float z0[8], z1[8];  // this lane's columns of the even row and of the odd one
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(buf + lane * 64 + (((e >> 2) ^ ((lane >> 1) & 3)) << 4)) =
-                    make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && 32 * (warp & 3) < hpt * C)
-                tma_store_3d(&a.tmap_o, smem_addr(buf), p.slice * EB + e0, p.h * G + mt * hpt,
-                             p.b * a.T + k * C + (warp & 3) * (32 / hpt));
-            } else if (store) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 8) {
-                float half[8];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) half[y] = z[e + y];
-                st_8(dst + e0 + e, half, wide);
-              }
+            for (int e = 0; e < 8; ++e) {
+              const float other = __shfl_xor_sync(0xffffffffu, odd_lane ? z[e] : z[8 + e], 1);
+              z0[e] = odd_lane ? other : z[e];
+              z1[e] = odd_lane ? z[8 + e] : other;
             }
+            if (store0) st_8(dst + e0, z0, wide);
+            if (store1) st_8(dst + next + e0, z1, wide);
           }
-          left(t);
         }
       }
     }
-    if (lane == 0) tma_stores_done();
-    __syncwarp();
   }
 
   tc::fence_before();
@@ -867,9 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_kernel(const __grid
 // next CTA: K^T W over chunks (all full), in tensor memory over groups of up to
 // kSumGroup of them - W's weights reach to the group's end - and from group to
 // group in registers. The state warps make W, the rest is copies and MMAs; K, V
-// and W are rings. 31 - 33 us at 1 x 32,768 tokens (134 MB, 4.2 TB/s) and at 16
-// ragged prompts, about 0.9 us a chunk: neither a fifth stage nor four W's on
-// their way at once (31 - 34 us) changed it.
+// and W are rings. 36 us under ncu at 1 x 32,768 tokens (127 MB, 3.5 TB/s), 41 at
+// 16 ragged prompts: W's three terms, about a microsecond a chunk.
 constexpr int kSumGroup = 4, kSumStages = 4;
 constexpr int kSumThreads = (kStateWarps + 2) * 32;
 enum : int { R_FULL, R_FREE = R_FULL + kSumStages, R_WREADY = R_FREE + kSumStages, R_WFREE = R_WREADY + 2,
@@ -879,12 +874,13 @@ template <int D>
 struct SumGeo {
   using Gm = Geo<D>;
   static constexpr int STAGE = Gm::K_TILE + Gm::V_TILE;
-  static constexpr int W_OFF = kSumStages * STAGE;             // [2] hi, lo
-  static constexpr int BAR_OFF = W_OFF + 4 * Gm::V_TILE;
+  static constexpr int W_OFF = kSumStages * STAGE;             // [2] the terms
+  static constexpr int BAR_OFF = W_OFF + 2 * kTerms * Gm::V_TILE;
   static constexpr int MISC_OFF = BAR_OFF + 8 * R_COUNT;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;
   static constexpr int ACC = D / 128 * Gm::EB;  // tensor memory columns of a group's sum, of which there are two
   static constexpr int T_COLS = 2 * ACC;
+  static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
 template <int D>
@@ -964,7 +960,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
         const int st = c % kSumStages;
         if (!warp_wait(R_FULL + st, (c / kSumStages) & 1) || !warp_wait(R_WREADY + (c & 1), (c >> 1) & 1)) break;
         tc::fence_after();
-        const uint32_t kt = sbase + st * Sg::STAGE, wt = sbase + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+        const uint32_t kt = sbase + st * Sg::STAGE, wt = sbase + Sg::W_OFF + (c & 1) * kTerms * Gm::V_TILE;
         const uint32_t d0 = tmem + ((c / kSumGroup) & 1) * Sg::ACC;
 #pragma unroll 1
         for (int m = 0; m < D / 128; ++m) {
@@ -972,10 +968,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
           const uint32_t d = d0 + m * EB;
           if (lead)
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) {
-              tc::mma(d, kd + 128 * kk, wd + 128 * kk, id_s, kk > 0 || c % kSumGroup > 0);
-              tc::mma(d, kd + 128 * kk, wd + 128 * kk + Gm::V_TILE / 16, id_s, true);
-            }
+            for (int x = kTerms - 1; x >= 0; --x)
+#pragma unroll
+              for (int kk = 0; kk < C / 16; ++kk)
+                tc::mma(d, kd + 128 * kk, wd + 128 * kk + x * (Gm::V_TILE / 16), id_s,
+                        x < kTerms - 1 || kk > 0 || c % kSumGroup > 0);
         }
         if (lead) tc::commit(bars + 8 * (R_FREE + st));
         if (lead) tc::commit(bars + 8 * (R_WFREE + (c & 1)));
@@ -1030,18 +1027,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) linear_sums_kernel(const __gri
         ok = warp_wait(R_FULL + st, (c / kSumStages) & 1) && (c < 2 || warp_wait(R_WFREE + (c & 1), ((c >> 1) - 1) & 1));
         if (!ok) break;
         const uint8_t* vt = smem + st * Sg::STAGE + Gm::K_TILE;
-        uint8_t* wt = smem + Sg::W_OFF + (c & 1) * 2 * Gm::V_TILE;
+        uint8_t* wt = smem + Sg::W_OFF + (c & 1) * kTerms * Gm::V_TILE;
 #pragma unroll 2
         for (int off = (threadIdx.x & 255) * 16; off < Gm::V_TILE; off += kStateWarps / 2 * 512) {
           const uint4 y = *reinterpret_cast<const uint4*>(vt + off);
           const float w = __ldg(pw + C - 1 - ((off >> 7) & (C - 1))) * g;
-          uint4 hi, lo;
-          split2(mul2(make_float2(bf16_lo(y.x), bf16_hi(y.x)), make_float2(w, w)), hi.x, lo.x);
-          split2(mul2(make_float2(bf16_lo(y.y), bf16_hi(y.y)), make_float2(w, w)), hi.y, lo.y);
-          split2(mul2(make_float2(bf16_lo(y.z), bf16_hi(y.z)), make_float2(w, w)), hi.z, lo.z);
-          split2(mul2(make_float2(bf16_lo(y.w), bf16_hi(y.w)), make_float2(w, w)), hi.w, lo.w);
-          *reinterpret_cast<uint4*>(wt + off) = hi;
-          *reinterpret_cast<uint4*>(wt + Gm::V_TILE + off) = lo;
+          uint4 z[kTerms];
+          split3(y, w, z);
+#pragma unroll
+          for (int e = 0; e < kTerms; ++e) *reinterpret_cast<uint4*>(wt + e * Gm::V_TILE + off) = z[e];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1151,10 +1145,10 @@ cudaError_t launch_linear_prompt(const LinearArgs& args, int D, int num_sms, cud
   const int chunks = (a.T + C - 1) / C;
   // Whether units are cut is decided on the device, from the counts (10 us where it
   // comes out against it); not even considered for short prompts (cut / uncut: 4 x
-  // 330 tokens of 8 heads of 128 29.2 / 26.5 us, 4 x 256 28.7 / 20.6) nor with more
-  // units than SMs, which even each other out (20 x 512 - 2,048, 160 units: 130 /
-  // 114 us, 32 x 1,024: 142 / 128, 48 x 512 - 2,048: 253 / 255, 64 x 16 - 4,096:
-  // 485 / 466).
+  // 330 tokens of 8 heads of 128 31.8 / 31.1 us, 4 x 256 30.9 / 23.6) nor with more
+  // units than SMs, where it depends on how they even each other out (20 x 512 -
+  // 2,048, 160 units: 139 / 146 us, 32 x 1,024: 162 / 146, 48 x 512 - 2,048: 276 /
+  // 288, 64 x 16 - 4,096: 588 / 635).
   a.split = chunks > 6 && units <= num_sms;
   a.ctas = num_sms;
   const int ctas = a.split ? num_sms : units;

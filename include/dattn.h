@@ -341,7 +341,7 @@ DATTN_API int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int 
  * DATTN_EINDEX (dattn_get_error). The caller then advances its metadata by
  * count[s].
  * On a state layer the chunked form of linear attention: up to rounding (about
- * 3e-6 of the outputs' size) the outputs and final state of count[s] decode
+ * 5e-7 of the outputs' size) the outputs and final state of count[s] decode
  * steps with write_back, whatever max_verify_rows is, in one launch, or three
  * where long streams are few; start_pos is not read. A stream with a count out
  * of range or without a state is reported and left as it is. */
