@@ -108,3 +108,47 @@ def one_hot(c, least=0):
     c.k = k.to(c.kind)
     c.k_new[:] = 0
     c.k_new[..., c.D - 1] = 1.0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B", [1, 160])
+def test_large_scores_keep_their_low_bits(dattn, fp8, B):
+    """Scores of 35 to 44 nats from single dims: nothing but the query's terms, its scale and the sum of the terms
+    stands between them and the weights. (Two bf16 terms instead of three miss by up to 2^-18 of the score.)"""
+    c = Case(33, 8, 2, 128, 16, [100], fp8=fp8, r=0, gate=False)
+    c.ks = 1.0
+    c.q = (400 + 100 * torch.rand(c.q.shape, generator=c.g)).to(torch.bfloat16)
+    one_hot(c)
+    want, size, reach = exact(c)
+    out, _ = repeat(c, B).run(dattn, 8, 1, 1)
+    check(out, want, 2 * (reach * 2.0 ** -21 + 2.0 ** -19)[:, None] * size)
+
+
+@pytest.mark.parametrize("where", [[], [0], [350], [699], [699, 350, 3], [3, 350, 699], "new"])
+@pytest.mark.parametrize("q_mul", [1, 8, 32])
+@pytest.mark.parametrize("fp8,B", [(False, 1), (False, 160), (True, 1), (True, 160)])
+def test_peaked_rows(dattn, fp8, B, q_mul, where):
+    """Keys along the group's query at the beginning, in the middle and at the end, each one larger than the one before
+    it in the list (the running maximum jumps, or is there at once), or the new token's.
+
+    Scores: an MMA adds 16 products to its sum, each of the 17 off by 2^-23 of the largest at most, 4 MMAs a chain at D
+    = 128, and the query's rounding: (4 * 17 * 2^-23 + 2^-20) sum |q_d k_d| / sqrt(D) nats. Outputs: 11 groups a warp of
+    three terms each, 17 * 2^-23 an MMA.
+
+    Where the keys with weight have no value in a dim, A is next to nothing and what small weights lose shows: a weight
+    below 2^-126 of its warp's largest is 0, and E4M3's terms of 2^15 p end at 2^-24, so that each of the 701 weights
+    is off by 2^-25 2^-15 = 2^-40 of a sum of at least 1 (after the joins: of more)."""
+    c = Case(34, 8, 2, 128, 16, [700], fp8=fp8, r=0, gate=False, q_mul=q_mul)
+    along = c.q.float().view(2, 4, 128).mean(1)
+    along /= along.pow(2).mean(-1, keepdim=True).sqrt()
+    if where == "new":
+        c.k_new = (3 * along)[None].to(torch.bfloat16)
+    else:
+        k = c.k.float()
+        for i, t in enumerate(where):
+            k[int(c.table[0, t // 16]), :, t % 16] = (2 + i) * along
+        c.k = k.to(c.kind)
+    want, size, reach = exact(c)
+    out, _ = repeat(c, B).run(dattn, 64, 1, 1)
+    e = reach * (4 * 17 * 2.0 ** -23 + 2.0 ** -20) + 11 * 3 * 17 * 2.0 ** -23 + 2.0 ** -19
+    check(out, want, 2 * e[:, None] * size + 701 * (2.0 ** -40 if fp8 else 2.0 ** -126) * c.v.float().abs().max().item() * c.vs)
