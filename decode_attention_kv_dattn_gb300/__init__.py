@@ -27,6 +27,7 @@ lib = ctypes.CDLL(LIB_PATH)
 OK, EINVAL, EXCEEDS, ECUDA, EINDEX, ETIMEOUT, EUNSUPPORTED, ELENGTH, ERANGE = range(9)
 CACHE_RING, CACHE_PAGED, CACHE_STATE = 0, 1, 2
 KV_BF16, KV_E4M3 = 0, 1
+_I32, _BF16 = torch.int32, torch.bfloat16
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -150,13 +151,16 @@ def _check(code, what):
 def _ptr(t):
     if t is None:
         return None
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch tensor")
     if not t.is_cuda:
         raise ValueError("dattn takes device tensors")
-    if not t.is_contiguous():
-        raise ValueError("dattn takes contiguous tensors")
-    return t.data_ptr()
+    raise ValueError("dattn takes contiguous tensors")
 
 
 # The current stream of a device as an integer. (torch.cuda.current_stream builds
@@ -205,6 +209,9 @@ def state_cache(state, stream_rows=None) -> Cache:
         raise TypeError("stream_rows: int32")
     c = Cache(_ptr(state), None, state.shape[0], None, None, _ptr(stream_rows), None, 0, None)
     c._tensors = (state, stream_rows)
+    # what a handle compares on every call: heads and dims, and the streams it has rows for
+    c._state = list(state.shape[1:3])
+    c._streams = None if stream_rows is None else stream_rows.numel()
     return c
 
 
@@ -240,6 +247,10 @@ class Handle:
                                     float(l.get("k_scale", 1.0)), float(l.get("v_scale", 1.0)),
                                     None if ld is None else ld.ctypes.data))
         self._layers = (LayerConfig * len(layers))(*cfgs)
+        # (for the checks of every call: plain Python values; a structure's field or a
+        # tensor's sliced shape takes longer than the whole check)
+        self._kinds = {i: l["kind"] for i, l in enumerate(layers)}
+        self._heads = [num_kv_heads, head_dim]
         self.config = Config(num_q_heads, num_kv_heads, head_dim, max_streams, max_context,
                              max_verify_rows, len(layers), self._layers, max_selected_pages)
         h = _vp()
@@ -257,30 +268,24 @@ class Handle:
 
     __del__ = close
 
-    def _kind(self, layer):
-        return self._layers[layer].cache_kind if 0 <= layer < len(self._layers) else None
-
-    def _check_state(self, layer, cache, streams):
+    def _check_state(self, cache, streams):
         """A state layer's call has states of this handle's heads, and a row for each stream."""
-        if self._kind(layer) != CACHE_STATE or not hasattr(cache, "_tensors"):
-            return
-        state, rows = cache._tensors[0], cache._tensors[-1]
-        want = (self.config.num_kv_heads, self.config.head_dim, self.config.head_dim)
-        if state.dtype != torch.float32 or tuple(state.shape[1:]) != want:
-            raise ValueError(f"a state layer's cache: {state.dtype} {tuple(state.shape)}, expected fp32 (rows, "
-                             f"{', '.join(map(str, want))})")
-        if rows is not None and rows.numel() < streams:
-            raise ValueError(f"stream_rows: {rows.numel()} rows for {streams} streams")
+        if not hasattr(cache, "_tensors"):
+            return  # (a descriptor of the caller's own)
+        if getattr(cache, "_state", None) != self._heads:
+            raise ValueError(f"a state layer's cache: {cache._tensors[0].dtype} {tuple(cache._tensors[0].shape)}, expected "
+                             f"state_cache of (rows, {self._heads[0]}, {self._heads[1]}, {self._heads[1]})")
+        if cache._streams is not None and cache._streams < streams:
+            raise ValueError(f"stream_rows: {cache._streams} rows for {streams} streams")
 
-    def _check_summary(self, layer, cache, summary):
+    def _check_summary(self, cache, summary):
         """A paged layer's summaries: one for each page and KV head."""
-        if self._kind(layer) != CACHE_PAGED or summary is None:
-            return
-        want = (self.config.num_kv_heads, self.config.head_dim)
-        if summary.dtype != torch.bfloat16:
+        if summary.dtype is not _BF16:
             raise TypeError(f"summary: {summary.dtype}, expected bf16")
-        if summary.dim() != 3 or tuple(summary.shape[1:]) != want or summary.shape[0] < cache.n_rows:
-            raise ValueError(f"summary: shape {tuple(summary.shape)}, expected ({cache.n_rows} pages, {want[0]}, {want[1]})")
+        pages, *heads = summary.shape
+        if pages < cache.n_rows or heads != self._heads:
+            raise ValueError(f"summary: shape {tuple(summary.shape)}, expected ({cache.n_rows} pages, {self._heads[0]}, "
+                             f"{self._heads[1]})")
 
     def append_kv(self, layer, cache: Cache, k, v, start_index, count, start_pos=None,
                   rotate=True, stream=None):
@@ -294,8 +299,10 @@ class Handle:
                write_back=True, stream=None):
         """q [B, Hq, D], k_new/v_new [B, Hkv, D] bf16; pos [B] int32; out [B, Hq, D] fp32;
         gate [B, Hq] bf16 or None."""
-        self._check_state(layer, cache, q.shape[0])
-        args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
+        B = q.shape[0]
+        if self._kinds.get(layer) == CACHE_STATE:
+            self._check_state(cache, B)
+        args = DecodeArgs(B, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
                                 _stream_ptr(stream, self.device)), "dattn_decode")
@@ -307,7 +314,8 @@ class Handle:
         [pages, Hkv, D] bf16 as `summarize` keeps it; selected [B, Hkv, num_pages] int32
         receives the pages (ascending, then -1) if given. The handle needs
         max_selected_pages >= num_pages."""
-        self._check_summary(layer, cache, summary)
+        if summary is not None and self._kinds.get(layer) == CACHE_PAGED:
+            self._check_summary(cache, summary)
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         if selected is not None and (selected.dtype != torch.int32 or selected.numel() !=
@@ -321,12 +329,13 @@ class Handle:
         """Summaries (bf16 means of the stored keys, [pages, Hkv, D]) of the pages that the
         new tokens [start_index, start_index + count) of each row completed; start_index,
         count: [B] int32, count <= max_tokens."""
-        self._check_summary(layer, cache, summary)
-        if start_index.dtype != torch.int32 or count.dtype != torch.int32 or count.numel() != start_index.shape[0]:
+        if summary is not None and self._kinds.get(layer) == CACHE_PAGED:
+            self._check_summary(cache, summary)
+        B = start_index.shape[0]
+        if start_index.dtype is not _I32 or count.dtype is not _I32 or count.numel() != B:
             raise ValueError("start_index, count: int32 [B]")
-        _check(lib.dattn_summarize(self._h, layer, ctypes.byref(cache), _ptr(summary), start_index.shape[0],
-                                   int(max_tokens), _ptr(start_index), _ptr(count), _stream_ptr(stream, self.device)),
-               "dattn_summarize")
+        _check(lib.dattn_summarize(self._h, layer, ctypes.byref(cache), _ptr(summary), B, int(max_tokens),
+                                   _ptr(start_index), _ptr(count), _stream_ptr(stream, self.device)), "dattn_summarize")
 
     def verify(self, layer, cache: Cache, q, k, v, parent, out, gate=None, max_prefix_len=0,
                write_back=True, pos=None, stream=None):
@@ -349,8 +358,10 @@ class Handle:
     def prefill(self, layer, cache: Cache, q, k, v, count, start_pos, out, gate=None, stream=None):
         """Ragged prefill: q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16, count/start_pos [S] int32,
         out [S, T, Hq, D] fp32 (rows t < count written), gate [S, T, Hq] bf16 or None."""
-        self._check_state(layer, cache, q.shape[0])
-        _check(lib.dattn_prefill(self._h, layer, ctypes.byref(cache), q.shape[0], q.shape[1], _ptr(q), _ptr(k),
+        B, T = q.shape[0], q.shape[1]
+        if self._kinds.get(layer) == CACHE_STATE:
+            self._check_state(cache, B)
+        _check(lib.dattn_prefill(self._h, layer, ctypes.byref(cache), B, T, _ptr(q), _ptr(k),
                                  _ptr(v), _ptr(gate), _ptr(count), _ptr(start_pos), _ptr(out),
                                  _stream_ptr(stream, self.device)), "dattn_prefill")
 
