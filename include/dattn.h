@@ -343,8 +343,11 @@ DATTN_API int dattn_commit(dattn_t* h, int layer, const dattn_cache* cache, int 
  * On a state layer the chunked form of linear attention: up to rounding (about
  * 5e-7 of the outputs' size) the outputs and final state of count[s] decode
  * steps with write_back, whatever max_verify_rows is, in one launch, or three
- * where long streams are few; start_pos is not read. A stream with a count out
- * of range or without a state is reported and left as it is. */
+ * where long streams are few; start_pos is not read. An infinity among the
+ * inputs or in a state may come out as no number where the steps give an
+ * infinity, for its token and those after it. A stream with a count out of range
+ * or without a state is reported and left as it is. The ordering rules of
+ * dattn_decode hold. */
 DATTN_API int dattn_prefill(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
                             const void* q, const void* k, const void* v, const void* gate,
                             const int32_t* count, const int32_t* start_pos, float* out, dattn_stream_t stream);
