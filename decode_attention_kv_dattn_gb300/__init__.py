@@ -26,7 +26,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, EXCEEDS, ECUDA, EINDEX, ETIMEOUT, EUNSUPPORTED, ELENGTH, ERANGE = range(9)
 CACHE_RING, CACHE_PAGED, CACHE_STATE = 0, 1, 2
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_INT4 = 0, 1, 2
 _I32, _BF16 = torch.int32, torch.bfloat16
 
 _vp = ctypes.c_void_p
@@ -115,6 +115,8 @@ lib.dattn_commit.argtypes = [_vp, _int, ctypes.POINTER(Cache), _int, _int, _vp, 
 lib.dattn_commit.restype = _int
 lib.dattn_prefill.argtypes = [_vp, _int, ctypes.POINTER(Cache), _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.dattn_prefill.restype = _int
+lib.dattn_read_kv.argtypes = [_vp, _int, ctypes.POINTER(Cache), _int, _int, _vp, _vp, _vp, _vp, _vp]
+lib.dattn_read_kv.restype = _int
 lib.dattn_get_error.argtypes = [_vp, _vp]
 lib.dattn_get_error.restype = _int
 lib.dattn_error_string.argtypes = [_int]
@@ -130,7 +132,7 @@ DEBUG_WITHHOLD_Q, DEBUG_WITHHOLD_KV = 1, 2
 
 EXPORTS = ("dattn_create", "dattn_append_kv", "dattn_decode", "dattn_verify", "dattn_commit", "dattn_prefill",
            "dattn_get_error", "dattn_error_string", "dattn_destroy", "dattn_decode_noalloc",
-           "dattn_debug_config", "dattn_sparse_decode", "dattn_summarize")
+           "dattn_debug_config", "dattn_sparse_decode", "dattn_summarize", "dattn_read_kv")
 
 
 class DattnError(RuntimeError):
@@ -190,12 +192,20 @@ def ring_cache(k, v, ring_head, ring_count, stream_rows=None) -> Cache:
 
 
 def paged_cache(k, v, block_table, seq_len) -> Cache:
-    """k, v: [pages, Hkv, P, D] bf16; block_table [B, max_pages] int32; seq_len [B] int32.
-    The descriptor holds the tensors it points to, so they live as long as it does."""
+    """k, v: [pages, Hkv, P, D] bf16 (KV_INT4: int4_pool); block_table [B, max_pages] int32;
+    seq_len [B] int32. The descriptor holds the tensors it points to, so they live as long as it does."""
     c = Cache(_ptr(k), _ptr(v), k.shape[0], None, None, None, _ptr(block_table),
               block_table.shape[1], _ptr(seq_len))
     c._tensors = (k, v, block_table, seq_len)
     return c
+
+
+def int4_pool(pages, kv_heads, page_size, head_dim, device="cuda"):
+    """A pool of a 4-bit layer (KV_INT4), K or V: uint8 [pages, Hkv, bytes], 4.5 bits for each
+    value. Its layout is the library's: append_kv and decode write it, read_kv reads it."""
+    if page_size <= 0 or page_size % 16:
+        raise ValueError(f"page_size {page_size}: a 4-bit page holds whole blocks of 16 tokens")
+    return torch.zeros(pages, kv_heads, page_size // 16 * 9 * head_dim, dtype=torch.uint8, device=device)
 
 
 def state_cache(state, stream_rows=None) -> Cache:
@@ -251,6 +261,9 @@ class Handle:
         # tensor's sliced shape takes longer than the whole check)
         self._kinds = {i: l["kind"] for i, l in enumerate(layers)}
         self._heads = [num_kv_heads, head_dim]
+        # (4-bit layers: heads and bytes of a page)
+        self._int4 = {i: [num_kv_heads, l.get("page_size", 0) // 16 * 9 * head_dim] for i, l in enumerate(layers)
+                      if l.get("kv_format", KV_BF16) == KV_INT4}
         self.config = Config(num_q_heads, num_kv_heads, head_dim, max_streams, max_context,
                              max_verify_rows, len(layers), self._layers, max_selected_pages)
         h = _vp()
@@ -287,13 +300,36 @@ class Handle:
             raise ValueError(f"summary: shape {tuple(summary.shape)}, expected ({cache.n_rows} pages, {self._heads[0]}, "
                              f"{self._heads[1]})")
 
+    def _check_int4(self, layer, cache):
+        """A 4-bit layer's call has pools of this handle's pages."""
+        for t in getattr(cache, "_tensors", ())[:2]:  # (a descriptor of the caller's own has none)
+            if t.dtype is not torch.uint8 or list(t.shape[1:]) != self._int4[layer]:
+                raise ValueError(f"a 4-bit layer's pool: {t.dtype} {tuple(t.shape)}, expected int4_pool's uint8 (pages, "
+                                 f"{self._int4[layer][0]}, {self._int4[layer][1]})")
+
     def append_kv(self, layer, cache: Cache, k, v, start_index, count, start_pos=None,
                   rotate=True, stream=None):
         """k, v: [B, T, Hkv, D] bf16; start_index, count (, start_pos): [B] int32."""
         B, T = k.shape[0], k.shape[1]
+        if layer in self._int4:
+            self._check_int4(layer, cache)
         _check(lib.dattn_append_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index),
                                    _ptr(start_pos), _ptr(count), _ptr(k), _ptr(v), int(rotate),
                                    _stream_ptr(stream, self.device)), "dattn_append_kv")
+
+    def read_kv(self, layer, cache: Cache, start_index, count, k, v, stream=None):
+        """Cached entries [start_index, start_index + count) of each row back as bf16 into rows
+        t < count of k, v [B, T, Hkv, D] (others are left as they are); start_index, count: [B] int32."""
+        if k.dtype is not _BF16 or v.dtype is not _BF16 or k.shape != v.shape or list(k.shape[2:]) != self._heads:
+            raise ValueError(f"k, v: bf16 [B, T, {self._heads[0]}, {self._heads[1]}], got {k.dtype} {tuple(k.shape)} and "
+                             f"{v.dtype} {tuple(v.shape)}")
+        B, T = k.shape[0], k.shape[1]
+        if start_index.dtype is not _I32 or count.dtype is not _I32 or start_index.numel() != B or count.numel() != B:
+            raise ValueError("start_index, count: int32 [B]")
+        if layer in self._int4:
+            self._check_int4(layer, cache)
+        _check(lib.dattn_read_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index), _ptr(count), _ptr(k),
+                                 _ptr(v), _stream_ptr(stream, self.device)), "dattn_read_kv")
 
     def decode(self, layer, cache: Cache, q, k_new, v_new, pos, out, gate=None, max_seq_len=0,
                write_back=True, stream=None):
@@ -302,6 +338,8 @@ class Handle:
         B = q.shape[0]
         if self._kinds.get(layer) == CACHE_STATE:
             self._check_state(cache, B)
+        if layer in self._int4:
+            self._check_int4(layer, cache)
         args = DecodeArgs(B, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),

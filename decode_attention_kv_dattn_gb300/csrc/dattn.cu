@@ -20,6 +20,7 @@
 #include <unordered_map>
 
 #include "dattn.h"
+#include "int4_format.h"
 #include "kernels.h"
 
 using namespace dattn;
@@ -339,7 +340,7 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   const dattn_layer_config& L = h->layers[layer];
   int rc = check_cache(L, cache);
   if (rc != DATTN_OK) return rc;
-  if (sel && L.cache_kind != DATTN_CACHE_PAGED) return DATTN_EUNSUPPORTED;
+  if (sel && (L.cache_kind != DATTN_CACHE_PAGED || L.kv_format == DATTN_KV_INT4)) return DATTN_EUNSUPPORTED;
   const int B = args->num_streams;
   if (B <= 0) return DATTN_EINVAL;
   if (B > h->max_streams) return DATTN_EXCEEDS;
@@ -373,12 +374,18 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
   if (sel) return sparse_call(h, layer, cache, args, sel, n_max, s);
-  const bool f8 = L.kv_format == DATTN_KV_E4M3;
-  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, f8));
+  const bool f8 = L.kv_format == DATTN_KV_E4M3, int4 = L.kv_format == DATTN_KV_INT4;
+  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, L.kv_format));
   if (static_cast<size_t>(ctas) + static_cast<size_t>(B) * h->Hkv > h->part_units) return DATTN_EXCEEDS;
   DecodeArgs da{};
   da.c = make_view(h, L, cache);
-  if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) return DATTN_EUNSUPPORTED;
+  if (int4) {
+    // (blocks are counted in 32 bits)
+    if (static_cast<int64_t>(cache->n_rows) * h->Hkv * (L.page_size / kInt4Block) > INT32_MAX) return DATTN_EUNSUPPORTED;
+    da.int4 = 1;
+  } else if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) {
+    return DATTN_EUNSUPPORTED;
+  }
   da.B = B;
   da.Hkv = h->Hkv;
   da.G = h->G;
@@ -467,7 +474,10 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
     if (L.rotary_dim < 0 || L.rotary_dim > D || L.rotary_dim % 2) return DATTN_EINVAL;
     if (L.rotary_dim > 0 && !(L.rope_theta > 0.0)) return DATTN_EINVAL;
     if ((L.q_norm_weight || L.k_norm_weight) && !(L.norm_eps >= 0.0)) return DATTN_EINVAL;
-    if (L.kv_format != DATTN_KV_BF16 && L.kv_format != DATTN_KV_E4M3) return DATTN_EINVAL;
+    if (L.kv_format != DATTN_KV_BF16 && L.kv_format != DATTN_KV_E4M3 && L.kv_format != DATTN_KV_INT4) return DATTN_EINVAL;
+    // a 4-bit cache is paged, its pages whole blocks of 16 tokens
+    if (L.kv_format == DATTN_KV_INT4 && (L.cache_kind != DATTN_CACHE_PAGED || L.page_size % kInt4Block != 0))
+      return DATTN_EUNSUPPORTED;
     if (L.kv_format == DATTN_KV_E4M3 &&
         !(L.k_scale > 0.f && L.v_scale > 0.f && std::isfinite(L.k_scale) && std::isfinite(L.v_scale)))
       return DATTN_EINVAL;
@@ -729,8 +739,41 @@ int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_str
   a.f8 = L.kv_format == DATTN_KV_E4M3;
   a.k_scale = L.k_scale;
   a.v_scale = L.v_scale;
-  rc = cuda_status(launch_append(a, reinterpret_cast<cudaStream_t>(stream)), "append");
+  rc = L.kv_format == DATTN_KV_INT4 ? cuda_status(launch_append_int4(a, reinterpret_cast<cudaStream_t>(stream)), "4-bit append")
+                                    : cuda_status(launch_append(a, reinterpret_cast<cudaStream_t>(stream)), "append");
   if (rc == DATTN_OK) record_launch(stream, cache->k);
+  return rc;
+}
+
+int dattn_read_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
+                  const int32_t* start_index, const int32_t* count, void* k, void* v, dattn_stream_t stream) {
+  if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
+  const dattn_layer_config& L = h->layers[layer];
+  if (L.cache_kind == DATTN_CACHE_STATE) return DATTN_EUNSUPPORTED;
+  int rc = check_cache(L, cache);
+  if (rc != DATTN_OK) return rc;
+  if (num_streams <= 0 || max_tokens < 0 || !start_index || !count || !k || !v) return DATTN_EINVAL;
+  if (!aligned16(k) || !aligned16(v)) return DATTN_EINVAL;
+  if (num_streams > 65535) return DATTN_EXCEEDS;
+  if (max_tokens == 0) return DATTN_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return DATTN_ECUDA;
+  ReadArgs a{};
+  a.c = make_view(h, L, cache);
+  a.B = num_streams;
+  a.Tmax = max_tokens;
+  a.Hkv = h->Hkv;
+  a.D = h->D;
+  a.start_index = start_index;
+  a.count = count;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.k_scale = L.k_scale;
+  a.v_scale = L.v_scale;
+  a.err = h->err;
+  rc = cuda_status(launch_read(a, L.kv_format == DATTN_KV_INT4, L.kv_format == DATTN_KV_E4M3,
+                               reinterpret_cast<cudaStream_t>(stream)), "read back");
+  if (rc == DATTN_OK) record_launch(stream, nullptr);
   return rc;
 }
 
@@ -791,7 +834,7 @@ int dattn_summarize(dattn_t* h, int layer, const dattn_cache* cache, void* summa
                     const int32_t* start_index, const int32_t* count, dattn_stream_t stream) {
   if (!h || layer < 0 || layer >= static_cast<int>(h->layers.size())) return DATTN_EINVAL;
   const dattn_layer_config& L = h->layers[layer];
-  if (L.cache_kind != DATTN_CACHE_PAGED) return DATTN_EUNSUPPORTED;
+  if (L.cache_kind != DATTN_CACHE_PAGED || L.kv_format == DATTN_KV_INT4) return DATTN_EUNSUPPORTED;
   int rc = check_cache(L, cache);
   if (rc != DATTN_OK) return rc;
   if (num_streams <= 0 || max_tokens < 0 || !summary || !start_index || !count) return DATTN_EINVAL;

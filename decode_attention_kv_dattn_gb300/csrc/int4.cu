@@ -1,0 +1,431 @@
+// Entries of a 4-bit cache (int4_format.h): quantised as they are written, and read
+// back. And the read-back of the other cache formats.
+//
+// Both are bound by memory: append reads 4 bytes a (key, value) pair of dims and
+// writes 9/8, the read-back the other way round. A warp takes one block of 16 tokens
+// of one KV head, K or V, in the lanes' order of the block itself: what it stores (or
+// loads) is 16 bytes a lane in one piece, what it loads (or stores) of the bf16 rows
+// whole 128-byte lines, and a group's least and largest value are 2 (K) or 3 (V)
+// shuffles away.
+#include <cuda_bf16.h>
+
+#include "bf16_exact.h"
+#include "common.cuh"
+#include "int4_format.h"
+#include "kernels.h"
+#include "mma.cuh"
+#include "qk_norm.cuh"
+#include "rope_angle.h"
+#include "round_f64.h"
+
+namespace dattn {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxWarps = 8;
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// (largest, -least) of the values packed in w[0..N), as one bf16 pair: the join of
+// two such pairs is a maximum.
+template <int N>
+__device__ __forceinline__ uint32_t extent(const uint32_t (&w)[N]) {
+  uint32_t mx = w[0], mn = w[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    mx = max2_nan(mx, w[i]);
+    mn = min2_nan(mn, w[i]);
+  }
+  mn ^= 0x80008000u;
+  // (the halves of each, beside one another)
+  return max2_nan(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
+}
+__device__ __forceinline__ Int4Grid grid_of(uint32_t e) { return int4_grid(-bf16_hi(e), bf16_lo(e)); }
+
+// Codes of N values (N / 2 words), the first in the low 4 bits.
+template <int N>
+__device__ __forceinline__ uint32_t codes(const uint32_t* w, const Int4Grid& q) {
+  uint32_t r = 0;
+  constexpr uint32_t bias = kInt4Bias * (N == 8 ? 0x11111111u : 0x1111u);
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) r = r * 16u + int4_code_biased(i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), q);
+  return (r - bias) & q.keep;
+}
+
+// The tokens of block blockIdx.x of call row b and where the block is.
+struct BlockSpan {
+  int t0;          // the block's first token, as an index into the row's new tokens (may be negative)
+  int cnt;
+  int64_t block;   // of the pool, for KV head 0
+  __device__ __forceinline__ bool has(int r) const { return t0 + r >= 0 && t0 + r < cnt; }
+};
+
+__device__ __forceinline__ bool find_block(const CacheView& c, int Hkv, int b, int start, int cnt, int t_max, int* err,
+                                           BlockSpan& s) {
+  const bool report = threadIdx.x == 0;
+  if (cnt < 0 || cnt > t_max) {
+    if (report && blockIdx.x == 0) raise_error(err, ERR_INDEX);
+    return false;
+  }
+  if (start < 0 && cnt > 0 && report && blockIdx.x == 0) raise_error(err, ERR_INDEX);  // (the tokens before 0)
+  if (cnt == 0) return false;
+  const int64_t at = static_cast<int64_t>(max(start, 0) / kInt4Block) + blockIdx.x;
+  const int64_t t0 = at * kInt4Block - start;
+  if (t0 >= cnt) return false;
+  const int bpp = c.P / kInt4Block;
+  const int64_t pi = at / bpp;
+  const int pg = pi < c.bt_stride ? c.block_table[static_cast<int64_t>(b) * c.bt_stride + pi] : -1;
+  if (pg < 0 || pg >= c.n_rows) {
+    if (report) raise_error(err, ERR_INDEX);
+    return false;
+  }
+  s.t0 = static_cast<int>(t0);
+  s.cnt = cnt;
+  s.block = static_cast<int64_t>(pg) * Hkv * bpp + (at - pi * bpp);
+  return true;
+}
+
+// Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so.
+template <int D, bool ROT>
+__device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* row, int d0, double inv, const float2* cs,
+                                          uint32_t (&w)[8]) {
+  const uint4 x0 = ld_nc_v4(row + d0), x1 = ld_nc_v4(row + d0 + 8);
+  w[0] = x0.x; w[1] = x0.y; w[2] = x0.z; w[3] = x0.w;
+  w[4] = x1.x; w[5] = x1.y; w[6] = x1.z; w[7] = x1.w;
+  if constexpr (ROT) {
+    const uint16_t* kn = a.k_norm;
+    auto normed = [&](uint32_t v, int d) {  // dims d, d + 1
+      if (!kn) return v;
+      return static_cast<uint32_t>(qk_norm_apply(static_cast<uint16_t>(v & 0xffffu), kn[d], inv)) |
+             (static_cast<uint32_t>(qk_norm_apply(static_cast<uint16_t>(v >> 16), kn[d + 1], inv)) << 16);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = normed(w[i], d0 + 2 * i);
+    if (d0 >= a.r) return;
+    const int half = a.r / 2;
+    uint32_t p[8];  // the dims they turn with
+    if (half % 16 == 0) {
+      const int p0 = d0 < half ? d0 + half : d0 - half;
+      const uint4 y0 = ld_nc_v4(row + p0), y1 = ld_nc_v4(row + p0 + 8);
+      p[0] = y0.x; p[1] = y0.y; p[2] = y0.z; p[3] = y0.w;
+      p[4] = y1.x; p[5] = y1.y; p[6] = y1.z; p[7] = y1.w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = normed(p[i], p0 + 2 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int d = d0 + i, pd = d < half ? d + half : d - half;
+        uint32_t v = 0;
+        if (d < a.r) {
+          v = row[pd];
+          if (kn) v = qk_norm_apply(static_cast<uint16_t>(v), kn[pd], inv);
+        }
+        p[i >> 1] = i & 1 ? p[i >> 1] | (v << 16) : v;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int d = d0 + i;
+      if (d < a.r) {
+        const bool first = d < half;
+        const float2 f = cs[first ? d : d - half];
+        const uint16_t x = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), y = static_cast<uint16_t>(p[i >> 1] >> (16 * (i & 1)));
+        // x c - y s, or y c + x s
+        const uint32_t v = bf16_dot2(x, __float_as_uint(f.x), y, __float_as_uint(f.y) ^ (first ? 0x80000000u : 0u));
+        w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | (v << 16) : (w[i >> 1] & 0xffff0000u) | v;
+      }
+    }
+  }
+}
+
+// One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V).
+// Tokens that the call does not bring stay as they are.
+template <int D, bool ROT>
+__global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const AppendArgs a) {
+  constexpr int NG = D / kInt4Group;
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  BlockSpan s;
+  if (!find_block(a.c, a.Hkv, b, a.start_index[b], a.count[b], a.Tmax, a.err, s)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int bpp = a.c.P / kInt4Block;
+  __shared__ float2 cs[ROT ? kInt4Block : 1][ROT ? D / 2 : 1];
+  if constexpr (ROT) {
+    const int half = a.r / 2;
+    const int64_t pos = a.start_pos ? a.start_pos[b] : 0;
+    for (int e = threadIdx.x; e < kInt4Block * half; e += blockDim.x) {
+      const int r = e / half, i = e - r * half;
+      if (s.has(r)) rope_cos_sin(pos + s.t0 + r, a.rope_step[i], cs[r][i].x, cs[r][i].y);
+    }
+    __syncthreads();
+  }
+  for (int task = warp; task < 2 * a.Hkv; task += blockDim.x >> 5) {
+    const int h = task >> 1;
+    const uint16_t* src = (task & 1 ? a.v : a.k) + ((static_cast<int64_t>(b) * a.in_T + a.row0 + s.t0) * a.Hkv + h) * D;
+    const int64_t pitch = static_cast<int64_t>(a.Hkv) * D;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(task & 1 ? a.c.v : a.c.k) + (s.block + static_cast<int64_t>(h) * bpp) * int4_block_bytes(D);
+    if ((task & 1) == 0) {
+      // keys: tokens g and g + 8, 16 dims a lane of every group
+      double inv[2] = {0.0, 0.0};
+      if (ROT && a.k_norm) {
+        for (int r = 0; r < kInt4Block; ++r) {
+          if (!s.has(r)) continue;
+          const double v = qk_norm_inv(src + r * pitch, D, a.norm_eps, lane);
+          if (r == g) inv[0] = v;
+          if (r == g + 8) inv[1] = v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        const bool on = s.has(r);
+        uint32_t pair[NG];
+#pragma unroll
+        for (int sec = 0; sec < D / 128; ++sec) {
+          uint32_t c[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[8] = {};
+            if (on) key_words<D, ROT>(a, src + r * pitch, sec * 128 + k * 64 + t * 16, inv[i], cs[ROT ? r : 0], w);
+            uint32_t e = extent(w);
+            e = max2_nan(e, __shfl_xor_sync(kFull, e, 1));
+            e = max2_nan(e, __shfl_xor_sync(kFull, e, 2));
+            const Int4Grid q = grid_of(e);
+            c[2 * k] = codes<8>(w, q);
+            c[2 * k + 1] = codes<8>(w + 4, q);
+            pair[sec * 2 + k] = q.pair;
+          }
+          if (on) *reinterpret_cast<uint4*>(dst + int4_key_word(r, sec * 16 + t * 2)) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+        if (on && t == 0) {
+          uint32_t* d = reinterpret_cast<uint32_t*>(dst + int4_pair(D, r, 0));
+          if constexpr (NG == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pair[0], pair[1]);
+          else *reinterpret_cast<uint4*>(d) = make_uint4(pair[0], pair[1], pair[2], pair[NG - 1]);
+        }
+      }
+    } else {
+      // values: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, 8 dims a lane of every group
+      int tok[4];
+      bool on[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        tok[i] = 2 * t + (i & 1) + 8 * (i >> 1);
+        on[i] = s.has(tok[i]);
+      }
+      uint32_t pair[4][NG];
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = on[i] ? ld_nc_v4(src + tok[i] * pitch + G * 64 + g * 8) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t half[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t e = extent(w);
+          e = max2_nan(e, __shfl_xor_sync(kFull, e, 4));
+          e = max2_nan(e, __shfl_xor_sync(kFull, e, 8));
+          e = max2_nan(e, __shfl_xor_sync(kFull, e, 16));
+          const Int4Grid q = grid_of(e);
+          half[i][0] = codes<4>(w, q) & 0xffffu;
+          half[i][1] = codes<4>(w + 2, q) & 0xffffu;
+          pair[i][G] = q.pair;
+        }
+        uint8_t* d = dst + G * 512 + lane * 16;
+        if (on[0] && on[1] && on[2] && on[3]) {
+          *reinterpret_cast<uint4*>(d) = make_uint4(half[0][0] | (half[1][0] << 16), half[0][1] | (half[1][1] << 16),
+                                                    half[2][0] | (half[3][0] << 16), half[2][1] | (half[3][1] << 16));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (on[i])
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint16_t*>(dst + int4_value_half(tok[i], G * 16 + g * 2 + j)) = static_cast<uint16_t>(half[i][j]);
+        }
+      }
+      if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!on[i]) continue;
+          uint32_t* d = reinterpret_cast<uint32_t*>(dst + int4_pair(D, tok[i], 0));
+          if constexpr (NG == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pair[i][0], pair[i][1]);
+          else *reinterpret_cast<uint4*>(d) = make_uint4(pair[i][0], pair[i][1], pair[i][2], pair[i][NG - 1]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- read back
+
+// Two codes (low 4 bits of each half of w) to their values as a bf16 pair, rounded
+// once: the codes become bf16 by their place in 128..143, exactly.
+__device__ __forceinline__ uint32_t values2(uint32_t w, uint32_t step2, uint32_t least2) {
+  uint32_t c, r;
+  const uint32_t x = (w & 0x000f000fu) | 0x43004300u;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0xc300c300u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(step2), "r"(least2));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMaxWarps * 32) int4_read_kernel(const ReadArgs a) {
+  constexpr int NG = D / kInt4Group;
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  BlockSpan s;
+  if (!find_block(a.c, a.Hkv, b, a.start_index[b], a.count[b], a.Tmax, a.err, s)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int bpp = a.c.P / kInt4Block;
+  for (int task = warp; task < 2 * a.Hkv; task += blockDim.x >> 5) {
+    const int h = task >> 1;
+    uint16_t* dst = (task & 1 ? a.v : a.k) + ((static_cast<int64_t>(b) * a.Tmax + s.t0) * a.Hkv + h) * D;
+    const int64_t pitch = static_cast<int64_t>(a.Hkv) * D;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(task & 1 ? a.c.v : a.c.k) + (s.block + static_cast<int64_t>(h) * bpp) * int4_block_bytes(D);
+    if ((task & 1) == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        if (!s.has(r)) continue;
+#pragma unroll
+        for (int sec = 0; sec < D / 128; ++sec) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + int4_key_word(r, sec * 16 + t * 2));
+          const uint2 pr = *reinterpret_cast<const uint2*>(src + int4_pair(D, r, sec * 2));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t pair = k ? pr.y : pr.x;
+            const uint32_t least2 = __byte_perm(pair, 0u, 0x1010), step2 = __byte_perm(pair, 0u, 0x3232);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = k ? (j ? x.w : x.z) : (j ? x.y : x.x);
+              // dims (0, 4), (1, 5), (2, 6), (3, 7)
+              const uint32_t v0 = values2(w, step2, least2), v1 = values2(w >> 4, step2, least2);
+              const uint32_t v2 = values2(w >> 8, step2, least2), v3 = values2(w >> 12, step2, least2);
+              *reinterpret_cast<uint4*>(dst + r * pitch + sec * 128 + k * 64 + t * 16 + j * 8) =
+                  make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632),
+                             __byte_perm(v2, v3, 0x7632));
+            }
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + G * 512 + lane * 16);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int r0 = 2 * t + 8 * p;
+          const uint32_t pa = *reinterpret_cast<const uint32_t*>(src + int4_pair(D, r0, G));
+          const uint32_t pb = *reinterpret_cast<const uint32_t*>(src + int4_pair(D, r0 + 1, G));
+          const uint32_t least2 = __byte_perm(pa, pb, 0x5410), step2 = __byte_perm(pa, pb, 0x7632);
+          uint32_t even[4], odd[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = p ? (j ? x.w : x.z) : (j ? x.y : x.x);
+            const uint32_t v0 = values2(w, step2, least2), v1 = values2(w >> 4, step2, least2);
+            const uint32_t v2 = values2(w >> 8, step2, least2), v3 = values2(w >> 12, step2, least2);
+            even[2 * j] = __byte_perm(v0, v1, 0x5410);
+            even[2 * j + 1] = __byte_perm(v2, v3, 0x5410);
+            odd[2 * j] = __byte_perm(v0, v1, 0x7632);
+            odd[2 * j + 1] = __byte_perm(v2, v3, 0x7632);
+          }
+          uint16_t* d = dst + r0 * pitch + G * 64 + g * 8;
+          if (s.has(r0)) *reinterpret_cast<uint4*>(d) = make_uint4(even[0], even[1], even[2], even[3]);
+          if (s.has(r0 + 1)) *reinterpret_cast<uint4*>(d + pitch) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+        }
+      }
+    }
+  }
+}
+
+// bf16 and E4M3 caches, paged or ring: one warp per token, 8 dims a lane and step.
+template <bool F8>
+__global__ void __launch_bounds__(kMaxWarps * 32) read_kernel(const ReadArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const CacheView& c = a.c;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kMaxWarps + (threadIdx.x >> 5);
+  const int cnt = a.count[b];
+  if (cnt < 0 || cnt > a.Tmax || (!c.paged && cnt > c.R)) {
+    if (t == 0 && lane == 0) raise_error(a.err, ERR_INDEX);
+    return;
+  }
+  if (t >= cnt) return;
+  const int64_t idx = static_cast<int64_t>(a.start_index[b]) + t;
+  int row = -1;
+  const int rows = c.paged ? c.P : c.R;  // of a head
+  if (idx >= 0) {
+    if (c.paged) {
+      if (idx / c.P < c.bt_stride) row = c.block_table[static_cast<int64_t>(b) * c.bt_stride + idx / c.P];
+    } else {
+      row = c.stream_rows ? c.stream_rows[b] : b;
+    }
+  }
+  if (row < 0 || row >= c.n_rows) {
+    if (lane == 0) raise_error(a.err, ERR_INDEX);
+    return;
+  }
+  const int64_t src0 = (static_cast<int64_t>(row) * a.Hkv * rows + idx % rows) * a.D;
+  const int64_t dst0 = (static_cast<int64_t>(b) * a.Tmax + t) * a.Hkv * a.D;
+  for (int e = lane; e < a.Hkv * a.D / 8; e += 32) {
+    const int h = e / (a.D / 8), d = (e - h * (a.D / 8)) * 8;
+    const int64_t o = src0 + static_cast<int64_t>(h) * rows * a.D + d;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint16_t* pool = i ? c.v : c.k;
+      uint4* dst = reinterpret_cast<uint4*>((i ? a.v : a.k) + dst0 + h * a.D + d);
+      if constexpr (F8) {
+        const float scale = i ? a.v_scale : a.k_scale;
+        const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(pool) + o);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t two = (j < 2 ? x.x : x.y) >> (16 * (j & 1));
+          w[j] = pack_bf16x2(e4m3_to_f32(static_cast<uint8_t>(two)) * scale, e4m3_to_f32(static_cast<uint8_t>(two >> 8)) * scale);
+        }
+        *dst = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        *dst = *reinterpret_cast<const uint4*>(pool + o);
+      }
+    }
+  }
+}
+
+// Blocks that `tokens` tokens in a row may touch.
+unsigned block_count(int tokens) { return static_cast<unsigned>((static_cast<int64_t>(tokens) + kInt4Block - 2) / kInt4Block + 1); }
+
+}  // namespace
+
+cudaError_t launch_append_int4(const AppendArgs& a, cudaStream_t s) {
+  const dim3 grid(block_count(a.Tmax), a.B), block(32 * (2 * a.Hkv < kMaxWarps ? 2 * a.Hkv : kMaxWarps));
+  const bool rot = a.rotate && (a.r > 0 || a.k_norm);
+  auto k = a.D == 128 ? (rot ? int4_append_kernel<128, true> : int4_append_kernel<128, false>)
+                      : (rot ? int4_append_kernel<256, true> : int4_append_kernel<256, false>);
+  return launch_pdl(k, grid, block, 0, s, a);
+}
+
+cudaError_t launch_read(const ReadArgs& a, bool int4, bool f8, cudaStream_t s) {
+  if (int4) {
+    const dim3 grid(block_count(a.Tmax), a.B), block(32 * (2 * a.Hkv < kMaxWarps ? 2 * a.Hkv : kMaxWarps));
+    return launch_pdl(a.D == 128 ? int4_read_kernel<128> : int4_read_kernel<256>, grid, block, 0, s, a);
+  }
+  const dim3 grid((static_cast<unsigned>(a.Tmax) + kMaxWarps - 1) / kMaxWarps, a.B);
+  return launch_pdl(f8 ? read_kernel<true> : read_kernel<false>, grid, dim3(kMaxWarps * 32), 0, s, a);
+}
+
+}  // namespace dattn

@@ -121,6 +121,7 @@ struct DecodeArgs {
   // cached value = e4m3 * scale. q_scale then includes k_scale.
   int f8;
   float k_scale, v_scale;
+  int int4;                    // 4-bit cache (int4_format.h): k, v of CacheView are byte arrays
 };
 
 // Page summaries: the bf16 mean of a page's stored keys (times k_scale), for
@@ -242,6 +243,18 @@ struct AppendArgs {
   const int32_t* parent;
 };
 
+// Cached entries [start_index, start_index + count) of each row back as bf16.
+struct ReadArgs {
+  CacheView c;
+  int B, Tmax, Hkv, D;
+  const int32_t* start_index;  // [B]
+  const int32_t* count;        // [B]
+  uint16_t* k;                 // out [B, Tmax, Hkv, D]
+  uint16_t* v;
+  float k_scale, v_scale;      // E4M3
+  int* err;
+};
+
 // Tensor-core pass of tree verify over each stream's paged prefix (stream-K
 // over (stream, KV head) units and their 128-key tiles; the G*T rows of a
 // unit are one 128-row MMA tile).
@@ -330,8 +343,12 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int ctas, cudaStream_t s, 
 // boxes of 16 rows x 64 dims.
 cudaError_t encode_cache_maps(const CacheView& c, int Hkv, int D, CUtensorMap* k, CUtensorMap* v, bool f8 = false);
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
-// decode over an E4M3 cache (decode_fp8.cu); GP = decode_group_pad(G)
+// the same into a 4-bit cache (no gather), and the read-back of any format
+cudaError_t launch_append_int4(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_read(const ReadArgs& a, bool int4, bool f8, cudaStream_t s);
+// decode over an E4M3 cache (decode_fp8.cu) and a 4-bit one (decode_int4.cu); GP = decode_group_pad(G)
 cudaError_t launch_decode_fp8(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl);
+cudaError_t launch_decode_int4(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_verify_split(const VerifySplitArgs& a, int D, cudaStream_t s);
 cudaError_t launch_verify_combine(const VerifyCombineArgs& a, int D, cudaStream_t s);
 // Keys per tile of the verify pass and its largest unit count.
@@ -351,8 +368,8 @@ cudaError_t encode_verify_maps(const CacheView& c, int Hkv, int D, const uint16_
 
 // Resident CTAs per SM of the decode kernel for (D, G) (0 if unsupported).
 int decode_ctas_per_sm(int D, int G);
-// Keys per stage tile of the decode kernel for (D, G).
-int decode_tile_keys(int D, int G, bool f8 = false);
+// Keys per stage tile of the decode kernel for (D, G) and a layer's kv_format.
+int decode_tile_keys(int D, int G, int format = 0);
 // Largest number of (stream, KV head) units of one decode call.
 int decode_max_units();
 

@@ -91,10 +91,29 @@ enum {
 /* Element format of a layer's K/V pools. */
 enum {
   DATTN_KV_BF16 = 0,  /* bf16 (raw 16-bit patterns)                                 */
-  DATTN_KV_E4M3 = 1   /* OCP FP8 E4M3 bytes; value = e4m3 * scale ("TensorFold PR
-                         #608" names the fp8 cache and leaves it out): decode and
-                         append only                                              */
+  DATTN_KV_E4M3 = 1,  /* OCP FP8 E4M3 bytes; value = e4m3 * scale ("TensorFold PR
+                         #608" names the fp8 cache and leaves it out): decode,
+                         append and read back only                                */
+  DATTN_KV_INT4 = 2   /* 4-bit codes with a least value and a step for each 64 dims
+                         of an entry (not on the pages; below): decode, append and
+                         read back of paged layers                                */
 };
+
+/* The 4-bit cache. Each entry is quantised as it is written: a group of 64 dims
+ * keeps its least value and step = bf16((most - least) / 15), and a code 0..15 for
+ * each dim, rint((x - least) / step), ties to even, which stands for least + code *
+ * step. (A step below 2^-100 is stored as 0. A group that holds a NaN, an infinity
+ * or a range past fp32 is stored as NaN as a whole.) Nothing is calibrated: the
+ * grid is each token's own. A pool is [pages, Hkv, DATTN_INT4_BYTES(P, D)] bytes,
+ * 4.5 bits for each value; P is a multiple of 16 (DATTN_EUNSUPPORTED otherwise).
+ * Sixteen tokens of a head are a block of 9 D bytes; token r of its block and dim d
+ * have their code in the low (even d) or high half of byte
+ *   K: (d / 128) 1024 + 64 r + ((d / 16) % 4) 16 + ((d / 64) % 2) 8 + (d % 16) / 2
+ *   V: (d / 64) 512 + (((d / 8) % 8) 4 + (r % 8) / 2) 16 + (r / 8) 8 + ((d / 4) % 2) 4
+ *      + (r % 2) 2 + (d % 4) / 2
+ * and the group's least value and step (bf16 each) at byte 8 D + (r D / 64 + d / 64) 4.
+ * What lies in a block beside the tokens written is never read as a value. */
+#define DATTN_INT4_BYTES(P, D) ((P) / 16 * 9 * (D))
 
 /* cudaStream_t without including the CUDA headers. */
 typedef struct CUstream_st* dattn_stream_t;
@@ -116,7 +135,7 @@ typedef struct {
   const uint16_t* q_norm_weight;
   const uint16_t* k_norm_weight;
   double norm_eps;    /* eps (>= 0) of both norms                               */
-  /* DATTN_KV_BF16 (0) or DATTN_KV_E4M3. An E4M3 layer's pools hold bytes
+  /* DATTN_KV_BF16 (0), DATTN_KV_E4M3 or DATTN_KV_INT4. An E4M3 layer's pools hold bytes
    * [.., D] instead of bf16; a cached K value is e4m3 * k_scale, a V value
    * e4m3 * v_scale (finite, > 0; quantisation divides by these fp32 values
    * in fp64). Decode scores the cache as stored, stores
@@ -124,7 +143,11 @@ typedef struct {
    * v_new / v_scale (ties to even, saturating at 448) and joins the new token
    * as stored; dattn_append_kv stores the same bytes. dattn_verify,
    * dattn_commit, dattn_prefill and dattn_decode_noalloc return
-   * DATTN_EUNSUPPORTED for such a layer. */
+   * DATTN_EUNSUPPORTED for such a layer.
+   * DATTN_KV_INT4 (paged layers): the same with the 4-bit form of the entry and of
+   * v_new; the scales are not read. The calls just named and dattn_sparse_decode
+   * and dattn_summarize return DATTN_EUNSUPPORTED: what they do over such a cache
+   * starts from dattn_read_kv (its entries appended to a bf16 layer, rotate = 0). */
   int kv_format;
   float k_scale;
   float v_scale;
@@ -157,7 +180,8 @@ typedef struct dattn_handle dattn_t;
  *          stream_rows[b] (identity when NULL); its valid slots are the
  *          ring_count[b] slots before ring_head[b]; the new entry is written
  *          at slot ring_head[b].
- *   paged: k, v = [n_rows (pages), Hkv, P, D] bf16. Token t of call row b is
+ *   paged: k, v = [n_rows (pages), Hkv, P, D] bf16 (4-bit: [n_rows, Hkv,
+ *          DATTN_INT4_BYTES(P, D)] bytes). Token t of call row b is
  *          offset t % P of page block_table[b * bt_stride + t / P]; the row
  *          holds seq_len[b] cached tokens; the new entry is written at token
  *          index seq_len[b].
@@ -242,6 +266,19 @@ DATTN_API int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, i
                     int max_tokens, const int32_t* start_index, const int32_t* start_pos,
                     const int32_t* count, const void* k, const void* v, int rotate,
                     dattn_stream_t stream);
+
+/* Cached entries back as bf16: token t < count[b] of call row b is read from cache
+ * index start_index[b] + t (as dattn_append_kv addresses them) into row t of k and v
+ * [B, max_tokens, Hkv, D]; rows t >= count[b] are left as they are. The entries as
+ * they are stored - keys with their rotation -, E4M3 times its scale, 4-bit values
+ * least + code * step, each rounded to the nearest bf16. Every cache format, paged
+ * and ring (at most R tokens of a row a call); state layers return
+ * DATTN_EUNSUPPORTED. A count outside 0..max_tokens, an index without a page and a
+ * row outside the pool are reported (DATTN_EINDEX) and their rows left as they are.
+ * One launch. */
+DATTN_API int dattn_read_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
+                            const int32_t* start_index, const int32_t* count, void* k, void* v,
+                            dattn_stream_t stream);
 
 /* Decode attention for one layer (see dattn_decode_args). One kernel launch.
  * On a state layer the step of linear attention: with lam = exp(log_decay),
