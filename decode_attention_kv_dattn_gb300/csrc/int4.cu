@@ -7,8 +7,6 @@
 // loads) is 16 bytes a lane in one piece, what it loads (or stores) of the bf16 rows
 // whole 128-byte lines, and a group's least and largest value are 2 (K) or 3 (V)
 // shuffles away.
-#include <cuda_bf16.h>
-
 #include "bf16_exact.h"
 #include "common.cuh"
 #include "int4_format.h"
@@ -52,13 +50,48 @@ __device__ __forceinline__ uint32_t extent(const uint32_t (&w)[N]) {
 }
 __device__ __forceinline__ Int4Grid grid_of(uint32_t e) { return int4_grid(-bf16_hi(e), bf16_lo(e)); }
 
-// Codes of N values (N / 2 words), the first in the low 4 bits.
+// Two floats at a time (the packed fp32 instructions: half the issue slots).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 wide2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+
+// Codes of N values (N / 2 words), the first in the low 4 bits: int4_code_biased of each.
 template <int N>
 __device__ __forceinline__ uint32_t codes(const uint32_t* w, const Int4Grid& q) {
-  uint32_t r = 0;
+  const F2 least = f2(-q.least, -q.least), inv = f2(q.inv, q.inv), step = f2(-q.step, -q.step), magic = f2(12582912.f, 12582912.f);
   constexpr uint32_t bias = kInt4Bias * (N == 8 ? 0x11111111u : 0x1111u);
+  uint32_t r = 0;
 #pragma unroll
-  for (int i = N - 1; i >= 0; --i) r = r * 16u + int4_code_biased(i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), q);
+  for (int i = N / 2 - 1; i >= 0; --i) {
+    const F2 d = add2(wide2(w[i]), least);
+    const F2 y = mul2(d, inv);
+    const F2 z = add2(fma2(fma2(y, step, d), inv, y), magic);
+    float c0, c1;
+    split(z, c0, c1);
+    r = (r * 16u + __float_as_uint(c1)) * 16u + __float_as_uint(c0);
+  }
   return (r - bias) & q.keep;
 }
 
@@ -95,63 +128,116 @@ __device__ __forceinline__ bool find_block(const CacheView& c, int Hkv, int b, i
   return true;
 }
 
+// cos and sin of pair j of the block's token r: pairs 2 c, 2 c + 1 as (cos, cos, sin, sin),
+// 16 bytes, in an order that spreads what 8 lanes (two tokens, four runs of 8 such) read
+// at a time over the banks.
+__device__ __forceinline__ int turn_at(int D, int r, int c) {
+  const int q = c >> 3;
+  return r * (D / 4) + (c & ~7) + ((c & 7) ^ ((q & 3) | ((r & 1) << 2)));
+}
+
+// Dims d, d + 1 (d even) of a key row, normalised and turned: bit for bit the entry
+// that every other path of the library stores. Out of line: the few values that the
+// short arithmetic below cannot decide, and rotations it does not take.
+__device__ __noinline__ uint32_t key_pair(const uint16_t* row, const uint16_t* kn, double inv, const float4* cs, int D, int tok, int r, int d) {
+  const int half = r / 2;
+  auto at = [&](int x) { return kn ? qk_norm_apply(row[x], kn[x], inv) : row[x]; };
+  uint32_t w = 0;
+  for (int x = d; x < d + 2; ++x) {
+    uint32_t v = at(x);
+    if (x < r) {
+      const bool first = x < half;
+      const int j = first ? x : x - half;
+      const float* f = reinterpret_cast<const float*>(cs + turn_at(D, tok, j >> 1)) + (j & 1);
+      // x c - y s, or y c + x s
+      v = bf16_dot2(static_cast<uint16_t>(v), __float_as_uint(f[0]), at(first ? x + half : x - half),
+                    __float_as_uint(f[2]) ^ (first ? 0x80000000u : 0u));
+    }
+    w = (w >> 16) | (v << 16);
+  }
+  return w;
+}
+
+// bf16 of two values known to within e0 and e1: false where that does not tell.
+__device__ __forceinline__ bool settled(F2 v, F2 e, uint32_t& w) {
+  float a, b, c, d;
+  split(add2(v, e), a, b);
+  split(fma2(e, f2(-1.f, -1.f), v), c, d);
+  w = pack_bf16x2(c, d);
+  return w == pack_bf16x2(a, b);
+}
+
 // Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so.
+// An entry is the bf16 nearest to the exact value. It is formed in fp32 with a bound
+// of its error - 2^-23 of the rotation's terms, 2^-22 of a normalised value, and 2^-110
+// for what underflows - and where both ends of the bound round alike, that is the
+// entry; about one value in 5,000 goes to key_pair instead (7 instructions a value
+// against ~30 of the exact sum: 64 ragged prompts 1,490 -> 233 us).
 template <int D, bool ROT>
-__device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* row, int d0, double inv, const float2* cs,
+__device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* row, int tok, int d0, double inv, const float4* cs,
                                           uint32_t (&w)[8]) {
   const uint4 x0 = ld_nc_v4(row + d0), x1 = ld_nc_v4(row + d0 + 8);
   w[0] = x0.x; w[1] = x0.y; w[2] = x0.z; w[3] = x0.w;
   w[4] = x1.x; w[5] = x1.y; w[6] = x1.z; w[7] = x1.w;
   if constexpr (ROT) {
-    const uint16_t* kn = a.k_norm;
-    auto normed = [&](uint32_t v, int d) {  // dims d, d + 1
-      if (!kn) return v;
-      return static_cast<uint32_t>(qk_norm_apply(static_cast<uint16_t>(v & 0xffffu), kn[d], inv)) |
-             (static_cast<uint32_t>(qk_norm_apply(static_cast<uint16_t>(v >> 16), kn[d + 1], inv)) << 16);
-    };
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = normed(w[i], d0 + 2 * i);
-    if (d0 >= a.r) return;
     const int half = a.r / 2;
-    uint32_t p[8];  // the dims they turn with
-    if (half % 16 == 0) {
-      const int p0 = d0 < half ? d0 + half : d0 - half;
-      const uint4 y0 = ld_nc_v4(row + p0), y1 = ld_nc_v4(row + p0 + 8);
-      p[0] = y0.x; p[1] = y0.y; p[2] = y0.z; p[3] = y0.w;
-      p[4] = y1.x; p[5] = y1.y; p[6] = y1.z; p[7] = y1.w;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = normed(p[i], p0 + 2 * i);
+    uint32_t open = 0;  // words that key_pair has to settle
+    if (half % 16 != 0) {
+      open = 0xffu;  // (a lane's dims may lie on both sides of the rotation's border)
     } else {
+      auto normed = [&](uint32_t (&x)[8], int d) {
+        if (!a.k_norm) return;
+        const uint4 k0 = ld_nc_v4(a.k_norm + d), k1 = ld_nc_v4(a.k_norm + d + 8);
+        const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        const float f = static_cast<float>(inv);
+        if (!(f >= 0x1p-120f && f <= 0x1p120f)) open = 0xffu;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d = d0 + i, pd = d < half ? d + half : d - half;
-        uint32_t v = 0;
-        if (d < a.r) {
-          v = row[pd];
-          if (kn) v = qk_norm_apply(static_cast<uint16_t>(v), kn[pd], inv);
+        for (int i = 0; i < 8; ++i) {
+          const F2 v = mul2(mul2(wide2(x[i]), wide2(kw[i])), f2(f, f));
+          float v0, v1;
+          split(v, v0, v1);
+          const F2 e = fma2(f2(fabsf(v0), fabsf(v1)), f2(0x1p-22f, 0x1p-22f), f2(0x1p-110f, 0x1p-110f));
+          if (!settled(v, e, x[i])) open |= 1u << i;
         }
-        p[i >> 1] = i & 1 ? p[i >> 1] | (v << 16) : v;
+      };
+      normed(w, d0);
+      if (d0 < a.r) {
+        const bool first = d0 < half;
+        const int p0 = first ? d0 + half : d0 - half;
+        const uint4 y0 = ld_nc_v4(row + p0), y1 = ld_nc_v4(row + p0 + 8);
+        uint32_t p[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        normed(p, p0);
+        const uint32_t sign = first ? 0x80008000u : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 f = cs[turn_at(D, tok, (first ? d0 : p0) / 2 + i)];
+          const F2 x = mul2(wide2(w[i]), f2(f.x, f.y));
+          const F2 v = fma2(wide2(p[i] ^ sign), f2(f.z, f.w), x);
+          float x0, x1, v0, v1;
+          split(x, x0, x1);
+          split(v, v0, v1);
+          const F2 e = fma2(f2(fabsf(x0) + fabsf(v0), fabsf(x1) + fabsf(v1)), f2(0x1p-23f, 0x1p-23f), f2(0x1p-110f, 0x1p-110f));
+          if (!settled(v, e, w[i])) open |= 1u << i;
+        }
       }
     }
+    while (open) {
+      const int i = __ffs(open) - 1;
+      open &= open - 1;
+      const uint32_t v = key_pair(row, a.k_norm, inv, cs, D, tok, a.r, d0 + 2 * i);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int d = d0 + i;
-      if (d < a.r) {
-        const bool first = d < half;
-        const float2 f = cs[first ? d : d - half];
-        const uint16_t x = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), y = static_cast<uint16_t>(p[i >> 1] >> (16 * (i & 1)));
-        // x c - y s, or y c + x s
-        const uint32_t v = bf16_dot2(x, __float_as_uint(f.x), y, __float_as_uint(f.y) ^ (first ? 0x80000000u : 0u));
-        w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | (v << 16) : (w[i >> 1] & 0xffff0000u) | v;
-      }
+      for (int j = 0; j < 8; ++j)
+        if (j == i) w[j] = v;
     }
   }
 }
 
 // One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V).
-// Tokens that the call does not bring stay as they are.
+// Tokens that the call does not bring stay as they are. Issue-bound, ~20 instructions a
+// value: 64 ragged prompts (133,000 tokens of 8 heads of 128, rotated) 233 us with 4
+// CTAs an SM, 254 with 3 and 236 with 5, where its 700 MB take 103.
 template <int D, bool ROT>
-__global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const AppendArgs a) {
   constexpr int NG = D / kInt4Group;
   pdl_wait();
   pdl_trigger();
@@ -160,13 +246,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const Appen
   if (!find_block(a.c, a.Hkv, b, a.start_index[b], a.count[b], a.Tmax, a.err, s)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int bpp = a.c.P / kInt4Block;
-  __shared__ float2 cs[ROT ? kInt4Block : 1][ROT ? D / 2 : 1];
+  __shared__ float4 cs[ROT ? kInt4Block * D / 4 : 1];
   if constexpr (ROT) {
     const int half = a.r / 2;
     const int64_t pos = a.start_pos ? a.start_pos[b] : 0;
     for (int e = threadIdx.x; e < kInt4Block * half; e += blockDim.x) {
       const int r = e / half, i = e - r * half;
-      if (s.has(r)) rope_cos_sin(pos + s.t0 + r, a.rope_step[i], cs[r][i].x, cs[r][i].y);
+      float* f = reinterpret_cast<float*>(cs + turn_at(D, r, i >> 1)) + (i & 1);
+      if (s.has(r)) rope_cos_sin(pos + s.t0 + r, a.rope_step[i], f[0], f[2]);
     }
     __syncthreads();
   }
@@ -177,42 +264,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const Appen
     uint8_t* dst = reinterpret_cast<uint8_t*>(task & 1 ? a.c.v : a.c.k) + (s.block + static_cast<int64_t>(h) * bpp) * int4_block_bytes(D);
     if ((task & 1) == 0) {
       // keys: tokens g and g + 8, 16 dims a lane of every group
-      double inv[2] = {0.0, 0.0};
+      double inv0 = 0.0, inv1 = 0.0;
       if (ROT && a.k_norm) {
         for (int r = 0; r < kInt4Block; ++r) {
           if (!s.has(r)) continue;
           const double v = qk_norm_inv(src + r * pitch, D, a.norm_eps, lane);
-          if (r == g) inv[0] = v;
-          if (r == g + 8) inv[1] = v;
+          if (r == g) inv0 = v;
+          if (r == g + 8) inv1 = v;
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = g + 8 * i;
+#pragma unroll 1
+      for (int x = 0; x < 2 * NG; ++x) {  // (group, token g or g + 8)
+        const int i = x & 1, r = g + 8 * i, G = x >> 1;
         const bool on = s.has(r);
-        uint32_t pair[NG];
-#pragma unroll
-        for (int sec = 0; sec < D / 128; ++sec) {
-          uint32_t c[4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t w[8] = {};
-            if (on) key_words<D, ROT>(a, src + r * pitch, sec * 128 + k * 64 + t * 16, inv[i], cs[ROT ? r : 0], w);
-            uint32_t e = extent(w);
-            e = max2_nan(e, __shfl_xor_sync(kFull, e, 1));
-            e = max2_nan(e, __shfl_xor_sync(kFull, e, 2));
-            const Int4Grid q = grid_of(e);
-            c[2 * k] = codes<8>(w, q);
-            c[2 * k + 1] = codes<8>(w + 4, q);
-            pair[sec * 2 + k] = q.pair;
-          }
-          if (on) *reinterpret_cast<uint4*>(dst + int4_key_word(r, sec * 16 + t * 2)) = make_uint4(c[0], c[1], c[2], c[3]);
-        }
-        if (on && t == 0) {
-          uint32_t* d = reinterpret_cast<uint32_t*>(dst + int4_pair(D, r, 0));
-          if constexpr (NG == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pair[0], pair[1]);
-          else *reinterpret_cast<uint4*>(d) = make_uint4(pair[0], pair[1], pair[2], pair[NG - 1]);
-        }
+        uint32_t w[8] = {};
+        if (on) key_words<D, ROT>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w);
+        uint32_t e = extent(w);
+        e = max2_nan(e, __shfl_xor_sync(kFull, e, 1));
+        e = max2_nan(e, __shfl_xor_sync(kFull, e, 2));
+        const Int4Grid q = grid_of(e);
+        if (!on) continue;
+        *reinterpret_cast<uint2*>(dst + int4_key_word(r, G * 8 + t * 2)) = make_uint2(codes<8>(w, q), codes<8>(w + 4, q));
+        if (t == 0) *reinterpret_cast<uint32_t*>(dst + int4_pair(D, r, G)) = q.pair;
       }
     } else {
       // values: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, 8 dims a lane of every group
@@ -223,8 +296,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const Appen
         tok[i] = 2 * t + (i & 1) + 8 * (i >> 1);
         on[i] = s.has(tok[i]);
       }
-      uint32_t pair[4][NG];
-#pragma unroll
+#pragma unroll 1
       for (int G = 0; G < NG; ++G) {
         uint4 x[4];
 #pragma unroll
@@ -241,7 +313,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const Appen
           const Int4Grid q = grid_of(e);
           half[i][0] = codes<4>(w, q) & 0xffffu;
           half[i][1] = codes<4>(w + 2, q) & 0xffffu;
-          pair[i][G] = q.pair;
+          if (g == 0 && on[i]) *reinterpret_cast<uint32_t*>(dst + int4_pair(D, tok[i], G)) = q.pair;
         }
         uint8_t* d = dst + G * 512 + lane * 16;
         if (on[0] && on[1] && on[2] && on[3]) {
@@ -254,15 +326,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_append_kernel(const Appen
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 *reinterpret_cast<uint16_t*>(dst + int4_value_half(tok[i], G * 16 + g * 2 + j)) = static_cast<uint16_t>(half[i][j]);
-        }
-      }
-      if (g == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!on[i]) continue;
-          uint32_t* d = reinterpret_cast<uint32_t*>(dst + int4_pair(D, tok[i], 0));
-          if constexpr (NG == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pair[i][0], pair[i][1]);
-          else *reinterpret_cast<uint4*>(d) = make_uint4(pair[i][0], pair[i][1], pair[i][2], pair[i][NG - 1]);
         }
       }
     }

@@ -48,12 +48,17 @@ DATTN_HD constexpr int int4_value_half(int r, int w) {
 DATTN_HD constexpr int int4_pair(int D, int r, int G) { return 8 * D + (r * (D / kInt4Group) + G) * 4; }
 
 struct Int4Grid {
-  float least, step, inv;  // inv = 1 / step, or 0 where the step is
+  float least, step, inv;  // inv = about 1 / step, or 0 where the step is
   uint32_t pair;           // as stored: least in the low half, step in the high half
   uint32_t keep;           // ~0, or 0 for a group stored as NaN (its codes are 0)
 };
 
 DATTN_HD uint32_t int4_bf16_bits(float x) {  // nearest bf16 of a finite x, ties to even
+#if defined(__CUDA_ARCH__)
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x));
+  return r;
+#endif
   const uint32_t b = f32_bits(x);
   return (b + 0x7fffu + ((b >> 16) & 1u)) >> 16;
 }
@@ -74,7 +79,9 @@ DATTN_HD Int4Grid int4_grid(float least, float most) {
   q.least = least;
   q.keep = ok ? 0xffffffffu : 0u;
 #if defined(__CUDA_ARCH__)
-  q.inv = s ? __frcp_rn(q.step) : 0.f;
+  float x;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(q.step));
+  q.inv = s ? x : 0.f;
 #else
   q.inv = s ? 1.f / q.step : 0.f;
 #endif
@@ -83,8 +90,10 @@ DATTN_HD Int4Grid int4_grid(float least, float most) {
 }
 
 // The code of x in the low 4 bits of the result, whose other bits are those of
-// kInt4Bias: the quotient correctly rounded (one correction; a tie of the exact
-// quotient is a tie of the rounded one), then rounded to a whole number by the add.
+// kInt4Bias: the quotient correctly rounded, then rounded to a whole number by the
+// add. y is off by 2 units at the most, its remainder is exact (a step has 8 bits),
+// and the correction by it, which the error of inv touches 2^22 times smaller, gives a
+// tie of the exact quotient as it is.
 constexpr uint32_t kInt4Bias = 0x4b400000u;  // 1.5 * 2^23
 DATTN_HD uint32_t int4_code_biased(float x, const Int4Grid& q) {
   const float d = f32_add(x, -q.least);
