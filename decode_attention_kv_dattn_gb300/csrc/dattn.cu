@@ -78,6 +78,10 @@ struct dattn_handle {
   uint64_t* sel_keys = nullptr;
   int32_t* sel_table = nullptr;
   int* sel_done = nullptr;
+  // Decode over 4-bit caches: the warps' states, then those of groups of CTAs; the units' new
+  // tokens. Two halves as above.
+  float* int4_part[2] = {nullptr, nullptr};
+  uint8_t* int4_token[2] = {nullptr, nullptr};
   std::vector<float*> decay;              // device, per layer ([Hkv][kDecayStride], state layers, or null)
   float* sums = nullptr;                  // state layers: the prompt form's slots, 2 x 16,384 elements and a note a CTA,
                                           // and two words
@@ -333,6 +337,52 @@ int sparse_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   return rc;
 }
 
+// Decode over a 4-bit cache (one launch).
+int int4_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args, int n_max, cudaStream_t s) {
+  const dattn_layer_config& L = h->layers[layer];
+  const int units = args->num_streams * h->Hkv;
+  // (blocks are counted in 32 bits)
+  if (static_cast<int64_t>(cache->n_rows) * h->Hkv * (L.page_size / kInt4Block) > INT32_MAX) return DATTN_EUNSUPPORTED;
+  if (static_cast<int64_t>(units) * ((static_cast<int64_t>(n_max) + kInt4Block - 1) / kInt4Block) > INT32_MAX / 2)
+    return DATTN_EUNSUPPORTED;
+  Int4DecodeArgs a{};
+  a.c = make_view(h, L, cache);
+  a.B = args->num_streams;
+  a.Hkv = h->Hkv;
+  a.G = h->G;
+  a.max_len = n_max;
+  a.q = static_cast<const uint16_t*>(args->q);
+  a.k_new = static_cast<const uint16_t*>(args->k_new);
+  a.v_new = static_cast<const uint16_t*>(args->v_new);
+  a.gate = static_cast<const uint16_t*>(args->gate);
+  a.pos = args->pos;
+  a.rope_step = h->rope_step[layer];
+  a.r = L.rotary_dim;
+  a.q_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(h->D)));
+  a.out = args->out;
+  a.write_back = args->write_back;
+  const unsigned half = h->decode_calls & 1u;
+  a.part = h->part[half];
+  a.wpart = h->int4_part[half];
+  a.gpart = a.wpart + static_cast<size_t>(h->num_sms) * kInt4Warps * h->GP * (h->D + 2);
+  a.token = h->int4_token[half];
+  a.counters = h->counters[half];
+  a.err = h->err;
+  a.early = !prev_launch_writes(s, cache->k);
+  a.wait_ns = h->wait_ns;
+  a.debug_flags = h->debug_flags;
+  a.q_norm = h->q_norm[layer];
+  a.k_norm = h->k_norm[layer];
+  a.norm_eps = L.norm_eps;
+  const int ctas = int4_decode_ctas(units, n_max, h->D, h->G, h->num_sms);
+  const int rc = cuda_status(launch_decode_int4(a, h->D, ctas, s), "4-bit decode");
+  if (rc == DATTN_OK) {
+    record_launch(s, args->write_back ? cache->k : nullptr);
+    ++h->decode_calls;
+  }
+  return rc;
+}
+
 // dattn_decode, and dattn_sparse_decode with a selection: one set of checks.
 int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                 const dattn_page_selection* sel, dattn_stream_t stream) {
@@ -374,18 +424,13 @@ int decode_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_dec
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
   if (sel) return sparse_call(h, layer, cache, args, sel, n_max, s);
-  const bool f8 = L.kv_format == DATTN_KV_E4M3, int4 = L.kv_format == DATTN_KV_INT4;
-  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, L.kv_format));
+  if (L.kv_format == DATTN_KV_INT4) return int4_call(h, layer, cache, args, n_max, s);
+  const bool f8 = L.kv_format == DATTN_KV_E4M3;
+  const int ctas = plan_decode_ctas(h->decode_resident, B * h->Hkv, n_max, decode_tile_keys(h->D, h->G, f8));
   if (static_cast<size_t>(ctas) + static_cast<size_t>(B) * h->Hkv > h->part_units) return DATTN_EXCEEDS;
   DecodeArgs da{};
   da.c = make_view(h, L, cache);
-  if (int4) {
-    // (blocks are counted in 32 bits)
-    if (static_cast<int64_t>(cache->n_rows) * h->Hkv * (L.page_size / kInt4Block) > INT32_MAX) return DATTN_EUNSUPPORTED;
-    da.int4 = 1;
-  } else if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) {
-    return DATTN_EUNSUPPORTED;
-  }
+  if (encode_cache_maps(da.c, h->Hkv, h->D, &da.tmap_k, &da.tmap_v, f8) != cudaSuccess) return DATTN_EUNSUPPORTED;
   da.B = B;
   da.Hkv = h->Hkv;
   da.G = h->G;
@@ -610,12 +655,21 @@ int dattn_create(const dattn_config* cfg, int device, dattn_t** out) {
   // then one per CTA (the group counters of units merged in two levels).
   if (static_cast<int64_t>(h->max_streams) * Hkv > decode_max_units()) return fail(DATTN_EUNSUPPORTED);
   h->part_units = static_cast<size_t>(h->decode_resident) + static_cast<size_t>(h->max_streams) * Hkv;
+  // (4-bit caches: one CTA an SM at the most, which decode_resident covers)
   // (the attention over selected pages runs two CTAs an SM)
   if (sel_pitch > 0) h->part_units = std::max(h->part_units, static_cast<size_t>(2 * h->num_sms));
   for (int i = 0; i < 2; ++i) {
     const size_t nc = static_cast<size_t>(h->max_streams) * Hkv + static_cast<size_t>(h->decode_resident);
     if (cudaMalloc(&h->counters[i], nc * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
     if (cudaMemset(h->counters[i], 0, nc * sizeof(int)) != cudaSuccess) return fail(DATTN_ECUDA);
+  }
+  const bool has_int4 = std::any_of(h->layers.begin(), h->layers.end(),
+                                    [](const dattn_layer_config& L) { return L.kv_format == DATTN_KV_INT4; });
+  for (int i = 0; i < 2 && has_int4; ++i) {
+    const size_t states = static_cast<size_t>(h->num_sms) * (kInt4Warps + 1) * h->GP * (D + 2);
+    const size_t tokens = static_cast<size_t>(h->max_streams) * Hkv * int4_token_bytes(D, h->GP);
+    if (cudaMalloc(&h->int4_part[i], states * sizeof(float)) != cudaSuccess) return fail(DATTN_ECUDA);
+    if (cudaMalloc(&h->int4_token[i], tokens) != cudaSuccess) return fail(DATTN_ECUDA);
   }
   if (cudaMalloc(&h->tiles, (4 * static_cast<size_t>(h->max_streams) * Hkv + 1) * sizeof(int)) != cudaSuccess)
     return fail(DATTN_ECUDA);
@@ -655,6 +709,10 @@ void dattn_destroy(dattn_t* h) {
   for (int i = 0; i < 2; ++i) {
     cudaFree(h->part[i]);
     cudaFree(h->counters[i]);
+  }
+  for (int i = 0; i < 2; ++i) {
+    cudaFree(h->int4_part[i]);
+    cudaFree(h->int4_token[i]);
   }
   cudaFree(h->vpart);
   cudaFree(h->sel_scores);

@@ -62,7 +62,6 @@
 //    rescaled only when some head's running maximum moved.
 #include "bf16_exact.h"
 #include "common.cuh"
-#include "decode_int4.cuh"
 #include "qk_norm.cuh"
 #include "round_f64.h"
 #include "mma.cuh"
@@ -72,35 +71,24 @@ namespace dattn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-// Cache formats (DATTN_KV_*), the kernels' template parameter FMT.
-constexpr int kFmtBf16 = 0, kFmtE4m3 = 1, kFmtInt4 = 2;
-#ifndef DATTN_INT4_W128
-#define DATTN_INT4_W128 11
-#endif
-#ifndef DATTN_INT4_W256
-#define DATTN_INT4_W256 11
-#endif
 // Streaming warps of a kernel variant: 4 with 16 KB stage tiles, or 7 with
 // 8 KB tiles for E4M3 at D = 256, so that every SM sub-partition runs two
 // warps (7 streaming + the helper; 255 registers a thread still fit each
 // sub-partition's register file) that hide one another's conversion chains:
 // 128k x 8 streams 241 -> 230 us per call. At D = 128 the same split measured
 // slower (bf16 paged batch 106 -> 121 us, E4M3 133 -> 149 us).
-template <int D, int NT, int FMT>
+template <int D, int NT, bool F8>
 constexpr int stream_warps() {
-  if (FMT == kFmtInt4) return NT == 1 ? (D == 128 ? DATTN_INT4_W128 : DATTN_INT4_W256) : (D == 128 ? 11 : 7);
-  return (FMT == kFmtE4m3 && D == 256) ? 7 : 4;
+  return (F8 && D == 256) ? 7 : 4;
 }
 // Stage tiles per streaming warp, and bytes of K and V in one stage tile.
-template <int D, int NT, int FMT>
+template <int D, int NT, bool F8>
 constexpr int stage_count() {
-  if (FMT == kFmtInt4) return D == 256 && NT == 2 ? 2 : 3;
   return 3;
 }
-template <int D, int NT, int FMT>
+template <int D, int NT, bool F8>
 constexpr int stage_bytes() {
-  if (FMT == kFmtInt4) return (D == 256 && NT == 1 ? 1 : 2) * 18 * D;
-  return stream_warps<D, NT, FMT>() > 4 ? 8192 : 16384;
+  return stream_warps<D, NT, F8>() > 4 ? 8192 : 16384;
 }
 constexpr int kMaxUnits = 512;           // (stream, KV head) units per call
 constexpr int kGroup = 16;               // keys per MMA group
@@ -114,10 +102,6 @@ constexpr int64_t kPrefetchLines = 1 << 15;  // largest page table (128-byte lin
 #define DATTN_SEGMENT_COST 12
 #endif
 constexpr int kSegmentCost = DATTN_SEGMENT_COST;
-#ifndef DATTN_INT4_SEGMENT_COST
-#define DATTN_INT4_SEGMENT_COST 40
-#endif
-constexpr int kInt4SegmentCost = DATTN_INT4_SEGMENT_COST;
 #ifndef DATTN_MERGE_BATCH
 #define DATTN_MERGE_BATCH 8
 #endif
@@ -134,21 +118,19 @@ constexpr int kPiecesSlack = DATTN_PIECES_SLACK;
 template <int D>
 constexpr bool kGroupBox = D == 128;
 
-template <int HEAD_DIM, int NT, int FMT = kFmtBf16>
+template <int D, int NT, bool F8 = false>
 struct Geo {
-  static constexpr int D = HEAD_DIM;
-  static constexpr bool F8 = FMT == kFmtE4m3, INT4 = FMT == kFmtInt4;
-  static constexpr int W = stream_warps<D, NT, FMT>();  // streaming warps; the helper is warp W
+  static constexpr int W = stream_warps<D, NT, F8>();  // streaming warps; the helper is warp W
   static constexpr int THREADS = (W + 1) * 32;
   static constexpr int GP = 4 * NT;                  // heads per partial slot
   static constexpr int KSTEPS = D / 16;              // MMA k-steps of a score, m-tiles of an output
   static constexpr int ROWB = F8 ? D : 2 * D;        // bytes of one cached row (bf16, or E4M3)
   static constexpr int BOXES = ROWB / 128;           // 128-byte boxes per 16-row group of K (or V)
-  static constexpr int GBYTES = INT4 ? int4_block_bytes(D) : BOXES * kBoxBytes;  // K (or V) bytes of one group
-  static constexpr int KG = stage_bytes<D, NT, FMT>() / (2 * GBYTES);  // groups per stage tile
+  static constexpr int GBYTES = BOXES * kBoxBytes;   // K (or V) bytes of one group
+  static constexpr int KG = stage_bytes<D, NT, F8>() / (2 * 16 * ROWB);  // groups per stage tile
   static constexpr int KHALF = KG * GBYTES;          // K part of a stage; V follows
   static constexpr int STAGE = 2 * KHALF;
-  static constexpr int NS = stage_count<D, NT, FMT>();
+  static constexpr int NS = stage_count<D, NT, F8>();
   // mbarriers: [W][NS] stages, 2 input slots, then the four hand-offs
   // between the streaming warps and the helper
   static constexpr int NBAR = W * NS + 2 + 4;
@@ -180,12 +162,9 @@ struct Geo {
   static constexpr int IN_BYTES = (IN_WB + 8 + 15) / 16 * 16;
   static constexpr int IN_OFF = (STEP_OFF + D / 2 * 8 + 15) / 16 * 16;  // 2 input slots
   static constexpr int TAB_OFF = IN_OFF + 2 * IN_BYTES;
-  // 4-bit caches: q's fragments of two units where they are kept here
-  static constexpr int QF_OFF = (TAB_OFF + (4 * kMaxUnits + 1) * 4 + 15) / 16 * 16;
-  static constexpr int QF_BYTES = INT4 && Int4Warp<D, NT>::kSharedQ ? Int4Warp<D, NT>::kQBytes : 0;
-  static constexpr int SMEM_MAX = QF_BYTES ? 1024 + QF_OFF + 2 * QF_BYTES : 1024 + TAB_OFF + (4 * kMaxUnits + 1) * 4;  // P, N, ring head/row
+  static constexpr int SMEM_MAX = 1024 + TAB_OFF + (4 * kMaxUnits + 1) * 4;  // P, N, ring head/row
   static_assert(D == 128 || D == 256, "head_dim");
-  static_assert(KG >= 1 && KG * 2 * GBYTES == STAGE && (INT4 || GBYTES == 16 * ROWB), "a stage tile holds whole 16-row groups");
+  static_assert(KG >= 1 && KG * 2 * 16 * ROWB == STAGE, "a stage tile holds whole 16-row groups");
   static_assert(GP * D * 4 <= STAGE, "a stage buffer holds one warp's partial output");
   static_assert(NS < kWin, "issue runs at most one window ahead");
   static_assert(SMEM_MAX <= 232448, "shared memory per CTA");
@@ -295,34 +274,13 @@ __device__ __forceinline__ void prep_q(const DecodeArgs& a, const uint16_t* src,
   }
 }
 
-// Least and greatest that keep a NaN.
-__device__ __forceinline__ float fmin_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float fmax_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Dim d of the new token as a 4-bit cache holds it (side 0: its key, 1: its value),
-// from the packed form that prep_token leaves.
-template <int D>
-__device__ __forceinline__ float int4_new(const uint8_t* packed, int side, int d) {
-  const uint32_t pair = reinterpret_cast<const uint32_t*>(packed + D)[side * (D / 64) + (d >> 6)];
-  const uint32_t code = (packed[side * (D / 2) + (d >> 1)] >> (4 * (d & 1))) & 15u;
-  return fmaf(static_cast<float>(code), bf16_hi(pair), bf16_lo(pair));
-}
-
 // The new token of a unit from its input slot: its K entry (the bf16 nearest
 // to the exact rotation with the cos/sin in cs - the value that is scored and
 // stored), its score per head (base 2, with the rotated q in qs) and the
 // heads' sigmoid(gate) (gate_raw: the bf16 logit of head t, for t < G), all
 // into the slot. Starts after cs and qs are complete for the team; ends with a
 // team barrier.
-template <int D, int GP, int FMT, int NTH>
+template <int D, int GP, int NTH>
 __device__ __forceinline__ void prep_token(const DecodeArgs& a, const float* qs, const float2* cs, uint8_t* slot,
                                            uint16_t gate_raw, int t) {
   using Gm = Geo<D, GP / 4>;
@@ -345,7 +303,7 @@ __device__ __forceinline__ void prep_token(const DecodeArgs& a, const float* qs,
       const float2 q = cs[e - half];  // y c + x s with y = k[e], x = k[e - half]
       v = bf16_dot2(ksrc[e], __float_as_uint(q.x), ksrc[e - half], __float_as_uint(q.y));
     }
-    if (FMT != kFmtInt4 && a.f8) {
+    if (a.f8) {
       k8[e] = e4m3_from_f64(static_cast<double>(bf16_to_f32(v)) / static_cast<double>(a.k_scale));
       k8[D + e] = e4m3_from_f64(static_cast<double>(bf16_to_f32(vsrc[e])) / static_cast<double>(a.v_scale));
     } else {
@@ -355,32 +313,10 @@ __device__ __forceinline__ void prep_token(const DecodeArgs& a, const float* qs,
   team_sync<NTH>();
   constexpr int W = NTH / 32;
   const int w = t >> 5, lane = t & 31;
-  if constexpr (FMT == kFmtInt4) {
-    // 4-bit cache: the entry and v_new as they are stored, over the raw key: the codes
-    // of both (in the dims' order), then the grids' pairs. A warp takes a group, two
-    // dims a lane.
-    uint8_t* packed = slot + Gm::IN_K;
-    for (int x = w; x < D / 32; x += W) {
-      const int G = x >> 1;
-      const uint32_t two = *reinterpret_cast<const uint32_t*>((x & 1 ? vsrc : kh) + G * 64 + 2 * lane);
-      float lo = fmin_nan(bf16_lo(two), bf16_hi(two)), hi = fmax_nan(bf16_lo(two), bf16_hi(two));
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        lo = fmin_nan(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmax_nan(hi, __shfl_xor_sync(kFull, hi, o));
-      }
-      const Int4Grid q = int4_grid(lo, hi);
-      packed[(x & 1) * (D / 2) + G * 32 + lane] =
-          static_cast<uint8_t>(int4_code(bf16_lo(two), q) | (int4_code(bf16_hi(two), q) << 4));
-      if (lane == 0) reinterpret_cast<uint32_t*>(packed + D)[(x & 1) * (D / 64) + G] = q.pair;
-    }
-    fence_proxy_async_smem();  // the slot is refilled by bulk copies later
-    team_sync<NTH>();
-  }
   for (int g = w; g < G; g += W) {
     float dot = 0.f;
     for (int d = lane; d < D; d += 32)
-      dot = fmaf(qs[g * D + d], FMT == kFmtInt4 ? int4_new<D>(slot + Gm::IN_K, 0, d) : a.f8 ? e4m3_to_f32(k8[d]) : bf16_to_f32(kh[d]), dot);
+      dot = fmaf(qs[g * D + d], a.f8 ? e4m3_to_f32(k8[d]) : bf16_to_f32(kh[d]), dot);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
     if (lane == 0) sn[g] = dot;
@@ -431,7 +367,7 @@ __device__ __forceinline__ int64_t write_back_offset(const DecodeArgs& a, int b,
 // Each thread takes 8 consecutive dims of one head; `states(g, d, mg)` folds
 // the unit's segment states for head g, dims d..d+7 into mg. Needs the new
 // token in the unit's input slot. No barrier at the end.
-template <int D, int GP, bool PAGED, int FMT, int NTH, typename States>
+template <int D, int GP, bool PAGED, int NTH, typename States>
 __device__ __forceinline__ void finish_unit(const DecodeArgs& a, int u, const uint8_t* slot, int t,
                                             States states) {
   using Gm = Geo<D, GP / 4>;
@@ -447,10 +383,7 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, int u, const ui
     Merge8 mg;
     mg.M = sn[g];
     mg.L = 1.f;
-    if constexpr (FMT == kFmtInt4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mg.o[i] = int4_new<D>(slot + Gm::IN_K, 1, d + i);
-    } else if (a.f8) {
+    if (a.f8) {
       const uint8_t* v8 = slot + Gm::IN_KH + D;  // the new token's V as stored
 #pragma unroll
       for (int i = 0; i < 8; ++i) mg.o[i] = e4m3_to_f32(v8[d + i]) * a.v_scale;
@@ -471,24 +404,7 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, int u, const ui
   // reading; its target was worked out when the unit's inputs were prepared
   if (a.write_back) {
     const int64_t wb = *reinterpret_cast<const int64_t*>(slot + Gm::IN_WB);
-    if constexpr (FMT == kFmtInt4) {
-      if (wb >= 0) {
-        // wb counts elements: D a token
-        const int64_t token = wb / D;
-        const int r = static_cast<int>(token % kInt4Block);
-        const int64_t base = token / kInt4Block * int4_block_bytes(D);
-        uint8_t* kd = reinterpret_cast<uint8_t*>(c.k) + base;
-        uint8_t* vd = reinterpret_cast<uint8_t*>(c.v) + base;
-        const uint8_t* packed = slot + Gm::IN_K;
-        for (int w = t; w < D / 8; w += NTH)
-          *reinterpret_cast<uint32_t*>(kd + int4_key_word(r, w)) = reinterpret_cast<const uint32_t*>(packed)[w];
-        for (int w = t; w < D / 4; w += NTH)
-          *reinterpret_cast<uint16_t*>(vd + int4_value_half(r, w)) = reinterpret_cast<const uint16_t*>(packed + D / 2)[w];
-        for (int x = t; x < D / 32; x += NTH)
-          *reinterpret_cast<uint32_t*>((x < D / 64 ? kd : vd) + int4_pair(D, r, x % (D / 64))) =
-              reinterpret_cast<const uint32_t*>(packed + D)[x];
-      }
-    } else if (wb >= 0 && a.f8) {
+    if (wb >= 0 && a.f8) {
       // E4M3 rows: wb counts elements, which are bytes here
       const uint8_t* k8 = slot + Gm::IN_KH;
       for (int d = t * 16; d < D; d += NTH * 16) {
@@ -507,10 +423,10 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, int u, const ui
 
 // The streaming warps' states of one segment (merge buffers: warp w's stage
 // SLOT[w], or none when SLOT[w] < 0) folded into mg for head g, dims d..d+7.
-template <int D, int NT, int FMT>
+template <int D, int NT, bool F8>
 __device__ __forceinline__ void fold_warps(const uint8_t* smem, const float* ML, const int* SLOT, int g, int d,
                                            Merge8& mg) {
-  using Gm = Geo<D, NT, FMT>;
+  using Gm = Geo<D, NT, F8>;
   constexpr int kWarps = Gm::W;
   constexpr int GP = Gm::GP;
 #pragma unroll
@@ -528,10 +444,10 @@ __device__ __forceinline__ void fold_warps(const uint8_t* smem, const float* ML,
 // The streaming warps' states of one segment merged into the partial slot
 // dst: o[GP][D] (relative to the merged maximum), then m[GP], l[GP]. No
 // barrier at the end.
-template <int D, int NT, int FMT, int NTH>
+template <int D, int NT, bool F8, int NTH>
 __device__ __forceinline__ void write_partial(const uint8_t* smem, const float* ML, const int* SLOT, float* dst,
                                               int t) {
-  using Gm = Geo<D, NT, FMT>;
+  using Gm = Geo<D, NT, F8>;
   constexpr int kWarps = Gm::W;
   constexpr int GP = Gm::GP;
   for (int e = t * 8; e < GP * D; e += NTH * 8) {
@@ -638,7 +554,7 @@ __device__ __forceinline__ void fold_slots(const float* part, int k0, int k1, Ok
 // counters), and the CTA that finishes the last group merges the groups'
 // results with the new token. Called by the whole CTA after its piece's
 // partial is stored and published.
-template <int D, int GP, bool PAGED, int FMT, int NTH, typename WaitPrev>
+template <int D, int GP, bool PAGED, int NTH, typename WaitPrev>
 __device__ void merge_in_groups(const DecodeArgs& a, int U, int pieces, int u, int cta, int unit_tiles,
                                 const uint8_t* slot, int* flag, int t, WaitPrev wait_prev) {
   constexpr int stride = GP * (D + 2);
@@ -706,7 +622,7 @@ __device__ void merge_in_groups(const DecodeArgs& a, int U, int pieces, int u, i
   auto group_ok = [&](int gi) { return group_first(gi * kMergeBatch) >= 0; };
   auto group_slot = [&](int gi) { return piece_slot(group_first(gi * kMergeBatch)); };
   const int ng = (S + kMergeBatch - 1) / kMergeBatch;
-  finish_unit<D, GP, PAGED, FMT, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
+  finish_unit<D, GP, PAGED, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
     fold_slots<D, GP>(a.part, 0, ng, group_ok, group_slot, g, d, mg);
   });
   if (t == 0) a.counters[u] = 0;
@@ -719,7 +635,7 @@ __device__ void merge_in_groups(const DecodeArgs& a, int U, int pieces, int u, i
 // segment's partial slot, and the CTA finishing the unit's last segment (a
 // per-unit counter) merges all of its partials. `release()` runs once the
 // merge buffers have been read; `wait_prev()` before the first output store.
-template <int D, int NT, bool PAGED, int FMT, int NTH, typename WaitPrev, typename Release>
+template <int D, int NT, bool PAGED, bool F8, int NTH, typename WaitPrev, typename Release>
 __device__ void end_segment(const DecodeArgs& a, const Split& sp, int pieces, int u, bool first_seg, int cta,
                             const uint8_t* smem, const float* ML, const int* SLOT, const uint8_t* slot, int* flag,
                             int t, WaitPrev wait_prev, Release release) {
@@ -737,21 +653,21 @@ __device__ void end_segment(const DecodeArgs& a, const Split& sp, int pieces, in
   if (nseg == 1) {
     // the whole unit lies in this CTA: the warps' states go straight into the output
     wait_prev();
-    finish_unit<D, GP, PAGED, FMT, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
-      fold_warps<D, NT, FMT>(smem, ML, SLOT, g, d, mg);
+    finish_unit<D, GP, PAGED, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
+      fold_warps<D, NT, F8>(smem, ML, SLOT, g, d, mg);
     });
     team_sync<NTH>();
     release();
     return;
   }
   const int pslot = first_seg ? cta : NC + u;
-  write_partial<D, NT, FMT, NTH>(smem, ML, SLOT, a.part + static_cast<int64_t>(pslot) * (GP * (D + 2)), t);
+  write_partial<D, NT, F8, NTH>(smem, ML, SLOT, a.part + static_cast<int64_t>(pslot) * (GP * (D + 2)), t);
   __threadfence();
   team_sync<NTH>();
   release();
   if constexpr (NTH != 32) {
     if (pieces && S > 2 * kMergeBatch) {
-      merge_in_groups<D, GP, PAGED, FMT, NTH>(a, sp.U, pieces, u, cta, p1 - p0, slot, flag, t, wait_prev);
+      merge_in_groups<D, GP, PAGED, NTH>(a, sp.U, pieces, u, cta, p1 - p0, slot, flag, t, wait_prev);
       return;
     }
   }
@@ -778,7 +694,7 @@ __device__ void end_segment(const DecodeArgs& a, const Split& sp, int pieces, in
     return k == 0 || sp.has_tiles_inside(c_lo + k);
   };
   const int stride = GP * (D + 2);
-  finish_unit<D, GP, PAGED, FMT, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
+  finish_unit<D, GP, PAGED, NTH>(a, u, slot, t, [&](int g, int d, Merge8& mg) {
     // kMergeBatch partials' loads in flight at a time: a long stream's last
     // segment merges ~76 of them, and each batch is one L2 round trip
     for (int k0 = 0; k0 < S; k0 += kMergeBatch) {
@@ -808,10 +724,9 @@ __device__ void end_segment(const DecodeArgs& a, const Split& sp, int pieces, in
   team_sync<NTH>();
 }
 
-template <int D, int NT, bool PAGED, int FMT>
-__global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  using Gm = Geo<D, NT, FMT>;
-  constexpr bool F8 = Gm::F8, INT4 = Gm::INT4;
+template <int D, int NT, bool PAGED, bool F8>
+__global__ void __launch_bounds__(Geo<D, NT, F8>::THREADS, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using Gm = Geo<D, NT, F8>;
   constexpr int kWarps = Gm::W, kHelper = Gm::W, kThreads = Gm::THREADS;
   constexpr int GP = Gm::GP, KSTEPS = Gm::KSTEPS, BOXES = Gm::BOXES, KG = Gm::KG, NS = Gm::NS;
   extern __shared__ uint8_t smem_raw[];
@@ -839,7 +754,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
   const uint32_t merge_full = smem_addr(smem + Gm::MERGE_FULL_OFF);
   const uint32_t merge_empty = smem_addr(smem + Gm::MERGE_EMPTY_OFF);
 
-  if (!INT4 && threadIdx.x == 32) {
+  if (threadIdx.x == 32) {
     prefetch_tmap(&a.tmap_k);
     prefetch_tmap(&a.tmap_v);
   }
@@ -980,8 +895,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
                 raise_error(a.err, ERR_INDEX);
                 pg = 0;
               }
-              // (the first tensor row, or the block of a 4-bit cache)
-              rows[kg] = INT4 ? (pg * Hkv + j) * gpp + gr : (pg * Hkv + j) * c.P + gr * kGroup;
+              rows[kg] = (pg * Hkv + j) * c.P + gr * kGroup;
               masks[kg] = static_cast<int>(row_bits(0, min(c.P - gr * kGroup, n - (pi * c.P + gr * kGroup))));
             }
           }
@@ -1020,11 +934,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
     uint32_t copies = 0;
     // The K and V rows of group kg of a stage from tensor row row0 on.
     auto load_group = [&](uint32_t kd, int kg, int row0, uint32_t bar) {
-      if constexpr (INT4) {
-        const int64_t at = static_cast<int64_t>(row0) * Gm::GBYTES;
-        bulk_copy_g2s(kd + kg * Gm::GBYTES, reinterpret_cast<const uint8_t*>(c.k) + at, Gm::GBYTES, bar, policy);
-        bulk_copy_g2s(kd + Gm::KHALF + kg * Gm::GBYTES, reinterpret_cast<const uint8_t*>(c.v) + at, Gm::GBYTES, bar, policy);
-      } else if constexpr (kGroupBox<D> || F8) {
+      if constexpr (kGroupBox<D> || F8) {
         // one box per group: 16 rows x every 128-byte region
         tma_load_3d(kd + kg * Gm::GBYTES, &a.tmap_k, 0, row0, 0, bar, policy);
         tma_load_3d(kd + Gm::KHALF + kg * Gm::GBYTES, &a.tmap_v, 0, row0, 0, bar, policy);
@@ -1155,14 +1065,8 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
       // fg of tile t holds one head's hi or lo part
       if (!failed) check(mbar_wait_bounded(prep_full, seg & 1, a.wait_ns));
       uint32_t qb[KSTEPS][NT][2];
-      Int4Warp<D, NT> q4;
-      const uint8_t* qf = smem + Gm::QF_OFF + (seg & 1) * Gm::QF_BYTES;
-      if constexpr (INT4) {
-        q4.get_query(qs, qf, lane);
-        q4.clear();
-      }
 #pragma unroll
-      for (int t = 0; t < (INT4 ? 0 : NT); ++t) {
+      for (int t = 0; t < NT; ++t) {
         const int head = NT == 1 ? (fg & 3) : fg;
         const bool lo = NT == 1 ? fg >= 4 : t == 1;
         const float* src = qs + head * D;
@@ -1230,11 +1134,6 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
             if (mask == 0u) continue;  // no valid row (past a unit's end, or a ring's unwritten block)
             const uint32_t kbase = wsm_a + stg * Gm::STAGE + kg * Gm::GBYTES;
             const uint32_t vbase = kbase + Gm::KHALF;
-            if constexpr (INT4) {
-              const uint8_t* kb = wsm + stg * Gm::STAGE + kg * Gm::GBYTES;
-              q4.block(kb, kb + Gm::KHALF, mask, qf, lane);
-              continue;
-            }
             if (mask != 0xffffu) {
               // zero the V rows of invalid keys (their probabilities are 0, but
               // the rows may hold NaN and 0 * NaN is NaN)
@@ -1402,7 +1301,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
       // merge buffer as o[head][dim] (hi + lo columns). The previous
       // segment's buffers must have been read first (ML and SLOT are reused).
 #pragma unroll
-      for (int e = 0; e < (INT4 ? 0 : 2); ++e) {
+      for (int e = 0; e < 2; ++e) {
         l_run[e] += __shfl_xor_sync(kFull, l_run[e], 4);
         l_run[e] += __shfl_xor_sync(kFull, l_run[e], 8);
         l_run[e] += __shfl_xor_sync(kFull, l_run[e], 16);
@@ -1415,10 +1314,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
         }
       }
       held = pend;
-      if constexpr (INT4) {
-        q4.finish(reinterpret_cast<float*>(wsm + max(last_stage, 0) * Gm::STAGE), ML + warp * 2 * GP, last_stage >= 0, GP, lane);
-        fence_proxy_async_smem();  // the buffer is refilled by bulk copies after the merge
-      } else if (last_stage >= 0) {
+      if (last_stage >= 0) {
         float* os = reinterpret_cast<float*>(wsm + last_stage * Gm::STAGE);
         const bool writer = NT == 2 || !lo_lane;
 #pragma unroll
@@ -1437,7 +1333,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
           }
         fence_proxy_async_smem();  // the buffer is refilled by TMA after the merge
       }
-      if (!INT4 && fg == 0 && (NT == 2 || !lo_lane)) {
+      if (fg == 0 && (NT == 2 || !lo_lane)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           ML[warp * 2 * GP + hbase + e] = last_stage >= 0 ? m_run[e] : -INFINITY;
@@ -1494,11 +1390,6 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
       prep_q<D, GP, 32>(a, reinterpret_cast<const uint16_t*>(slot + Gm::IN_Q), sl ? pos_s[1] : pos_s[0], step,
                         qs, cs, lane);
       __syncwarp();
-      if constexpr (Gm::QF_BYTES > 0) {
-        // (the fragments of the unit before last: every streaming warp is past that unit)
-        Int4Warp<D, NT>::put_query(qs, smem + Gm::QF_OFF + (k & 1) * Gm::QF_BYTES, lane);
-        __syncwarp();
-      }
       // (a testing aid can withhold the first unit's q, so that every
       // streaming warp's bounded wait for it runs out)
       if (lane == 0 && !(k == 0 && (a.debug_flags & kDebugWithholdQ))) mbar_arrive(prep_full);
@@ -1508,7 +1399,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
         const int uk = sl ? unit_s[1] : unit_s[0];
         *reinterpret_cast<int64_t*>(slot + Gm::IN_WB) = write_back_offset<PAGED>(a, uk / Hkv, uk % Hkv, D);
       }
-      prep_token<D, GP, FMT, 32>(a, qs, cs, slot, sl ? gate_s[1] : gate_s[0], lane);
+      prep_token<D, GP, 32>(a, qs, cs, slot, sl ? gate_s[1] : gate_s[0], lane);
     };
     if (u_first < U) {
       stage(u_first);
@@ -1527,7 +1418,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
       prep(seg + 1);
       // this segment's end
       if (!failed) check(mbar_wait_bounded(merge_full, seg & 1, a.wait_ns));
-      end_segment<D, NT, PAGED, FMT, 32>(a, sp, pieces, u, seg == 0, cta, smem, ML, SLOT,
+      end_segment<D, NT, PAGED, F8, 32>(a, sp, pieces, u, seg == 0, cta, smem, ML, SLOT,
                                     in_slots + (seg & 1) * Gm::IN_BYTES, flag, lane, wait_prev, [&] {
                                       fence_proxy_async_smem();
                                       __syncwarp();
@@ -1544,7 +1435,7 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
   __syncthreads();
   if (u_last < U) {
     const int sl = n_segs - 1;
-    end_segment<D, NT, PAGED, FMT, kThreads>(a, sp, pieces, u_last, sl == 0, cta, smem, ML, SLOT,
+    end_segment<D, NT, PAGED, F8, kThreads>(a, sp, pieces, u_last, sl == 0, cta, smem, ML, SLOT,
                                         in_slots + (sl & 1) * Gm::IN_BYTES, flag, threadIdx.x, wait_prev, [] {});
   }
 
@@ -1567,9 +1458,9 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
     if (a.write_back && threadIdx.x == 0)
       *reinterpret_cast<int64_t*>(slot + Gm::IN_WB) = write_back_offset<PAGED>(a, b, j, D);
     __syncthreads();
-    prep_token<D, GP, FMT, kThreads>(a, qs, cs, slot, gr, threadIdx.x);
+    prep_token<D, GP, kThreads>(a, qs, cs, slot, gr, threadIdx.x);
     wait_prev();
-    finish_unit<D, GP, PAGED, FMT, kThreads>(a, u, slot, threadIdx.x, [](int, int, Merge8&) {});
+    finish_unit<D, GP, PAGED, kThreads>(a, u, slot, threadIdx.x, [](int, int, Merge8&) {});
     ++n;
   }
   wait_prev();
@@ -1577,14 +1468,14 @@ __global__ void __launch_bounds__(Geo<D, NT, FMT>::THREADS, 1) decode_kernel(con
 
 // ---------------------------------------------------------------- launch
 
-template <int D, int NT, bool PAGED, int FMT>
+template <int D, int NT, bool PAGED, bool F8>
 cudaError_t decode_launch(const DecodeArgs& a, int ctas, cudaStream_t s, bool pdl) {
-  using Gm = Geo<D, NT, FMT>;
-  auto k = decode_kernel<D, NT, PAGED, FMT>;
+  using Gm = Geo<D, NT, F8>;
+  auto k = decode_kernel<D, NT, PAGED, F8>;
   static std::atomic<uint64_t> opted{0};
   const cudaError_t e = opt_in_smem(k, Gm::SMEM_MAX, opted);
   if (e != cudaSuccess) return e;
-  const size_t smem = Gm::QF_BYTES ? Gm::SMEM_MAX : 1024 + Gm::TAB_OFF + (4 * a.B * a.Hkv + 1) * sizeof(int);
+  const size_t smem = 1024 + Gm::TAB_OFF + (4 * a.B * a.Hkv + 1) * sizeof(int);
   if (!pdl) {
     k<<<ctas, Gm::THREADS, smem, s>>>(a);
     return cudaGetLastError();
@@ -1592,39 +1483,30 @@ cudaError_t decode_launch(const DecodeArgs& a, int ctas, cudaStream_t s, bool pd
   return launch_pdl(k, dim3(ctas), dim3(Gm::THREADS), smem, s, a);
 }
 
-template <int D, int NT, int FMT>
+template <int D, int NT, bool F8>
 cudaError_t decode_dispatch_paged(const DecodeArgs& a, int ctas, cudaStream_t s, bool pdl) {
-  if constexpr (FMT == kFmtInt4) {  // (4-bit caches are paged)
-    return a.c.paged ? decode_launch<D, NT, true, FMT>(a, ctas, s, pdl) : cudaErrorNotSupported;
-  } else {
-    return a.c.paged ? decode_launch<D, NT, true, FMT>(a, ctas, s, pdl) : decode_launch<D, NT, false, FMT>(a, ctas, s, pdl);
-  }
+  return a.c.paged ? decode_launch<D, NT, true, F8>(a, ctas, s, pdl) : decode_launch<D, NT, false, F8>(a, ctas, s, pdl);
 }
 
-template <int FMT>
+template <bool F8>
 cudaError_t decode_dispatch(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl) {
   if (D == 256) {
-    if (GP == 4) return decode_dispatch_paged<256, 1, FMT>(a, ctas, s, pdl);
-    if (GP == 8) return decode_dispatch_paged<256, 2, FMT>(a, ctas, s, pdl);
+    if (GP == 4) return decode_dispatch_paged<256, 1, F8>(a, ctas, s, pdl);
+    if (GP == 8) return decode_dispatch_paged<256, 2, F8>(a, ctas, s, pdl);
   } else if (D == 128) {
-    if (GP == 4) return decode_dispatch_paged<128, 1, FMT>(a, ctas, s, pdl);
-    if (GP == 8) return decode_dispatch_paged<128, 2, FMT>(a, ctas, s, pdl);
+    if (GP == 4) return decode_dispatch_paged<128, 1, F8>(a, ctas, s, pdl);
+    if (GP == 8) return decode_dispatch_paged<128, 2, F8>(a, ctas, s, pdl);
   }
   return cudaErrorNotSupported;
 }
 
 }  // namespace
 
-#if defined(DATTN_DECODE_FP8_UNIT)
+#ifdef DATTN_DECODE_FP8_UNIT
 // This translation unit holds the E4M3-cache instantiations only (compiled
 // beside the bf16 ones, in parallel).
 cudaError_t launch_decode_fp8(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl) {
-  return decode_dispatch<kFmtE4m3>(a, D, GP, ctas, s, pdl);
-}
-#elif defined(DATTN_DECODE_INT4_UNIT)
-// The same for the 4-bit caches.
-cudaError_t launch_decode_int4(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl) {
-  return decode_dispatch<kFmtInt4>(a, D, GP, ctas, s, pdl);
+  return decode_dispatch<true>(a, D, GP, ctas, s, pdl);
 }
 #else
 namespace {
@@ -1759,42 +1641,37 @@ cudaError_t launch_decode(const DecodeArgs& args, int D, int ctas, cudaStream_t 
   if (a.B * a.Hkv > kMaxUnits) return cudaErrorNotSupported;
   if (a.r > D || a.r % 2 != 0) return cudaErrorNotSupported;
   if (a.f8) return launch_decode_fp8(a, D, GP, ctas, s, pdl);
-  if (a.int4) {
-    a.unit_cost = kInt4SegmentCost;
-    return launch_decode_int4(a, D, GP, ctas, s, pdl);
-  }
-  return decode_dispatch<kFmtBf16>(a, D, GP, ctas, s, pdl);
-}
-
-// f(Geo) of the kernel variant for (D, GP, format).
-template <typename F>
-int by_geometry(int D, int GP, int format, F f) {
-  auto pick = [&](auto d) {
-    constexpr int kD = decltype(d)::D;
-    if (format == kFmtInt4) return GP == 4 ? f(Geo<kD, 1, kFmtInt4>()) : f(Geo<kD, 2, kFmtInt4>());
-    if (format == kFmtE4m3) return GP == 4 ? f(Geo<kD, 1, kFmtE4m3>()) : f(Geo<kD, 2, kFmtE4m3>());
-    return GP == 4 ? f(Geo<kD, 1>()) : f(Geo<kD, 2>());
-  };
-  return D == 256 ? pick(Geo<256, 1>()) : pick(Geo<128, 1>());
+  return decode_dispatch<false>(a, D, GP, ctas, s, pdl);
 }
 
 // Keys of one round of stage tiles over the streaming warps, in units of 4
 // tiles (the grid plan gives each CTA at least one round).
-int decode_tile_keys(int D, int G, int format) {
+int decode_tile_keys(int D, int G, bool f8) {
   const int GP = decode_group_pad(G);
   if (GP == 0 || (D != 128 && D != 256)) return 0;
-  return by_geometry(D, GP, format, [](auto geo) { return kGroup * geo.KG * geo.W / 4; });
+  auto keys = [](int kg, int w) { return kGroup * kg * w / 4; };
+  if (D == 256) {
+    if (f8) return GP == 4 ? keys(Geo<256, 1, true>::KG, Geo<256, 1, true>::W) : keys(Geo<256, 2, true>::KG, Geo<256, 2, true>::W);
+    return GP == 4 ? keys(Geo<256, 1>::KG, Geo<256, 1>::W) : keys(Geo<256, 2>::KG, Geo<256, 2>::W);
+  }
+  if (f8) return GP == 4 ? keys(Geo<128, 1, true>::KG, Geo<128, 1, true>::W) : keys(Geo<128, 2, true>::KG, Geo<128, 2, true>::W);
+  return GP == 4 ? keys(Geo<128, 1>::KG, Geo<128, 1>::W) : keys(Geo<128, 2>::KG, Geo<128, 2>::W);
 }
 
 int decode_ctas_per_sm(int D, int G) {
   const int GP = decode_group_pad(G);
-  if (GP == 0 || (D != 128 && D != 256)) return 0;
-  // (the largest layout of the cache formats)
   int smem = 0;
-  for (int format = kFmtBf16; format <= kFmtInt4; ++format) {
-    const int x = by_geometry(D, GP, format, [](auto geo) { return geo.SMEM_MAX; });
-    if (x > smem) smem = x;
-  }
+  // (the larger of the bf16 and E4M3 layouts: an E4M3 tile holds more groups)
+  const auto larger = [](int x, int y) { return x > y ? x : y; };
+  if (D == 256)
+    smem = GP == 4   ? larger(Geo<256, 1>::SMEM_MAX, Geo<256, 1, true>::SMEM_MAX)
+           : GP == 8 ? larger(Geo<256, 2>::SMEM_MAX, Geo<256, 2, true>::SMEM_MAX)
+                     : 0;
+  if (D == 128)
+    smem = GP == 4   ? larger(Geo<128, 1>::SMEM_MAX, Geo<128, 1, true>::SMEM_MAX)
+           : GP == 8 ? larger(Geo<128, 2>::SMEM_MAX, Geo<128, 2, true>::SMEM_MAX)
+                     : 0;
+  if (smem == 0) return 0;
   // 228 KB of shared memory per SM; 1 KB reserved and the static block-scan scratch per CTA
   const int per_sm = 233472 / (smem + 1024 + 64);
   return per_sm > 2 ? 2 : per_sm;

@@ -1,24 +1,25 @@
-// The streaming warp's arithmetic over a 4-bit cache (int4_format.h), for
-// decode_kernel.
+// A warp's arithmetic over blocks of a 4-bit cache (int4_format.h).
 //
 // With code c, step s and least value b of a (key k, group G of 64 dims):
 //   score    q . K_k = sum_G [ s_kG (q_G . c_kG) + b_kG sum(q_G) ]
 //   output   O_d    += sum_k p_k s_kG c_kd  +  sum_k p_k b_kG     (d in G)
 // so the codes enter the tensor cores as they are - whole numbers, exact in fp16 -
 // and the grid is applied to 4 scores (K) or folded into the weights (V): a group of
-// 64 dims costs a few FMAs instead of one for every value. A code becomes an fp16
-// operand by a mask alone: bits 0-3 of a half are the subnormal c 2^-24, bits 4-7 are
-// c 2^-20, and a shift by 8 brings the other two codes there; 5 instructions for 8
-// values. The power of two between the two kinds is taken out of q's terms (K) or of
-// the finished outputs (V).
+// 64 dims costs a few FMAs instead of one for every value. Codes become fp16 operands
+// by a mask alone: the low byte of a half, codes c0 and c1, is the fp16 number (c0 + 16
+// c1) 2^-24, its low 4 bits are c0 2^-24, and one byte permute brings the other two codes
+// of the half there: 4 instructions for 8 values. The products are with c0 and c0 +
+// 16 c1: q0 c0 + q1 c1 = (q0 - q1 / 16) c0 + (q1 / 16) (c0 + 16 c1), and the outputs
+// of c1 are taken apart at the end (both exact but for the terms' own rounding: c0 is
+// a sixteenth of the byte). Masking c1 too took 5 instructions: FIG1.
 //
 // Columns of the MMAs: head h's high and low term side by side (2 h, 2 h + 1), so a
 // lane's score and output fragments belong to one head (t = lane % 4, and t + 4 with
 // NT = 2), and a head's hi + lo is one add without a shuffle.
 //
-// Precision. q and the weights p s enter as two fp16 terms, 22 bits, where fp16 holds
-// them: q is scaled by a power of two that brings the head's largest to 2^10 .. 2^11
-// (2^15 for the dims that need the factor 16), the weights by f_G, a power of two that
+// Precision. q's factors and the weights p s enter as two fp16 terms, 22 bits, where fp16
+// holds them: q is scaled by a power of two that brings the head's largest to 2^13 ..
+// 2^14, the weights by f_G, a power of two that
 // follows the largest step seen so far (step f_G in 2^6 .. 2^8), p being at most 2^6:
 // the running maximum is only moved when a score passes it by 6, which saves the
 // cross-lane maximum of every group of keys. Sums are fp32.
@@ -56,26 +57,27 @@ __device__ __forceinline__ void int4_query(const float* qs, int lane, uint32_t (
     }
     mx = fmaxf(mx, __shfl_xor_sync(full, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(full, mx, 2));
-    // 2^(10 - floor(log2 mx)), 2^100 at the most (a head of zeros)
-    const int e = 264 - static_cast<int>(__float_as_uint(mx) >> 23);
+    // 2^(13 - floor(log2 mx)), 2^100 at the most (a head of zeros)
+    const int e = 267 - static_cast<int>(__float_as_uint(mx) >> 23);
     const float S = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 227)) << 23);
-    const float S16 = S * 16.f;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
+      // dims i of the word: halves 0 .. 3 and 4 .. 7, bytes (0, 1) and (2, 3) of a half
       const float* x = src + (w >> 1) * 64 + t * 16 + (w & 1) * 8;
       const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
+      const float z = S * 0.0625f;
       uint32_t hi, lo;
-      split_f16x2(a.x * S16, b.x * S16, hi, lo);
+      split_f16x2(fmaf(a.y, -z, a.x * S), fmaf(b.y, -z, b.x * S), hi, lo);
       qb[2 * w][nt][0] = g & 1 ? lo : hi;
-      split_f16x2(a.y * S, b.y * S, hi, lo);
+      split_f16x2(a.y * z, b.y * z, hi, lo);
       qb[2 * w][nt][1] = g & 1 ? lo : hi;
-      split_f16x2(a.z * S16, b.z * S16, hi, lo);
+      split_f16x2(fmaf(a.w, -z, a.z * S), fmaf(b.w, -z, b.z * S), hi, lo);
       qb[2 * w + 1][nt][0] = g & 1 ? lo : hi;
-      split_f16x2(a.w * S, b.w * S, hi, lo);
+      split_f16x2(a.w * z, b.w * z, hi, lo);
       qb[2 * w + 1][nt][1] = g & 1 ? lo : hi;
     }
-    // accumulators hold S 2^-20 times q . c
-    const float unit = S * 0x1p-20f, back = 0x1p20f / S;
+    // accumulators hold S 2^-24 times q . c
+    const float unit = S * 0x1p-24f, back = 0x1p24f / S;
 #pragma unroll
     for (int G = 0; G < D / 64; ++G) qsum[nt][G] = __shfl_sync(full, sum[G] * unit, 8 * t);
     inv[nt] = __shfl_sync(full, back, 8 * t);
@@ -87,9 +89,9 @@ template <int D, int NT>
 struct Int4Warp {
   static constexpr int KS = D / 16, NG = D / 64, MT = D / 16;
   // At 16 m-tiles and two column tiles the outputs alone are 128 registers: q's
-  // fragments then stay in shared memory, written by the helper warp.
+  // fragments then stay in shared memory.
   static constexpr bool kSharedQ = D == 256 && NT == 2;
-  static constexpr int kQBytes = KS * 512 + 32 * 4 * NT * (NG + 1);  // of one unit's fragments, sums and factors
+  static constexpr int kQBytes = KS * 256 * NT + 32 * 4 * NT * (NG + 1);  // of one unit's fragments, sums and factors
 
   uint32_t qb[kSharedQ ? 1 : KS][NT][2];
   float qsum[NT][NG], inv[NT];
@@ -97,25 +99,30 @@ struct Int4Warp {
   float m[NT], l[NT], cst[NT][NG];  // base-2 maximum, sum of weights, sum of p b
   float f[NG];                      // power of two of the weights of group G
 
-  // The helper warp's share with kSharedQ, and the streaming warps' with or without.
+  // The fragments into shared memory (kSharedQ), and the warp's own part of them.
   static __device__ __forceinline__ void put_query(const float* qs, uint8_t* dst, int lane) {
     uint32_t q[KS][NT][2];
     float s[NT][NG], v[NT];
     int4_query<D, NT>(qs, lane, q, s, v);
+    __syncwarp();  // (dst may be where qs is)
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      *reinterpret_cast<uint4*>(dst + ks * 512 + lane * 16) = make_uint4(q[ks][0][0], q[ks][0][1], q[ks][NT - 1][0], q[ks][NT - 1][1]);
-    float* x = reinterpret_cast<float*>(dst + KS * 512);
+    for (int i = 0; i < KS * NT / 2; ++i) {  // (a k-step's two column tiles, or two k-steps)
+      const uint32_t(&a)[2] = q[NT == 2 ? i : 2 * i][0];
+      const uint32_t(&b)[2] = q[NT == 2 ? i : 2 * i + 1][NT - 1];
+      *reinterpret_cast<uint4*>(dst + i * 512 + lane * 16) = make_uint4(a[0], a[1], b[0], b[1]);
+    }
+    float* x = reinterpret_cast<float*>(dst + KS * 256 * NT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int G = 0; G < NG; ++G) x[(nt * (NG + 1) + G) * 32 + lane] = s[nt][G];
       x[(nt * (NG + 1) + NG) * 32 + lane] = v[nt];
     }
+    __syncwarp();
   }
   __device__ __forceinline__ void get_query(const float* qs, const uint8_t* src, int lane) {
     if constexpr (kSharedQ) {
-      const float* x = reinterpret_cast<const float*>(src + KS * 512);
+      const float* x = reinterpret_cast<const float*>(src + KS * 256 * NT);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -145,24 +152,39 @@ struct Int4Warp {
     for (int G = 0; G < NG; ++G) f[G] = 0x1p100f;
   }
 
+  // The steps of keys g and g + 8 of a block's values, groups G and G + 1, and the least values.
+  static __device__ __forceinline__ void pairs(const uint8_t* vb, int row, int G, float (&st)[2], float (&ls)[2]) {
+    const uint2 p = *reinterpret_cast<const uint2*>(vb + 8 * D + row * (4 * NG) + G * 4);
+    st[0] = bf16_hi(p.x), ls[0] = bf16_lo(p.x);
+    st[1] = bf16_hi(p.y), ls[1] = bf16_lo(p.y);
+  }
+
   // A score passed its head's maximum by 6, or a step its group's scale: both are
   // brought up to date and what was summed so far is rescaled.
-  __device__ __forceinline__ void rescale(const float (&s)[NT][2], const float (&st)[2][NG]) {
+  template <int N>
+  __device__ __forceinline__ void rescale(const float (&s)[N][NT][2], const uint8_t* vb, int pitch, int g) {
     constexpr unsigned full = 0xffffffffu;
     float fac[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx = fmaxf(s[nt][0], s[nt][1]);
+      float mx = m[nt];
+#pragma unroll
+      for (int b = 0; b < N; ++b) mx = fmaxf(mx, fmaxf(s[b][nt][0], s[b][nt][1]));
       mx = fmaxf(mx, __shfl_xor_sync(full, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(full, mx, 8));
-      mx = fmaxf(m[nt], fmaxf(mx, __shfl_xor_sync(full, mx, 16)));
+      mx = fmaxf(mx, __shfl_xor_sync(full, mx, 16));
       fac[nt] = mx == -INFINITY ? 1.f : exp2_fast(m[nt] - mx);
       m[nt] = mx;
       l[nt] *= fac[nt];
     }
 #pragma unroll
     for (int G = 0; G < NG; ++G) {
-      float x = fmaxf(st[0][G], st[1][G]);
+      float x = 0.f;
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          x = fmaxf(x, bf16_hi(*reinterpret_cast<const uint32_t*>(vb + b * pitch + 8 * D + (g + 8 * i) * (4 * NG) + G * 4)));
       x = fmaxf(x, __shfl_xor_sync(full, x, 4));
       x = fmaxf(x, __shfl_xor_sync(full, x, 8));
       x = fmaxf(x, __shfl_xor_sync(full, x, 16));
@@ -186,112 +208,171 @@ struct Int4Warp {
     }
   }
 
-  // One block of 16 keys: kb, vb are its K and V bytes in shared memory, bit r of mask
-  // says whether key r counts (at least one does), qf the unit's fragments with kSharedQ.
-  __device__ __forceinline__ void block(const uint8_t* kb, const uint8_t* vb, uint32_t mask, const uint8_t* qf, int lane) {
+  // The values' grids of the keys that do not count, in shared memory: they may hold
+  // anything (0 x NaN is NaN). Ends with a warp barrier.
+  static __device__ __forceinline__ void clear_rows(uint8_t* vb, uint32_t mask, int lane) {
+    for (int i = lane; i < kInt4Block * NG; i += 32)
+      if (!((mask >> (i / NG)) & 1u)) *reinterpret_cast<uint32_t*>(vb + 8 * D + i * 4) = 0u;
+    fence_proxy_async_smem();  // before the stage is refilled by bulk copies
+    __syncwarp();
+  }
+
+  // N blocks of 16 keys at once (their chains of products, exponentials and transposes
+  // run beside one another): kb, vb are the K and V bytes of the first in shared memory,
+  // the others follow; bit r of mask[b] says whether key r of block b counts (one of
+  // them does; the others' V grids are zero), qf the unit's fragments with kSharedQ.
+  template <int N>
+  __device__ __forceinline__ void blocks(const uint8_t* kb, const uint8_t* vb, const uint32_t (&mask)[N], const uint8_t* qf,
+                                         int lane) {
     constexpr unsigned full = 0xffffffffu;
-    constexpr uint32_t m0 = 0x000f000fu, m1 = 0x00f000f0u;
+    constexpr uint32_t m0 = 0x000f000fu, m1 = 0x00ff00ffu;
+    constexpr int pitch = int4_block_bytes(D);
     const int g = lane >> 2, t = lane & 3;
-    // ---- scores of keys g and g + 8 for the lane's heads
-    float s[NT][2];
+    // ---- scores of keys g and g + 8 of each block for the lane's heads
+    float s[N][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = 0.f;
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[b][nt][0] = s[b][nt][1] = 0.f;
 #pragma unroll
     for (int sec = 0; sec < D / 128; ++sec) {
-      const uint4 xa = *reinterpret_cast<const uint4*>(kb + sec * 1024 + g * 64 + t * 16);
-      const uint4 xb = *reinterpret_cast<const uint4*>(kb + sec * 1024 + g * 64 + t * 16 + 512);
-      const uint2 pa = *reinterpret_cast<const uint2*>(kb + 8 * D + g * (4 * NG) + sec * 8);
-      const uint2 pb = *reinterpret_cast<const uint2*>(kb + 8 * D + (g + 8) * (4 * NG) + sec * 8);
+      uint4 xa[N], xb[N];
+      uint2 pa[N], pb[N];
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        const uint8_t* src = kb + b * pitch;
+        xa[b] = *reinterpret_cast<const uint4*>(src + sec * 1024 + g * 64 + t * 16);
+        xb[b] = *reinterpret_cast<const uint4*>(src + sec * 1024 + g * 64 + t * 16 + 512);
+        pa[b] = *reinterpret_cast<const uint2*>(src + 8 * D + g * (4 * NG) + sec * 8);
+        pb[b] = *reinterpret_cast<const uint2*>(src + 8 * D + (g + 8) * (4 * NG) + sec * 8);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int G = sec * 2 + k;
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        float acc[N][NT][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t wa = k ? (j ? xa.w : xa.z) : (j ? xa.y : xa.x), wb = k ? (j ? xb.w : xb.z) : (j ? xb.y : xb.x);
+          uint4 v1 = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (kSharedQ && NT == 1) v1 = *reinterpret_cast<const uint4*>(qf + (G * 2 + j) * 512 + lane * 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int ks = (G * 2 + j) * 2 + i;
-            const uint32_t a[4] = {wa & m0, wb & m0, wa & m1, wb & m1};
-            if constexpr (kSharedQ) {
-              const uint4 q = *reinterpret_cast<const uint4*>(qf + ks * 512 + lane * 16);
-              mma_f16(acc[0], a, q.x, q.y);
-              mma_f16(acc[NT - 1], a, q.z, q.w);
+            uint32_t q[NT][2];
+            if constexpr (kSharedQ && NT == 1) {
+              q[0][0] = i ? v1.z : v1.x, q[0][1] = i ? v1.w : v1.y;
+            } else if constexpr (kSharedQ) {
+              const uint4 v = *reinterpret_cast<const uint4*>(qf + ks * 512 + lane * 16);
+              q[0][0] = v.x, q[0][1] = v.y, q[NT - 1][0] = v.z, q[NT - 1][1] = v.w;
             } else {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a, qb[ks][nt][0], qb[ks][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) q[nt][0] = qb[ks][nt][0], q[nt][1] = qb[ks][nt][1];
             }
-            wa >>= 8;
-            wb >>= 8;
+#pragma unroll
+            for (int b = 0; b < N; ++b) {
+              const uint32_t wa = k ? (j ? xa[b].w : xa[b].z) : (j ? xa[b].y : xa[b].x);
+              const uint32_t wb = k ? (j ? xb[b].w : xb[b].z) : (j ? xb[b].y : xb[b].x);
+              const uint32_t ba = i ? prmt(wa, 0u, 0x4341u) : wa & m1, bb = i ? prmt(wb, 0u, 0x4341u) : wb & m1;
+              const uint32_t a[4] = {ba & m0, bb & m0, ba, bb};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (j + i == 0) mma_f16_first(acc[b][nt], a, q[nt][0], q[nt][1]);
+                else mma_f16(acc[b][nt], a, q[nt][0], q[nt][1]);
+              }
+            }
           }
         }
-        const uint32_t p0 = k ? pa.y : pa.x, p1 = k ? pb.y : pb.x;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][0] = fmaf(bf16_hi(p0), acc[nt][0] + acc[nt][1], fmaf(bf16_lo(p0), qsum[nt][G], s[nt][0]));
-          s[nt][1] = fmaf(bf16_hi(p1), acc[nt][2] + acc[nt][3], fmaf(bf16_lo(p1), qsum[nt][G], s[nt][1]));
+        for (int b = 0; b < N; ++b) {
+          const uint32_t p0 = k ? pa[b].y : pa[b].x, p1 = k ? pb[b].y : pb[b].x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float(&c)[4] = acc[b][nt];
+            s[b][nt][0] = fmaf(bf16_hi(p0), c[0] + c[1], fmaf(bf16_lo(p0), qsum[nt][G], s[b][nt][0]));
+            s[b][nt][1] = fmaf(bf16_hi(p1), c[2] + c[3], fmaf(bf16_lo(p1), qsum[nt][G], s[b][nt][1]));
+          }
         }
       }
     }
-    // ---- the values' grids of the same keys; keys that do not count weigh nothing
-    const bool on0 = (mask >> g) & 1u, on1 = (mask >> (g + 8)) & 1u;
-    float st[2][NG], ls[2][NG], top = 0.f;
+    // ---- do the maximum and the weights' scales still hold?
+    float top = 0.f;
 #pragma unroll
-    for (int G = 0; G < NG; G += 2) {
-      uint2 pa = *reinterpret_cast<const uint2*>(vb + 8 * D + g * (4 * NG) + G * 4);
-      uint2 pb = *reinterpret_cast<const uint2*>(vb + 8 * D + (g + 8) * (4 * NG) + G * 4);
-      if (!on0) pa = make_uint2(0u, 0u);
-      if (!on1) pb = make_uint2(0u, 0u);
-      st[0][G] = bf16_hi(pa.x), ls[0][G] = bf16_lo(pa.x);
-      st[0][G + 1] = bf16_hi(pa.y), ls[0][G + 1] = bf16_lo(pa.y);
-      st[1][G] = bf16_hi(pb.x), ls[1][G] = bf16_lo(pb.x);
-      st[1][G + 1] = bf16_hi(pb.y), ls[1][G + 1] = bf16_lo(pb.y);
+    for (int b = 0; b < N; ++b)
 #pragma unroll
-      for (int x = G; x < G + 2; ++x) top = fmaxf(top, fmaxf(st[0][x], st[1][x]) * f[x]);
-    }
+      for (int G = 0; G < NG; G += 2) {
+        float s0[2], s1[2], x[2];
+        pairs(vb + b * pitch, g, G, s0, x);
+        pairs(vb + b * pitch, g + 8, G, s1, x);
+        top = fmaxf(top, fmaxf(fmaxf(s0[0], s1[0]) * f[G], fmaxf(s0[1], s1[1]) * f[G + 1]));
+      }
     bool move = top > 256.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      s[nt][0] = on0 ? s[nt][0] * inv[nt] : -INFINITY;
-      s[nt][1] = on1 ? s[nt][1] * inv[nt] : -INFINITY;
-      move = move || fmaxf(s[nt][0], s[nt][1]) > m[nt] + 6.f;
+    for (int b = 0; b < N; ++b) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        s[b][nt][0] *= inv[nt];
+        s[b][nt][1] *= inv[nt];
+      }
+      if (mask[b] != 0xffffu) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!((mask[b] >> g) & 1u)) s[b][nt][0] = -INFINITY;
+          if (!((mask[b] >> (g + 8)) & 1u)) s[b][nt][1] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) move = move || fmaxf(s[b][nt][0], s[b][nt][1]) > m[nt] + 6.f;
     }
-    if (__any_sync(full, move)) rescale(s, st);
-    float p[NT][2];
+    if (__any_sync(full, move)) rescale<N>(s, vb, pitch, g);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float ms = m[nt] == -INFINITY ? 0.f : m[nt];
-      p[nt][0] = exp2_fast(s[nt][0] - ms);
-      p[nt][1] = exp2_fast(s[nt][1] - ms);
-      l[nt] += p[nt][0] + p[nt][1];
+#pragma unroll
+      for (int b = 0; b < N; ++b) {  // (the scores become the weights)
+        s[b][nt][0] = exp2_fast(s[b][nt][0] - ms);
+        s[b][nt][1] = exp2_fast(s[b][nt][1] - ms);
+        l[nt] += s[b][nt][0] + s[b][nt][1];
+      }
     }
     // ---- outputs, a group of 64 dims at a time: its weights as B fragments, hi and lo
     // beside one another, then its four m-tiles
 #pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      uint32_t pb[NT][2];
+    for (int G = 0; G < NG; G += 2) {
+      float s0[N][2], s1[N][2], l0[N][2], l1[N][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        cst[nt][G] = fmaf(p[nt][0], ls[0][G], fmaf(p[nt][1], ls[1][G], cst[nt][G]));
-        uint32_t hi, lo;
-        split_f16x2(p[nt][0] * (st[0][G] * f[G]), p[nt][1] * (st[1][G] * f[G]), hi, lo);
-        pb[nt][0] = movm_t(prmt(hi, lo, 0x5410u));
-        pb[nt][1] = movm_t(prmt(hi, lo, 0x7632u));
+      for (int b = 0; b < N; ++b) {
+        pairs(vb + b * pitch, g, G, s0[b], l0[b]);
+        pairs(vb + b * pitch, g + 8, G, s1[b], l1[b]);
       }
-      const uint4 x = *reinterpret_cast<const uint4*>(vb + G * 512 + lane * 16);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t wa = j ? x.y : x.x, wb = j ? x.w : x.z;
+      for (int k = 0; k < 2; ++k) {
+        uint32_t pb[N][NT][2];
+        uint4 x[N];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a[4] = {wa & m0, wa & m1, wb & m0, wb & m1};
+        for (int b = 0; b < N; ++b) {
+          x[b] = *reinterpret_cast<const uint4*>(vb + b * pitch + (G + k) * 512 + lane * 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(o[G * 4 + j * 2 + i][nt], a, pb[nt][0], pb[nt][1]);
-          wa >>= 8;
-          wb >>= 8;
+          for (int nt = 0; nt < NT; ++nt) {
+            const float p0 = s[b][nt][0], p1 = s[b][nt][1];
+            cst[nt][G + k] = fmaf(p0, l0[b][k], fmaf(p1, l1[b][k], cst[nt][G + k]));
+            uint32_t hi, lo;
+            split_f16x2(p0 * (s0[b][k] * f[G + k]), p1 * (s1[b][k] * f[G + k]), hi, lo);
+            pb[b][nt][0] = movm_t(prmt(hi, lo, 0x5410u));
+            pb[b][nt][1] = movm_t(prmt(hi, lo, 0x7632u));
+          }
         }
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t wa = j ? x[b].y : x[b].x, wb = j ? x[b].w : x[b].z;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t ba = i ? prmt(wa, 0u, 0x4341u) : wa & m1, bb = i ? prmt(wb, 0u, 0x4341u) : wb & m1;
+              const uint32_t a[4] = {ba & m0, ba, bb & m0, bb};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(o[(G + k) * 4 + j * 2 + i][nt], a, pb[b][nt][0], pb[b][nt][1]);
+            }
+          }
       }
     }
   }
@@ -322,10 +403,11 @@ struct Int4Warp {
           float4 v;
           const float(&a)[4] = o[G * 4 + j * 2][nt];
           const float(&b)[4] = o[G * 4 + j * 2 + 1][nt];
-          v.x = fmaf((a[0] + a[1]) * 0x1p24f, back, c);
-          v.y = fmaf((a[2] + a[3]) * 0x1p20f, back, c);
-          v.z = fmaf((b[0] + b[1]) * 0x1p24f, back, c);
-          v.w = fmaf((b[2] + b[3]) * 0x1p20f, back, c);
+          const float a0 = a[0] + a[1], b0 = b[0] + b[1];
+          v.x = fmaf(a0 * 0x1p24f, back, c);
+          v.y = fmaf(((a[2] + a[3]) - a0) * 0x1p20f, back, c);
+          v.z = fmaf(b0 * 0x1p24f, back, c);
+          v.w = fmaf(((b[2] + b[3]) - b0) * 0x1p20f, back, c);
           *reinterpret_cast<float4*>(os + (4 * nt + t) * D + G * 64 + g * 8 + j * 4) = v;
         }
       }

@@ -9,7 +9,7 @@
 // shuffles away.
 #include "bf16_exact.h"
 #include "common.cuh"
-#include "int4_format.h"
+#include "int4.cuh"
 #include "kernels.h"
 #include "mma.cuh"
 #include "qk_norm.cuh"
@@ -22,78 +22,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxWarps = 8;
-
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// (largest, -least) of the values packed in w[0..N), as one bf16 pair: the join of
-// two such pairs is a maximum.
-template <int N>
-__device__ __forceinline__ uint32_t extent(const uint32_t (&w)[N]) {
-  uint32_t mx = w[0], mn = w[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) {
-    mx = max2_nan(mx, w[i]);
-    mn = min2_nan(mn, w[i]);
-  }
-  mn ^= 0x80008000u;
-  // (the halves of each, beside one another)
-  return max2_nan(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
-}
-__device__ __forceinline__ Int4Grid grid_of(uint32_t e) { return int4_grid(-bf16_hi(e), bf16_lo(e)); }
-
-// Two floats at a time (the packed fp32 instructions: half the issue slots).
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 wide2(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
-
-// Codes of N values (N / 2 words), the first in the low 4 bits: int4_code_biased of each.
-template <int N>
-__device__ __forceinline__ uint32_t codes(const uint32_t* w, const Int4Grid& q) {
-  const F2 least = f2(-q.least, -q.least), inv = f2(q.inv, q.inv), step = f2(-q.step, -q.step), magic = f2(12582912.f, 12582912.f);
-  constexpr uint32_t bias = kInt4Bias * (N == 8 ? 0x11111111u : 0x1111u);
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = N / 2 - 1; i >= 0; --i) {
-    const F2 d = add2(wide2(w[i]), least);
-    const F2 y = mul2(d, inv);
-    const F2 z = add2(fma2(fma2(y, step, d), inv, y), magic);
-    float c0, c1;
-    split(z, c0, c1);
-    r = (r * 16u + __float_as_uint(c1)) * 16u + __float_as_uint(c0);
-  }
-  return (r - bias) & q.keep;
-}
 
 // The tokens of block blockIdx.x of call row b and where the block is.
 struct BlockSpan {

@@ -121,7 +121,36 @@ struct DecodeArgs {
   // cached value = e4m3 * scale. q_scale then includes k_scale.
   int f8;
   float k_scale, v_scale;
-  int int4;                    // 4-bit cache (int4_format.h): k, v of CacheView are byte arrays
+};
+
+// The same over a 4-bit cache (int4_format.h; the pools are byte arrays). A unit's blocks
+// of 16 tokens are split over the warps of all CTAs.
+struct Int4DecodeArgs {
+  CacheView c;
+  int B, Hkv, G;
+  int max_len;                 // host bound on cached length
+  const uint16_t* q;           // [B, Hq, D]
+  const uint16_t* k_new;       // [B, Hkv, D]
+  const uint16_t* v_new;       // [B, Hkv, D]
+  const uint16_t* gate;        // [B, Hq] or null
+  const int32_t* pos;          // [B]
+  const uint64_t* rope_step;   // [r / 2]
+  int r;
+  float q_scale;               // log2(e) / sqrt(D)
+  float* out;                  // [B, Hq, D]
+  int write_back;
+  float* part;                 // [ctas + B*Hkv][GP*(D+2)]: as DecodeArgs::part
+  float* wpart;                // [ctas * warps][GP*(D+2)]: a warp's state of a unit that it leaves for another
+  float* gpart;                // [ctas][GP*(D+2)]: the states of groups of CTAs
+  uint8_t* token;              // [B*Hkv][int4_token_bytes]: the new token of a unit, quantised and scored
+  int* counters;               // [B*Hkv] CTAs done with a unit, then [ctas] of groups; zero between calls
+  int* err;
+  int early;                   // as DecodeArgs::early
+  uint64_t wait_ns;
+  int debug_flags;
+  const uint16_t* q_norm;      // [D] or null
+  const uint16_t* k_norm;
+  double norm_eps;
 };
 
 // Page summaries: the bf16 mean of a page's stored keys (times k_scale), for
@@ -346,9 +375,14 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 // the same into a 4-bit cache (no gather), and the read-back of any format
 cudaError_t launch_append_int4(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_read(const ReadArgs& a, bool int4, bool f8, cudaStream_t s);
-// decode over an E4M3 cache (decode_fp8.cu) and a 4-bit one (decode_int4.cu); GP = decode_group_pad(G)
+// decode over an E4M3 cache (decode_fp8.cu); GP = decode_group_pad(G)
 cudaError_t launch_decode_fp8(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl);
-cudaError_t launch_decode_int4(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl);
+// decode over a 4-bit cache: CTAs of a call, the floats of a warp's state and the bytes of
+// a unit's token in the workspace (per (stream, KV head)), the most warps of a CTA.
+int int4_decode_ctas(int units, int n_max, int D, int G, int num_sms);
+constexpr size_t int4_token_bytes(int D, int GP) { return 8 * static_cast<size_t>(GP) + D + D / 8; }
+constexpr int kInt4Warps = 12;
+cudaError_t launch_decode_int4(const Int4DecodeArgs& a, int D, int ctas, cudaStream_t s);
 cudaError_t launch_verify_split(const VerifySplitArgs& a, int D, cudaStream_t s);
 cudaError_t launch_verify_combine(const VerifyCombineArgs& a, int D, cudaStream_t s);
 // Keys per tile of the verify pass and its largest unit count.
@@ -368,8 +402,8 @@ cudaError_t encode_verify_maps(const CacheView& c, int Hkv, int D, const uint16_
 
 // Resident CTAs per SM of the decode kernel for (D, G) (0 if unsupported).
 int decode_ctas_per_sm(int D, int G);
-// Keys per stage tile of the decode kernel for (D, G) and a layer's kv_format.
-int decode_tile_keys(int D, int G, int format = 0);
+// Keys per stage tile of the decode kernel for (D, G).
+int decode_tile_keys(int D, int G, bool f8 = false);
 // Largest number of (stream, KV head) units of one decode call.
 int decode_max_units();
 
