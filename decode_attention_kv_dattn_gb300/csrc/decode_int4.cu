@@ -3,27 +3,33 @@
 // the gate, the fp32 store and the write-back of the new entry.
 //
 // A unit is one (stream, KV head); its cache is a row of blocks of 16 tokens. What
-// bounds the pass is memory (4.5 bits a value) with little to spare: 47% of the issue
-// slots go into a block that streams at the copy rate, so every sub-partition of every
-// SM has to work all the time. Hence:
+// bounds the pass is memory (4.5 bits a value) with little to spare: its arithmetic alone
+// takes 0.93 of the copies' time on 256-wide heads of 4 queries, and 1.5 times that time
+// on groups of 5 to 8, whose scores and outputs are two column tiles of the MMAs. So
+// every sub-partition of every SM has to work all the time:
 //  * The split is made for warps, not CTAs. All units' blocks are laid end to end, each
 //    unit charged a fixed cost in blocks before them (Split), and every warp of the grid
 //    takes an equal contiguous range: it turns its own query, streams its own blocks
 //    through its own ring of stage buffers and meets no other warp until its CTA is done.
-//    A unit that lies within one warp's range is finished by that warp on the way.
-//    12 warps (3 a sub-partition, 168 registers) or 8 (256-wide heads of 5 to 8 queries:
-//    outputs and weights take 255 registers) - multiples of 4, since the sub-partition
-//    with the most warps sets the pace. A helper warp beside 10 or 11 streaming ones, the
-//    layout of the other formats, ran at FIG.
-//  * At the end of a CTA the warps' states of each unit are merged (in shared memory, a
-//    warp for each unit or all warps for one); states of units that cross CTAs go to
-//    global memory and the CTA that counts last for a unit joins them, in two levels
-//    where they are many.
+//    A unit that lies within one warp's range is finished by that warp on the way. The
+//    warps are a multiple of 4, as the sub-partition with the most sets the pace. (The
+//    other formats' layout, 10 or 11 streaming warps that share a CTA's units beside a
+//    helper warp, took 244 us for 8 x 262,144 tokens, where this one takes 193, 53 for 64
+//    ragged streams, where it takes 42, and 193 for 32 x 16,384 tokens of 24 / 4 heads,
+//    where it takes 144; one stream of 5,003 tokens 19.3, where it takes 20.)
+//  * At the end of a CTA the warps' states of each unit are merged by a team of its warps,
+//    the teams of several units side by side; states of units that cross CTAs go to global
+//    memory and the team that counts last for a unit joins them, in two levels where they
+//    are many.
 //  * The new token of a unit is quantised, scored and gated by the warp that starts the
 //    unit, and lies ready in global memory when the unit is finished.
 // Copies are whole blocks (9 D bytes of K and of V, one bulk copy each; neighbouring
 // blocks of a page go as one), issued by one lane NS stages ahead; the page table is
 // read 32 blocks ahead, a block a lane, and handed on by shuffles.
+//
+// Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 193 us,
+// 6.3 TB/s; 1 x 1,048,576 109 us; of the former ~8 us pass before the first copies land and
+// ~10 between the last block and the last output.
 #include "decode_int4.cuh"
 #include "int4.cuh"
 #include "bf16_exact.h"
@@ -37,27 +43,27 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxUnits = 512;
 constexpr int kMergeBatch = 8;  // CTAs of a group of the two-level merge
-#ifndef I4FB
-#define I4FB 12
-#endif
-constexpr int kFoldBatch = I4FB;  // states read per round trip
+constexpr int kFoldBatch = 12;  // states read per round trip
 constexpr int64_t kPrefetchLines = 1 << 15;  // largest page table (128-byte lines) put in L2 at start
-#ifndef I4COST
-#define I4COST 6
-#endif
-#ifndef I4MIN
-#define I4MIN 3
-#endif
-constexpr int kUnitCost = I4COST;   // of a unit's start and end, in blocks of a warp
-constexpr int kMinBlocks = I4MIN;  // a warp's share that is worth another warp
+// Cost of a unit's start (its query and new token) in blocks of a warp: 2 / 4 / 6 / 9
+// blocks, 64 ragged streams of 8 heads of 128 45.1 / 42.1 / 44.5 / 42.6 us, 32 x 16,384 tokens of
+// 24 / 4 heads of 256 145.5 / 144.4 / 142.3 / 142.5.
+constexpr int kUnitCost = 4;
+// Blocks that are worth another warp where a call has few: 1 / 2 / 3 / 4, one stream of
+// 5,003 tokens (with the entry's read-back) 34 / 22.1 / 20.3 / 21.6 us.
+constexpr int kMinBlocks = 3;
 
 template <int HEAD_DIM, int NT>
 struct Geo4 {
   static constexpr int D = HEAD_DIM, GP = 4 * NT;
-  static constexpr int W = D == 256 && NT == 2 ? 8 : 12;  // warps
+  // Warps, blocks of a stage, stages of a warp's ring. Two blocks are taken at once: their
+  // chains of dependent steps overlap (one at a time, 8 x 262,144 tokens 193 -> 208 us).
+  // 256-wide heads then need up to 255 registers, which leaves 8 warps (12 with one block
+  // a stage: 220 us); 128-wide ones fit 168 and 12 warps (8: 44.5 -> 46.9 us on 64 ragged).
+  static constexpr int W = D == 256 ? 8 : 12;
+  static constexpr int KG = 2;
+  static constexpr int NS = D == 256 ? 2 : 3;
   static constexpr int THREADS = W * 32;
-  static constexpr int KG = D == 256 && NT == 1 ? 1 : 2;  // blocks of a stage
-  static constexpr int NS = D == 256 && NT == 2 ? 2 : 3;  // stages of a warp's ring
   static constexpr int BLK = int4_block_bytes(D);
   static constexpr int HALF = KG * BLK;                   // K part of a stage; V follows
   static constexpr int RING = NS * 2 * HALF;
@@ -81,6 +87,7 @@ struct Geo4 {
   static_assert(STATE * 4 <= RING && SCRATCH % 16 == 0, "a state fits where a warp leaves it");
   static_assert(SMEM_MAX <= 232448 - 256, "shared memory per CTA");
   static_assert(2 * W <= 32, "the states of a CTA, a lane each");
+  static_assert(KG == 2, "issue() and the tail of a unit know two blocks a stage");
 };
 
 // Some warps of a CTA, one beside the other, that work on a unit's states together.
@@ -557,13 +564,12 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) int4_decode_kernel(co
       win_next = window(win_at + 1);
     }
     const int r0 = __shfl_sync(kFull, win, ix & 31);
-    int r1 = 0;
-    if constexpr (KG == 2) r1 = __shfl_sync(kFull, ((ix + 1) >> 5) == win_at ? win : win_next, (ix + 1) & 31);
+    const int r1 = __shfl_sync(kFull, ((ix + 1) >> 5) == win_at ? win : win_next, (ix + 1) & 31);
     if (lane == 0 && !withhold) {
       const uint32_t bar = bar0 + 8 * is, dst = ring_a + is * 2 * Gm::HALF;
       const uint8_t* k = reinterpret_cast<const uint8_t*>(c.k) + static_cast<int64_t>(r0) * BLK;
       const uint8_t* v = reinterpret_cast<const uint8_t*>(c.v) + static_cast<int64_t>(r0) * BLK;
-      const bool joined = KG == 2 && n == 2 && r1 == r0 + 1;
+      const bool joined = n == 2 && r1 == r0 + 1;
       const uint32_t bytes = joined ? 2 * BLK : BLK;
       mbar_arrive_expect_tx(bar, 2u * n * BLK);
       bulk_copy_g2s(dst, k, bytes, bar, policy);
@@ -733,16 +739,15 @@ cudaError_t launch(const Int4DecodeArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-int int4_decode_ctas(int units, int n_max, int D, int G, int num_sms) {
-  const int W = D == 256 && G > 4 ? Geo4<256, 2>::W : Geo4<128, 1>::W;
+int int4_decode_ctas(int units, int n_max, int D, int num_sms) {
+  const int W = D == 256 ? Geo4<256, 1>::W : Geo4<128, 1>::W;
   const int64_t blocks = static_cast<int64_t>(units) * ((static_cast<int64_t>(n_max) + kInt4Block - 1) / kInt4Block + kUnitCost);
   const int64_t ctas = (blocks + kMinBlocks * W - 1) / (kMinBlocks * W);
   return static_cast<int>(ctas < 1 ? 1 : ctas > num_sms ? num_sms : ctas);
 }
 
 cudaError_t launch_decode_int4(const Int4DecodeArgs& args, int D, int ctas, cudaStream_t s) {
-  static_assert(Geo4<128, 1>::W <= kInt4Warps && Geo4<128, 2>::W <= kInt4Warps && Geo4<256, 1>::W <= kInt4Warps &&
-                Geo4<256, 2>::W <= kInt4Warps, "the workspace's warps");
+  static_assert(Geo4<128, 1>::W <= kInt4Warps && Geo4<256, 1>::W <= kInt4Warps, "the workspace's warps");
   Int4DecodeArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kDefaultWaitNs;
   const int GP = decode_group_pad(a.G);

@@ -11,7 +11,7 @@
 // of the half there: 4 instructions for 8 values. The products are with c0 and c0 +
 // 16 c1: q0 c0 + q1 c1 = (q0 - q1 / 16) c0 + (q1 / 16) (c0 + 16 c1), and the outputs
 // of c1 are taken apart at the end (both exact but for the terms' own rounding: c0 is
-// a sixteenth of the byte). Masking c1 too took 5 instructions: FIG1.
+// a sixteenth of the byte).
 //
 // Columns of the MMAs: head h's high and low term side by side (2 h, 2 h + 1), so a
 // lane's score and output fragments belong to one head (t = lane % 4, and t + 4 with
@@ -30,6 +30,24 @@
 #include "mma.cuh"
 
 namespace dattn {
+
+// The MMAs and the transpose as pure functions, which the compiler may move past one
+// another (8 x 262,144 tokens 201 -> 193 us against the volatile ones of mma.cuh).
+__device__ __forceinline__ void mma_codes(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_codes_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // d = A * B
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 // q of the 4 NT heads (fp32 [4 NT][D], base-2 scale) as B fragments, and what the
 // scores need: sums of q over each group, in the units of the accumulators, and
@@ -275,8 +293,8 @@ struct Int4Warp {
               const uint32_t a[4] = {ba & m0, bb & m0, ba, bb};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (j + i == 0) mma_f16_first(acc[b][nt], a, q[nt][0], q[nt][1]);
-                else mma_f16(acc[b][nt], a, q[nt][0], q[nt][1]);
+                if (j + i == 0) mma_codes_first(acc[b][nt], a, q[nt][0], q[nt][1]);
+                else mma_codes(acc[b][nt], a, q[nt][0], q[nt][1]);
               }
             }
           }
@@ -356,8 +374,8 @@ struct Int4Warp {
             cst[nt][G + k] = fmaf(p0, l0[b][k], fmaf(p1, l1[b][k], cst[nt][G + k]));
             uint32_t hi, lo;
             split_f16x2(p0 * (s0[b][k] * f[G + k]), p1 * (s1[b][k] * f[G + k]), hi, lo);
-            pb[b][nt][0] = movm_t(prmt(hi, lo, 0x5410u));
-            pb[b][nt][1] = movm_t(prmt(hi, lo, 0x7632u));
+            pb[b][nt][0] = transposed(prmt(hi, lo, 0x5410u));
+            pb[b][nt][1] = transposed(prmt(hi, lo, 0x7632u));
           }
         }
 #pragma unroll
@@ -370,7 +388,7 @@ struct Int4Warp {
               const uint32_t ba = i ? prmt(wa, 0u, 0x4341u) : wa & m1, bb = i ? prmt(wb, 0u, 0x4341u) : wb & m1;
               const uint32_t a[4] = {ba & m0, ba, bb & m0, bb};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(o[(G + k) * 4 + j * 2 + i][nt], a, pb[b][nt][0], pb[b][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_codes(o[(G + k) * 4 + j * 2 + i][nt], a, pb[b][nt][0], pb[b][nt][1]);
             }
           }
       }
