@@ -197,6 +197,8 @@ def paged_cache(k, v, block_table, seq_len) -> Cache:
     c = Cache(_ptr(k), _ptr(v), k.shape[0], None, None, None, _ptr(block_table),
               block_table.shape[1], _ptr(seq_len))
     c._tensors = (k, v, block_table, seq_len)
+    # what a handle compares on every call of a 4-bit layer: heads and bytes of a page
+    c._int4 = list(k.shape[1:]) if k.dtype is torch.uint8 and v.dtype is torch.uint8 and k.shape == v.shape else None
     return c
 
 
@@ -302,10 +304,12 @@ class Handle:
 
     def _check_int4(self, layer, cache):
         """A 4-bit layer's call has pools of this handle's pages."""
-        for t in getattr(cache, "_tensors", ())[:2]:  # (a descriptor of the caller's own has none)
-            if t.dtype is not torch.uint8 or list(t.shape[1:]) != self._int4[layer]:
-                raise ValueError(f"a 4-bit layer's pool: {t.dtype} {tuple(t.shape)}, expected int4_pool's uint8 (pages, "
-                                 f"{self._int4[layer][0]}, {self._int4[layer][1]})")
+        if not hasattr(cache, "_tensors"):
+            return  # (a descriptor of the caller's own)
+        if getattr(cache, "_int4", None) != self._int4[layer]:
+            k, v = cache._tensors[:2]
+            raise ValueError(f"a 4-bit layer's pools: {k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}, expected "
+                             f"int4_pool's uint8 (pages, {self._int4[layer][0]}, {self._int4[layer][1]}) for both")
 
     def append_kv(self, layer, cache: Cache, k, v, start_index, count, start_pos=None,
                   rotate=True, stream=None):
@@ -320,10 +324,10 @@ class Handle:
     def read_kv(self, layer, cache: Cache, start_index, count, k, v, stream=None):
         """Cached entries [start_index, start_index + count) of each row back as bf16 into rows
         t < count of k, v [B, T, Hkv, D] (others are left as they are); start_index, count: [B] int32."""
-        if k.dtype is not _BF16 or v.dtype is not _BF16 or k.shape != v.shape or list(k.shape[2:]) != self._heads:
+        B, T, *heads = shape = k.shape
+        if k.dtype is not _BF16 or v.dtype is not _BF16 or v.shape != shape or heads != self._heads:
             raise ValueError(f"k, v: bf16 [B, T, {self._heads[0]}, {self._heads[1]}], got {k.dtype} {tuple(k.shape)} and "
                              f"{v.dtype} {tuple(v.shape)}")
-        B, T = k.shape[0], k.shape[1]
         if start_index.dtype is not _I32 or count.dtype is not _I32 or start_index.numel() != B or count.numel() != B:
             raise ValueError("start_index, count: int32 [B]")
         if layer in self._int4:

@@ -49,9 +49,11 @@ constexpr int64_t kPrefetchLines = 1 << 15;  // largest page table (128-byte lin
 // blocks, 64 ragged streams of 8 heads of 128 45.1 / 42.1 / 44.5 / 42.6 us, 32 x 16,384 tokens of
 // 24 / 4 heads of 256 145.5 / 144.4 / 142.3 / 142.5.
 constexpr int kUnitCost = 4;
-// Blocks that are worth another warp where a call has few: 1 / 2 / 3 / 4, one stream of
-// 5,003 tokens (with the entry's read-back) 34 / 22.1 / 20.3 / 21.6 us.
-constexpr int kMinBlocks = 3;
+// Blocks that are worth another warp where a call has few: 2 / 3 / 4 / 5, in a graph of such
+// calls, one stream of 5,003 tokens of 8 / 2 heads of 256 9.9 / 11.2 / 11.4 / 13.1 us, 20,000
+// tokens 18.2 / 12.6 / 12.3 / 13.2 us, 4 streams of 2,000 - 4,000 tokens of 24 / 4 heads 26.1 /
+// 26.4 / 18.5 / 18.0 us (more CTAs are more partial states to join).
+constexpr int kMinBlocks = 4;
 
 template <int HEAD_DIM, int NT>
 struct Geo4 {

@@ -78,3 +78,48 @@ def test_summaries_have_the_caches_shape(dattn, handle, monkeypatch):
     for start, count in ((torch.zeros(4, dtype=torch.int64), i32(4)), (i32(4), torch.zeros(4)), (i32(4), i32(3))):
         with pytest.raises(ValueError):
             handle.summarize(0, cache, bf(9, 2, 128), start, count, 16)
+
+
+def test_4_bit_layers_are_paged_in_whole_blocks(dattn):
+    """Refused before anything is allocated or launched."""
+    def status(**layer):
+        cfg = dattn.LayerConfig(layer.get("kind", dattn.CACHE_PAGED), layer.get("ring_slots", 0), layer.get("page_size", 16), 0, 0.0,
+                                None, None, 0.0, layer.get("fmt", dattn.KV_INT4), 1.0, 1.0, layer.get("log_decay"))
+        c = dattn.Config(8, 2, 128, 4, 64, 0, 1, ctypes.pointer(cfg), 0)
+        return dattn.lib.dattn_create(ctypes.byref(c), 0, ctypes.byref(ctypes.c_void_p()))
+    for page in (1, 8, 24, 100):
+        assert status(page_size=page) == dattn.EUNSUPPORTED
+    assert status(kind=dattn.CACHE_RING, ring_slots=64) == dattn.EUNSUPPORTED
+    decay = (ctypes.c_float * 2)(0.0, 0.0)
+    assert status(kind=dattn.CACHE_STATE, log_decay=ctypes.addressof(decay)) == dattn.EUNSUPPORTED
+    assert status(fmt=3) == dattn.EINVAL and status(fmt=-1) == dattn.EINVAL
+    assert dattn.lib.dattn_read_kv(None, 0, None, 1, 1, None, None, None, None, None) == dattn.EINVAL
+    for page in (0, 8, 24):
+        with pytest.raises(ValueError):
+            dattn.int4_pool(4, 2, page, 128, device="cpu")
+    assert dattn.int4_pool(4, 2, 48, 256, device="cpu").shape == (4, 2, 3 * 9 * 256)
+
+
+def test_4_bit_pools_have_the_handles_shape(dattn, monkeypatch):
+    monkeypatch.setattr(dattn, "_ptr", lambda t: None)
+    monkeypatch.setattr(dattn.lib, "dattn_create", lambda cfg, dev, out: dattn.OK)
+    h = dattn.Handle(8, 2, 128, [{"kind": dattn.CACHE_PAGED, "page_size": 32, "kv_format": dattn.KV_INT4}], 4, max_context=64, device=0)
+    h._h = ctypes.c_void_p()
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    pool = lambda *s: dattn.int4_pool(*s, device="cpu")  # noqa: E731
+    good, row = pool(9, 2, 32, 128), (i32(4, 4), i32(4))
+    for k, v in ((pool(9, 1, 32, 128), good), (good, pool(9, 2, 16, 128)), (pool(9, 2, 32, 256), pool(9, 2, 32, 256)),
+                 (good, good.to(torch.int8)), (bf(9, 2, 32, 128), bf(9, 2, 32, 128)), (good, pool(8, 2, 32, 128))):
+        c = dattn.paged_cache(k, v, *row)
+        for call in (lambda: h.decode(0, c, bf(4, 8, 128), bf(4, 2, 128), bf(4, 2, 128), i32(4), torch.zeros(4, 8, 128)),
+                     lambda: h.append_kv(0, c, bf(4, 3, 2, 128), bf(4, 3, 2, 128), i32(4), i32(4), rotate=False),
+                     lambda: h.read_kv(0, c, i32(4), i32(4), bf(4, 3, 2, 128), bf(4, 3, 2, 128))):
+            with pytest.raises(ValueError):
+                call()
+    c = dattn.paged_cache(good, good.clone(), *row)
+    out = bf(4, 3, 2, 128)
+    for args in ((i32(4), i32(4), out.float(), out), (i32(4), i32(4), out, out[:, :2]), (i32(4), i32(4), bf(4, 3, 1, 128), bf(4, 3, 1, 128)),
+                 (i32(4).long(), i32(4), out, out), (i32(4), i32(3), out, out), (i32(3), i32(4), out, out)):
+        with pytest.raises(ValueError):
+            h.read_kv(0, c, *args)

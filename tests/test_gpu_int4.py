@@ -119,8 +119,8 @@ class Case:
                 ref.store(pool["v"], "v", *at, *nv)
         return out, tol, pool
 
-    def check(self, dattn, oracle, write=True, **kw):
-        h = self.handle(dattn)
+    def check(self, dattn, oracle, write=True, max_context=None, **kw):
+        h = self.handle(dattn, max_context)
         cache = self.upload(dattn)
         out = torch.full((len(self.lens), self.Hq, self.D), float("nan"), device="cuda")
         h.decode(0, cache, dev(self.q), dev(self.k_new), dev(self.v_new), dev(self.pos), out,
@@ -169,6 +169,28 @@ def test_decode_of_many_units(dattn, oracle):
 def test_decode_of_one_long_stream(dattn, oracle, Hq, Hkv, D):
     """One stream over every SM, merged across CTAs in two levels."""
     Case(30 + Hq, Hq, Hkv, D, 64, [12001], (64, 5e6)).check(dattn, oracle)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 256), (6, 1, 256), (4, 2, 128), (8, 1, 128)])
+@pytest.mark.parametrize("lens", [[40], [1], [0], [700, 3], [300, 0, 17, 0, 0, 2000, 16]])
+def test_decode_far_below_the_bound(dattn, oracle, Hq, Hkv, D, lens):
+    """A grid for a bound of 100,000 tokens: most warps and CTAs have no block, a unit's CTAs lie far apart."""
+    Case(35 + len(lens), Hq, Hkv, D, 32, lens, (64, 5e6), True).check(dattn, oracle, max_context=100000)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 128), (16, 2, 128), (8, 4, 256), (12, 2, 256)])
+def test_decode_of_tiny_units_beside_a_long_one(dattn, oracle, Hq, Hkv, D):
+    """More units than warps in a CTA, whole units and parts of units in one warp's range, and a unit over many CTAs."""
+    rng = np.random.default_rng(36)
+    lens = [int(x) for x in rng.integers(0, 20, 40)] + [9000] + [int(x) for x in rng.integers(0, 50, 20)] + [0, 333]
+    Case(37, Hq, Hkv, D, 16, lens, (32, 1e4)).check(dattn, oracle)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 128, 129, 511, 512, 513, 1023, 1025])
+def test_decode_around_block_borders(dattn, oracle, n):
+    """Every tail of a stage of two blocks and of a window of 32."""
+    Case(38, 4, 1, 128, 16, [n]).check(dattn, oracle)
+    Case(39, 6, 1, 256, 32, [n]).check(dattn, oracle)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 256), (6, 1, 256), (8, 4, 128), (8, 1, 128)])
@@ -256,6 +278,30 @@ def test_a_length_outside_the_bound(dattn, oracle, bad):
             at = c.bt[b, n // 16]
             pool[s][at] = before[s][at]
     c.same_pools(pool)
+
+
+def test_steps_on_one_cache_behind_one_another(dattn, oracle):
+    """Calls without a wait between them, each over what the one before it wrote, on one stream."""
+    c = Case(94, 8, 2, 256, 16, [30, 200], (64, 5e6), room=20)
+    h, cache = c.handle(dattn, max_context=260), c.upload(dattn)
+    seq, steps, ins = c.keep[1], 18, []
+    for _ in range(steps):
+        q, k, v = ref.bf16_bits(c.rng.standard_normal(c.q.shape)), entries(c.rng, 2, 2, 256), entries(c.rng, 2, 2, 256)
+        ins.append((q, k, v, [dev(x) for x in (q, k, v)], torch.zeros(2, 8, 256, device="cuda"),
+                    seq + len(ins)))
+    torch.cuda.synchronize()
+    for _, _, _, d, out, pos in ins:  # (each call its own lengths, ready before the first)
+        h.decode(0, dattn.paged_cache(c.dev["k"], c.dev["v"], c.keep[0], pos), *d, pos, out)
+    assert h.get_error() == dattn.OK
+    for i, (q, k, v, _, out, _) in enumerate(ins):
+        c.q, c.k_new, c.v_new, c.pos = q, k, v, np.array(c.lens, np.int32)
+        want, tol, c.pool = c.expect(oracle, True)
+        assert (np.abs(out.cpu().numpy() - want) <= tol).all(), i
+        for b in range(2):
+            for s, e in zip("kv", c.new(oracle, b)):
+                c.values[s][b] = np.concatenate([c.values[s][b], ref.value(*e)[None]])
+            c.lens[b] += 1
+    c.same_pools(c.pool)
 
 
 def test_a_page_outside_the_pool(dattn):
