@@ -27,9 +27,10 @@
 // blocks of a page go as one), issued by one lane NS stages ahead; the page table is
 // read 32 blocks ahead, a block a lane, and handed on by shuffles.
 //
-// Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 193 us,
-// 6.3 TB/s; 1 x 1,048,576 109 us; of the former ~8 us pass before the first copies land and
-// ~10 between the last block and the last output.
+// Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 253 us,
+// 4.8 TB/s; 1 x 1,048,576 135 us; 64 ragged streams 48 us; 32 x 16,384 of 24 / 4 heads 172.
+// Of the first ~8 us pass before the first copies land and ~10 between the last block and
+// the last output.
 #include "decode_int4.cuh"
 #include "int4.cuh"
 #include "bf16_exact.h"

@@ -2,27 +2,39 @@
 //
 // With code c, step s and least value b of a (key k, group G of 64 dims):
 //   score    q . K_k = sum_G [ s_kG (q_G . c_kG) + b_kG sum(q_G) ]
-//   output   O_d    += sum_k p_k s_kG c_kd  +  sum_k p_k b_kG     (d in G)
+//   output   O_d    += sum_k p_k s_kG (c_kd - 8)  +  sum_k p_k (b_kG + 8 s_kG)     (d in G)
 // so the codes enter the tensor cores as they are - whole numbers, exact in fp16 -
 // and the grid is applied to 4 scores (K) or folded into the weights (V): a group of
-// 64 dims costs a few FMAs instead of one for every value. Codes become fp16 operands
-// by a mask alone: the low byte of a half, codes c0 and c1, is the fp16 number (c0 + 16
-// c1) 2^-24, its low 4 bits are c0 2^-24, and one byte permute brings the other two codes
-// of the half there: 4 instructions for 8 values. The products are with c0 and c0 +
-// 16 c1: q0 c0 + q1 c1 = (q0 - q1 / 16) c0 + (q1 / 16) (c0 + 16 c1), and the outputs
-// of c1 are taken apart at the end (both exact but for the terms' own rounding: c0 is
-// a sixteenth of the byte).
+// 64 dims costs a few FMAs instead of one for every value. The products are not with
+// c0 and c1 of a byte but with c0 and the byte c0 + 16 c1, which one mask or byte permute
+// each brings into a half: q0 c0 + q1 c1 = (q0 - q1 / 16) c0 + (q1 / 16) (c0 + 16 c1),
+// and the outputs of c1 are taken apart at the end.
 //
 // Columns of the MMAs: head h's high and low term side by side (2 h, 2 h + 1), so a
 // lane's score and output fragments belong to one head (t = lane % 4, and t + 4 with
 // NT = 2), and a head's hi + lo is one add without a shuffle.
 //
-// Precision. q's factors and the weights p s enter as two fp16 terms, 22 bits, where fp16
-// holds them: q is scaled by a power of two that brings the head's largest to 2^13 ..
-// 2^14, the weights by f_G, a power of two that
-// follows the largest step seen so far (step f_G in 2^6 .. 2^8), p being at most 2^6:
-// the running maximum is only moved when a score passes it by 6, which saves the
-// cross-lane maximum of every group of keys. Sums are fp32.
+// Precision: that of fp32 sums (1.0 - 1.6e-7 of the outputs' size, against 64 bits).
+//  * q's factors and the weights p s enter as two fp16 terms, 22 bits, where fp16 holds
+//    them: q is scaled by a power of two that brings the head's largest to 2^18 .. 2^19
+//    (2^14 .. 2^15 as a byte's factor, which is a sixteenth), the weights by f_G, a power of
+//    two that follows the largest step seen so far (step f_G in 2^6 .. 2^8), p being at
+//    most 2^6: the running maximum is only moved when a score passes it by 6, which saves
+//    the cross-lane maximum of every group of keys.
+//  * An MMA lines its products up by the operands' exponents and drops what lies below, and
+//    a subnormal operand counts as 2^-14 there, however small. A code masked out of its
+//    word is a subnormal, c 2^-24: as it is it costs c0's products 6 bits and the bytes' 2.
+//    The keys' bytes can stand that (their factors are a sixteenth of c0's); c0 and the
+//    values' operands are made normal numbers by one more operation each (the mask sets
+//    the exponent of 1024, which is then taken off): with subnormals alone the outputs were
+//    off by 2 - 4e-6.
+//  * The values' codes are centred (c - 8): sums of codes 0 .. 15 grow with the context
+//    while the outputs do not, and the 7.5 sum(p s) in them, taken off at the end, left
+//    errors of 4e-5 over a million tokens.
+//  * The MMAs' sums are cut off, not rounded, so long chains shrink: each pair of blocks is
+//    summed from zero and added in fp32 (one chain: 7.5e-6 over 262,144 tokens).
+// All of it together takes 8 x 262,144 tokens from 198 to 253 us, 64 ragged streams from 42
+// to 48.
 #pragma once
 
 #include "common.cuh"
@@ -42,6 +54,26 @@ __device__ __forceinline__ void mma_codes_first(float (&d)[4], const uint32_t (&
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t less(uint32_t x, uint32_t y) {  // of fp16 pairs
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void add4(float (&o)[4], const float (&x)[4]) {  // o += x, two at a time
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    uint64_t a, b;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(o[e]), "f"(o[e + 1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x[e]), "f"(x[e + 1]));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o[e]), "=f"(o[e + 1]) : "l"(a));
+  }
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t x) {  // (x - 1024) 2^-10 of an fp16 pair
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0x14001400u), "r"(0xbc00bc00u));
+  return r;
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -75,21 +107,22 @@ __device__ __forceinline__ void int4_query(const float* qs, int lane, uint32_t (
     }
     mx = fmaxf(mx, __shfl_xor_sync(full, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(full, mx, 2));
-    // 2^(13 - floor(log2 mx)), 2^100 at the most (a head of zeros)
-    const int e = 267 - static_cast<int>(__float_as_uint(mx) >> 23);
+    // 2^(18 - floor(log2 mx)), 2^100 at the most (a head of zeros)
+    const int e = 272 - static_cast<int>(__float_as_uint(mx) >> 23);
     const float S = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 227)) << 23);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-      // dims i of the word: halves 0 .. 3 and 4 .. 7, bytes (0, 1) and (2, 3) of a half
+      // dims i of the word: halves 0 .. 3 and 4 .. 7, bytes (0, 1) and (2, 3) of a half; c0
+      // is an operand in units of 2^-10, a byte in units of 2^-24
       const float* x = src + (w >> 1) * 64 + t * 16 + (w & 1) * 8;
       const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
       const float z = S * 0.0625f;
       uint32_t hi, lo;
-      split_f16x2(fmaf(a.y, -z, a.x * S), fmaf(b.y, -z, b.x * S), hi, lo);
+      split_f16x2(fmaf(a.y, -z, a.x * S) * 0x1p-14f, fmaf(b.y, -z, b.x * S) * 0x1p-14f, hi, lo);
       qb[2 * w][nt][0] = g & 1 ? lo : hi;
       split_f16x2(a.y * z, b.y * z, hi, lo);
       qb[2 * w][nt][1] = g & 1 ? lo : hi;
-      split_f16x2(fmaf(a.w, -z, a.z * S), fmaf(b.w, -z, b.z * S), hi, lo);
+      split_f16x2(fmaf(a.w, -z, a.z * S) * 0x1p-14f, fmaf(b.w, -z, b.z * S) * 0x1p-14f, hi, lo);
       qb[2 * w + 1][nt][0] = g & 1 ? lo : hi;
       split_f16x2(a.w * z, b.w * z, hi, lo);
       qb[2 * w + 1][nt][1] = g & 1 ? lo : hi;
@@ -114,7 +147,7 @@ struct Int4Warp {
   uint32_t qb[kSharedQ ? 1 : KS][NT][2];
   float qsum[NT][NG], inv[NT];
   float o[MT][NT][4];
-  float m[NT], l[NT], cst[NT][NG];  // base-2 maximum, sum of weights, sum of p b
+  float m[NT], l[NT], cst[NT][NG];  // base-2 maximum, sum of weights, sum of p (b + 8 s)
   float f[NG];                      // power of two of the weights of group G
 
   // The fragments into shared memory (kSharedQ), and the warp's own part of them.
@@ -290,7 +323,7 @@ struct Int4Warp {
               const uint32_t wa = k ? (j ? xa[b].w : xa[b].z) : (j ? xa[b].y : xa[b].x);
               const uint32_t wb = k ? (j ? xb[b].w : xb[b].z) : (j ? xb[b].y : xb[b].x);
               const uint32_t ba = i ? prmt(wa, 0u, 0x4341u) : wa & m1, bb = i ? prmt(wb, 0u, 0x4341u) : wb & m1;
-              const uint32_t a[4] = {ba & m0, bb & m0, ba, bb};
+              const uint32_t a[4] = {scaled((ba & m0) | 0x64006400u), scaled((bb & m0) | 0x64006400u), ba, bb};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 if (j + i == 0) mma_codes_first(acc[b][nt], a, q[nt][0], q[nt][1]);
@@ -313,15 +346,24 @@ struct Int4Warp {
     }
     // ---- do the maximum and the weights' scales still hold?
     float top = 0.f;
+    {
+      uint32_t mx[NG];
 #pragma unroll
-    for (int b = 0; b < N; ++b)
+      for (int G = 0; G < NG; ++G) mx[G] = 0u;
 #pragma unroll
-      for (int G = 0; G < NG; G += 2) {
-        float s0[2], s1[2], x[2];
-        pairs(vb + b * pitch, g, G, s0, x);
-        pairs(vb + b * pitch, g + 8, G, s1, x);
-        top = fmaxf(top, fmaxf(fmaxf(s0[0], s1[0]) * f[G], fmaxf(s0[1], s1[1]) * f[G + 1]));
-      }
+      for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int G = 0; G < NG; G += 2) {
+            const uint2 p = *reinterpret_cast<const uint2*>(vb + b * pitch + 8 * D + (g + 8 * i) * (4 * NG) + G * 4);
+            // (steps are not negative: the larger pair as a number has the larger step)
+            mx[G] = max(mx[G], p.x);
+            mx[G + 1] = max(mx[G + 1], p.y);
+          }
+#pragma unroll
+      for (int G = 0; G < NG; ++G) top = fmaxf(top, __uint_as_float(mx[G] & 0xffff0000u) * f[G]);
+    }
     bool move = top > 256.f;
 #pragma unroll
     for (int b = 0; b < N; ++b) {
@@ -371,7 +413,7 @@ struct Int4Warp {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float p0 = s[b][nt][0], p1 = s[b][nt][1];
-            cst[nt][G + k] = fmaf(p0, l0[b][k], fmaf(p1, l1[b][k], cst[nt][G + k]));
+            cst[nt][G + k] = fmaf(p0, fmaf(8.f, s0[b][k], l0[b][k]), fmaf(p1, fmaf(8.f, s1[b][k], l1[b][k]), cst[nt][G + k]));
             uint32_t hi, lo;
             split_f16x2(p0 * (s0[b][k] * f[G + k]), p1 * (s1[b][k] * f[G + k]), hi, lo);
             pb[b][nt][0] = transposed(prmt(hi, lo, 0x5410u));
@@ -379,17 +421,25 @@ struct Int4Warp {
           }
         }
 #pragma unroll
-        for (int b = 0; b < N; ++b)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t wa = j ? x[b].y : x[b].x, wb = j ? x[b].w : x[b].z;
+          for (int i = 0; i < 2; ++i) {
+            float sum[NT][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t ba = i ? prmt(wa, 0u, 0x4341u) : wa & m1, bb = i ? prmt(wb, 0u, 0x4341u) : wb & m1;
-              const uint32_t a[4] = {ba & m0, ba, bb & m0, bb};
+            for (int b = 0; b < N; ++b) {
+              const uint32_t wa = j ? x[b].y : x[b].x, wb = j ? x[b].w : x[b].z;
+              const uint32_t ba = i ? prmt(wa, 0x64646464u, 0x4341u) : (wa & m1) | 0x64006400u;
+              const uint32_t bb = i ? prmt(wb, 0x64646464u, 0x4341u) : (wb & m1) | 0x64006400u;
+              const uint32_t a[4] = {less((ba & m0) | 0x64006400u, 0x64086408u), less(ba, 0x64886488u),
+                                     less((bb & m0) | 0x64006400u, 0x64086408u), less(bb, 0x64886488u)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_codes(o[(G + k) * 4 + j * 2 + i][nt], a, pb[b][nt][0], pb[b][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if (b == 0) mma_codes_first(sum[nt], a, pb[b][nt][0], pb[b][nt][1]);
+                else mma_codes(sum[nt], a, pb[b][nt][0], pb[b][nt][1]);
+              }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) add4(o[(G + k) * 4 + j * 2 + i][nt], sum[nt]);
           }
       }
     }
@@ -422,10 +472,10 @@ struct Int4Warp {
           const float(&a)[4] = o[G * 4 + j * 2][nt];
           const float(&b)[4] = o[G * 4 + j * 2 + 1][nt];
           const float a0 = a[0] + a[1], b0 = b[0] + b[1];
-          v.x = fmaf(a0 * 0x1p24f, back, c);
-          v.y = fmaf(((a[2] + a[3]) - a0) * 0x1p20f, back, c);
-          v.z = fmaf(b0 * 0x1p24f, back, c);
-          v.w = fmaf(((b[2] + b[3]) - b0) * 0x1p20f, back, c);
+          v.x = fmaf(a0, back, c);
+          v.y = fmaf(((a[2] + a[3]) - a0) * 0.0625f, back, c);
+          v.z = fmaf(b0, back, c);
+          v.w = fmaf(((b[2] + b[3]) - b0) * 0.0625f, back, c);
           *reinterpret_cast<float4*>(os + (4 * nt + t) * D + G * 64 + g * 8 + j * 4) = v;
         }
       }
