@@ -162,8 +162,8 @@ __device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* r
 
 // One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V).
 // Tokens that the call does not bring stay as they are. Issue-bound, ~20 instructions a
-// value: 64 ragged prompts (133,000 tokens of 8 heads of 128, rotated) 233 us with 4
-// CTAs an SM, 254 with 3 and 236 with 5, where its 700 MB take 103.
+// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 233 us with 4
+// CTAs an SM, 254 with 3 and 236 with 5, where its 660 MB take 98.
 template <int D, bool ROT>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const AppendArgs a) {
   constexpr int NG = D / kInt4Group;

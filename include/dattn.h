@@ -406,6 +406,7 @@ DATTN_API int dattn_get_error(dattn_t* h, dattn_stream_t stream);
  *                   the limit. The call still completes (the copies it issued
  *                   land before it exits) and the context stays usable; the
  *                   output and any write-back of that call are undefined.
+ *                   4-bit layers: each warp's first blocks are not copied.
  *                   Prompts on state layers: a CTA's first tile of queries is
  *                   not copied; the heads that wait for it keep their state.
  *                   DATTN_DEBUG_WITHHOLD_KV: in each later prompt on a state
