@@ -261,6 +261,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
 }
 
 // ---------------------------------------------------------------- read back
+//
+// These kernels do not let the next launch start before they end: what they write is
+// the caller's, who may give it to a decode as its new token, and a decode reads its
+// inputs before it waits for the launch ahead of it.
 
 // Two codes (low 4 bits of each half of w) to their values as a bf16 pair, rounded
 // once: the codes become bf16 by their place in 128..143, exactly.
@@ -276,7 +280,6 @@ template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32) int4_read_kernel(const ReadArgs a) {
   constexpr int NG = D / kInt4Group;
   pdl_wait();
-  pdl_trigger();
   const int b = blockIdx.y;
   BlockSpan s;
   if (!find_block(a.c, a.Hkv, b, a.start_index[b], a.count[b], a.Tmax, a.err, s)) return;
@@ -347,7 +350,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_read_kernel(const ReadArg
 template <bool F8>
 __global__ void __launch_bounds__(kMaxWarps * 32) read_kernel(const ReadArgs a) {
   pdl_wait();
-  pdl_trigger();
   const CacheView& c = a.c;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kMaxWarps + (threadIdx.x >> 5);

@@ -275,7 +275,7 @@ DATTN_API int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, i
  * and ring (at most R tokens of a row a call); state layers return
  * DATTN_EUNSUPPORTED. A count outside 0..max_tokens, an index without a page and a
  * row outside the pool are reported (DATTN_EINDEX) and their rows left as they are.
- * One launch. */
+ * One launch, behind which every launch waits: k and v may be the next call's inputs. */
 DATTN_API int dattn_read_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_streams, int max_tokens,
                             const int32_t* start_index, const int32_t* count, void* k, void* v,
                             dattn_stream_t stream);
@@ -292,7 +292,8 @@ DATTN_API int dattn_read_kv(dattn_t* h, int layer, const dattn_cache* cache, int
  * append of this library) does not write into the same cache; its outputs and
  * the write-back always wait for the earlier launch to complete. Inputs (q,
  * k_new, v_new, gate, pos, cache metadata) must not be produced by the
- * immediately preceding launch if that launch is one of this library's. */
+ * immediately preceding launch if that launch is one of this library's
+ * (dattn_read_kv excepted). */
 DATTN_API int dattn_decode(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decode_args* args,
                  dattn_stream_t stream);
 

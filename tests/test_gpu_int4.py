@@ -603,6 +603,57 @@ def test_layers_in_one_graph_and_on_two_streams(dattn, oracle):
         cs[i].same_pools(pool)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_entries_read_back_are_the_next_calls_input(dattn, fmt):
+    """A decode whose new tokens the call just before it reads back, without a wait in between,
+    eager and in a graph: the outputs of a decode with those tokens in place."""
+    rng = np.random.default_rng(151)
+    H, Hq, D, P, lens, steps = 2, 8, 128, 16, [70, 5, 33, 128], 12
+    B = len(lens)
+    bt, pages = tables(rng, lens, P)
+    layers = [{"kind": dattn.CACHE_PAGED, "page_size": P, "kv_format": f}
+              for f in (dattn.KV_INT4, dattn.KV_INT4 if fmt == "int4" else dattn.KV_BF16)]
+    h = dattn.Handle(Hq, H, D, layers, B, max_context=256)
+    seq = dev(np.array(lens, np.int32))
+    src = dattn.paged_cache(dev(ref.random_pool(rng, pages, H, P, D)), dev(ref.random_pool(rng, pages, H, P, D)), dev(bt), seq)
+    count, at = dev(np.array(lens, np.int32)), [dev(np.full(B, i % min(lens), np.int32)) for i in range(steps)]
+    start, one = dev(np.zeros(B, np.int32)), dev(np.ones(B, np.int32))
+    vals = [dev(entries(rng, B, max(lens), H, D)).view(torch.bfloat16) for _ in range(4)]
+    h.append_kv(0, src, *vals[:2], start, count, rotate=False)
+    shape = (pages, H, P, D)
+    pools = [dattn.int4_pool(pages, H, P, D) if fmt == "int4" else torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    cache = dattn.paged_cache(*pools, dev(bt), seq)
+    h.append_kv(1, cache, *vals[2:], start, count, rotate=False)
+    q = dev(ref.bf16_bits(rng.standard_normal((B, Hq, D)))).view(torch.bfloat16)
+    new = [torch.empty(B, 1, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out = torch.zeros(steps, B, Hq, D, device="cuda")
+
+    def run(wait):
+        for i in range(steps):
+            h.read_kv(0, src, at[i], one, *new)
+            if wait:
+                torch.cuda.synchronize()
+            h.decode(1, cache, q, new[0].view(B, H, D), new[1].view(B, H, D), seq, out[i], max_seq_len=256, write_back=False)
+
+    run(True)
+    want = out.clone()
+    assert not torch.equal(want[0], want[1])
+    out.zero_()
+    run(False)
+    assert torch.equal(out, want)
+    out.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(False)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert h.get_error() == dattn.OK
+
+
 def test_calls_that_do_not_take_a_4_bit_layer(dattn):
     c = Case(160, 8, 2, 128, 16, [20])
     h = c.handle(dattn, max_verify_rows=4, max_selected_pages=4)
