@@ -346,6 +346,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32) int4_read_kernel(const ReadArg
   }
 }
 
+// E4M3 value times scale in fp32, for one rounding to bf16 in all: a product (28 bits)
+// that fp32 rounds onto the middle between two bf16 values goes back to its own side.
+__device__ __forceinline__ float scaled_e4m3(uint8_t x, float scale) {
+  const float v = e4m3_to_f32(x), p = v * scale, e = fmaf(v, scale, -p);
+  const uint32_t b = __float_as_uint(p);
+  if ((b & 0xffffu) != 0x8000u || !(e > 0.f || e < 0.f)) return p;
+  return __uint_as_float((e > 0.f) == (p > 0.f) ? b + 1u : b - 1u);
+}
+
 // bf16 and E4M3 caches, paged or ring: one warp per token, 8 dims a lane and step.
 template <bool F8>
 __global__ void __launch_bounds__(kMaxWarps * 32) read_kernel(const ReadArgs a) {
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) read_kernel(const ReadArgs a) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t two = (j < 2 ? x.x : x.y) >> (16 * (j & 1));
-          w[j] = pack_bf16x2(e4m3_to_f32(static_cast<uint8_t>(two)) * scale, e4m3_to_f32(static_cast<uint8_t>(two >> 8)) * scale);
+          w[j] = pack_bf16x2(scaled_e4m3(static_cast<uint8_t>(two), scale), scaled_e4m3(static_cast<uint8_t>(two >> 8), scale));
         }
         *dst = make_uint4(w[0], w[1], w[2], w[3]);
       } else {

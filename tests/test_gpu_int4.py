@@ -500,6 +500,43 @@ def test_read_back_of_the_other_formats(dattn, kind, fp8):
         assert torch.equal(o.cpu(), e)
 
 
+def nearest_bf16(x):
+    """bf16 bits nearest to fp64 values (normal numbers and zeros), ties to even, in one rounding."""
+    b = np.asarray(x, np.float64).view(np.uint64)
+    keep = np.uint64(45)  # 52 - 7 bits of the fraction
+    b = (b + np.uint64(2 ** 44 - 1) + ((b >> keep) & np.uint64(1))) >> keep << keep
+    return ref.bf16_bits(b.view(np.float64))
+
+
+def test_read_back_of_e4m3_rounds_once(dattn):
+    """Scales that put the product of an E4M3 value just beside the middle between two bf16 values, where fp32 has
+    only the middle itself: the nearest bf16 to the exact product (by integers), of every finite byte."""
+    D, P = 128, 16
+    bits = np.arange(256, dtype=np.uint8)
+    value = np.nan_to_num(torch.from_numpy(bits).view(torch.float8_e4m3fn).double().numpy())
+    hard = 0
+    for m in (1.125, 1.375, 1.75, 1.625):
+        for mid in range(1, 40, 2):
+            scale = float(np.float32((1 + mid / 256) / m))
+            exact = value * scale  # 4 + 24 bits: exact in 64
+            want, twice = nearest_bf16(exact), ref.bf16_bits(exact)  # (by way of fp32)
+            if (want == twice).all():
+                continue
+            hard += 1
+            pools = [torch.from_numpy(np.tile(bits, 8 * D * P // 256).reshape(8, 1, P, D)).cuda() for _ in range(2)]
+            layer = {"kind": dattn.CACHE_PAGED, "page_size": P, "kv_format": dattn.KV_E4M3, "k_scale": scale, "v_scale": scale}
+            h = dattn.Handle(1, 1, D, [layer], 1, max_context=8 * P)
+            bt, z = dev(np.arange(8, dtype=np.int32)[None]), torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = [torch.zeros(1, 8 * P, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            h.read_kv(0, dattn.paged_cache(*pools, bt, z), z, dev(np.array([8 * P], np.int32)), *out)
+            assert h.get_error() == dattn.OK
+            finite = np.tile(bits & 127 != 127, 8 * D * P // 256)
+            for o in out:
+                got = host_u16(o).reshape(-1)
+                assert np.array_equal(got[finite], np.tile(want, 8 * D * P // 256)[finite])
+    assert hard > 5
+
+
 # ---------------------------------------------------------------- runs
 
 def test_prompts_then_steps(dattn, oracle):
