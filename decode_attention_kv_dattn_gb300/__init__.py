@@ -302,11 +302,15 @@ class Handle:
             raise ValueError(f"summary: shape {tuple(summary.shape)}, expected ({cache.n_rows} pages, {self._heads[0]}, "
                              f"{self._heads[1]})")
 
-    def _check_int4(self, layer, cache):
-        """A 4-bit layer's call has pools of this handle's pages."""
+    def _check_pools(self, layer, cache):
+        """A 4-bit layer's call has pools of this handle's pages, and no other layer's has such pools."""
         if not hasattr(cache, "_tensors"):
             return  # (a descriptor of the caller's own)
-        if getattr(cache, "_int4", None) != self._int4[layer]:
+        pages = getattr(cache, "_int4", None)
+        if layer not in self._int4:
+            if pages is not None and len(pages) == 2:
+                raise ValueError(f"layer {layer} is not a 4-bit layer, its call has int4_pool's pools")
+        elif pages != self._int4[layer]:
             k, v = cache._tensors[:2]
             raise ValueError(f"a 4-bit layer's pools: {k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}, expected "
                              f"int4_pool's uint8 (pages, {self._int4[layer][0]}, {self._int4[layer][1]}) for both")
@@ -315,8 +319,7 @@ class Handle:
                   rotate=True, stream=None):
         """k, v: [B, T, Hkv, D] bf16; start_index, count (, start_pos): [B] int32."""
         B, T = k.shape[0], k.shape[1]
-        if layer in self._int4:
-            self._check_int4(layer, cache)
+        self._check_pools(layer, cache)
         _check(lib.dattn_append_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index),
                                    _ptr(start_pos), _ptr(count), _ptr(k), _ptr(v), int(rotate),
                                    _stream_ptr(stream, self.device)), "dattn_append_kv")
@@ -330,8 +333,7 @@ class Handle:
                              f"{v.dtype} {tuple(v.shape)}")
         if start_index.dtype is not _I32 or count.dtype is not _I32 or start_index.numel() != B or count.numel() != B:
             raise ValueError("start_index, count: int32 [B]")
-        if layer in self._int4:
-            self._check_int4(layer, cache)
+        self._check_pools(layer, cache)
         _check(lib.dattn_read_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index), _ptr(count), _ptr(k),
                                  _ptr(v), _stream_ptr(stream, self.device)), "dattn_read_kv")
 
@@ -342,8 +344,7 @@ class Handle:
         B = q.shape[0]
         if self._kinds.get(layer) == CACHE_STATE:
             self._check_state(cache, B)
-        if layer in self._int4:
-            self._check_int4(layer, cache)
+        self._check_pools(layer, cache)
         args = DecodeArgs(B, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
                           _ptr(out), int(max_seq_len), int(write_back))
         _check(lib.dattn_decode(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
@@ -356,6 +357,7 @@ class Handle:
         [pages, Hkv, D] bf16 as `summarize` keeps it; selected [B, Hkv, num_pages] int32
         receives the pages (ascending, then -1) if given. The handle needs
         max_selected_pages >= num_pages."""
+        self._check_pools(layer, cache)
         if summary is not None and self._kinds.get(layer) == CACHE_PAGED:
             self._check_summary(cache, summary)
         args = DecodeArgs(q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(gate), _ptr(pos),
@@ -371,6 +373,7 @@ class Handle:
         """Summaries (bf16 means of the stored keys, [pages, Hkv, D]) of the pages that the
         new tokens [start_index, start_index + count) of each row completed; start_index,
         count: [B] int32, count <= max_tokens."""
+        self._check_pools(layer, cache)
         if summary is not None and self._kinds.get(layer) == CACHE_PAGED:
             self._check_summary(cache, summary)
         B = start_index.shape[0]
@@ -384,6 +387,7 @@ class Handle:
         """q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16; parent [S, T] int32; out [S, T, Hq, D]
         fp32; gate [S, T, Hq] bf16 or None; pos [S] int32 root positions (default: the
         cache's seq_len; ring layers need it and take write_back=False)."""
+        self._check_pools(layer, cache)
         args = VerifyArgs(q.shape[0], q.shape[1], _ptr(q), _ptr(k), _ptr(v), _ptr(parent),
                           _ptr(gate), _ptr(out), int(max_prefix_len), int(write_back), _ptr(pos))
         _check(lib.dattn_verify(self._h, layer, ctypes.byref(cache), ctypes.byref(args),
@@ -393,6 +397,7 @@ class Handle:
         """Write each stream's accepted path (accepted [S, T] int32 node indices root
         first, num_accepted [S]) at the cache's next indices, rotated at pos + d;
         k, v, parent as given to the verify call."""
+        self._check_pools(layer, cache)
         _check(lib.dattn_commit(self._h, layer, ctypes.byref(cache), k.shape[0], k.shape[1], _ptr(k),
                                 _ptr(v), _ptr(parent), _ptr(accepted), _ptr(num_accepted), _ptr(pos),
                                 _stream_ptr(stream, self.device)), "dattn_commit")
@@ -400,6 +405,7 @@ class Handle:
     def prefill(self, layer, cache: Cache, q, k, v, count, start_pos, out, gate=None, stream=None):
         """Ragged prefill: q [S, T, Hq, D], k/v [S, T, Hkv, D] bf16, count/start_pos [S] int32,
         out [S, T, Hq, D] fp32 (rows t < count written), gate [S, T, Hq] bf16 or None."""
+        self._check_pools(layer, cache)
         B, T = q.shape[0], q.shape[1]
         if self._kinds.get(layer) == CACHE_STATE:
             self._check_state(cache, B)

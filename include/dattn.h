@@ -112,7 +112,8 @@ enum {
  *   V: (d / 64) 512 + (((d / 8) % 8) 4 + (r % 8) / 2) 16 + (r / 8) 8 + ((d / 4) % 2) 4
  *      + (r % 2) 2 + (d % 4) / 2
  * and the group's least value and step (bf16 each) at byte 8 D + (r D / 64 + d / 64) 4.
- * What lies in a block beside the tokens written is never read as a value. */
+ * What lies in a block beside the tokens written is never read as a value. Decode
+ * takes keys below 2^98 in magnitude (the scores of larger ones may pass fp32). */
 #define DATTN_INT4_BYTES(P, D) ((P) / 16 * 9 * (D))
 
 /* cudaStream_t without including the CUDA headers. */

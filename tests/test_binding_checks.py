@@ -123,3 +123,31 @@ def test_4_bit_pools_have_the_handles_shape(dattn, monkeypatch):
                  (i32(4).long(), i32(4), out, out), (i32(4), i32(3), out, out), (i32(3), i32(4), out, out)):
         with pytest.raises(ValueError):
             h.read_kv(0, c, *args)
+
+
+def test_4_bit_pools_stay_off_other_layers(dattn, monkeypatch):
+    """(A bf16 layer would take their bytes for entries three to four times as long.)"""
+    monkeypatch.setattr(dattn, "_ptr", lambda t: None)
+    monkeypatch.setattr(dattn.lib, "dattn_create", lambda cfg, dev, out: dattn.OK)
+    h = dattn.Handle(8, 2, 128, [{"kind": dattn.CACHE_PAGED, "page_size": 16},
+                                 {"kind": dattn.CACHE_PAGED, "page_size": 16, "kv_format": dattn.KV_E4M3, "k_scale": 1.0, "v_scale": 1.0}],
+                     4, max_context=64, max_verify_rows=3, device=0)
+    h._h = ctypes.c_void_p()
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    pool, row = dattn.int4_pool(9, 2, 16, 128, device="cpu"), (i32(4, 4), i32(4))
+    c = dattn.paged_cache(pool, pool.clone(), *row)
+    q, kv, out = bf(4, 3, 8, 128), bf(4, 3, 2, 128), torch.zeros(4, 3, 8, 128)
+    summary = bf(9, 2, 128)
+    one = (q[:, 0], kv[:, 0], kv[:, 0], i32(4), out[:, 0])
+    for layer in (0, 1):
+        for call in (lambda: h.decode(layer, c, *one), lambda: h.append_kv(layer, c, kv, kv, i32(4), i32(4), rotate=False),
+                     lambda: h.read_kv(layer, c, i32(4), i32(4), kv, kv), lambda: h.sparse_decode(layer, c, summary, *one, 2),
+                     lambda: h.summarize(layer, c, summary, i32(4), i32(4), 3), lambda: h.verify(layer, c, q, kv, kv, i32(4, 3), out),
+                     lambda: h.commit(layer, c, kv, kv, i32(4, 3), i32(4, 3), i32(4), i32(4)),
+                     lambda: h.prefill(layer, c, q, kv, kv, i32(4), i32(4), out)):
+            with pytest.raises(ValueError, match="4-bit"):
+                call()
+    # (a byte pool of an E4M3 layer is none)
+    e4m3 = torch.zeros(9, 2, 16, 128, dtype=torch.uint8)
+    h._check_pools(1, dattn.paged_cache(e4m3, e4m3.clone(), *row))
