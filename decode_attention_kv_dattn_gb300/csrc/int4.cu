@@ -95,75 +95,116 @@ __device__ __forceinline__ bool settled(F2 v, F2 e, uint32_t& w) {
   return w == pack_bf16x2(a, b);
 }
 
-// Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so.
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
+  const uint4 x = ld_nc_v4(p), y = ld_nc_v4(p + 8);
+  w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+}
+
 // An entry is the bf16 nearest to the exact value. It is formed in fp32 with a bound
 // of its error - 2^-23 of the rotation's terms, 2^-22 of a normalised value, and 2^-110
 // for what underflows - and where both ends of the bound round alike, that is the
 // entry; about one value in 5,000 goes to key_pair instead (7 instructions a value
 // against ~30 of the exact sum: 64 ragged prompts 1,490 -> 233 us).
+//
+// Sixteen values from dim d on, normalised; the words that key_pair has to settle into open.
+__device__ __forceinline__ void normed(const AppendArgs& a, uint32_t (&x)[8], int d, double inv, uint32_t& open) {
+  if (!a.k_norm) return;
+  uint32_t kw[8];
+  load16(a.k_norm + d, kw);
+  const float f = static_cast<float>(inv);
+  if (!(f >= 0x1p-120f && f <= 0x1p120f)) open = 0xffu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const F2 v = mul2(mul2(wide2(x[i]), wide2(kw[i])), f2(f, f));
+    float v0, v1;
+    split(v, v0, v1);
+    const F2 e = fma2(f2(fabsf(v0), fabsf(v1)), f2(0x1p-22f, 0x1p-22f), f2(0x1p-110f, 0x1p-110f));
+    if (!settled(v, e, x[i])) open |= 1u << i;
+  }
+}
+
+// x + y s with the bound of its error, into w; whether it settled.
+__device__ __forceinline__ bool turned(F2 x, F2 y, F2 s, uint32_t& w) {
+  const F2 v = fma2(y, s, x);
+  float x0, x1, v0, v1;
+  split(x, x0, x1);
+  split(v, v0, v1);
+  return settled(v, fma2(f2(fabsf(x0) + fabsf(v0), fabsf(x1) + fabsf(v1)), f2(0x1p-23f, 0x1p-23f), f2(0x1p-110f, 0x1p-110f)), w);
+}
+
+// The words of w, dims d0 on, that are open, by the exact sum.
+__device__ __forceinline__ void settle(const AppendArgs& a, const uint16_t* row, int D, int tok, int d0, double inv, const float4* cs,
+                                       uint32_t open, uint32_t (&w)[8]) {
+  while (open) {
+    const int i = __ffs(open) - 1;
+    open &= open - 1;
+    const uint32_t v = key_pair(row, a.k_norm, inv, cs, D, tok, a.r, d0 + 2 * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j == i) w[j] = v;
+  }
+}
+
+// Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so.
 template <int D, bool ROT>
 __device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* row, int tok, int d0, double inv, const float4* cs,
                                           uint32_t (&w)[8]) {
-  const uint4 x0 = ld_nc_v4(row + d0), x1 = ld_nc_v4(row + d0 + 8);
-  w[0] = x0.x; w[1] = x0.y; w[2] = x0.z; w[3] = x0.w;
-  w[4] = x1.x; w[5] = x1.y; w[6] = x1.z; w[7] = x1.w;
+  load16(row + d0, w);
   if constexpr (ROT) {
     const int half = a.r / 2;
-    uint32_t open = 0;  // words that key_pair has to settle
+    uint32_t open = 0;
     if (half % 16 != 0) {
       open = 0xffu;  // (a lane's dims may lie on both sides of the rotation's border)
     } else {
-      auto normed = [&](uint32_t (&x)[8], int d) {
-        if (!a.k_norm) return;
-        const uint4 k0 = ld_nc_v4(a.k_norm + d), k1 = ld_nc_v4(a.k_norm + d + 8);
-        const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-        const float f = static_cast<float>(inv);
-        if (!(f >= 0x1p-120f && f <= 0x1p120f)) open = 0xffu;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const F2 v = mul2(mul2(wide2(x[i]), wide2(kw[i])), f2(f, f));
-          float v0, v1;
-          split(v, v0, v1);
-          const F2 e = fma2(f2(fabsf(v0), fabsf(v1)), f2(0x1p-22f, 0x1p-22f), f2(0x1p-110f, 0x1p-110f));
-          if (!settled(v, e, x[i])) open |= 1u << i;
-        }
-      };
-      normed(w, d0);
+      normed(a, w, d0, inv, open);
       if (d0 < a.r) {
         const bool first = d0 < half;
         const int p0 = first ? d0 + half : d0 - half;
-        const uint4 y0 = ld_nc_v4(row + p0), y1 = ld_nc_v4(row + p0 + 8);
-        uint32_t p[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-        normed(p, p0);
+        uint32_t p[8];
+        load16(row + p0, p);
+        normed(a, p, p0, inv, open);
         const uint32_t sign = first ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float4 f = cs[turn_at(D, tok, (first ? d0 : p0) / 2 + i)];
-          const F2 x = mul2(wide2(w[i]), f2(f.x, f.y));
-          const F2 v = fma2(wide2(p[i] ^ sign), f2(f.z, f.w), x);
-          float x0, x1, v0, v1;
-          split(x, x0, x1);
-          split(v, v0, v1);
-          const F2 e = fma2(f2(fabsf(x0) + fabsf(v0), fabsf(x1) + fabsf(v1)), f2(0x1p-23f, 0x1p-23f), f2(0x1p-110f, 0x1p-110f));
-          if (!settled(v, e, w[i])) open |= 1u << i;
+          if (!turned(mul2(wide2(w[i]), f2(f.x, f.y)), wide2(p[i] ^ sign), f2(f.z, f.w), w[i])) open |= 1u << i;
         }
       }
     }
-    while (open) {
-      const int i = __ffs(open) - 1;
-      open &= open - 1;
-      const uint32_t v = key_pair(row, a.k_norm, inv, cs, D, tok, a.r, d0 + 2 * i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j == i) w[j] = v;
-    }
+    settle(a, row, D, tok, d0, inv, cs, open, w);
   }
 }
 
-// One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V).
+// The same of both sides of a rotation, w from dim d0 and p from d0 + half on.
+template <int D>
+__device__ __forceinline__ void key_words2(const AppendArgs& a, const uint16_t* row, int tok, int d0, double inv, const float4* cs,
+                                           uint32_t (&w)[8], uint32_t (&p)[8]) {
+  const int p0 = d0 + a.r / 2;
+  load16(row + d0, w);
+  load16(row + p0, p);
+  uint32_t wopen = 0, popen = 0;
+  normed(a, w, d0, inv, wopen);
+  normed(a, p, p0, inv, popen);
+  wopen = popen = wopen | popen;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 f = cs[turn_at(D, tok, d0 / 2 + i)];
+    const F2 x = wide2(w[i]), y = wide2(p[i]), c = f2(f.x, f.y), s = f2(f.z, f.w);
+    if (!turned(mul2(x, c), y, mul2(s, f2(-1.f, -1.f)), w[i])) wopen |= 1u << i;
+    if (!turned(mul2(y, c), x, s, p[i])) popen |= 1u << i;
+  }
+  settle(a, row, D, tok, d0, inv, cs, wopen, w);
+  settle(a, row, D, tok, p0, inv, cs, popen, p);
+}
+
+// One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V):
+// keys first, so that every warp of many heads has keys and values (a rotated key costs
+// twice a value, and warps with keys alone would share two of the SM's four schedulers).
 // Tokens that the call does not bring stay as they are. Issue-bound, ~20 instructions a
-// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 233 us with 4
-// CTAs an SM, 254 with 3 and 236 with 5, where its 660 MB take 98.
+// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 205 us with 4
+// CTAs an SM and 224 with 3 (with keys and values by turns 233, and 215 before a lane
+// turned both sides of a pair), where its 660 MB take 98.
 template <int D, bool ROT>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const AppendArgs a) {
   constexpr int NG = D / kInt4Group;
@@ -185,12 +226,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
     }
     __syncthreads();
   }
-  for (int task = warp; task < 2 * a.Hkv; task += blockDim.x >> 5) {
-    const int h = task >> 1;
-    const uint16_t* src = (task & 1 ? a.v : a.k) + ((static_cast<int64_t>(b) * a.in_T + a.row0 + s.t0) * a.Hkv + h) * D;
+  const int warps = blockDim.x >> 5;
+  for (int task = warp; task < 2 * a.Hkv; task += warps) {
+    const int h = task < a.Hkv ? task : task - a.Hkv;
+    const bool value = task >= a.Hkv;
+    const uint16_t* src = (value ? a.v : a.k) + ((static_cast<int64_t>(b) * a.in_T + a.row0 + s.t0) * a.Hkv + h) * D;
     const int64_t pitch = static_cast<int64_t>(a.Hkv) * D;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(task & 1 ? a.c.v : a.c.k) + (s.block + static_cast<int64_t>(h) * bpp) * int4_block_bytes(D);
-    if ((task & 1) == 0) {
+    uint8_t* dst = reinterpret_cast<uint8_t*>(value ? a.c.v : a.c.k) + (s.block + static_cast<int64_t>(h) * bpp) * int4_block_bytes(D);
+    if (!value) {
       // keys: tokens g and g + 8, 16 dims a lane of every group
       double inv0 = 0.0, inv1 = 0.0;
       if (ROT && a.k_norm) {
@@ -201,19 +244,33 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
           if (r == g + 8) inv1 = v;
         }
       }
-#pragma unroll 1
-      for (int x = 0; x < 2 * NG; ++x) {  // (group, token g or g + 8)
-        const int i = x & 1, r = g + 8 * i, G = x >> 1;
-        const bool on = s.has(r);
-        uint32_t w[8] = {};
-        if (on) key_words<D, ROT>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w);
+      auto put = [&](const uint32_t (&w)[8], int r, int G, bool on) {
         uint32_t e = extent(w);
         e = max2_nan(e, __shfl_xor_sync(kFull, e, 1));
         e = max2_nan(e, __shfl_xor_sync(kFull, e, 2));
         const Int4Grid q = grid_of(e);
-        if (!on) continue;
+        if (!on) return;
         *reinterpret_cast<uint2*>(dst + int4_key_word(r, G * 8 + t * 2)) = make_uint2(codes<8>(w, q), codes<8>(w + 4, q));
         if (t == 0) *reinterpret_cast<uint32_t*>(dst + int4_pair(D, r, G)) = q.pair;
+      };
+      // where the two sides of the rotation are whole groups, a lane has both of a pair
+      const int across = ROT && a.r > 0 && a.r % 128 == 0 ? a.r / 128 : 0;
+#pragma unroll 1
+      for (int x = 0; x < 2 * across; ++x) {  // (group, token g or g + 8)
+        const int i = x & 1, r = g + 8 * i, G = x >> 1;
+        const bool on = s.has(r);
+        uint32_t w[8] = {}, p[8] = {};
+        if (on) key_words2<D>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w, p);
+        put(w, r, G, on);
+        put(p, r, G + across, on);
+      }
+#pragma unroll 1
+      for (int x = 4 * across; x < 2 * NG; ++x) {
+        const int i = x & 1, r = g + 8 * i, G = x >> 1;
+        const bool on = s.has(r);
+        uint32_t w[8] = {};
+        if (on) key_words<D, ROT>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w);
+        put(w, r, G, on);
       }
     } else {
       // values: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, 8 dims a lane of every group
