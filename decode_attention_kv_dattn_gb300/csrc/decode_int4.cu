@@ -180,7 +180,7 @@ __device__ __forceinline__ int stream_length(const Int4DecodeArgs& a, int b, boo
   return n < 0 ? 0 : cap;
 }
 
-// Dim d of a new key row (global): the entry, normalised and turned.
+// Dim d of a new key row (global): the entry, normalised and turned (as key_exact says).
 __device__ __forceinline__ uint32_t key_entry(const Int4DecodeArgs& a, const uint16_t* row, double inv, int pos, int d) {
   const uint16_t* kn = a.k_norm;
   auto at = [&](int x) { return kn ? qk_norm_apply(row[x], kn[x], inv) : row[x]; };
@@ -189,9 +189,12 @@ __device__ __forceinline__ uint32_t key_entry(const Int4DecodeArgs& a, const uin
   const int half = a.r / 2;
   const bool first = d < half;
   float c, s;
-  rope_cos_sin(pos, a.rope_step[first ? d : d - half], c, s);
-  // x c - y s, or y c + x s
-  return bf16_dot2(x, __float_as_uint(c), at(first ? d + half : d - half), __float_as_uint(s) ^ (first ? 0x80000000u : 0u));
+  rope_cos_sin_near(pos, a.rope_step[first ? d : d - half], c, s);
+  const float xc = bf16_to_f32(x) * c, y = bf16_to_f32(at(first ? d + half : d - half));
+  const float v = fmaf(y, first ? -s : s, xc), e = fmaf(fabsf(xc) + fabsf(v), kTurnError, 0x1p-110f);
+  const uint32_t w = pack_bf16x2(v - e, v + e);
+  if ((w >> 16) == (w & 0xffffu)) return w & 0xffffu;
+  return key_exact(row, kn, inv, pos, a.rope_step, a.r, d);
 }
 
 // One lane: the inputs of unit u into a warp's scratch, counted on bar: its query rows in

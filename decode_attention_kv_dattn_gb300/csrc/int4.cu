@@ -64,27 +64,20 @@ __device__ __forceinline__ int turn_at(int D, int r, int c) {
   return r * (D / 4) + (c & ~7) + ((c & 7) ^ ((q & 3) | ((r & 1) << 2)));
 }
 
-// Dims d, d + 1 (d even) of a key row, normalised and turned: bit for bit the entry
-// that every other path of the library stores. Out of line: the few values that the
-// short arithmetic below cannot decide, and rotations it does not take.
-__device__ __noinline__ uint32_t key_pair(const uint16_t* row, const uint16_t* kn, double inv, const float4* cs, int D, int tok, int r, int d) {
-  const int half = r / 2;
-  auto at = [&](int x) { return kn ? qk_norm_apply(row[x], kn[x], inv) : row[x]; };
-  uint32_t w = 0;
-  for (int x = d; x < d + 2; ++x) {
-    uint32_t v = at(x);
-    if (x < r) {
-      const bool first = x < half;
-      const int j = first ? x : x - half;
-      const float* f = reinterpret_cast<const float*>(cs + turn_at(D, tok, j >> 1)) + (j & 1);
-      // x c - y s, or y c + x s
-      v = bf16_dot2(static_cast<uint16_t>(v), __float_as_uint(f[0]), at(first ? x + half : x - half),
-                    __float_as_uint(f[2]) ^ (first ? 0x80000000u : 0u));
-    }
-    w = (w >> 16) | (v << 16);
+// Where the new keys of a token are: its row, position and norm, and the layer's rotation.
+struct KeyRow {
+  const uint16_t* row;
+  const uint16_t* kn;
+  const uint64_t* step;
+  int64_t pos;
+  double inv;
+  int r;
+  // Dims d, d + 1 (d even) in 64 bits: what the short arithmetic below cannot decide, and
+  // rotations that it does not take.
+  __device__ __forceinline__ uint32_t exact2(int d) const {
+    return key_exact(row, kn, inv, pos, step, r, d) | (key_exact(row, kn, inv, pos, step, r, d + 1) << 16);
   }
-  return w;
-}
+};
 
 // bf16 of two values known to within e0 and e1: false where that does not tell.
 __device__ __forceinline__ bool settled(F2 v, F2 e, uint32_t& w) {
@@ -101,18 +94,17 @@ __device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8]) {
   w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
 }
 
-// An entry is the bf16 nearest to the exact value. It is formed in fp32 with a bound
-// of its error - 2^-23 of the rotation's terms, 2^-22 of a normalised value, and 2^-110
-// for what underflows - and where both ends of the bound round alike, that is the
-// entry; about one value in 5,000 goes to key_pair instead (7 instructions a value
-// against ~30 of the exact sum: 64 ragged prompts 1,490 -> 233 us).
+// A normalised value is the bf16 nearest to the exact one, formed in fp32 with a bound of
+// 2^-22, a turned one as key_exact says, with kTurnError; about one in 3,000 is not
+// decided so and goes to exact2 (7 instructions a value against ~30 of an exact sum for all,
+// which took 1,490 us for the prompts below).
 //
 // Sixteen values from dim d on, normalised; the words that key_pair has to settle into open.
-__device__ __forceinline__ void normed(const AppendArgs& a, uint32_t (&x)[8], int d, double inv, uint32_t& open) {
-  if (!a.k_norm) return;
+__device__ __forceinline__ void normed(const KeyRow& a, uint32_t (&x)[8], int d, uint32_t& open) {
+  if (!a.kn) return;
   uint32_t kw[8];
-  load16(a.k_norm + d, kw);
-  const float f = static_cast<float>(inv);
+  load16(a.kn + d, kw);
+  const float f = static_cast<float>(a.inv);
   if (!(f >= 0x1p-120f && f <= 0x1p120f)) open = 0xffu;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -130,40 +122,39 @@ __device__ __forceinline__ bool turned(F2 x, F2 y, F2 s, uint32_t& w) {
   float x0, x1, v0, v1;
   split(x, x0, x1);
   split(v, v0, v1);
-  return settled(v, fma2(f2(fabsf(x0) + fabsf(v0), fabsf(x1) + fabsf(v1)), f2(0x1p-23f, 0x1p-23f), f2(0x1p-110f, 0x1p-110f)), w);
+  return settled(v, fma2(f2(fabsf(x0) + fabsf(v0), fabsf(x1) + fabsf(v1)), f2(kTurnError, kTurnError), f2(0x1p-110f, 0x1p-110f)), w);
 }
 
-// The words of w, dims d0 on, that are open, by the exact sum.
-__device__ __forceinline__ void settle(const AppendArgs& a, const uint16_t* row, int D, int tok, int d0, double inv, const float4* cs,
-                                       uint32_t open, uint32_t (&w)[8]) {
+// The words of w, dims d0 on, that are open.
+__device__ __forceinline__ void settle(const KeyRow& a, int d0, uint32_t open, uint32_t (&w)[8]) {
   while (open) {
     const int i = __ffs(open) - 1;
     open &= open - 1;
-    const uint32_t v = key_pair(row, a.k_norm, inv, cs, D, tok, a.r, d0 + 2 * i);
+    const uint32_t v = a.exact2(d0 + 2 * i);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j == i) w[j] = v;
   }
 }
 
-// Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so.
+// Sixteen values of a key row from dim d0 on, normalised and turned where ROT says so;
+// cs: turn_at of the block's token tok.
 template <int D, bool ROT>
-__device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* row, int tok, int d0, double inv, const float4* cs,
-                                          uint32_t (&w)[8]) {
-  load16(row + d0, w);
+__device__ __forceinline__ void key_words(const KeyRow& a, int tok, int d0, const float4* cs, uint32_t (&w)[8]) {
+  load16(a.row + d0, w);
   if constexpr (ROT) {
     const int half = a.r / 2;
     uint32_t open = 0;
     if (half % 16 != 0) {
       open = 0xffu;  // (a lane's dims may lie on both sides of the rotation's border)
     } else {
-      normed(a, w, d0, inv, open);
+      normed(a, w, d0, open);
       if (d0 < a.r) {
         const bool first = d0 < half;
         const int p0 = first ? d0 + half : d0 - half;
         uint32_t p[8];
-        load16(row + p0, p);
-        normed(a, p, p0, inv, open);
+        load16(a.row + p0, p);
+        normed(a, p, p0, open);
         const uint32_t sign = first ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -172,20 +163,19 @@ __device__ __forceinline__ void key_words(const AppendArgs& a, const uint16_t* r
         }
       }
     }
-    settle(a, row, D, tok, d0, inv, cs, open, w);
+    settle(a, d0, open, w);
   }
 }
 
 // The same of both sides of a rotation, w from dim d0 and p from d0 + half on.
 template <int D>
-__device__ __forceinline__ void key_words2(const AppendArgs& a, const uint16_t* row, int tok, int d0, double inv, const float4* cs,
-                                           uint32_t (&w)[8], uint32_t (&p)[8]) {
+__device__ __forceinline__ void key_words2(const KeyRow& a, int tok, int d0, const float4* cs, uint32_t (&w)[8], uint32_t (&p)[8]) {
   const int p0 = d0 + a.r / 2;
-  load16(row + d0, w);
-  load16(row + p0, p);
+  load16(a.row + d0, w);
+  load16(a.row + p0, p);
   uint32_t wopen = 0, popen = 0;
-  normed(a, w, d0, inv, wopen);
-  normed(a, p, p0, inv, popen);
+  normed(a, w, d0, wopen);
+  normed(a, p, p0, popen);
   wopen = popen = wopen | popen;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -194,8 +184,8 @@ __device__ __forceinline__ void key_words2(const AppendArgs& a, const uint16_t* 
     if (!turned(mul2(x, c), y, mul2(s, f2(-1.f, -1.f)), w[i])) wopen |= 1u << i;
     if (!turned(mul2(y, c), x, s, p[i])) popen |= 1u << i;
   }
-  settle(a, row, D, tok, d0, inv, cs, wopen, w);
-  settle(a, row, D, tok, p0, inv, cs, popen, p);
+  settle(a, d0, wopen, w);
+  settle(a, p0, popen, p);
 }
 
 // One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V):
@@ -216,13 +206,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int bpp = a.c.P / kInt4Block;
   __shared__ float4 cs[ROT ? kInt4Block * D / 4 : 1];
+  const int64_t pos = ROT && a.start_pos ? a.start_pos[b] : 0;
   if constexpr (ROT) {
     const int half = a.r / 2;
-    const int64_t pos = a.start_pos ? a.start_pos[b] : 0;
     for (int e = threadIdx.x; e < kInt4Block * half; e += blockDim.x) {
       const int r = e / half, i = e - r * half;
       float* f = reinterpret_cast<float*>(cs + turn_at(D, r, i >> 1)) + (i & 1);
-      if (s.has(r)) rope_cos_sin(pos + s.t0 + r, a.rope_step[i], f[0], f[2]);
+      if (s.has(r)) rope_cos_sin_near(pos + s.t0 + r, a.rope_step[i], f[0], f[2]);
     }
     __syncthreads();
   }
@@ -244,6 +234,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
           if (r == g + 8) inv1 = v;
         }
       }
+      auto key = [&](int r, int i) {
+        return KeyRow{src + r * pitch, a.k_norm, a.rope_step, pos + s.t0 + r, i ? inv1 : inv0, a.r};
+      };
       auto put = [&](const uint32_t (&w)[8], int r, int G, bool on) {
         uint32_t e = extent(w);
         e = max2_nan(e, __shfl_xor_sync(kFull, e, 1));
@@ -260,7 +253,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
         const int i = x & 1, r = g + 8 * i, G = x >> 1;
         const bool on = s.has(r);
         uint32_t w[8] = {}, p[8] = {};
-        if (on) key_words2<D>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w, p);
+        if (on) key_words2<D>(key(r, i), r, G * 64 + t * 16, cs, w, p);
         put(w, r, G, on);
         put(p, r, G + across, on);
       }
@@ -269,7 +262,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
         const int i = x & 1, r = g + 8 * i, G = x >> 1;
         const bool on = s.has(r);
         uint32_t w[8] = {};
-        if (on) key_words<D, ROT>(a, src + r * pitch, r, G * 64 + t * 16, i ? inv1 : inv0, cs, w);
+        if (on) key_words<D, ROT>(key(r, i), r, G * 64 + t * 16, cs, w);
         put(w, r, G, on);
       }
     } else {

@@ -4,6 +4,10 @@
 
 #include "common.cuh"
 #include "int4_format.h"
+#include "mma.cuh"
+#include "qk_norm.cuh"
+#include "rope_angle.h"
+#include "round_f64.h"
 
 namespace dattn {
 
@@ -77,6 +81,30 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* w, const Int4Grid& q) 
     r = (r * 16u + __float_as_uint(c1)) * 16u + __float_as_uint(c0);
   }
   return (r - bias) & q.keep;
+}
+
+// A key's entry in a 4-bit cache is x c - y s (y c + x s on the other side) with c and s to 64
+// bits, rounded to fp32 and then to bf16: a code is a step of the grid, which an entry
+// that is off by one of bf16's may change by a whole one, so the entry is that of
+// arithmetic in 64 bits. It is formed in fp32 with a bound of its error, and where both
+// ends of the bound round alike, that is the entry. With rope_cos_sin_near's c and s the
+// error is below 2^-24 (3.2 |x c| + 2.4 |v|): kTurnError of |x c| + |v|, and 2^-110 for what underflows.
+constexpr float kTurnError = 0x1.ap-23f;
+
+// Dim d of a key row at pos, in 64 bits.
+__device__ __noinline__ inline uint32_t key_exact(const uint16_t* row, const uint16_t* kn, double inv, int64_t pos, const uint64_t* step,
+                                                  int r, int d) {
+  auto at = [&](int x) { return kn ? qk_norm_apply(row[x], kn[x], inv) : row[x]; };
+  const uint16_t x = at(d);
+  if (d >= r) return x;
+  const int half = r / 2;
+  const bool first = d < half;
+  int64_t cq, sq;
+  rope_cos_sin_q62(pos, step[first ? d : d - half], cq, sq);
+  const double c = static_cast<double>(cq) * 0x1p-62, s = static_cast<double>(first ? -sq : sq) * 0x1p-62;
+  const double y = bf16_to_f32(at(first ? d + half : d - half));
+  const float v = static_cast<float>(fma(y, s, static_cast<double>(bf16_to_f32(x)) * c));
+  return pack_bf16x2(v, 0.f) & 0xffffu;
 }
 
 }  // namespace dattn

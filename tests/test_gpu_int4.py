@@ -1,5 +1,5 @@
-"""The 4-bit cache on the GPU against 64-bit arithmetic (int4_ref.py; rotated entries and
-QK-norms from the oracle): append, read back, decode, and runs of them together.
+"""The 4-bit cache on the GPU against 64-bit arithmetic (int4_ref.py; QK-norms from the
+oracle): append, read back, decode, and runs of them together.
 
 Written bytes are compared bit for bit, and so is everything beside them. Decode
 outputs: with the cache's values given, what differs from 64 bits is q (two fp16 terms:
@@ -81,11 +81,11 @@ class Case:
         return dattn.paged_cache(self.dev["k"], self.dev["v"], *self.keep)
 
     def entry(self, oracle, x, pos, rotate=True):
-        """A key head's bf16 entry: normalised and turned."""
+        """A key head's entry: normalised, and turned in 64 bits, rounded to bf16 by way of fp32."""
         if rotate and self.norm:
             x = oracle.qk_norm(x, self.norm[1], self.norm[2])
         if rotate and self.rope[0]:
-            x = oracle.rope_bf16(x, self.rope[0], self.rope[1], int(pos))
+            x = ref.bf16_bits(ref.rotate(ref.f64(x), self.rope[0], self.rope[1], int(pos)))
         return x
 
     def new(self, oracle, b):
