@@ -192,9 +192,10 @@ __device__ __forceinline__ void key_words2(const KeyRow& a, int tok, int d0, con
 // keys first, so that every warp of many heads has keys and values (a rotated key costs
 // twice a value, and warps with keys alone would share two of the SM's four schedulers).
 // Tokens that the call does not bring stay as they are. Issue-bound, ~20 instructions a
-// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 205 us with 4
-// CTAs an SM and 224 with 3 (with keys and values by turns 233, and 215 before a lane
-// turned both sides of a pair), where its 660 MB take 98.
+// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 219 us, where its
+// 660 MB take 98. With keys turned by rope_cos_sin, which is off by up to 1.5e-7 and moved 50
+// of 65 million codes, 205 (3 instead of 4 CTAs an SM 224; keys and values by turns 233;
+// one side of a rotation in a lane 215), with one exact step behind the bound 255.
 template <int D, bool ROT>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const AppendArgs a) {
   constexpr int NG = D / kInt4Group;

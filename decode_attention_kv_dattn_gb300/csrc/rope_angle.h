@@ -64,8 +64,9 @@ DATTN_HD float f32_of_i64(int64_t x) {
 // cos and sin of the same angle as fp32 values near the nearest: within 0.85 x 2^-24 of
 // the one above 0.7 in magnitude, relative, and 1.4 x 2^-24 of the other. The remainder keeps
 // its 62 bits as a sum t + tl, the square of t its rounding error, and what is added
-// last to t and to 1 - t^2 / 2 is small, so that one rounding remains.
-DATTN_HD void rope_cos_sin_near(int64_t pos, uint64_t step, float& c, float& s) {
+// last to t and to 1 - t^2 / 2 is small, so that one rounding remains. cl and sl are what
+// that rounding took off: c + cl and s + sl are within 0.5 x 2^-24, relative.
+DATTN_HD void rope_cos_sin_near(int64_t pos, uint64_t step, float& c, float& s, float& cl, float& sl) {
   const uint64_t w = static_cast<uint64_t>(pos) * step + (1ull << 61);
   const uint32_t quad = static_cast<uint32_t>(w >> 62);
   const int64_t rho = static_cast<int64_t>(w & 0x3fffffffffffffffull) - (1ll << 61);  // 2^-64 turns
@@ -77,17 +78,26 @@ DATTN_HD void rope_cos_sin_near(int64_t pos, uint64_t step, float& c, float& s) 
   sp = f32_fma(t2, sp, 8.33333333e-03f);
   sp = f32_fma(t2, sp, -1.66666667e-01f);
   const float half = f32_mul(0.5f, t2);
-  const float sn = f32_add(t, f32_fma(f32_mul(t, t2), sp, f32_fma(-half, tl, tl)));
+  const float r1 = f32_fma(f32_mul(t, t2), sp, f32_fma(-half, tl, tl));
+  const float sn = f32_add(t, r1), snl = f32_add(r1, -f32_add(sn, -t));
   float cp = f32_fma(t2, -2.75573192e-07f, 2.48015873e-05f);
   cp = f32_fma(t2, cp, -1.38888889e-03f);
   cp = f32_fma(t2, cp, 4.16666667e-02f);
   const float a1 = f32_add(1.0f, -half);
   const float e1 = f32_add(f32_add(1.0f, -a1), -half);  // (exact)
-  const float cs = f32_add(a1, f32_fma(f32_mul(t2, t2), cp, f32_fma(-0.5f, t2l, e1)));
-  const float a = (quad & 1u) ? sn : cs;
-  const float b = (quad & 1u) ? cs : sn;
-  c = (quad == 1u || quad == 2u) ? -a : a;
-  s = (quad >= 2u) ? -b : b;
+  const float r2 = f32_fma(f32_mul(t2, t2), cp, f32_fma(-0.5f, t2l, e1));
+  const float cs = f32_add(a1, r2), csl = f32_add(r2, -f32_add(cs, -a1));
+  const float a = (quad & 1u) ? sn : cs, al = (quad & 1u) ? snl : csl;
+  const float b = (quad & 1u) ? cs : sn, bl = (quad & 1u) ? csl : snl;
+  const bool cneg = quad == 1u || quad == 2u, sneg = quad >= 2u;
+  c = cneg ? -a : a;
+  s = sneg ? -b : b;
+  cl = cneg ? -al : al;
+  sl = sneg ? -bl : bl;
+}
+DATTN_HD void rope_cos_sin_near(int64_t pos, uint64_t step, float& c, float& s) {
+  float cl, sl;
+  rope_cos_sin_near(pos, step, c, s, cl, sl);
 }
 
 // Signed product of two Q62 fixed-point numbers (value * 2^62), rounded down.

@@ -1,7 +1,8 @@
 """Host check of the 4-bit cache's RoPE angle routine (csrc/rope_angle.h: rope_cos_sin_near)
 against the exact cos and sin of its fixed-point phase, in rational arithmetic: the
-larger of the two within 0.85 x 2^-24 of its size, the smaller within 1.4 x 2^-24 of its own -
-what the bound of a key entry's error (int4.cuh) is made of.
+larger of the two within 0.85 x 2^-24 of its size, the smaller within 1.4 x 2^-24 of its own,
+both within 0.5 x 2^-24 with their second terms - what the bounds of a key entry's error
+(int4.cuh) are made of.
 """
 import shutil
 import subprocess
@@ -20,9 +21,9 @@ int main() {
   long long pos;
   unsigned long long step;
   while (std::scanf("%lld %llu", &pos, &step) == 2) {
-    float c, s;
-    dattn::rope_cos_sin_near(static_cast<int64_t>(pos), static_cast<uint64_t>(step), c, s);
-    std::printf("%a %a\n", (double)c, (double)s);
+    float c, s, cl, sl;
+    dattn::rope_cos_sin_near(static_cast<int64_t>(pos), static_cast<uint64_t>(step), c, s, cl, sl);
+    std::printf("%a %a %a %a\n", (double)c, (double)s, (double)c + (double)cl, (double)s + (double)sl);
   }
   return 0;
 }
@@ -45,14 +46,12 @@ def test_against_rational_arithmetic(tmp_path):
     cases += [(1, int(x)) for x in rng.integers(0, 2 ** 63, 2000)] + [(0, 12345), (-77, phase_step(1e4, 64, 8))]
     text = "\n".join(f"{p} {s}" for p, s in cases)
     got = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split()
-    worst = [Fraction(0), Fraction(0)]
-    for (p, s), c, n in zip(cases, got[::2], got[1::2]):
-        for g, w in sorted(zip((c, n), exact(p, s)), key=lambda x: abs(x[1]))[::-1][:1]:
-            worst[0] = max(worst[0], abs(Fraction(float.fromhex(g)) - w) / abs(w))
-        g, w = min(zip((c, n), exact(p, s)), key=lambda x: abs(x[1]))
-        if abs(w) > Fraction(1, 2 ** 80):
-            worst[1] = max(worst[1], abs(Fraction(float.fromhex(g)) - w) / abs(w))
-        else:
-            assert abs(float.fromhex(g)) < 2.0 ** -79
-    print([float(x * 2 ** 24) for x in worst])
-    assert worst[0] <= Fraction(85, 100) / 2 ** 24 and worst[1] <= Fraction(14, 10) / 2 ** 24
+    worst = [Fraction(0)] * 3
+    for (p, step), *terms in zip(cases, *(got[i::4] for i in range(4))):
+        c, n, c2, n2 = (Fraction(float.fromhex(x)) for x in terms)
+        want = exact(p, step)
+        big = int(abs(want[1]) > abs(want[0]))
+        off = [abs(x - w) / max(abs(w), Fraction(1, 2 ** 80)) for x, w in ((c, want[0]), (n, want[1]), (c2, want[0]), (n2, want[1]))]
+        worst = [max(worst[0], off[big]), max(worst[1], off[1 - big]), max(worst[2], off[2], off[3])]
+    assert worst[0] <= Fraction(85, 100) / 2 ** 24 and worst[1] <= Fraction(14, 10) / 2 ** 24, [float(x * 2 ** 24) for x in worst]
+    assert worst[2] <= Fraction(1, 2) / 2 ** 24, float(worst[2] * 2 ** 24)
