@@ -3,10 +3,11 @@
 // the gate, the fp32 store and the write-back of the new entry.
 //
 // A unit is one (stream, KV head); its cache is a row of blocks of 16 tokens. What
-// bounds the pass is memory (4.5 bits a value) with little to spare: its arithmetic alone
-// takes 0.93 of the copies' time on 256-wide heads of 4 queries, and 1.5 times that time
-// on groups of 5 to 8, whose scores and outputs are two column tiles of the MMAs. So
-// every sub-partition of every SM has to work all the time:
+// bounds the pass is its arithmetic, more than its memory traffic (4.5 bits a value): with
+// operands as they come out of the codes it took 0.93 of the copies' time on 256-wide heads
+// of 4 queries and 1.5 times that time on groups of 5 to 8, whose scores and outputs are two
+// column tiles of the MMAs, and precision (decode_int4.cuh) cost a quarter more. So every
+// sub-partition of every SM has to work all the time:
 //  * The split is made for warps, not CTAs. All units' blocks are laid end to end, each
 //    unit charged a fixed cost in blocks before them (Split), and every warp of the grid
 //    takes an equal contiguous range: it turns its own query, streams its own blocks
@@ -14,9 +15,9 @@
 //    A unit that lies within one warp's range is finished by that warp on the way. The
 //    warps are a multiple of 4, as the sub-partition with the most sets the pace. (The
 //    other formats' layout, 10 or 11 streaming warps that share a CTA's units beside a
-//    helper warp, took 244 us for 8 x 262,144 tokens, where this one takes 193, 53 for 64
-//    ragged streams, where it takes 42, and 193 for 32 x 16,384 tokens of 24 / 4 heads,
-//    where it takes 144; one stream of 5,003 tokens 19.3, where it takes 20.)
+//    helper warp, took 244 us for 8 x 262,144 tokens, where this one took 193 with the
+//    same operands, 53 for 64 ragged streams, 42 here, and 193 for 32 x 16,384 tokens of
+//    24 / 4 heads, 144 here; one stream of 5,003 tokens 19.3, and 20 here.)
 //  * At the end of a CTA the warps' states of each unit are merged by a team of its warps,
 //    the teams of several units side by side; states of units that cross CTAs go to global
 //    memory and the team that counts last for a unit joins them, in two levels where they
@@ -27,8 +28,8 @@
 // blocks of a page go as one), issued by one lane NS stages ahead; the page table is
 // read 32 blocks ahead, a block a lane, and handed on by shuffles.
 //
-// Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 253 us,
-// 4.8 TB/s; 1 x 1,048,576 135 us; 64 ragged streams 48 us; 32 x 16,384 of 24 / 4 heads 172.
+// Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 248 us,
+// 4.9 TB/s; 1 x 1,048,576 135 us; 64 ragged streams 48 us; 32 x 16,384 of 24 / 4 heads 174.
 // Of the first ~8 us pass before the first copies land and ~10 between the last block and
 // the last output.
 #include "decode_int4.cuh"
@@ -47,22 +48,24 @@ constexpr int kMergeBatch = 8;  // CTAs of a group of the two-level merge
 constexpr int kFoldBatch = 12;  // states read per round trip
 constexpr int64_t kPrefetchLines = 1 << 15;  // largest page table (128-byte lines) put in L2 at start
 // Cost of a unit's start (its query and new token) in blocks of a warp: 2 / 4 / 6 / 9
-// blocks, 64 ragged streams of 8 heads of 128 45.1 / 42.1 / 44.5 / 42.6 us, 32 x 16,384 tokens of
-// 24 / 4 heads of 256 145.5 / 144.4 / 142.3 / 142.5.
+// blocks, 64 ragged streams of 8 heads of 128 52.1 / 48.1 / 49.5 / 48.5 us, 32 x 16,384 tokens of
+// 24 / 4 heads of 256 176.3 / 173.8 / 173.9 / 173.9.
 constexpr int kUnitCost = 4;
 // Blocks that are worth another warp where a call has few: 2 / 3 / 4 / 5, in a graph of such
 // calls, one stream of 5,003 tokens of 8 / 2 heads of 256 9.9 / 11.2 / 11.4 / 13.1 us, 20,000
 // tokens 18.2 / 12.6 / 12.3 / 13.2 us, 4 streams of 2,000 - 4,000 tokens of 24 / 4 heads 26.1 /
-// 26.4 / 18.5 / 18.0 us (more CTAs are more partial states to join).
+// 26.4 / 18.5 / 18.0 us (more CTAs are more partial states to join; with the first operands:
+// with those of today 5,003 tokens with write-back and read back, 2 / 4 / 6 blocks: 23.5 / 23.4 / 25.6).
 constexpr int kMinBlocks = 4;
 
 template <int HEAD_DIM, int NT>
 struct Geo4 {
   static constexpr int D = HEAD_DIM, GP = 4 * NT;
   // Warps, blocks of a stage, stages of a warp's ring. Two blocks are taken at once: their
-  // chains of dependent steps overlap (one at a time, 8 x 262,144 tokens 193 -> 208 us).
-  // 256-wide heads then need up to 255 registers, which leaves 8 warps (12 with one block
-  // a stage: 220 us); 128-wide ones fit 168 and 12 warps (8: 44.5 -> 46.9 us on 64 ragged).
+  // chains of dependent steps overlap (one at a time, 8 x 262,144 tokens 193 -> 208 us
+  // before the operands were made precise). 256-wide heads then need up to 255 registers,
+  // which leaves 8 warps (12 with one block a stage: 220 us then); 128-wide ones fit 168 and
+  // 12 warps (8: 48.1 -> 51.8 us on 64 ragged).
   static constexpr int W = D == 256 ? 8 : 12;
   static constexpr int KG = 2;
   static constexpr int NS = D == 256 ? 2 : 3;

@@ -146,8 +146,8 @@ typedef struct {
    * dattn_commit, dattn_prefill and dattn_decode_noalloc return
    * DATTN_EUNSUPPORTED for such a layer.
    * DATTN_KV_INT4 (paged layers): the same with the 4-bit form of the entry (its
-   * rotation in 64 bits, rounded to fp32 and then to bf16) and of v_new; the scales are not read. The calls just named and dattn_sparse_decode
-   * and dattn_summarize return DATTN_EUNSUPPORTED: what they do over such a cache
+   * rotation in 64 bits, rounded to fp32 and then to bf16) and of v_new; the scales
+   * are not read. The calls just named, dattn_sparse_decode and dattn_summarize return DATTN_EUNSUPPORTED: what they do over such a cache
    * starts from dattn_read_kv (its entries appended to a bf16 layer, rotate = 0). */
   int kv_format;
   float k_scale;
