@@ -54,8 +54,8 @@ constexpr int kUnitCost = 4;
 // Blocks that are worth another warp where a call has few: 2 / 3 / 4 / 5, in a graph of such
 // calls, one stream of 5,003 tokens of 8 / 2 heads of 256 9.9 / 11.2 / 11.4 / 13.1 us, 20,000
 // tokens 18.2 / 12.6 / 12.3 / 13.2 us, 4 streams of 2,000 - 4,000 tokens of 24 / 4 heads 26.1 /
-// 26.4 / 18.5 / 18.0 us (more CTAs are more partial states to join; with the first operands:
-// with those of today 5,003 tokens with write-back and read back, 2 / 4 / 6 blocks: 23.5 / 23.4 / 25.6).
+// 26.4 / 18.5 / 18.0 us (more CTAs are more partial states to join; with the operands as
+// they are now, 5,003 tokens with write-back and read back, 2 / 4 / 6 blocks, 23.5 / 23.4 / 25.6).
 constexpr int kMinBlocks = 4;
 
 template <int HEAD_DIM, int NT>

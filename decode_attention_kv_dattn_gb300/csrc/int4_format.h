@@ -3,7 +3,9 @@
 //
 // A group keeps its least value and a step, both bf16, and a code 0..15 a dim:
 //   step = bf16((most - least) / 15), code = rint((x - least) / step), ties to even,
-// and stands for least + code * step. The entries are bf16, so the least value is
+// x - least being rounded to fp32 (which holds it unless the two are 2^15 apart in size:
+// then a value that is nothing beside the least one may meet a tie that it misses by
+// that nothing). A code stands for least + code * step. The entries are bf16, so the least value is
 // exact, and an asymmetric grid spends no code outside the group's own range (a
 // key's dims may lie far from zero all on one side). A step below 2^-100 is stored as
 // 0 (its inverse stays a normal number; the codes are then 0, off by 15 steps at the

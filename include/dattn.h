@@ -101,10 +101,11 @@ enum {
 
 /* The 4-bit cache. Each entry is quantised as it is written: a group of 64 dims
  * keeps its least value and step = bf16((most - least) / 15), and a code 0..15 for
- * each dim, rint((x - least) / step), ties to even, which stands for least + code *
- * step. (A step below 2^-100 is stored as 0. A group that holds a NaN, an infinity
- * or a range past fp32 is stored as NaN as a whole.) Nothing is calibrated: the
- * grid is each token's own. A pool is [pages, Hkv, DATTN_INT4_BYTES(P, D)] bytes,
+ * each dim, rint((x - least) / step), ties to even (x - least in fp32, which holds it
+ * unless the two are 2^15 apart in size), which stands for least + code * step. (A
+ * step below 2^-100 is stored as 0. A group that holds a NaN, an infinity or a range
+ * past fp32 is stored as NaN as a whole.) Nothing is calibrated: the grid is each
+ * token's own. A pool is [pages, Hkv, DATTN_INT4_BYTES(P, D)] bytes,
  * 4.5 bits for each value; P is a multiple of 16 (DATTN_EUNSUPPORTED otherwise).
  * Sixteen tokens of a head are a block of 9 D bytes; token r of its block and dim d
  * have their code in the low (even d) or high half of byte

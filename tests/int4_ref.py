@@ -19,7 +19,10 @@ def bf16_bits(x):
 
 
 def quantise(x):
-    """Entries [..., D] (fp64 of bf16 values) -> codes [..., D], least and step [..., D / 64] as bf16 bits."""
+    """Entries [..., D] (fp64 of bf16 values) -> codes [..., D], least and step [..., D / 64] as bf16 bits.
+
+    x - least is rounded to fp32, as the format says. It is a multiple of the smaller one's last bit and below twice
+    the larger one, so fp32's 24 bits hold it where the two are within 2^15 of one another: then nothing is rounded."""
     g = np.asarray(x, np.float64).reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     with np.errstate(invalid="ignore", over="ignore"):
         lo, hi = g.min(-1), g.max(-1)
@@ -30,7 +33,7 @@ def quantise(x):
     step = np.where(step < 2.0 ** -100, 0.0, step)
     lb = np.where(ok, bf16_bits(lo), 0x7fc0).astype(np.uint16)
     sb = np.where(step == 0, 0, sb).astype(np.uint16)
-    d = np.where(ok[..., None], g - lo[..., None], 0.0)
+    d = np.where(ok[..., None], np.float32(np.where(ok[..., None], g - lo[..., None], 0.0)).astype(np.float64), 0.0)
     with np.errstate(divide="ignore", invalid="ignore"):
         code = np.where(step[..., None] > 0, np.rint(d / step[..., None]), 0.0)
     return code.clip(0, 15).astype(np.uint8).reshape(x.shape), lb, sb

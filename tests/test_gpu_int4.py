@@ -424,6 +424,52 @@ def test_append_of_special_entries(dattn, D):
     c.same_pools(pool)
 
 
+@pytest.mark.parametrize("D,r", [(128, 128), (128, 64), (256, 256), (256, 40)])
+def test_turned_keys_are_those_of_64_bits(dattn, D, r):
+    """Keys of every size, of halves that cancel, with NaN and infinities, and dims beside the middle between two bf16 values,
+    turned and stored by an append and, one stream a token, by a decode's write-back: the same bytes from both."""
+    rng = np.random.default_rng(112 + D + r)
+    T, H, P, theta = 64, 2, 16, 1e4
+    x = rng.standard_normal((1, T, H, D))
+    x[0, 0:16] *= 2.0 ** rng.integers(-126, 126, (16, 1, 1))
+    x[0, 16:24] *= 2.0 ** rng.integers(-40, 40, (8, H, D))
+    x[0, 24] = 3.3e38 * np.sign(x[0, 24])
+    x[0, 25] = 2.0 ** -130 * np.sign(x[0, 25])
+    c = Case(113, H, H, D, P, [0] * T, (r, theta), room=1)
+    pos = 5 + np.arange(T)
+    i = np.arange(r // 2)
+    angle = pos[:, None] * theta ** (-2.0 * i / r)
+    # x c = y s nearly
+    t = slice(32, 48)
+    x[0, t, :, :r // 2] = (x[0, t, :, r // 2:r] * np.tan(angle[t])[:, None]).clip(-1e30, 1e30)
+    # x c - y s near a middle: y of that size, rounded to bf16 as it is
+    t = slice(48, 64)
+    mid = (1 + (2 * rng.integers(0, 128, (16, H, r // 2)) + 1) / 256) * 2.0 ** rng.integers(-3, 4, (16, H, r // 2))
+    x[0, t, :, r // 2:r] = ((ref.f64(ref.bf16_bits(x[0, t, :, :r // 2])) * np.cos(angle[t])[:, None] - mid)
+                            / np.sin(angle[t])[:, None]).clip(-1e30, 1e30)
+    bits = ref.bf16_bits(x)
+    bits[0, 26, 0, 1], bits[0, 27, 1, r - 1], bits[0, 28, 0, 3] = 0x7fc0, 0x7f80, 0xff80
+    n, at = torch.full((1,), T, dtype=torch.int32, device="cuda"), torch.tensor([5], dtype=torch.int32, device="cuda")
+    zero, h, cache = torch.zeros(1, dtype=torch.int32, device="cuda"), c.handle(dattn, max_context=T), c.upload(dattn)
+    flat = Case(114, H, H, D, P, [0], (r, theta), room=T)
+    hf, fc = flat.handle(dattn, max_context=T), flat.upload(dattn)
+    hf.append_kv(0, fc, dev(bits), dev(bits), zero, n, start_pos=at)
+    assert hf.get_error() == dattn.OK
+    kv = dev(bits[0])
+    h.decode(0, cache, kv, kv, kv, dev(pos.astype(np.int32)), torch.zeros(T, H, D, device="cuda"))
+    assert h.get_error() == dattn.OK
+    pool, fpool = ({s: y.pool[s].copy() for s in "kv"} for y in (c, flat))
+    with np.errstate(over="ignore", invalid="ignore"):
+        for t in range(T):
+            key = ref.bf16_bits(ref.rotate(ref.f64(bits[0, t]), r, theta, int(pos[t])))
+            for s, y in (("k", key), ("v", bits[0, t])):
+                q = ref.quantise(ref.f64(y))
+                ref.store(fpool[s], s, flat.bt[0, t // P], t % P, *q)
+                ref.store(pool[s], s, c.bt[t, 0], 0, *q)
+    flat.same_pools(fpool)
+    c.same_pools(pool)
+
+
 def test_append_and_read_of_bad_rows(dattn):
     """A count out of range, a start before 0, an index past the table and a page outside the pool are reported; the
     other rows are served and nothing else is touched."""
