@@ -16,32 +16,24 @@
 #include <new>
 #include <vector>
 
-#include <mutex>
-#include <unordered_map>
-
 #include "dattn.h"
 #include "int4_format.h"
 #include "kernels.h"
+#include "launch_order.h"
 
 using namespace dattn;
 
 namespace dattn {
 
 namespace {
-std::mutex g_order_mutex;
-std::unordered_map<void*, const void*> g_last_written;  // stream -> cache K written by its last launch
+LaunchOrder g_order;
 }  // namespace
 
-bool prev_launch_writes(void* stream, const void* cache_k) {
-  std::lock_guard<std::mutex> lock(g_order_mutex);
-  const auto it = g_last_written.find(stream);
-  return it != g_last_written.end() && it->second == cache_k;
-}
-
-void record_launch(void* stream, const void* cache_k) {
-  std::lock_guard<std::mutex> lock(g_order_mutex);
-  g_last_written[stream] = cache_k;
-}
+bool prev_launch_writes(void* stream, const void* cache_k) { return g_order.writes(stream, cache_k); }
+void record_launch(void* stream, const void* cache_k) { g_order.record(stream, cache_k); }
+void record_results(void* stream) { g_order.record_results(stream); }
+bool launch_in_order(void* stream) { return g_order.in_order(stream); }
+void launch_started(void* stream) { g_order.started(stream); }
 
 }  // namespace dattn
 
@@ -831,7 +823,7 @@ int dattn_read_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_strea
   a.err = h->err;
   rc = cuda_status(launch_read(a, L.kv_format == DATTN_KV_INT4, L.kv_format == DATTN_KV_E4M3,
                                reinterpret_cast<cudaStream_t>(stream)), "read back");
-  if (rc == DATTN_OK) record_launch(stream, nullptr);
+  if (rc == DATTN_OK) record_results(stream);
   return rc;
 }
 

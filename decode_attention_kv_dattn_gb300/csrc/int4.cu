@@ -313,9 +313,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
 
 // ---------------------------------------------------------------- read back
 //
-// These kernels do not let the next launch start before they end: what they write is
-// the caller's, who may give it to a decode as its new token, and a decode reads its
-// inputs before it waits for the launch ahead of it.
+// What these kernels write is the caller's, who may give it to a decode as its new token,
+// and a decode reads its inputs before it waits for the launch ahead of it: the launch
+// behind them is made in the stream's full order (launch_order.h), and no signal of theirs
+// would let it start earlier.
 
 // Two codes (low 4 bits of each half of w) to their values as a bf16 pair, rounded
 // once: the codes become bf16 by their place in 128..143, exactly.

@@ -425,15 +425,17 @@ cudaError_t launch_linear_step(const LinearArgs& a, int D, int num_sms, cudaStre
 cudaError_t launch_linear_prompt(const LinearArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t encode_linear_maps(LinearArgs& a, int D);
 
-// Launch order per stream, for early cache reads. A kernel launched with
-// programmatic stream serialization may run while the launch before it on the
-// stream finishes; that launch is the only one that can still be writing.
+// Launch order per stream (launch_order.h).
 // True when the last launch recorded on `stream` writes into the cache whose
 // K array is `cache_k`.
 bool prev_launch_writes(void* stream, const void* cache_k);
 // Record a launch made on `stream` that writes into the cache with K array
-// `cache_k` (null: writes no cache).
+// `cache_k` (null: writes no cache), or one whose results may be the next call's inputs.
 void record_launch(void* stream, const void* cache_k);
+void record_results(void* stream);
+// Whether the next launch on `stream` is made in the stream's full order, and that it was.
+bool launch_in_order(void* stream);
+void launch_started(void* stream);
 
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device, once per device (`done` holds one bit per device id below 64; the
@@ -452,7 +454,8 @@ cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
 
 // Launch with programmatic stream serialization: the kernel may begin while
 // its predecessor in the stream finishes; every kernel here waits on the
-// predecessor (griddepcontrol.wait) before it touches the predecessor's output.
+// predecessor (griddepcontrol.wait) before it touches the predecessor's output -
+// except for what is its input, so behind a launch of such results it has no such leave.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args&&... args) {
@@ -465,8 +468,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  const bool in_order = launch_in_order(stream);
+  cfg.numAttrs = in_order ? 0 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (in_order && e == cudaSuccess) launch_started(stream);
+  return e;
 }
 
 }  // namespace dattn
