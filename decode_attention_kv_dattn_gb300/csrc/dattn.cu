@@ -27,13 +27,18 @@ namespace dattn {
 
 namespace {
 LaunchOrder g_order;
+const void* key(void* stream) {
+  int device = 0;
+  cudaGetDevice(&device);  // (that of the call)
+  return stream_key(stream, device);
+}
 }  // namespace
 
-bool prev_launch_writes(void* stream, const void* cache_k) { return g_order.writes(stream, cache_k); }
-void record_launch(void* stream, const void* cache_k) { g_order.record(stream, cache_k); }
-void record_results(void* stream) { g_order.record_results(stream); }
-bool launch_in_order(void* stream) { return g_order.in_order(stream); }
-void launch_started(void* stream) { g_order.started(stream); }
+bool prev_launch_writes(void* stream, const void* cache_k) { return g_order.writes(key(stream), cache_k); }
+void record_launch(void* stream, const void* cache_k) { g_order.record(key(stream), cache_k); }
+void record_results(void* stream) { g_order.record_results(key(stream)); }
+bool launch_in_order(void* stream) { return g_order.in_order(key(stream)); }
+void launch_started(void* stream) { g_order.started(key(stream)); }
 
 }  // namespace dattn
 
