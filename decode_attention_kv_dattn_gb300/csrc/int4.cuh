@@ -87,9 +87,8 @@ __device__ __forceinline__ uint32_t codes(const uint32_t* w, const Int4Grid& q) 
 // bits, rounded to fp32 and then to bf16: a code is a step of the grid, which an entry
 // that is off by one of bf16's may change by a whole one, so the entry is that of
 // arithmetic in 64 bits. It is formed in fp32 with a bound of its error, and where both
-// ends of the bound round alike, that is the entry. With rope_cos_sin_near's c and s the
-// error is below 2^-24 (3.2 |x c| + 2.4 |v|): kTurnError of |x c| + |v|, and 2^-110 for what underflows.
-constexpr float kTurnError = 0x1.ap-23f;
+// ends of the bound round alike, that is the entry. The bound is kTurnError of |x c| + |v|,
+// and 2^-110 for what underflows.
 
 // Dim d of a key row at pos: with c and s in two fp32 terms and exact products, which decide
 // five of six such values at a fifth of the price, or in 64 bits.

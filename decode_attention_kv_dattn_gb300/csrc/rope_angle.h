@@ -100,6 +100,13 @@ DATTN_HD void rope_cos_sin_near(int64_t pos, uint64_t step, float& c, float& s) 
   rope_cos_sin_near(pos, step, c, s, cl, sl);
 }
 
+// How far v = fma(y, s, p), p = x c rounded, with these c and s is from x cos + y sin, as a
+// share of |p| + |v|. In units of 2^-24, p is off by 1 and by c's error, y s, which is at
+// most |x cos| + |v|, by s's, v by its own rounding: (1 + 0.85 + 1.4) |p| + (1 + 1.4) |v|, and
+// 3.25 are not enough where |v| is nothing beside |p|: terms of the second order and the
+// roundings of the bound itself come on top.
+constexpr float kTurnError = 0x1.a8p-23f;
+
 // Signed product of two Q62 fixed-point numbers (value * 2^62), rounded down.
 DATTN_HD int64_t mul_q62(int64_t a, int64_t b) {
 #if defined(__CUDA_ARCH__)

@@ -55,3 +55,25 @@ def test_against_rational_arithmetic(tmp_path):
         worst = [max(worst[0], off[big]), max(worst[1], off[1 - big]), max(worst[2], off[2], off[3])]
     assert worst[0] <= Fraction(85, 100) / 2 ** 24 and worst[1] <= Fraction(14, 10) / 2 ** 24, [float(x * 2 ** 24) for x in worst]
     assert worst[2] <= Fraction(1, 2) / 2 ** 24, float(worst[2] * 2 ** 24)
+
+
+def test_the_bound_of_a_turned_value_covers_its_errors(tmp_path):
+    """kTurnError from the errors above: |computed - exact| <= kTurnError (|p| + |v|) as fp32 forms that, whatever the
+    signs of the roundings, for every ratio of |v| to |p|."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no host compiler")
+    src, exe = tmp_path / "k.cpp", str(tmp_path / "k")
+    src.write_text('#include <cstdio>\n#include "rope_angle.h"\nint main() { std::printf("%a\\n", (double)dattn::kTurnError); }\n')
+    subprocess.run([cxx, "-O2", "-std=c++17", "-I", CSRC, str(src), "-o", exe], check=True)
+    bound = Fraction(float.fromhex(subprocess.run([exe], capture_output=True, text=True, check=True).stdout))
+    u = Fraction(1, 2 ** 24)
+    for ec, es in ((Fraction(85, 100) * u, Fraction(14, 10) * u), (Fraction(14, 10) * u, Fraction(85, 100) * u)):
+        for v in (Fraction(0), Fraction(1, 2 ** 24), Fraction(1, 2 ** 12), Fraction(1, 16), Fraction(1), Fraction(3), Fraction(2 ** 20)):
+            p = Fraction(1)
+            xc = p / ((1 - ec) * (1 - u))                  # |x cos| is at most that
+            off_p = xc * ((1 + ec) * (1 + u) - 1)          # p from x cos
+            # v from p + y s: u |v|; y s from y sin: es |y sin|; |y sin| <= |v| + |x cos| + the error itself
+            off = (off_p + u * v + es * (v + xc)) / (1 - es)
+            formed = bound * (p + v) * (1 - u) ** 2        # two roundings down
+            assert off <= formed, (float(v), float(off / u), float(formed / u))
