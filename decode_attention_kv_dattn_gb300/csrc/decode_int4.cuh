@@ -17,10 +17,15 @@
 // Precision: that of fp32 sums (1.0 - 1.6e-7 of the outputs' size, against 64 bits).
 //  * q's factors and the weights p s enter as two fp16 terms, 22 bits, where fp16 holds
 //    them: q is scaled by a power of two that brings the head's largest to 2^18 .. 2^19
-//    (2^14 .. 2^15 as a byte's factor, which is a sixteenth), the weights by f_G, a power of
-//    two that follows the largest step seen so far (step f_G in 2^6 .. 2^8), p being at
-//    most 2^6: the running maximum is only moved when a score passes it by 6, which saves
-//    the cross-lane maximum of every group of keys.
+//    (2^14 .. 2^15 as a byte's factor, which is a sixteenth), the weights by f_hG, a power of
+//    two for each head and group that keeps the largest p s of what has been summed in
+//    2^5 .. 2^15. It follows the product, up and down: a key may have a step as large as it
+//    likes beside no weight, in one head or in all, and takes no bits from the others'. (With
+//    f of the largest step alone, a value 2^24 times the others' size and of no weight cost
+//    the outputs 3e-3 of theirs, one of 2^32 all.) The running maximum is a whole number and
+//    only moved when a score passes it by 6 (p is at most 2^6), and the products are only
+//    looked at where a step times f is above 2^9, which saves the cross-lane maxima of every
+//    group of keys.
 //  * An MMA lines its products up by the operands' exponents and drops what lies below, and
 //    a subnormal operand counts as 2^-14 there, however small. A code masked out of its
 //    word is a subnormal, c 2^-24: as it is it costs c0's products 6 bits and the bytes' 2.
@@ -148,7 +153,7 @@ struct Int4Warp {
   float qsum[NT][NG], inv[NT];
   float o[MT][NT][4];
   float m[NT], l[NT], cst[NT][NG];  // base-2 maximum, sum of weights, sum of p (b + 8 s)
-  float f[NG];                      // power of two of the weights of group G
+  float f[NT][NG];                  // power of two of the weights of the lane's head and group G
 
   // The fragments into shared memory (kSharedQ), and the warp's own part of them.
   static __device__ __forceinline__ void put_query(const float* qs, uint8_t* dst, int lane) {
@@ -197,10 +202,11 @@ struct Int4Warp {
       m[nt] = -INFINITY;
       l[nt] = 0.f;
 #pragma unroll
-      for (int G = 0; G < NG; ++G) cst[nt][G] = 0.f;
+      for (int G = 0; G < NG; ++G) {
+        cst[nt][G] = 0.f;
+        f[nt][G] = 0x1p100f;
+      }
     }
-#pragma unroll
-    for (int G = 0; G < NG; ++G) f[G] = 0x1p100f;
   }
 
   // The steps of keys g and g + 8 of a block's values, groups G and G + 1, and the least values.
@@ -210,12 +216,16 @@ struct Int4Warp {
     st[1] = bf16_hi(p.y), ls[1] = bf16_lo(p.y);
   }
 
-  // A score passed its head's maximum by 6, or a step its group's scale: both are
-  // brought up to date and what was summed so far is rescaled.
+  // 2^(e - 127), or 0 where that is no normal number (e < 1).
+  static __device__ __forceinline__ float power(int e) { return e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f; }
+
+  // A score passed its head's maximum by 6, or a weight p s may pass its scale: both are
+  // brought up to date and what was summed so far is rescaled, by powers of two. The
+  // maximum's rise by d makes all of the past 2^-d times as large, which f takes back
+  // as far as the new keys let it. (Large steps of keys of little weight change nothing.)
   template <int N>
   __device__ __forceinline__ void rescale(const float (&s)[N][NT][2], const uint8_t* vb, int pitch, int g) {
     constexpr unsigned full = 0xffffffffu;
-    float fac[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float mx = m[nt];
@@ -223,38 +233,34 @@ struct Int4Warp {
       for (int b = 0; b < N; ++b) mx = fmaxf(mx, fmaxf(s[b][nt][0], s[b][nt][1]));
       mx = fmaxf(mx, __shfl_xor_sync(full, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(full, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(full, mx, 16));
-      fac[nt] = mx == -INFINITY ? 1.f : exp2_fast(m[nt] - mx);
+      mx = ceilf(fmaxf(mx, __shfl_xor_sync(full, mx, 16)));
+      const int d = mx == m[nt] ? 0 : static_cast<int>(fminf(mx - m[nt], 1000.f));
+      const float fac = power(127 - d);
       m[nt] = mx;
-      l[nt] *= fac[nt];
-    }
+      l[nt] *= fac;
+      const float ms = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      float x = 0.f;
+      for (int G = 0; G < NG; ++G) {
+        cst[nt][G] *= fac;
+        float x = 0.f;  // the largest p s of the new keys
 #pragma unroll
-      for (int b = 0; b < N; ++b)
+        for (int b = 0; b < N; ++b)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          x = fmaxf(x, bf16_hi(*reinterpret_cast<const uint32_t*>(vb + b * pitch + 8 * D + (g + 8 * i) * (4 * NG) + G * 4)));
-      x = fmaxf(x, __shfl_xor_sync(full, x, 4));
-      x = fmaxf(x, __shfl_xor_sync(full, x, 8));
-      x = fmaxf(x, __shfl_xor_sync(full, x, 16));
-      float ratio = 1.f;
-      if (x * f[G] > 256.f) {
-        // x f in 2^6 .. 2^7
-        const int e = 260 - static_cast<int>(__float_as_uint(x) >> 23);
-        const float fn = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 227)) << 23);
-        ratio = fn * (1.f / f[G]);
-        f[G] = fn;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        cst[nt][G] *= fac[nt];
-        const float r = fac[nt] * ratio;
+          for (int i = 0; i < 2; ++i)
+            x = fmaxf(x, exp2_fast(s[b][nt][i] - ms) *
+                             bf16_hi(*reinterpret_cast<const uint32_t*>(vb + b * pitch + 8 * D + (g + 8 * i) * (4 * NG) + G * 4)));
+        x = fmaxf(x, __shfl_xor_sync(full, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(full, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(full, x, 16));
+        // the past's stays where it is, or x f in 2^5 .. 2^6 if that is less
+        const int e = static_cast<int>(__float_as_uint(f[nt][G]) >> 23);
+        const int en = max(min(min(e + d, 227), x > 0.f ? 259 - static_cast<int>(__float_as_uint(x) >> 23) : 227), 1);
+        f[nt][G] = power(en);
+        const float r = power(127 + en - e - d);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[G * 4 + j][nt][e] *= r;
+          for (int i = 0; i < 4; ++i) o[G * 4 + j][nt][i] *= r;
       }
     }
   }
@@ -345,7 +351,7 @@ struct Int4Warp {
       }
     }
     // ---- do the maximum and the weights' scales still hold?
-    float top = 0.f;
+    float top[NT];  // the lane's largest step, times f
     {
       uint32_t mx[NG];
 #pragma unroll
@@ -362,25 +368,26 @@ struct Int4Warp {
             mx[G + 1] = max(mx[G + 1], p.y);
           }
 #pragma unroll
-      for (int G = 0; G < NG; ++G) top = fmaxf(top, __uint_as_float(mx[G] & 0xffff0000u) * f[G]);
-    }
-    bool move = top > 256.f;
-#pragma unroll
-    for (int b = 0; b < N; ++b) {
-#pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        top[nt] = 0.f;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) top[nt] = fmaxf(top[nt], __uint_as_float(mx[G] & 0xffff0000u) * f[nt][G]);
+      }
+    }
+    bool move = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
         s[b][nt][0] *= inv[nt];
         s[b][nt][1] *= inv[nt];
-      }
-      if (mask[b] != 0xffffu) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        if (mask[b] != 0xffffu) {
           if (!((mask[b] >> g) & 1u)) s[b][nt][0] = -INFINITY;
           if (!((mask[b] >> (g + 8)) & 1u)) s[b][nt][1] = -INFINITY;
         }
+        move = move || fmaxf(s[b][nt][0], s[b][nt][1]) > m[nt] + 6.f;
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) move = move || fmaxf(s[b][nt][0], s[b][nt][1]) > m[nt] + 6.f;
+      move = move || top[nt] > 512.f;
     }
     if (__any_sync(full, move)) rescale<N>(s, vb, pitch, g);
 #pragma unroll
@@ -415,7 +422,7 @@ struct Int4Warp {
             const float p0 = s[b][nt][0], p1 = s[b][nt][1];
             cst[nt][G + k] = fmaf(p0, fmaf(8.f, s0[b][k], l0[b][k]), fmaf(p1, fmaf(8.f, s1[b][k], l1[b][k]), cst[nt][G + k]));
             uint32_t hi, lo;
-            split_f16x2(p0 * (s0[b][k] * f[G + k]), p1 * (s1[b][k] * f[G + k]), hi, lo);
+            split_f16x2((p0 * s0[b][k]) * f[nt][G + k], (p1 * s1[b][k]) * f[nt][G + k], hi, lo);
             pb[b][nt][0] = transposed(prmt(hi, lo, 0x5410u));
             pb[b][nt][1] = transposed(prmt(hi, lo, 0x7632u));
           }
@@ -465,7 +472,7 @@ struct Int4Warp {
         c += __shfl_xor_sync(full, c, 4);
         c += __shfl_xor_sync(full, c, 8);
         c += __shfl_xor_sync(full, c, 16);
-        const float back = 1.f / f[G];
+        const float back = 1.f / f[nt][G];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float4 v;

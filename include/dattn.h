@@ -114,7 +114,8 @@ enum {
  *      + (r % 2) 2 + (d % 4) / 2
  * and the group's least value and step (bf16 each) at byte 8 D + (r D / 64 + d / 64) 4.
  * What lies in a block beside the tokens written is never read as a value. Decode
- * takes keys below 2^98 in magnitude (the scores of larger ones may pass fp32). */
+ * takes keys and values below 2^98 in magnitude (scores and sums of larger ones may pass
+ * fp32), values of any size beside one another. */
 #define DATTN_INT4_BYTES(P, D) ((P) / 16 * 9 * (D))
 
 /* cudaStream_t without including the CUDA headers. */
