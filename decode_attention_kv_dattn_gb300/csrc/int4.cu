@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) int4_append_kernel(const Ap
 //
 // What these kernels write is the caller's, who may give it to a decode as its new token,
 // and a decode reads its inputs before it waits for the launch ahead of it: the launch
-// behind them is made in the stream's full order (launch_order.h), and no signal of theirs
-// would let it start earlier.
+// behind them is made in the stream's full order (launch_order.h), unless it waits before
+// all else.
 
 // Two codes (low 4 bits of each half of w) to their values as a bf16 pair, rounded
 // once: the codes become bf16 by their place in 128..143, exactly.
@@ -470,16 +470,16 @@ cudaError_t launch_append_int4(const AppendArgs& a, cudaStream_t s) {
   const bool rot = a.rotate && (a.r > 0 || a.k_norm);
   auto k = a.D == 128 ? (rot ? int4_append_kernel<128, true> : int4_append_kernel<128, false>)
                       : (rot ? int4_append_kernel<256, true> : int4_append_kernel<256, false>);
-  return launch_pdl(k, grid, block, 0, s, a);
+  return launch_pdl_waiting(k, grid, block, 0, s, a);
 }
 
 cudaError_t launch_read(const ReadArgs& a, bool int4, bool f8, cudaStream_t s) {
   if (int4) {
     const dim3 grid(block_count(a.Tmax), a.B), block(32 * (2 * a.Hkv < kMaxWarps ? 2 * a.Hkv : kMaxWarps));
-    return launch_pdl(a.D == 128 ? int4_read_kernel<128> : int4_read_kernel<256>, grid, block, 0, s, a);
+    return launch_pdl_waiting(a.D == 128 ? int4_read_kernel<128> : int4_read_kernel<256>, grid, block, 0, s, a);
   }
   const dim3 grid((static_cast<unsigned>(a.Tmax) + kMaxWarps - 1) / kMaxWarps, a.B);
-  return launch_pdl(f8 ? read_kernel<true> : read_kernel<false>, grid, dim3(kMaxWarps * 32), 0, s, a);
+  return launch_pdl_waiting(f8 ? read_kernel<true> : read_kernel<false>, grid, dim3(kMaxWarps * 32), 0, s, a);
 }
 
 }  // namespace dattn

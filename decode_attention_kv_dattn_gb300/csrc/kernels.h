@@ -433,7 +433,8 @@ bool prev_launch_writes(void* stream, const void* cache_k);
 // `cache_k` (null: writes no cache), or one whose results may be the next call's inputs.
 void record_launch(void* stream, const void* cache_k);
 void record_results(void* stream);
-// Whether the next launch on `stream` is made in the stream's full order, and that it was.
+// Whether the next launch on `stream` has to come behind the whole of the last one, and
+// that one has been made that does.
 bool launch_in_order(void* stream);
 void launch_started(void* stream);
 
@@ -452,13 +453,9 @@ cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-// Launch with programmatic stream serialization: the kernel may begin while
-// its predecessor in the stream finishes; every kernel here waits on the
-// predecessor (griddepcontrol.wait) before it touches the predecessor's output -
-// except for what is its input, so behind a launch of such results it has no such leave.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
+cudaError_t launch_as(bool programmatic, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                      cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -468,10 +465,30 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = programmatic ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Launch with programmatic stream serialization: the kernel may begin while
+// its predecessor in the stream finishes; every kernel here waits on the
+// predecessor (griddepcontrol.wait) before it touches the predecessor's output -
+// except for what is its input, so behind a launch of such results it has no such leave.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Args&&... args) {
   const bool in_order = launch_in_order(stream);
-  cfg.numAttrs = in_order ? 0 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  const cudaError_t e = launch_as(!in_order, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
   if (in_order && e == cudaSuccess) launch_started(stream);
+  return e;
+}
+
+// The same of a kernel that reads nothing at all before it waits: behind such a launch it
+// may begin early, and what it lets begin in turn comes after its wait.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_waiting(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t stream, Args&&... args) {
+  const cudaError_t e = launch_as(true, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+  if (e == cudaSuccess) launch_started(stream);
   return e;
 }
 

@@ -36,7 +36,8 @@ class LaunchOrder {
     const Last l = get(stream);
     return l.written != nullptr && l.written == cache_k;
   }
-  // Whether the next launch has to wait for the whole of the last one before it starts.
+  // Whether the next launch has to wait for the whole of the last one before it starts
+  // (or, in the kernel, before it reads anything).
   bool in_order(const void* stream) const { return get(stream).results; }
   // A launch that waits so has been made: those behind it need not.
   void started(const void* stream) {

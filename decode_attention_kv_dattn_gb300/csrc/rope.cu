@@ -375,7 +375,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s, bool pdl) {
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   if (a.Hkv > kMaxAppendHeads) return cudaErrorNotSupported;
   dim3 grid(a.Tmax, a.B);
-  return launch_pdl(append_kernel, grid, dim3(kRopeThreads), 0, s, a);
+  return launch_pdl_waiting(append_kernel, grid, dim3(kRopeThreads), 0, s, a);
 }
 
 }  // namespace dattn

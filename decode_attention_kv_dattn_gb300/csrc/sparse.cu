@@ -1526,7 +1526,7 @@ cudaError_t launch_summarize(const SummarizeArgs& a, int D, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((pages * a.Hkv + 7) / 8), a.B);
   auto k = D == 128 ? (a.f8 ? summarize_kernel<128, true> : summarize_kernel<128, false>)
                     : (a.f8 ? summarize_kernel<256, true> : summarize_kernel<256, false>);
-  return launch_pdl(k, grid, dim3(256), 0, s, a);
+  return launch_pdl_waiting(k, grid, dim3(256), 0, s, a);
 }
 
 // Threads of the score and selection kernel: 16 warps for long streams, whose
