@@ -366,6 +366,7 @@ int int4_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decod
   a.counters = h->counters[half];
   a.err = h->err;
   a.early = !prev_launch_writes(s, cache->k);
+  a.late = launch_in_order(s);
   a.wait_ns = h->wait_ns;
   a.debug_flags = h->debug_flags;
   a.q_norm = h->q_norm[layer];

@@ -525,12 +525,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) int4_decode_kernel(co
   const int b0 = first_block(P, U, kUnitCost, weight, worker, NC * W, lane);
   const int nb = first_block(P, U, kUnitCost, weight, worker + 1, NC * W, lane) - b0;
   const int u_first = nb > 0 ? unit_at(P, U, 0, b0, lane) : U;
-  // the inputs first: every warp's, ahead of any warp's blocks
-  if (nb > 0 && lane == 0) stage_inputs<D, GP>(args, u_first, b0 == P[u_first], smem_addr(scratch), inbar);
-
   // Ordering with the preceding launch on the stream: as decode_kernel. Inputs, metadata
-  // and this call's half of the workspace are not written by it; the cache may be read
-  // early where it does not write that; outputs and the write-back come after the wait.
+  // and this call's half of the workspace are not written by it (but for inputs that it
+  // reads back: then they wait); the cache may be read early where it does not write that;
+  // outputs and the write-back come after the wait.
   bool waited = false;
   auto wait_prev = [&]() {
     if (!waited) {
@@ -539,6 +537,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) int4_decode_kernel(co
       waited = true;
     }
   };
+  if (args.late) wait_prev();
+  // the inputs first: every warp's, ahead of any warp's blocks
+  if (nb > 0 && lane == 0) stage_inputs<D, GP>(args, u_first, b0 == P[u_first], smem_addr(scratch), inbar);
+
   if (!args.early) wait_prev();
 
   // ---- copies: the pool blocks of the range 32 at a time, a block a lane (the current
@@ -743,7 +745,8 @@ cudaError_t launch(const Int4DecodeArgs& a, int ctas, cudaStream_t s) {
   const cudaError_t e = opt_in_smem(k, Gm::SMEM_MAX, opted);
   if (e != cudaSuccess) return e;
   const size_t smem = 128 + Gm::TAB_OFF + (2 * a.B * a.Hkv + 1) * sizeof(int);
-  return launch_pdl(k, dim3(ctas), dim3(Gm::THREADS), smem, s, a);
+  return a.late ? launch_pdl_waiting(k, dim3(ctas), dim3(Gm::THREADS), smem, s, a)
+                : launch_pdl(k, dim3(ctas), dim3(Gm::THREADS), smem, s, a);
 }
 
 }  // namespace

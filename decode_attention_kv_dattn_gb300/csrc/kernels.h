@@ -146,6 +146,7 @@ struct Int4DecodeArgs {
   int* counters;               // [B*Hkv] CTAs done with a unit, then [ctas] of groups; zero between calls
   int* err;
   int early;                   // as DecodeArgs::early
+  int late;                    // the launch before may be writing the inputs: they are fetched after the wait
   uint64_t wait_ns;
   int debug_flags;
   const uint16_t* q_norm;      // [D] or null
@@ -482,7 +483,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return e;
 }
 
-// The same of a kernel that reads nothing at all before it waits: behind such a launch it
+// The same of a kernel that reads no inputs before it waits: behind such a launch it
 // may begin early, and what it lets begin in turn comes after its wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_waiting(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,

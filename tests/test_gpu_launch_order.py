@@ -1,7 +1,7 @@
 """The order in which a captured run of calls is launched: behind a read-back, whose rows
-may be the next call's inputs, a kernel waits for the whole of it, unless it reads nothing
-before it waits (append, read-back); behind a decode it may start while that ends. Read
-from the graph's edges; nothing is launched."""
+may be the next call's inputs, a kernel waits for the whole of it, unless it reads no
+inputs before it waits (append, read-back, a 4-bit layer's decode); behind a decode it may
+start while that ends. Read from the graph's edges; nothing is launched."""
 import ctypes
 
 import pytest
@@ -54,7 +54,7 @@ def test_what_follows_a_read_back_waits_for_all_of_it(fmt):
     append = lambda i: h.append_kv(i, caches[i], k, v, z, one, rotate=False)  # noqa: E731
     verify = lambda i: h.verify(i, caches[i], qq, kk, kk, parent, wide, write_back=False)  # noqa: E731
     runs = [
-        (lambda: (decode(1), read(), decode(1), decode(2), read(), decode(2), read(), append(1), decode(2)), [1, 0, 1, 1, 0, 1, 1, 1]),
+        (lambda: (decode(1), read(), decode(1), decode(2), read(), decode(2), read(), append(1), decode(2)), [1, 1, 1, 1, 0, 1, 1, 1]),
         (lambda: (read(), read(), verify(2)), [1, 0, 1, 1]),
     ]
     side = torch.cuda.Stream()
