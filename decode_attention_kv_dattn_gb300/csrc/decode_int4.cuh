@@ -376,18 +376,23 @@ struct Int4Warp {
     }
     bool move = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) move = move || top[nt] > 512.f;
 #pragma unroll
-      for (int b = 0; b < N; ++b) {
+    for (int b = 0; b < N; ++b) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         s[b][nt][0] *= inv[nt];
         s[b][nt][1] *= inv[nt];
-        if (mask[b] != 0xffffu) {
+      }
+      if (mask[b] != 0xffffu) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           if (!((mask[b] >> g) & 1u)) s[b][nt][0] = -INFINITY;
           if (!((mask[b] >> (g + 8)) & 1u)) s[b][nt][1] = -INFINITY;
         }
-        move = move || fmaxf(s[b][nt][0], s[b][nt][1]) > m[nt] + 6.f;
       }
-      move = move || top[nt] > 512.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) move = move || fmaxf(s[b][nt][0], s[b][nt][1]) > m[nt] + 6.f;
     }
     if (__any_sync(full, move)) rescale<N>(s, vb, pitch, g);
 #pragma unroll
