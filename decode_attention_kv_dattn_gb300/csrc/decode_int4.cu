@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) int4_decode_kernel(co
       float* state = whole || (last && failed) ? scratch
                      : last                    ? reinterpret_cast<float*>(ring)
                                                : args.wpart + static_cast<int64_t>(worker) * Gm::STATE;
-      q4.finish(state, state + GP * D, true, GP, lane);
+      q4.finish(state, state + GP * D, GP, lane);
       if (!whole && lane == 0) SEG[2 * warp + (last ? 1 : 0)] = u;
     }
     if (from_start && to_end) {

@@ -161,12 +161,10 @@ struct Int4Warp {
     float s[NT][NG], v[NT];
     int4_query<D, NT>(qs, lane, q, s, v);
     __syncwarp();  // (dst may be where qs is)
+    static_assert(!kSharedQ || NT == 2, "16 bytes of a lane: a k-step's two column tiles");
 #pragma unroll
-    for (int i = 0; i < KS * NT / 2; ++i) {  // (a k-step's two column tiles, or two k-steps)
-      const uint32_t(&a)[2] = q[NT == 2 ? i : 2 * i][0];
-      const uint32_t(&b)[2] = q[NT == 2 ? i : 2 * i + 1][NT - 1];
-      *reinterpret_cast<uint4*>(dst + i * 512 + lane * 16) = make_uint4(a[0], a[1], b[0], b[1]);
-    }
+    for (int i = 0; i < KS; ++i)
+      *reinterpret_cast<uint4*>(dst + i * 512 + lane * 16) = make_uint4(q[i][0][0], q[i][0][1], q[i][NT - 1][0], q[i][NT - 1][1]);
     float* x = reinterpret_cast<float*>(dst + KS * 256 * NT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -309,15 +307,11 @@ struct Int4Warp {
         float acc[N][NT][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint4 v1 = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (kSharedQ && NT == 1) v1 = *reinterpret_cast<const uint4*>(qf + (G * 2 + j) * 512 + lane * 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int ks = (G * 2 + j) * 2 + i;
             uint32_t q[NT][2];
-            if constexpr (kSharedQ && NT == 1) {
-              q[0][0] = i ? v1.z : v1.x, q[0][1] = i ? v1.w : v1.y;
-            } else if constexpr (kSharedQ) {
+            if constexpr (kSharedQ) {
               const uint4 v = *reinterpret_cast<const uint4*>(qf + ks * 512 + lane * 16);
               q[0][0] = v.x, q[0][1] = v.y, q[NT - 1][0] = v.z, q[NT - 1][1] = v.w;
             } else {
@@ -458,7 +452,7 @@ struct Int4Warp {
   }
 
   // The state: outputs [4 NT][D] relative to m, and m and l of each head.
-  __device__ __forceinline__ void finish(float* os, float* ml, bool any, int GP, int lane) {
+  __device__ __forceinline__ void finish(float* os, float* ml, int GP, int lane) {
     constexpr unsigned full = 0xffffffffu;
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -467,10 +461,9 @@ struct Int4Warp {
       l[nt] += __shfl_xor_sync(full, l[nt], 8);
       l[nt] += __shfl_xor_sync(full, l[nt], 16);
       if (g == 0) {
-        ml[4 * nt + t] = any ? m[nt] : -INFINITY;
-        ml[GP + 4 * nt + t] = any ? l[nt] : 0.f;
+        ml[4 * nt + t] = m[nt];
+        ml[GP + 4 * nt + t] = l[nt];
       }
-      if (!any) continue;
 #pragma unroll
       for (int G = 0; G < NG; ++G) {
         float c = cst[nt][G];
