@@ -372,7 +372,7 @@ int int4_call(dattn_t* h, int layer, const dattn_cache* cache, const dattn_decod
   a.q_norm = h->q_norm[layer];
   a.k_norm = h->k_norm[layer];
   a.norm_eps = L.norm_eps;
-  const int ctas = int4_decode_ctas(units, n_max, h->D, h->num_sms);
+  const int ctas = int4_decode_ctas(units, n_max, h->D, h->GP, h->num_sms);
   const int rc = cuda_status(launch_decode_int4(a, h->D, ctas, s), "4-bit decode");
   if (rc == DATTN_OK) {
     record_launch(s, args->write_back ? cache->k : nullptr);

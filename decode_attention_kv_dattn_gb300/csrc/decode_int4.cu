@@ -64,9 +64,12 @@ struct Geo4 {
   // Warps, blocks of a stage, stages of a warp's ring. Two blocks are taken at once: their
   // chains of dependent steps overlap (one at a time, 8 x 262,144 tokens 193 -> 208 us
   // before the operands were made precise). 256-wide heads then need up to 255 registers,
-  // which leaves 8 warps (12 with one block a stage: 220 us then); 128-wide ones fit 168 and
-  // 12 warps (8: 48.1 -> 51.8 us on 64 ragged).
-  static constexpr int W = D == 256 ? 8 : 12;
+  // which leaves 8 warps (12 with one block a stage: 220 us then). 128-wide ones of up to 4
+  // queries fit 168 and 12 warps (8: 48.1 -> 51.8 us on 64 ragged); with a second column tile
+  // 168 spill, and 8 warps are faster (12 -> 8: 64 / 8 heads, 64 ragged streams 91 -> 86 us and
+  // 16 x 16,384 tokens 109.7 -> 107.8; 8 / 1, 8 x 262,144 109.6 -> 107.3, 64 ragged 23.0 -> 21.4;
+  // 6 / 1, 32 x 16,384 39.6 -> 36.3; one stream of 5,003 13.9 -> 12.9).
+  static constexpr int W = D == 256 || NT == 2 ? 8 : 12;
   static constexpr int KG = 2;
   static constexpr int NS = D == 256 ? 2 : 3;
   static constexpr int THREADS = W * 32;
@@ -751,15 +754,16 @@ cudaError_t launch(const Int4DecodeArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-int int4_decode_ctas(int units, int n_max, int D, int num_sms) {
-  const int W = D == 256 ? Geo4<256, 1>::W : Geo4<128, 1>::W;
+int int4_decode_ctas(int units, int n_max, int D, int GP, int num_sms) {
+  const int W = D == 256 ? Geo4<256, 1>::W : GP == 4 ? Geo4<128, 1>::W : Geo4<128, 2>::W;
   const int64_t blocks = static_cast<int64_t>(units) * ((static_cast<int64_t>(n_max) + kInt4Block - 1) / kInt4Block + kUnitCost);
   const int64_t ctas = (blocks + kMinBlocks * W - 1) / (kMinBlocks * W);
   return static_cast<int>(ctas < 1 ? 1 : ctas > num_sms ? num_sms : ctas);
 }
 
 cudaError_t launch_decode_int4(const Int4DecodeArgs& args, int D, int ctas, cudaStream_t s) {
-  static_assert(Geo4<128, 1>::W <= kInt4Warps && Geo4<256, 1>::W <= kInt4Warps, "the workspace's warps");
+  static_assert(Geo4<128, 1>::W <= kInt4Warps && Geo4<128, 2>::W <= kInt4Warps && Geo4<256, 1>::W <= kInt4Warps &&
+                    Geo4<256, 2>::W == Geo4<256, 1>::W, "the workspace's warps");
   Int4DecodeArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kDefaultWaitNs;
   const int GP = decode_group_pad(a.G);

@@ -380,7 +380,7 @@ cudaError_t launch_read(const ReadArgs& a, bool int4, bool f8, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeArgs& a, int D, int GP, int ctas, cudaStream_t s, bool pdl);
 // decode over a 4-bit cache: CTAs of a call, the floats of a warp's state and the bytes of
 // a unit's token in the workspace (per (stream, KV head)), the most warps of a CTA.
-int int4_decode_ctas(int units, int n_max, int D, int num_sms);
+int int4_decode_ctas(int units, int n_max, int D, int GP, int num_sms);
 constexpr size_t int4_token_bytes(int D, int GP) { return 8 * static_cast<size_t>(GP) + D + D / 8; }
 constexpr int kInt4Warps = 12;
 cudaError_t launch_decode_int4(const Int4DecodeArgs& a, int D, int ctas, cudaStream_t s);
