@@ -266,6 +266,8 @@ class Handle:
         # (4-bit layers: heads and bytes of a page)
         self._int4 = {i: [num_kv_heads, l.get("page_size", 0) // 16 * 9 * head_dim] for i, l in enumerate(layers)
                       if l.get("kv_format", KV_BF16) == KV_INT4}
+        self._page_bytes = {i: num_kv_heads * l.get("page_size", 0) * head_dim * (1 if l.get("kv_format", KV_BF16) == KV_E4M3 else 2)
+                            for i, l in enumerate(layers) if l["kind"] == CACHE_PAGED}
         self.config = Config(num_q_heads, num_kv_heads, head_dim, max_streams, max_context,
                              max_verify_rows, len(layers), self._layers, max_selected_pages)
         h = _vp()
@@ -308,7 +310,8 @@ class Handle:
             return  # (a descriptor of the caller's own)
         pages = getattr(cache, "_int4", None)
         if layer not in self._int4:
-            if pages is not None and len(pages) == 2:
+            # (an E4M3 layer's bytes may be flat too: as many of them as its pages have)
+            if pages is not None and len(pages) == 2 and pages[0] * pages[1] != self._page_bytes.get(layer):
                 raise ValueError(f"layer {layer} is not a 4-bit layer, its call has int4_pool's pools")
         elif pages != self._int4[layer]:
             k, v = cache._tensors[:2]

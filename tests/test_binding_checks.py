@@ -151,3 +151,23 @@ def test_4_bit_pools_stay_off_other_layers(dattn, monkeypatch):
     # (a byte pool of an E4M3 layer is none)
     e4m3 = torch.zeros(9, 2, 16, 128, dtype=torch.uint8)
     h._check_pools(1, dattn.paged_cache(e4m3, e4m3.clone(), *row))
+
+
+def test_byte_pools_of_a_layers_own_pages_are_no_4_bit_pools(dattn, monkeypatch):
+    """An E4M3 layer's bytes (or a bf16 layer's, viewed so) with a head's rows flat: as many as its pages have."""
+    monkeypatch.setattr(dattn, "_ptr", lambda t: None)
+    monkeypatch.setattr(dattn.lib, "dattn_create", lambda cfg, dev, out: dattn.OK)
+    H, P, D = 2, 16, 128
+    h = dattn.Handle(8, H, D, [{"kind": dattn.CACHE_PAGED, "page_size": P},
+                               {"kind": dattn.CACHE_PAGED, "page_size": P, "kv_format": dattn.KV_E4M3, "k_scale": 1.0, "v_scale": 1.0}],
+                     4, max_context=64, device=0)
+    h._h = ctypes.c_void_p()
+    row = torch.zeros(4, 4, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    for layer, size in ((0, 2), (1, 1)):
+        for shape in ((9, H, P * D * size), (9, H * P, D * size), (9, H, P, D * size)):
+            pool = torch.zeros(shape, dtype=torch.uint8)
+            h._check_pools(layer, dattn.paged_cache(pool, pool.clone(), *row))
+        for few in (P * D * size - 1, P // 16 * 9 * D, P * D * size + 16):
+            pool = torch.zeros(9, H, few, dtype=torch.uint8)
+            with pytest.raises(ValueError, match="4-bit"):
+                h._check_pools(layer, dattn.paged_cache(pool, pool.clone(), *row))
