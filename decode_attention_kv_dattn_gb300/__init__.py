@@ -188,6 +188,7 @@ def ring_cache(k, v, ring_head, ring_count, stream_rows=None) -> Cache:
     c = Cache(_ptr(k), _ptr(v), k.shape[0], _ptr(ring_head), _ptr(ring_count),
               _ptr(stream_rows), None, 0, None)
     c._tensors = (k, v, ring_head, ring_count, stream_rows)
+    c._rows = None if stream_rows is None else stream_rows.numel()  # streams it names rows for
     return c
 
 
@@ -197,6 +198,7 @@ def paged_cache(k, v, block_table, seq_len) -> Cache:
     c = Cache(_ptr(k), _ptr(v), k.shape[0], None, None, None, _ptr(block_table),
               block_table.shape[1], _ptr(seq_len))
     c._tensors = (k, v, block_table, seq_len)
+    c._rows = block_table.shape[0]
     # what a handle compares on every call of a 4-bit layer: heads and bytes of a page
     c._int4 = list(k.shape[1:]) if k.dtype is torch.uint8 and v.dtype is torch.uint8 and k.shape == v.shape else None
     return c
@@ -336,6 +338,9 @@ class Handle:
                              f"{v.dtype} {tuple(v.shape)}")
         if start_index.dtype is not _I32 or count.dtype is not _I32 or start_index.numel() != B or count.numel() != B:
             raise ValueError("start_index, count: int32 [B]")
+        rows = getattr(cache, "_rows", None)
+        if rows is not None and rows < B:
+            raise ValueError(f"the cache names the pages or rows of {rows} streams, k and v have {B}")
         self._check_pools(layer, cache)
         _check(lib.dattn_read_kv(self._h, layer, ctypes.byref(cache), B, T, _ptr(start_index), _ptr(count), _ptr(k),
                                  _ptr(v), _stream_ptr(stream, self.device)), "dattn_read_kv")

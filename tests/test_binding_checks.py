@@ -171,3 +171,27 @@ def test_byte_pools_of_a_layers_own_pages_are_no_4_bit_pools(dattn, monkeypatch)
             pool = torch.zeros(9, H, few, dtype=torch.uint8)
             with pytest.raises(ValueError, match="4-bit"):
                 h._check_pools(layer, dattn.paged_cache(pool, pool.clone(), *row))
+
+
+def test_read_back_of_more_streams_than_the_cache_names(dattn, monkeypatch):
+    monkeypatch.setattr(dattn, "_ptr", lambda t: None)
+    monkeypatch.setattr(dattn.lib, "dattn_create", lambda cfg, dev, out: dattn.OK)
+    monkeypatch.setattr(dattn.lib, "dattn_read_kv", lambda *a: dattn.OK)
+    monkeypatch.setattr(dattn, "_stream_ptr", lambda stream, device=None: 0)
+    H, P, D = 2, 16, 128
+    h = dattn.Handle(8, H, D, [{"kind": dattn.CACHE_PAGED, "page_size": P}, {"kind": dattn.CACHE_RING, "ring_slots": 32},
+                               {"kind": dattn.CACHE_PAGED, "page_size": P, "kv_format": dattn.KV_INT4}], 4, max_context=64, device=0)
+    h._h = ctypes.c_void_p()
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    four = [dattn.int4_pool(9, H, P, D, device="cpu") for _ in range(2)]
+    caches = {0: [dattn.paged_cache(bf(9, H, P, D), bf(9, H, P, D), i32(3, 4), i32(1))],
+              1: [dattn.ring_cache(bf(9, H, 32, D), bf(9, H, 32, D), i32(9), i32(9), i32(3))],
+              2: [dattn.paged_cache(*four, i32(3, 4), i32(3))]}
+    for layer, (cache,) in caches.items():
+        h.read_kv(layer, cache, i32(3), i32(3), bf(3, 2, H, D), bf(3, 2, H, D))
+        h.read_kv(layer, cache, i32(1), i32(1), bf(1, 2, H, D), bf(1, 2, H, D))
+        with pytest.raises(ValueError, match="3 streams"):
+            h.read_kv(layer, cache, i32(4), i32(4), bf(4, 2, H, D), bf(4, 2, H, D))
+    # (rows named by their numbers: the library compares each with the pool's)
+    h.read_kv(1, dattn.ring_cache(bf(9, H, 32, D), bf(9, H, 32, D), i32(1), i32(1)), i32(4), i32(4), bf(4, 2, H, D), bf(4, 2, H, D))
