@@ -771,7 +771,7 @@ int dattn_append_kv(dattn_t* h, int layer, const dattn_cache* cache, int num_str
   if (rotate && L.rotary_dim > 0 && !start_pos) return DATTN_EINVAL;
   if (!aligned16(k) || !aligned16(v)) return DATTN_EINVAL;
   if (max_tokens == 0) return DATTN_OK;
-  if (max_tokens > 65535) return DATTN_EXCEEDS;
+  if (max_tokens > 65535 || num_streams > 65535) return DATTN_EXCEEDS;
   DeviceGuard guard(h->device);
   if (!guard.ok) return DATTN_ECUDA;
   AppendArgs a{};
