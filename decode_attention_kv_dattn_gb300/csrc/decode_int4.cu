@@ -29,7 +29,7 @@
 // read 32 blocks ahead, a block a lane, and handed on by shuffles.
 //
 // Measured (GB300, a call among others): 8 x 262,144 tokens of 8 / 2 heads of 256 248 us,
-// 4.9 TB/s; 1 x 1,048,576 135 us; 64 ragged streams 48 us; 32 x 16,384 of 24 / 4 heads 174.
+// 4.9 TB/s; 1 x 1,048,576 134 us; 64 ragged streams 48 us; 32 x 16,384 of 24 / 4 heads 176.
 // Of the first ~8 us pass before the first copies land and ~10 between the last block and
 // the last output.
 #include "decode_int4.cuh"

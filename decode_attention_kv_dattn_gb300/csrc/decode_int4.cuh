@@ -14,9 +14,10 @@
 // lane's score and output fragments belong to one head (t = lane % 4, and t + 4 with
 // NT = 2), and a head's hi + lo is one add without a shuffle.
 //
-// Precision: that of fp32 sums (1.0 - 1.6e-7 of the outputs' size, against 64 bits).
+// Precision: that of fp32 sums (0.9 - 1.2e-7 of the outputs' size, against 64 bits).
 //  * q's factors and the weights p s enter as two fp16 terms, 22 bits, where fp16 holds
-//    them: q is scaled by a power of two that brings the head's largest to 2^18 .. 2^19
+//    them (a dim of q is off by 2^-22 of itself, or 2^-29 of the head's largest where that
+//    is more): q is scaled by a power of two that brings the head's largest to 2^18 .. 2^19
 //    (2^14 .. 2^15 as a byte's factor, which is a sixteenth), the weights by f_hG, a power of
 //    two for each head and group that keeps the largest p s of what has been summed in
 //    2^5 .. 2^15. It follows the product, up and down: a key may have a step as large as it
@@ -38,8 +39,10 @@
 //    errors of 4e-5 over a million tokens.
 //  * The MMAs' sums are cut off, not rounded, so long chains shrink: each pair of blocks is
 //    summed from zero and added in fp32 (one chain: 7.5e-6 over 262,144 tokens).
-// All of it together takes 8 x 262,144 tokens from 198 to 253 us, 64 ragged streams from 42
-// to 48.
+// All of it together takes 8 x 262,144 tokens from 198 to 248 us, 64 ragged streams from 42
+// to 48, 32 x 16,384 of 24 / 4 heads from 148 to 176 (of it the scales of heads and products
+// instead of groups and steps 2). Where a step passes 2^9 / f in most blocks, as with 64
+// times the values' size in every second token and little weight there, 13% come on top.
 #pragma once
 
 #include "common.cuh"

@@ -191,9 +191,13 @@ __device__ __forceinline__ void key_words2(const KeyRow& a, int tok, int d0, con
 // One CTA per block of 16 tokens of a call row; its warps share out (KV head, K or V):
 // keys first, so that every warp of many heads has keys and values (a rotated key costs
 // twice a value, and warps with keys alone would share two of the SM's four schedulers).
-// Tokens that the call does not bring stay as they are. Issue-bound, ~20 instructions a
-// value: 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 219 us, where its
-// 660 MB take 98. With keys turned by rope_cos_sin, which is off by up to 1.5e-7 and moved 50
+// Tokens that the call does not bring stay as they are. Bound by issue (70% of the slots, ~20
+// instructions a value) and by loads that nothing of the warp's covers (the largest stall):
+// 64 ragged prompts (126,000 tokens of 8 heads of 128, rotated) 219 us, not rotated 145, where
+// their 660 MB take 98. Two kinds of keys cost more: a rotation whose half is not a multiple
+// of 16 has every dim of a key formed by key_exact (rotary_dim 40 / 80 595 /
+// 868 us, 64 204), and a key norm has a warp sum its 16 rows in fp64, one behind the other
+// (1,634 us not rotated, 1,772 rotated; 2 heads of 256 rotated by 64 104 -> 602). With keys turned by rope_cos_sin, which is off by up to 1.5e-7 and moved 50
 // of 65 million codes, 205 (3 instead of 4 CTAs an SM 224; keys and values by turns 233;
 // one side of a rotation in a lane 215), with one exact step behind the bound 255.
 template <int D, bool ROT>
