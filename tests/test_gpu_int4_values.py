@@ -5,9 +5,9 @@ Tolerance of one output, from the 64-bit softmax p and A_k, the largest value of
 output's group of 64 dims (what its grid's parts are of the size of): a score is off by
 e_k = (2^-22 + 4 sqrt(D) 2^-24) |q| . |k| / sqrt(D) at the most - q as two fp16 terms, fp32
 sums of D products taken as four times their walk of D roundings -, which moves an output by
-sum p_k e_k (A_k + A), A = sum p_k A_k; the weights' two fp16 terms (2^-22 of them, and 2^-33 of
-the largest product of weight and step, which A bounds, for each of up to 2,000 keys) and the
-fp32 sums are within 2^-20 A.
+sum p_k e_k (A_k + A), A = sum p_k A_k; the weights' two fp16 terms (2^-22 of them, or 2^-30 of
+the largest product of weight and step that their warp has met: for its 64 keys 2^-24 of what A
+has of them) and the fp32 sums are within 2^-20 A.
 """
 import numpy as np
 import pytest
